@@ -495,6 +495,138 @@ int moe_read_device_status(void* ws, void* stream);
 #define MOE_STALL_GRID_BARRIER 0x2u
 int moe_debug_stall(void* ws, uint32_t what, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Layer operators: what surrounds the block in a decoder layer.  The rows
+ * that enter the router are normed rows of a residual stream (decode.rs,
+ * encode_block; prefill.rs, pf_layer), the dense projections are products
+ * with quantised weights of the records' kind (prefill.rs: qmm), and the
+ * mixer reads a key/value cache.  One decoder layer over t rows runs
+ *   moe_add_rms_norm -> moe_qmv (q, k, v) -> moe_kv_append ->
+ *   moe_kv_attention -> moe_qmv -> moe_add_rms_norm -> moe_forward.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Residual addition and RMS norm, with an optional 8-bit output:
+ *
+ *   a[r][i] = x[r][i] + residual[r][i]            (residual NULL: a = x)
+ *   y[r][i] = a[r][i] / sqrt(mean_i a[r][i]^2 + eps) * gamma[i]
+ *
+ * in fp32, each output rounded once from it.  x, residual bf16 [t][h] with
+ * row strides in elements (multiples of 8, 0 allowed: one row for all);
+ * gamma bf16 [h].  Outputs, each optional but one at least:
+ *   sum    bf16 [t][h]: a; may be x's or residual's own rows (same stride h)
+ *   y      bf16 [t][h]
+ *   codes, scales: y in 8 bits, one scale per row and 64 channels: with
+ *          m = max |y| of the 64, scales fp32 [t][h/64] = m / 127 and codes
+ *          int8 [t][h] = y * 127 / m to the nearest whole number, ties to
+ *          even (m = 0: codes 0; m * 127 not finite: codes 0, scale NaN, so
+ *          that the group's values are NaN).  Both or neither; h % 64 == 0.
+ * 1 <= t <= 65536; h a multiple of 8 in [8, 16384].
+ * Errors: MOE_EINVAL, MOE_ESHAPE, MOE_ECUDA.
+ */
+int moe_add_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, int64_t residual_stride,
+                     const uint16_t* gamma, float eps, int32_t t, int32_t h, uint16_t* sum, uint16_t* y,
+                     int8_t* codes, float* scales, void* stream);
+
+/*
+ * Product of rows with 4-bit weights:  y[r][o] = sum_i x[r][i] * W[o][i],
+ * W[o][i] = q[o][i] * s[o][i/64] + b[o][i/64], the records' affine kind
+ * (moe_qweights, one row-major matrix): codes uint8 [n][k/2] with the low
+ * nibble at the even i, scales and biases fp16 [n][k/64].  The codes, scales
+ * and biases enter exactly (no rounding of W to bf16), products are summed
+ * in fp32 and the result is rounded once.
+ *
+ * Rows: x bf16 [t][k] with row stride x_stride (elements, a multiple of 8;
+ * x_codes and x_scales NULL), or 8-bit rows as moe_add_rms_norm writes them
+ * (x NULL; x_codes int8 [t][k], x_scales fp32 [t][k/64], contiguous).
+ * y: bf16 [t][n], or fp32 [t][n] when y_fp32 != 0.
+ * 1 <= t <= 65536, 1 <= n <= 1048576, k a multiple of 64 in [64, 65536].
+ * Errors: MOE_EINVAL, MOE_ESHAPE, MOE_ECUDA.
+ */
+int moe_qmv(const uint16_t* x, int64_t x_stride, const int8_t* x_codes, const float* x_scales,
+            const moe_qweights* w, int32_t t, int32_t n, int32_t k, void* y, int32_t y_fp32, void* stream);
+
+/*
+ * A paged key/value cache held in 8 bits, with one scale per block of
+ * `block` tokens and head (a page holds one block).  All arrays device,
+ * caller-owned:
+ *   codes  int8 [2][n_pages][hkv][block][d]: keys, then values
+ *   scales fp32 [2][n_pages][hkv]: a value stands for code * scale
+ *   tail   bf16 [n_seq][2][hkv][2*block][d]: the last tokens' keys and
+ *          values as given, token p at place p % (2*block): what a block
+ *          that is still filling is quantised from, each time it grows
+ *   table  int32 [n_seq][max_blocks]: page of each block of a sequence
+ *   lens   int32 [n_seq]: tokens of each sequence, the new ones included
+ * A call takes t new rows, sequence s owning rows starts[s] .. starts[s+1]-1
+ * (starts int32 [n_seq+1], device, starts[0] = 0, starts[n_seq] = t): its
+ * last starts[s+1] - starts[s] tokens.  A sequence may have none.
+ * d is 64 or 128; block 16, 32, 64 or 128.
+ */
+typedef struct {
+  int8_t* codes;
+  float* scales;
+  uint16_t* tail;
+  const int32_t* table;
+  const int32_t* lens;
+  int32_t n_seq;
+  int32_t n_pages;
+  int32_t max_blocks;
+  int32_t block;
+  int32_t hkv;
+  int32_t d;
+} moe_kv_cache;
+
+/*
+ * Write the new tokens' keys and values into the cache.  Every block that a
+ * sequence's new tokens touch is quantised as a whole from its tokens as
+ * given (those before the call from `tail`): m = max |v| over the block's
+ * tokens and channels of one head, scale = m / 127, code = v * 127 / m to
+ * the nearest whole number, ties to even; the places past the length become
+ * zero.  So the cache depends on its tokens alone, not on how many came per
+ * call, and a sequence may be cut back by up to `block` tokens (smaller
+ * lens) and continued.  `tail` then holds the new tokens of the last two
+ * blocks.
+ *
+ * k, v: bf16 [t][hkv][d], heads contiguous, rows `k_stride`, `v_stride`
+ * elements apart (multiples of 8).  A key or value whose 127-fold is not
+ * finite is stored as zero and raises MOE_EDEVICE in moe_read_device_status, as do
+ * lens, starts or page ids out of range, whose blocks are skipped.
+ * ws: moe_kv_workspace_bytes() bytes, set to zero once before its first use.
+ * Two sequences must not share a page that either of them still writes.
+ * Errors: MOE_EINVAL, MOE_ESHAPE, MOE_EWORKSPACE, MOE_ECUDA.
+ */
+int moe_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* starts,
+                  int32_t t, const moe_kv_cache* cache, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Causal attention of the new rows over the cache (after moe_kv_append of
+ * the same rows).  Row i of a sequence's n new ones stands at position
+ * p = lens - n + i and sees the positions 0 .. p:
+ *
+ *   out[r][a] = sum_j exp(z_j - max z) * v_j / sum_j exp(z_j - max z),
+ *   z_j = scale * (q[r][a] . k_j),   head a reading key/value head a / (hq / hkv),
+ *
+ * keys and values being code * scale.  Codes enter the products exactly;
+ * scores, statistics and sums are fp32, the weights are rounded to fp16
+ * (2^-12 of each) for the second product.  The order of the sums depends on
+ * the sizes and lengths only, never on timing.
+ *
+ * q bf16 [t][hq][d], heads contiguous, rows `q_stride` elements apart (a
+ * multiple of 8); out bf16 [t][hq][d].  hq a multiple of hkv.  The rows
+ * of a sequence whose lens or starts are out of range are left unwritten, and
+ * a page id out of range hides its block's tokens (a row left without any
+ * becomes zero); both raise MOE_EDEVICE in moe_read_device_status.
+ * ws: moe_kv_workspace_bytes() bytes, set to zero once before its first use;
+ * calls that share it are ordered on one stream.
+ * Errors: MOE_EINVAL, MOE_ESHAPE, MOE_EWORKSPACE, MOE_ECUDA.
+ */
+int moe_kv_attention(const uint16_t* q, int64_t q_stride, const int32_t* starts, int32_t t, int32_t hq, float scale,
+                     const moe_kv_cache* cache, uint16_t* out, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moe_kv_append and moe_kv_attention on the current
+ * device for caches of width d (one buffer serves both); 0 on a bad d. */
+size_t moe_kv_workspace_bytes(int32_t d);
+
 /*
  * Launch accounting (benchmark support; no counterpart in the method).
  * While enabled, every kernel the library launches is counted and

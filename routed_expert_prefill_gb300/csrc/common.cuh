@@ -21,6 +21,8 @@ enum : uint32_t {
   FLAG_BAD_ROW = 1u << 1,     // a CSR row index outside [0, t)
   FLAG_BAD_OFFSETS = 1u << 2, // CSR offsets not monotone / out of range
   FLAG_ROUTE_BOUND = 1u << 3, // a router score left its error bound
+  FLAG_BAD_CACHE = 1u << 4,   // cache lengths, starts or page ids out of range
+  FLAG_NOT_FINITE = 1u << 5,  // a key or value that is not finite reached the cache
   FLAG_TIMEOUT = 1u << 8,     // a bounded device wait gave up
 };
 

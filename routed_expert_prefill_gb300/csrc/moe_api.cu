@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "api_checks.cuh"
 #include "common.cuh"
 #include "experts.cuh"
 #include "residency.cuh"
@@ -136,12 +137,6 @@ int check_dims(const moe_dims* d) {
   return MOE_OK;
 }
 
-int check_ptr(const void* p, const char* name, size_t align, bool nullable = false) {
-  if (!p) return nullable ? MOE_OK : set_error(MOE_EINVAL, "%s is NULL", name);
-  if ((uintptr_t)p % align) return set_error(MOE_EINVAL, "%s is not %zu-byte aligned", name, align);
-  return MOE_OK;
-}
-
 int check_ws(const moe_dims* d, uint32_t flags, void* ws, size_t ws_bytes) {
   if (!ws) return set_error(MOE_EWORKSPACE, "workspace is NULL");
   if ((uintptr_t)ws % 256) return set_error(MOE_EWORKSPACE, "workspace is not 256-byte aligned");
@@ -150,17 +145,6 @@ int check_ws(const moe_dims* d, uint32_t flags, void* ws, size_t ws_bytes) {
     return set_error(MOE_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   return MOE_OK;
 }
-
-int cuda_status(cudaError_t e, const char* what) {
-  if (e == cudaSuccess) return MOE_OK;
-  return set_error(MOE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-#define TRY(expr)            \
-  do {                       \
-    int _s = (expr);         \
-    if (_s != MOE_OK) return _s; \
-  } while (0)
 
 }  // namespace
 
@@ -658,12 +642,15 @@ int moe_read_device_status(void* ws, void* stream) {
   TRY(cuda_status(cudaStreamSynchronize(s), "status clear sync"));
   if (st.flags & FLAG_TIMEOUT)
     return set_error(MOE_ETIMEOUT, "a bounded device wait gave up (site %u)", st.timeout_site);
-  if (st.flags & (FLAG_BAD_EXPERT | FLAG_BAD_ROW | FLAG_BAD_OFFSETS | FLAG_ROUTE_BOUND))
-    return set_error(MOE_EDEVICE, "device-side check failed (flags 0x%x: %s%s%s%s)", st.flags,
+  if (st.flags & (FLAG_BAD_EXPERT | FLAG_BAD_ROW | FLAG_BAD_OFFSETS | FLAG_ROUTE_BOUND | FLAG_BAD_CACHE |
+                  FLAG_NOT_FINITE))
+    return set_error(MOE_EDEVICE, "device-side check failed (flags 0x%x: %s%s%s%s%s%s)", st.flags,
                      (st.flags & FLAG_BAD_EXPERT) ? "expert id out of range " : "",
                      (st.flags & FLAG_BAD_ROW) ? "row out of range " : "",
                      (st.flags & FLAG_BAD_OFFSETS) ? "bad offsets " : "",
-                     (st.flags & FLAG_ROUTE_BOUND) ? "router score outside its error bound" : "");
+                     (st.flags & FLAG_ROUTE_BOUND) ? "router score outside its error bound " : "",
+                     (st.flags & FLAG_BAD_CACHE) ? "cache lengths, starts or pages out of range " : "",
+                     (st.flags & FLAG_NOT_FINITE) ? "a key or value that is not finite" : "");
   return MOE_OK;
 }
 

@@ -57,6 +57,11 @@ EXPORTS = (
     "moe_streamer_destroy",
     "moe_streamer_pool",
     "moe_forward_streamed",
+    "moe_add_rms_norm",
+    "moe_qmv",
+    "moe_kv_append",
+    "moe_kv_attention",
+    "moe_kv_workspace_bytes",
 )
 
 
@@ -99,6 +104,13 @@ class MoeStreamStats(ctypes.Structure):
     _fields_ = [("resident", ctypes.c_int32), ("filled", ctypes.c_int32), ("streamed", ctypes.c_int32),
                 ("batches", ctypes.c_int32), ("bytes", ctypes.c_int64), ("prefetched", ctypes.c_int32),
                 ("prefetch_used", ctypes.c_int32)]
+
+
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tail", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("n_seq", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("hkv", ctypes.c_int32), ("d", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -172,6 +184,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                          ctypes.POINTER(MoeStreamStats)]
     lib.moe_pack_experts.restype = ctypes.c_int
     lib.moe_pack_experts.argtypes = [ctypes.POINTER(MoeQWeights), ctypes.POINTER(MoeDims), ctypes.c_int, vp, sz, vp]
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.moe_add_rms_norm.restype = ctypes.c_int
+    lib.moe_add_rms_norm.argtypes = [vp, i64, vp, i64, vp, f32, i32, i32, vp, vp, vp, vp, vp]
+    lib.moe_qmv.restype = ctypes.c_int
+    lib.moe_qmv.argtypes = [vp, i64, vp, vp, ctypes.POINTER(MoeQWeights), i32, i32, i32, vp, i32, vp]
+    lib.moe_kv_append.restype = ctypes.c_int
+    lib.moe_kv_append.argtypes = [vp, i64, vp, i64, vp, i32, ctypes.POINTER(MoeKvCache), vp, sz, vp]
+    lib.moe_kv_attention.restype = ctypes.c_int
+    lib.moe_kv_attention.argtypes = [vp, i64, vp, i32, i32, f32, ctypes.POINTER(MoeKvCache), vp, vp, sz, vp]
+    lib.moe_kv_workspace_bytes.restype = sz
+    lib.moe_kv_workspace_bytes.argtypes = [i32]
     _lib = lib
     return lib
 
