@@ -189,6 +189,331 @@ __global__ void __launch_bounds__(QMV_WARPS * 32) qmv_kernel(QmvParams p, int KS
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: weights streamed through shared memory.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int QS_ROW = 160;  // bytes of a weight row's 4 groups in shared memory: 128 and a shift of 8 banks
+constexpr int QS_STAGE = 16 * (QS_ROW + 16);  // a unit: codes, then 4 scales and 4 biases a row
+
+// Bytes between rows of x in shared memory, 2 bytes a value: lanes of two rows
+// read together, 16 bytes each at steps of 32; the pad puts the second row's
+// reads on the other banks.
+constexpr int qs_x_pitch(int k) { return 2 * k + 16; }
+
+// Codes as operands without arithmetic: the bits of a code, masked in place,
+// read as a number.  Below the smallest normal exponent, and in the first
+// binade above it, the value is linear in the bits: bits * 2^-133 in bf16 (up
+// to 255), bits * 2^-24 in fp16 (up to 2047).  A code 4 bits up weighs 16
+// times as much, which the staged x makes up for; one shift brings the upper
+// two codes of a half down.
+__device__ __forceinline__ void codes_raw(uint32_t w, uint32_t (&o)[4]) {
+  const uint32_t h = w >> 8;
+  o[0] = w & 0x000F000Fu;
+  o[1] = w & 0x00F000F0u;
+  o[2] = h & 0x000F000Fu;
+  o[3] = h & 0x00F000F0u;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// v * 2^e for any e in [-252, 254], as two exact powers of two.
+__device__ __forceinline__ float times_pow2(float v, int e) {
+  const int a = e / 2, b = e - a;
+  return v * __uint_as_float((uint32_t)(127 + a) << 23) * __uint_as_float((uint32_t)(127 + b) << 23);
+}
+
+size_t qs_smem(const QmvParams& p, int nt, int teams, int stages) {
+  return (size_t)teams * QMV_WARPS * stages * QS_STAGE            // rings
+         + (size_t)teams * 2 * QMV_WARPS * 16 * 8 * nt * 4         // sums
+         + (size_t)(p.k >> 6) * 8 * nt * 4                         // group sums of x
+         + (size_t)p.t * qs_x_pitch(p.k);                          // x
+}
+
+// The products of qmv_kernel for t <= 8 NT rows, when what counts is how
+// fast the weights come.  The CTA stages x once; then each of its TEAMS teams
+// of eight warps walks tiles of 16 weight rows.  A team's warps split k in
+// units of 4 groups (128 bytes of a weight row), the same units in every
+// tile, and each warp keeps S - 1 units in flight by asynchronous copies into
+// a ring of its own, across tiles: only the sums at a tile's end make a
+// team's warps wait for one another.  VEC: a row's scales are 8-byte aligned
+// at every unit (k a multiple of 256).
+//
+// The kernel is bound by instructions before it is by memory unless a code
+// costs little, so codes enter as they are (codes_raw) and x carries the
+// rest: bf16 rows are scaled by a power of two that takes the row's largest
+// magnitude to [2^120, 2^121), where products with code * 2^-133 are ordinary
+// fp32 numbers, and the result is scaled back; 8-bit rows need no scaling.
+// The pairs that meet codes 4 bits up are divided by 16.  All of it is exact
+// but for values more than 2^240 below their row's largest.
+template <int NT, int TEAMS, int S, bool F16, bool VEC>
+__global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(QmvParams p, bool out32) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int rowmax[8 * NT];
+  constexpr int THREADS = TEAMS * QMV_WARPS * 32;
+  const int lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
+  const int team = threadIdx.x / (QMV_WARPS * 32), warp = (threadIdx.x >> 5) % QMV_WARPS;
+  const int groups = p.k >> 6, units = (groups + 3) >> 2, x_pitch = qs_x_pitch(p.k);
+  unsigned char* ring = smem + (size_t)(threadIdx.x >> 5) * S * QS_STAGE;
+  float* red = reinterpret_cast<float*>(smem + (size_t)TEAMS * QMV_WARPS * S * QS_STAGE) +
+               (size_t)team * 2 * QMV_WARPS * 8 * NT * 16;  // [2][warp][8 NT][16]
+  float* xsum = reinterpret_cast<float*>(smem + (size_t)TEAMS * QMV_WARPS * (S * QS_STAGE + 2 * 8 * NT * 16 * 4));
+  unsigned char* xsm = reinterpret_cast<unsigned char*>(xsum + groups * 8 * NT);
+  const int ub = units * warp / QMV_WARPS, ue = units * (warp + 1) / QMV_WARPS;
+  const int tiles = (p.n + 15) >> 4, step = gridDim.x * TEAMS, tile0 = blockIdx.x * TEAMS + team;
+  const size_t row_bytes = (size_t)p.k >> 1;
+  pdl_wait();
+  pdl_trigger();
+
+  int it = tile0, iu = ub;  // the next unit to copy
+  auto issue = [&](int stage) {
+    if (it < tiles && iu < ue) {
+      unsigned char* dst = ring + stage * QS_STAGE;
+      const int g0 = iu * 4, row0 = it * 16, c = lane & 7;
+      const uint8_t* src = p.codes + (size_t)(g0 * 32 + 16 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        // rows past the end read the last row; their results are not stored
+        if (VEC || g0 + (c >> 1) < groups) cp_async16(dst + r * QS_ROW + 16 * c, src + min(row0 + r, p.n - 1) * row_bytes);
+      }
+      const int r = lane >> 1;
+      const uint16_t* sc = (lane & 1 ? p.biases : p.scales) + (size_t)min(row0 + r, p.n - 1) * groups + g0;
+      unsigned char* to = dst + 16 * QS_ROW + r * 16 + 8 * (lane & 1);
+      if (VEC) {
+        cp_async8(to, sc);
+      } else {
+        uint16_t v[4] = {};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (g0 + e < groups) v[e] = __ldg(sc + e);
+        *reinterpret_cast<uint2*>(to) = make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+      }
+      if (++iu == ue) {
+        iu = ub;
+        it += step;
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(i);
+
+  // ---- x: each row's largest magnitude, then its values in operand order
+  const int per = p.k >> 3;  // vectors of 8 values
+  if (!F16) {
+    if (threadIdx.x < 8 * NT) rowmax[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i0 = threadIdx.x - lane; i0 < p.t * per; i0 += THREADS) {  // whole warps
+      const int i = min(i0 + lane, p.t * per - 1), r = i / per;
+      const uint4 v = *reinterpret_cast<const uint4*>(p.x + (size_t)r * p.x_stride + 8 * (i % per));
+      // magnitudes compare as whole numbers, infinity and NaN last
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7FFF0000u, w[e] << 16 & 0x7FFF0000u));
+      if (__all_sync(~0u, r == __shfl_sync(~0u, r, 0))) {
+        m = __reduce_max_sync(~0u, m);
+        if (lane == 0) atomicMax(rowmax + r, (int)m);
+      } else {
+        atomicMax(rowmax + r, (int)m);
+      }
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < p.t * per; i += THREADS) {
+    const int r = i / per, c = i % per;
+    uint4 o;
+    if (F16) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p.xc + (size_t)r * p.k + 8 * c);
+      const int8_t* b = reinterpret_cast<const int8_t*>(&v);
+      auto pair = [&](int e, float f) {
+        const __half2 h = __floats2half2_rn(f * b[e], f * b[e + 4]);
+        return *reinterpret_cast<const uint32_t*>(&h);
+      };
+      o = make_uint4(pair(0, 1.f), pair(1, 0.0625f), pair(2, 1.f), pair(3, 0.0625f));
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(p.x + (size_t)r * p.x_stride + 8 * c);
+      const int ex = rowmax[r] >> 23, up = ex == 255 || rowmax[r] == 0 ? 0 : 120 + 127 - max(ex, 1);
+      auto pair = [&](uint32_t lo, uint32_t hi, bool odd, int sh) {
+        const float a = sh ? bf16hi(lo) : bf16lo(lo), b = sh ? bf16hi(hi) : bf16lo(hi);
+        return pack_bf16x2(times_pow2(a, up - 4 * odd), times_pow2(b, up - 4 * odd));
+      };
+      o = make_uint4(pair(v.x, v.z, false, 0), pair(v.x, v.z, true, 1), pair(v.y, v.w, false, 0),
+                     pair(v.y, v.w, true, 1));
+    }
+    *reinterpret_cast<uint4*>(xsm + (size_t)r * x_pitch + 16 * c) = o;
+  }
+  __syncthreads();
+  // X of every group: with a constant for A (1, and 16 where x was divided)
+  // each row of the product is the sums of x, in the scale of the others.
+  constexpr uint32_t C1 = 0x00010001u, C16 = 0x00100010u;
+  const uint32_t ones[4] = {C1, C1, C16, C16};
+  for (int gr = threadIdx.x >> 5; gr < groups; gr += TEAMS * QMV_WARPS)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
+      uint4 v[2] = {};
+      if (r < p.t) {
+        v[0] = *reinterpret_cast<const uint4*>(xsm + (size_t)r * x_pitch + gr * 128 + 32 * j);
+        v[1] = *reinterpret_cast<const uint4*>(xsm + (size_t)r * x_pitch + gr * 128 + 32 * j + 16);
+      }
+      float X[4];
+      mma_first<F16>(X, ones, v[0].x, v[0].y);
+      mma_16816(X, ones, v[0].z, v[0].w, F16);
+      mma_16816(X, ones, v[1].x, v[1].y, F16);
+      mma_16816(X, ones, v[1].z, v[1].w, F16);
+      if (g == 0) *reinterpret_cast<float2*>(xsum + (gr * NT + nt) * 8 + 2 * j) = make_float2(X[0], X[1]);
+    }
+  __syncthreads();
+
+  int stage = 0, buf = 0;
+  for (int tile = tile0; tile < tiles; tile += step) {
+    float acc[NT][4] = {};
+    for (int u = ub; u < ue; ++u) {
+      cp_async_wait<S - 2>();
+      __syncwarp();  // this unit is there, and the last one is read by every lane
+      issue(stage == 0 ? S - 1 : stage - 1);
+      const unsigned char* src = ring + stage * QS_STAGE;
+      stage = stage + 1 == S ? 0 : stage + 1;
+      const uint4 A = *reinterpret_cast<const uint4*>(src + 16 * QS_ROW + g * 16);
+      const uint4 B = *reinterpret_cast<const uint4*>(src + 16 * QS_ROW + (8 + g) * 16);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int gr = 4 * u + q;
+        if (!VEC && gr >= groups) break;
+        const uint2 wa = *reinterpret_cast<const uint2*>(src + g * QS_ROW + 32 * q + 8 * j);
+        const uint2 wb = *reinterpret_cast<const uint2*>(src + (8 + g) * QS_ROW + 32 * q + 8 * j);
+        uint32_t pa[2][4], pb[2][4];
+        codes_raw(wa.x, pa[0]);
+        codes_raw(wa.y, pa[1]);
+        codes_raw(wb.x, pb[0]);
+        codes_raw(wb.y, pb[1]);
+        // scale and bias of group q: halves q of the row's 4 and 4
+        auto half_of = [](uint32_t w, int hi) { return __half2float(__ushort_as_half((uint16_t)(hi ? w >> 16 : w))); };
+        const float s0 = half_of(q < 2 ? A.x : A.y, q & 1), s1 = half_of(q < 2 ? B.x : B.y, q & 1);
+        const float b0 = half_of(q < 2 ? A.z : A.w, q & 1), b1 = half_of(q < 2 ? B.z : B.w, q & 1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = 8 * nt + g;
+          uint4 v[2] = {};
+          if (r < p.t) {
+            v[0] = *reinterpret_cast<const uint4*>(xsm + (size_t)r * x_pitch + gr * 128 + 32 * j);
+            v[1] = *reinterpret_cast<const uint4*>(xsm + (size_t)r * x_pitch + gr * 128 + 32 * j + 16);
+          }
+          const float2 X = *reinterpret_cast<const float2*>(xsum + (gr * NT + nt) * 8 + 2 * j);
+          const uint32_t xo[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+          float P[4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const int w = s >> 1, h = 2 * (s & 1);
+            const uint32_t a[4] = {pa[w][h], pb[w][h], pa[w][h + 1], pb[w][h + 1]};
+            if (s == 0)
+              mma_first<F16>(P, a, xo[0], xo[1]);
+            else
+              mma_16816(P, a, xo[2 * s], xo[2 * s + 1], F16);
+          }
+          float(&d)[4] = acc[nt];
+          if (F16) {  // the rows' scales of this group
+            const int c = 8 * nt + 2 * j;
+            const float f0 = c < p.t ? __ldg(p.xs + (size_t)c * groups + gr) : 0.f;
+            const float f1 = c + 1 < p.t ? __ldg(p.xs + (size_t)(c + 1) * groups + gr) : 0.f;
+            d[0] = fmaf(f0, fmaf(s0, P[0], b0 * X.x), d[0]);
+            d[1] = fmaf(f1, fmaf(s0, P[1], b0 * X.y), d[1]);
+            d[2] = fmaf(f0, fmaf(s1, P[2], b1 * X.x), d[2]);
+            d[3] = fmaf(f1, fmaf(s1, P[3], b1 * X.y), d[3]);
+          } else {
+            d[0] = fmaf(s0, P[0], fmaf(b0, X.x, d[0]));
+            d[1] = fmaf(s0, P[1], fmaf(b0, X.y, d[1]));
+            d[2] = fmaf(s1, P[2], fmaf(b1, X.x, d[2]));
+            d[3] = fmaf(s1, P[3], fmaf(b1, X.y, d[3]));
+          }
+        }
+      }
+    }
+    // the warps' sums, in a buffer that alternates: one barrier a tile
+    float* mine = red + (size_t)(buf * QMV_WARPS + warp) * 8 * NT * 16;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float* q = mine + (8 * nt + 2 * j) * 16 + g;
+      q[0] = acc[nt][0];
+      q[16] = acc[nt][1];
+      q[8] = acc[nt][2];
+      q[24] = acc[nt][3];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(QMV_WARPS * 32) : "memory");
+    for (int i = threadIdx.x % (QMV_WARPS * 32); i < p.t * 16; i += QMV_WARPS * 32) {
+      const int c = i & 15, r = i >> 4, col = tile * 16 + c;
+      if (col >= p.n) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < QMV_WARPS; ++w) v += red[((size_t)(buf * QMV_WARPS + w) * 8 * NT + r) * 16 + c];
+      if (F16) {
+        v *= 0x1p24f;
+      } else {
+        const int ex = rowmax[r] >> 23, up = ex == 255 || rowmax[r] == 0 ? 0 : 120 + 127 - max(ex, 1);
+        v = times_pow2(v, 133 - up);
+      }
+      const size_t o = (size_t)r * p.n + col;
+      if (out32)
+        static_cast<float*>(p.y)[o] = v;
+      else
+        static_cast<uint16_t*>(p.y)[o] = f2bf(v);
+    }
+    buf ^= 1;
+  }
+  cp_async_wait<0>();
+}
+
+constexpr size_t QS_MAX_SMEM = 227 * 1024;
+
+template <int NT, int TEAMS, int S, bool F16>
+bool try_config(const QmvParams& p, bool out32, cudaStream_t s, cudaError_t& e) {
+  const size_t smem = qs_smem(p, NT, TEAMS, S);
+  if (smem > QS_MAX_SMEM) return false;
+  const int tiles = (p.n + 15) / 16, ctas = (tiles + TEAMS - 1) / TEAMS;
+  auto* kern = p.k % 256 == 0 ? qmv_stream_kernel<NT, TEAMS, S, F16, true> : qmv_stream_kernel<NT, TEAMS, S, F16, false>;
+  if ((e = set_smem_limit_once(kern, (int)smem)) != cudaSuccess) return true;
+  const dim3 grid(ctas < sm_count() ? ctas : sm_count()), block(TEAMS * QMV_WARPS * 32);
+  MOE_LAUNCH("qmv_stream", s, { e = launch_k(kern, grid, block, smem, s, p, out32); });
+  return true;
+}
+
+// The streaming kernel, if the rows of x fit beside its rings: two teams a
+// CTA when there are tiles for them.
+template <int NT, bool F16>
+bool try_stream(const QmvParams& p, bool out32, cudaStream_t s, cudaError_t& e) {
+  if ((p.n + 15) / 16 > sm_count() && (try_config<NT, 2, 4, F16>(p, out32, s, e) || try_config<NT, 2, 3, F16>(p, out32, s, e)))
+    return true;
+  return try_config<NT, 1, 4, F16>(p, out32, s, e) || try_config<NT, 1, 3, F16>(p, out32, s, e);
+}
+
 template <int NT, bool F16>
 cudaError_t launch_qmv(const QmvParams& p, bool out32, cudaStream_t s) {
   const int tiles = (p.n + 15) / 16, groups = p.k / 64;
@@ -235,6 +560,9 @@ extern "C" int moe_qmv(const uint16_t* x, int64_t x_stride, const int8_t* x_code
   const bool f = x_codes != nullptr, o = y_fp32 != 0;
   const int nt = (t + 7) / 8;
   cudaError_t e;
+  if (t <= 8 ? (f ? try_stream<1, true>(p, o, s, e) : try_stream<1, false>(p, o, s, e))
+             : t <= 16 && (f ? try_stream<2, true>(p, o, s, e) : try_stream<2, false>(p, o, s, e)))
+    return cuda_status(e, "moe_qmv launch");
   if (nt <= 1)
     e = f ? launch_qmv<1, true>(p, o, s) : launch_qmv<1, false>(p, o, s);
   else if (nt <= 2)

@@ -26,7 +26,7 @@ from typing import NamedTuple
 
 import torch
 
-from .moe import (_BF16, _F16, MoeError, MoeKvCache, MoeQWeights, _check, _need, _on_current_device, _ptr,
+from .moe import (_BF16, _F16, MoeError, MoeKvCache, MoeQWeights, _check, _need, _on_current_device,
                   load_library, read_device_status)
 
 __all__ = ["NormOut", "moe_add_rms_norm", "moe_qmv", "KvCache", "moe_kv_append", "moe_kv_attention"]
@@ -34,14 +34,21 @@ __all__ = ["NormOut", "moe_add_rms_norm", "moe_qmv", "KvCache", "moe_kv_append",
 GROUP = 64  # weights per scale, and channels per scale of an 8-bit row
 
 
-def _stream_of(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+_BF = torch.bfloat16
+_current_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: no Stream object is made
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _alloc_on(stream):
     """Allocations made inside belong to `stream`, so that the memory is not
     handed out again before its work is done."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
+
+
+def _raw(stream, dev: int) -> int:
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _need_rows(t, name: str, inner: tuple):
@@ -61,6 +68,12 @@ def _need_rows(t, name: str, inner: tuple):
         raise ValueError(f"{name}: rows must be a multiple of 8 elements apart, got {t.stride(0)}")
     return t
 
+
+# Each call first asks in one expression whether its tensors are the ordinary
+# ones (their own types and shapes, contiguous, on one device); only when that
+# is false do the checks that name what is wrong run, and pass the rarer valid
+# forms (16-bit patterns, strided rows).  A decoded token's call is host time:
+# the checks by name cost 10 us of it, the expression 1 us.
 
 def _row_stride(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else 0
@@ -89,32 +102,42 @@ def moe_add_rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tenso
     lib = load_library()
     if x.dim() != 2:
         raise ValueError("x must be [t, h]")
-    t, h = x.shape
-    _need_rows(x, "x", (h,))
-    _need(gamma, "gamma", _BF16, shape=(h,))
-    if residual is not None:
-        _need_rows(residual, "residual", (h,))
-        if residual.shape[0] != t:
-            raise ValueError(f"residual must have {t} rows, got {residual.shape[0]}")
-    if sum_out is not None:
-        _need(sum_out, "sum_out", _BF16, shape=(t, h))
-    if quantize and h % GROUP:
-        raise ValueError(f"h={h} must be a multiple of {GROUP} for 8-bit rows")
-    _on_current_device(x=x, gamma=gamma, residual=residual, sum_out=sum_out)
+    t, h = shape = x.shape
+    dev = x.get_device()
+    if not (dev >= 0 and dev == torch.cuda.current_device() == gamma.get_device()
+            and x.dtype is _BF and x.is_contiguous() and gamma.dtype is _BF and gamma.shape == (h,) and gamma.is_contiguous()
+            and (residual is None or (residual.dtype is _BF and residual.shape == shape and residual.is_contiguous()
+                                      and residual.get_device() == dev))
+            and sum_out is None and not (quantize and h % GROUP)):
+        _need_rows(x, "x", (h,))
+        _need(gamma, "gamma", _BF16, shape=(h,))
+        if residual is not None:
+            _need_rows(residual, "residual", (h,))
+            if residual.shape[0] != t:
+                raise ValueError(f"residual must have {t} rows, got {residual.shape[0]}")
+        if sum_out is not None:
+            _need(sum_out, "sum_out", _BF16, shape=(t, h))
+        if quantize and h % GROUP:
+            raise ValueError(f"h={h} must be a multiple of {GROUP} for 8-bit rows")
+        _on_current_device(x=x, gamma=gamma, residual=residual, sum_out=sum_out)
     if want_y is None:
         want_y = not quantize
     y = codes = scales = None
     with _alloc_on(stream):
         if sum_out is None and residual is not None:
-            sum_out = torch.empty((t, h), dtype=torch.bfloat16, device=x.device)
+            sum_out = torch.empty(shape, dtype=_BF, device=x.device)
         if want_y:
-            y = torch.empty((t, h), dtype=torch.bfloat16, device=x.device)
+            y = torch.empty(shape, dtype=_BF, device=x.device)
         if quantize:
-            codes = torch.empty((t, h), dtype=torch.int8, device=x.device)
+            codes = torch.empty(shape, dtype=torch.int8, device=x.device)
             scales = torch.empty((t, h // GROUP), dtype=torch.float32, device=x.device)
-    _check(lib.moe_add_rms_norm(x.data_ptr(), _row_stride(x), _ptr(residual),
-                                0 if residual is None else _row_stride(residual), gamma.data_ptr(), eps, t, h,
-                                _ptr(sum_out), _ptr(y), _ptr(codes), _ptr(scales), _stream_of(stream)))
+    status = lib.moe_add_rms_norm(
+        x.data_ptr(), _row_stride(x), None if residual is None else residual.data_ptr(),
+        0 if residual is None else _row_stride(residual), gamma.data_ptr(), eps, t, h,
+        None if sum_out is None else sum_out.data_ptr(), None if y is None else y.data_ptr(),
+        None if codes is None else codes.data_ptr(), None if scales is None else scales.data_ptr(), _raw(stream, dev))
+    if status:
+        _check(status)
     return NormOut(sum_out, y, codes, scales)
 
 
@@ -131,30 +154,49 @@ def moe_qmv(x, weights: tuple, out: torch.Tensor | None = None, out_dtype: torch
     codes, scales, biases = weights
     if codes.dim() != 2:
         raise ValueError("weight codes must be [n, k / 2]")
-    n, k = codes.shape[0], 2 * codes.shape[1]
-    _need(codes, "weight codes", (torch.uint8,))
-    _need(scales, "weight scales", _F16, shape=(n, k // GROUP))
-    _need(biases, "weight biases", _F16, shape=(n, k // GROUP))
+    n, kh = codes.shape
+    k = 2 * kh
+    dev = codes.get_device()
     rows = xc = xs = None
     if isinstance(x, torch.Tensor):
-        rows = _need_rows(x, "x", (k,))
+        rows = x
         t = x.shape[0]
+        plain = x.dtype is _BF and x.shape == (t, k) and x.is_contiguous() and x.get_device() == dev
     else:
         xc, xs = x
         t = xc.shape[0]
-        _need(xc, "x codes", (torch.int8,), shape=(t, k))
-        _need(xs, "x scales", (torch.float32,), shape=(t, k // GROUP))
-    if out is not None:
-        _need(out, "out", (torch.bfloat16, torch.float32), shape=(t, n))
-    elif out_dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
-    _on_current_device(x=rows, x_codes=xc, x_scales=xs, codes=codes, scales=scales, biases=biases, out=out)
+        plain = (xc.dtype is torch.int8 and xc.shape == (t, k) and xc.is_contiguous() and xc.get_device() == dev
+                 and xs.dtype is torch.float32 and xs.shape == (t, k // GROUP) and xs.is_contiguous()
+                 and xs.get_device() == dev)
+    groups = (n, k // GROUP)
+    if not (plain and dev >= 0 and dev == torch.cuda.current_device() == scales.get_device() == biases.get_device()
+            and codes.dtype is torch.uint8 and codes.is_contiguous()
+            and scales.dtype is torch.float16 and scales.shape == groups and scales.is_contiguous()
+            and biases.dtype is torch.float16 and biases.shape == groups and biases.is_contiguous()
+            and out is None and (out_dtype is _BF or out_dtype is torch.float32)):
+        _need(codes, "weight codes", (torch.uint8,))
+        _need(scales, "weight scales", _F16, shape=groups)
+        _need(biases, "weight biases", _F16, shape=groups)
+        if rows is not None:
+            _need_rows(rows, "x", (k,))
+        else:
+            _need(xc, "x codes", (torch.int8,), shape=(t, k))
+            _need(xs, "x scales", (torch.float32,), shape=(t, k // GROUP))
+        if out is not None:
+            _need(out, "out", (torch.bfloat16, torch.float32), shape=(t, n))
+        elif out_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+        _on_current_device(x=rows, x_codes=xc, x_scales=xs, codes=codes, scales=scales, biases=biases, out=out)
     if out is None:
         with _alloc_on(stream):
             out = torch.empty((t, n), dtype=out_dtype, device=codes.device)
     w = MoeQWeights(codes.data_ptr(), scales.data_ptr(), biases.data_ptr())
-    _check(lib.moe_qmv(_ptr(rows), 0 if rows is None else _row_stride(rows), _ptr(xc), _ptr(xs), ctypes.byref(w), t, n,
-                       k, out.data_ptr(), out.dtype == torch.float32, _stream_of(stream)))
+    status = lib.moe_qmv(
+        None if rows is None else rows.data_ptr(), 0 if rows is None else _row_stride(rows),
+        None if xc is None else xc.data_ptr(), None if xs is None else xs.data_ptr(), ctypes.byref(w), t, n, k,
+        out.data_ptr(), out.dtype is torch.float32, _raw(stream, dev))
+    if status:
+        _check(status)
     return out
 
 
@@ -190,8 +232,12 @@ class KvCache:
         self.codes, self.scales, self.tail, self.table, self.lens = codes, scales, tail, table, lens
         self.n_seq, self.hkv, self.block, self.d = n_seq, hkv, block, d
         self.ws = torch.zeros(n, dtype=torch.uint8, device=codes.device)
+        self._dev = codes.get_device()
+        self._starts, self._kv, self._scale = (n_seq + 1,), (hkv, d), 1 / math.sqrt(d)
+        self._ws = self.ws.data_ptr(), n
         self._c = MoeKvCache(codes.data_ptr(), scales.data_ptr(), tail.data_ptr(), table.data_ptr(), lens.data_ptr(),
                              n_seq, n_pages, max_blocks, block, hkv, d)
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def new(cls, n_seq: int, n_pages: int, max_blocks: int, hkv: int, d: int, block: int = 64, device="cuda"):
@@ -217,16 +263,23 @@ def moe_kv_append(k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, cache:
     strided) into the cache; sequence s owns rows starts[s] .. starts[s+1]-1
     (int32 [n_seq + 1], on the device), its last tokens."""
     lib = load_library()
-    _need_starts(starts, cache)
-    inner = (cache.hkv, cache.d)
-    _need_rows(k, "k", inner)
-    _need_rows(v, "v", inner)
     t = k.shape[0]
-    if v.shape[0] != t:
-        raise ValueError(f"v must have {t} rows, got {v.shape[0]}")
-    _on_current_device(k=k, v=v, starts=starts, codes=cache.codes)
-    _check(lib.moe_kv_append(k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), starts.data_ptr(), t,
-                             ctypes.byref(cache._c), cache.ws.data_ptr(), cache.ws.numel(), _stream_of(stream)))
+    dev = k.get_device()
+    if not (type(cache) is KvCache and dev >= 0 and dev == torch.cuda.current_device() == cache._dev
+            and v.get_device() == dev == starts.get_device()
+            and k.dtype is _BF and k.shape[1:] == cache._kv and k.is_contiguous()
+            and v.dtype is _BF and v.shape == k.shape and v.is_contiguous()
+            and starts.dtype is torch.int32 and starts.shape == cache._starts and starts.is_contiguous()):
+        _need_starts(starts, cache)
+        _need_rows(k, "k", cache._kv)
+        _need_rows(v, "v", cache._kv)
+        if v.shape[0] != t:
+            raise ValueError(f"v must have {t} rows, got {v.shape[0]}")
+        _on_current_device(k=k, v=v, starts=starts, codes=cache.codes)
+    status = lib.moe_kv_append(k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), starts.data_ptr(), t,
+                               cache._ref, *cache._ws, _raw(stream, dev))
+    if status:
+        _check(status)
 
 
 def moe_kv_attention(q: torch.Tensor, starts: torch.Tensor, cache: KvCache, scale: float | None = None,
@@ -235,18 +288,24 @@ def moe_kv_attention(q: torch.Tensor, starts: torch.Tensor, cache: KvCache, scal
     strided) over the cache; ``scale`` defaults to 1 / sqrt(d).  Returns bf16
     [t, hq, d]."""
     lib = load_library()
-    _need_starts(starts, cache)
     if q.dim() != 3:
         raise ValueError("q must be [t, hq, d]")
-    t, hq, d = q.shape
-    _need_rows(q, "q", (hq, cache.d))
-    if out is not None:
-        _need(out, "out", _BF16, shape=(t, hq, d))
-    _on_current_device(q=q, starts=starts, out=out, codes=cache.codes)
+    t, hq, d = shape = q.shape
+    dev = q.get_device()
+    if not (type(cache) is KvCache and dev >= 0 and dev == torch.cuda.current_device() == cache._dev
+            and starts.get_device() == dev and q.dtype is _BF and d == cache.d and q.is_contiguous() and out is None
+            and starts.dtype is torch.int32 and starts.shape == cache._starts and starts.is_contiguous()):
+        _need_starts(starts, cache)
+        _need_rows(q, "q", (hq, cache.d))
+        if out is not None:
+            _need(out, "out", _BF16, shape=(t, hq, d))
+        _on_current_device(q=q, starts=starts, out=out, codes=cache.codes)
     if out is None:
         with _alloc_on(stream):
-            out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=q.device)
-    _check(lib.moe_kv_attention(q.data_ptr(), _row_stride(q), starts.data_ptr(), t, hq,
-                                1 / math.sqrt(d) if scale is None else scale, ctypes.byref(cache._c), out.data_ptr(),
-                                cache.ws.data_ptr(), cache.ws.numel(), _stream_of(stream)))
+            out = torch.empty(shape, dtype=_BF, device=q.device)
+    status = lib.moe_kv_attention(q.data_ptr(), _row_stride(q), starts.data_ptr(), t, hq,
+                                  cache._scale if scale is None else scale, cache._ref, out.data_ptr(), *cache._ws,
+                                  _raw(stream, dev))
+    if status:
+        _check(status)
     return out
