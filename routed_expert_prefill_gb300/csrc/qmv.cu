@@ -197,10 +197,6 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
                : "memory");
 }
-__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-               : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -208,12 +204,18 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 constexpr int QS_ROW = 160;  // bytes of a weight row's 4 groups in shared memory: 128 and a shift of 8 banks
-constexpr int QS_STAGE = 16 * (QS_ROW + 16);  // a unit: codes, then 4 scales and 4 biases a row
+constexpr int QS_STAGE = 16 * QS_ROW;  // a unit's codes
+constexpr int QS_CHUNKS = 4;            // 16-byte pieces of a tile's scales and biases that a thread carries
+constexpr int QS_MAX_K = 64 * 64 * QS_CHUNKS;
+
+// Bytes between rows of a tile's scales in shared memory: eight rows read
+// together, 8 bytes each, fall on different banks.
+__host__ __device__ constexpr int qs_s_pitch(int groups) { return ((2 * groups + 15) & ~15) + 16; }
 
 // Bytes between rows of x in shared memory, 2 bytes a value: lanes of two rows
 // read together, 16 bytes each at steps of 32; the pad puts the second row's
 // reads on the other banks.
-constexpr int qs_x_pitch(int k) { return 2 * k + 16; }
+__host__ __device__ constexpr int qs_x_pitch(int k) { return 2 * k + 16; }
 
 // Codes as operands without arithmetic: the bits of a code, masked in place,
 // read as a number.  Below the smallest normal exponent, and in the first
@@ -252,7 +254,8 @@ __device__ __forceinline__ float times_pow2(float v, int e) {
 size_t qs_smem(const QmvParams& p, int nt, int teams, int stages) {
   return (size_t)teams * QMV_WARPS * stages * QS_STAGE            // rings
          + (size_t)teams * 2 * QMV_WARPS * 16 * 8 * nt * 4         // sums
-         + (size_t)(p.k >> 6) * 8 * nt * 4                         // group sums of x
+         + (size_t)teams * 2 * 2 * 16 * qs_s_pitch(p.k >> 6)       // scales and biases of two tiles
+         + (size_t)(p.k >> 6) * 8 * nt * (p.xc ? 8 : 4)            // group sums of x, scales of 8-bit rows
          + (size_t)p.t * qs_x_pitch(p.k);                          // x
 }
 
@@ -262,8 +265,12 @@ size_t qs_smem(const QmvParams& p, int nt, int teams, int stages) {
 // units of 4 groups (128 bytes of a weight row), the same units in every
 // tile, and each warp keeps S - 1 units in flight by asynchronous copies into
 // a ring of its own, across tiles: only the sums at a tile's end make a
-// team's warps wait for one another.  VEC: a row's scales are 8-byte aligned
-// at every unit (k a multiple of 256).
+// team's warps wait for one another.  A tile's scales and biases, contiguous
+// in memory, pass through the team's registers one tile ahead: fetched row by
+// row with the codes they cost a shared-memory pass a row and unit, as much
+// as all reads of the codes (62.5 us a call of 4 rows of 4096 with 131072
+// weight rows that way).  VEC: 16-byte pieces of the scales lie within rows
+// (k a multiple of 512).
 //
 // The kernel is bound by instructions before it is by memory unless a code
 // costs little, so codes enter as they are (codes_raw) and x carries the
@@ -283,8 +290,11 @@ __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(Q
   unsigned char* ring = smem + (size_t)(threadIdx.x >> 5) * S * QS_STAGE;
   float* red = reinterpret_cast<float*>(smem + (size_t)TEAMS * QMV_WARPS * S * QS_STAGE) +
                (size_t)team * 2 * QMV_WARPS * 8 * NT * 16;  // [2][warp][8 NT][16]
-  float* xsum = reinterpret_cast<float*>(smem + (size_t)TEAMS * QMV_WARPS * (S * QS_STAGE + 2 * 8 * NT * 16 * 4));
-  unsigned char* xsm = reinterpret_cast<unsigned char*>(xsum + groups * 8 * NT);
+  const int s_pitch = qs_s_pitch(groups);
+  unsigned char* scb = smem + (size_t)TEAMS * QMV_WARPS * (S * QS_STAGE + 2 * 8 * NT * 16 * 4);
+  float* xsum = reinterpret_cast<float*>(scb + (size_t)TEAMS * 2 * 2 * 16 * s_pitch);
+  scb += (size_t)team * 2 * 2 * 16 * s_pitch;  // [2][scales, biases][16] rows of s_pitch bytes
+  unsigned char* xsm = reinterpret_cast<unsigned char*>(xsum + groups * 8 * NT * (F16 ? 2 : 1));
   const int ub = units * warp / QMV_WARPS, ue = units * (warp + 1) / QMV_WARPS;
   const int tiles = (p.n + 15) >> 4, step = gridDim.x * TEAMS, tile0 = blockIdx.x * TEAMS + team;
   const size_t row_bytes = (size_t)p.k >> 1;
@@ -296,24 +306,17 @@ __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(Q
     if (it < tiles && iu < ue) {
       unsigned char* dst = ring + stage * QS_STAGE;
       const int g0 = iu * 4, row0 = it * 16, c = lane & 7;
-      const uint8_t* src = p.codes + (size_t)(g0 * 32 + 16 * c);
+      const uint8_t* src = p.codes + ((size_t)row0 + (lane >> 3)) * row_bytes + g0 * 32 + 16 * c;
+      dst += (lane >> 3) * QS_ROW + 16 * c;
+      if (VEC || g0 + (c >> 1) < groups) {
+        if (row0 + 16 <= p.n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        // rows past the end read the last row; their results are not stored
-        if (VEC || g0 + (c >> 1) < groups) cp_async16(dst + r * QS_ROW + 16 * c, src + min(row0 + r, p.n - 1) * row_bytes);
-      }
-      const int r = lane >> 1;
-      const uint16_t* sc = (lane & 1 ? p.biases : p.scales) + (size_t)min(row0 + r, p.n - 1) * groups + g0;
-      unsigned char* to = dst + 16 * QS_ROW + r * 16 + 8 * (lane & 1);
-      if (VEC) {
-        cp_async8(to, sc);
-      } else {
-        uint16_t v[4] = {};
+          for (int i = 0; i < 4; ++i) cp_async16(dst + 4 * i * QS_ROW, src + i * 4 * row_bytes);
+        } else {  // rows past the end stay as they are; their results are not stored
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (g0 + e < groups) v[e] = __ldg(sc + e);
-        *reinterpret_cast<uint2*>(to) = make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+          for (int i = 0; i < 4; ++i)
+            if (row0 + 4 * i + (lane >> 3) < p.n) cp_async16(dst + 4 * i * QS_ROW, src + i * 4 * row_bytes);
+        }
       }
       if (++iu == ue) {
         iu = ub;
@@ -324,6 +327,55 @@ __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(Q
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(i);
+
+  // a tile's scales and biases: 2 * groups pieces of 16 bytes each
+  const int tt = threadIdx.x % (QMV_WARPS * 32);
+  const size_t s_end = (size_t)p.n * groups * 2;  // bytes of either array
+  uint4 sc[QS_CHUNKS];
+  int s_off[QS_CHUNKS];  // where a piece goes (VEC)
+#pragma unroll
+  for (int i = 0; i < QS_CHUNKS; ++i) {
+    const int c = tt + i * QMV_WARPS * 32, which = c >= 2 * groups, o = 8 * (c - which * 2 * groups);
+    s_off[i] = (which * 16 + o / groups) * s_pitch + 2 * (o % groups);
+  }
+  auto fetch_scales = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < QS_CHUNKS; ++i) {
+      if (i * QMV_WARPS * 32 >= 4 * groups) break;
+      const int c = tt + i * QMV_WARPS * 32, which = c >= 2 * groups;
+      const size_t at = (size_t)tile * 32 * groups + 16 * (c - which * 2 * groups);
+      if (c >= 4 * groups || tile >= tiles || at >= s_end) continue;
+      const unsigned char* src = reinterpret_cast<const unsigned char*>(which ? p.biases : p.scales) + at;
+      if (VEC || at + 16 <= s_end) {
+        sc[i] = __ldg(reinterpret_cast<const uint4*>(src));
+      } else {  // the arrays end inside the piece
+        uint32_t w[4] = {};
+        for (int e = 0; e < 8; ++e)
+          if (at + 2 * e < s_end) w[e >> 1] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src) + e) << (16 * (e & 1));
+        sc[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  };
+  auto store_scales = [&](int buf) {
+    unsigned char* dst = scb + (size_t)buf * 32 * s_pitch;
+#pragma unroll
+    for (int i = 0; i < QS_CHUNKS; ++i) {
+      if (i * QMV_WARPS * 32 >= 4 * groups) break;
+      const int c = tt + i * QMV_WARPS * 32;
+      if (c >= 4 * groups) continue;
+      if (VEC) {
+        *reinterpret_cast<uint4*>(dst + s_off[i]) = sc[i];
+      } else {
+        const int which = c >= 2 * groups, o = 8 * (c - which * 2 * groups);
+        const uint32_t w[4] = {sc[i].x, sc[i].y, sc[i].z, sc[i].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint16_t*>(dst + (which * 16 + (o + e) / groups) * s_pitch + 2 * ((o + e) % groups)) =
+              (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+  };
+  fetch_scales(tile0);
 
   // ---- x: each row's largest magnitude, then its values in operand order
   const int per = p.k >> 3;  // vectors of 8 values
@@ -371,6 +423,10 @@ __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(Q
     *reinterpret_cast<uint4*>(xsm + (size_t)r * x_pitch + 16 * c) = o;
   }
   __syncthreads();
+  // lanes past the rows read the last row; their columns are not stored
+  const unsigned char* xrow[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) xrow[nt] = xsm + (size_t)min(8 * nt + g, p.t - 1) * x_pitch + 32 * j;
   // X of every group: with a constant for A (1, and 16 where x was divided)
   // each row of the product is the sums of x, in the scale of the others.
   constexpr uint32_t C1 = 0x00010001u, C16 = 0x00100010u;
@@ -378,23 +434,33 @@ __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(Q
   for (int gr = threadIdx.x >> 5; gr < groups; gr += TEAMS * QMV_WARPS)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = 8 * nt + g;
-      uint4 v[2] = {};
-      if (r < p.t) {
-        v[0] = *reinterpret_cast<const uint4*>(xsm + (size_t)r * x_pitch + gr * 128 + 32 * j);
-        v[1] = *reinterpret_cast<const uint4*>(xsm + (size_t)r * x_pitch + gr * 128 + 32 * j + 16);
-      }
+      const unsigned char* xr = xrow[nt] + gr * 128;
+      const uint4 v[2] = {*reinterpret_cast<const uint4*>(xr), *reinterpret_cast<const uint4*>(xr + 16)};
       float X[4];
       mma_first<F16>(X, ones, v[0].x, v[0].y);
       mma_16816(X, ones, v[0].z, v[0].w, F16);
       mma_16816(X, ones, v[1].x, v[1].y, F16);
       mma_16816(X, ones, v[1].z, v[1].w, F16);
-      if (g == 0) *reinterpret_cast<float2*>(xsum + (gr * NT + nt) * 8 + 2 * j) = make_float2(X[0], X[1]);
+      if (g == 0) {
+        float* to = xsum + (gr * NT + nt) * (F16 ? 16 : 8) + 2 * j;
+        if (F16) {  // and the 8-bit rows' scales of this group
+          const int c = 8 * nt + 2 * j;
+          const float f0 = c < p.t ? __ldg(p.xs + (size_t)c * groups + gr) : 0.f;
+          const float f1 = c + 1 < p.t ? __ldg(p.xs + (size_t)(c + 1) * groups + gr) : 0.f;
+          *reinterpret_cast<float2*>(to + 8) = make_float2(f0, f1);
+          X[0] *= f0;
+          X[1] *= f1;
+        }
+        *reinterpret_cast<float2*>(to) = make_float2(X[0], X[1]);
+      }
     }
+  store_scales(0);
   __syncthreads();
 
   int stage = 0, buf = 0;
   for (int tile = tile0; tile < tiles; tile += step) {
+    fetch_scales(tile + step);
+    const unsigned char* srow = scb + (size_t)buf * 32 * s_pitch + g * s_pitch;
     float acc[NT][4] = {};
     for (int u = ub; u < ue; ++u) {
       cp_async_wait<S - 2>();
@@ -402,8 +468,11 @@ __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(Q
       issue(stage == 0 ? S - 1 : stage - 1);
       const unsigned char* src = ring + stage * QS_STAGE;
       stage = stage + 1 == S ? 0 : stage + 1;
-      const uint4 A = *reinterpret_cast<const uint4*>(src + 16 * QS_ROW + g * 16);
-      const uint4 B = *reinterpret_cast<const uint4*>(src + 16 * QS_ROW + (8 + g) * 16);
+      // scales and biases of rows g and g + 8; past the last group: not used
+      const uint2 As = *reinterpret_cast<const uint2*>(srow + 8 * u);
+      const uint2 Bs = *reinterpret_cast<const uint2*>(srow + 8 * u + 8 * s_pitch);
+      const uint2 Ab = *reinterpret_cast<const uint2*>(srow + 8 * u + 16 * s_pitch);
+      const uint2 Bb = *reinterpret_cast<const uint2*>(srow + 8 * u + 24 * s_pitch);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int gr = 4 * u + q;
@@ -417,17 +486,14 @@ __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(Q
         codes_raw(wb.y, pb[1]);
         // scale and bias of group q: halves q of the row's 4 and 4
         auto half_of = [](uint32_t w, int hi) { return __half2float(__ushort_as_half((uint16_t)(hi ? w >> 16 : w))); };
-        const float s0 = half_of(q < 2 ? A.x : A.y, q & 1), s1 = half_of(q < 2 ? B.x : B.y, q & 1);
-        const float b0 = half_of(q < 2 ? A.z : A.w, q & 1), b1 = half_of(q < 2 ? B.z : B.w, q & 1);
+        const float s0 = half_of(q < 2 ? As.x : As.y, q & 1), s1 = half_of(q < 2 ? Bs.x : Bs.y, q & 1);
+        const float b0 = half_of(q < 2 ? Ab.x : Ab.y, q & 1), b1 = half_of(q < 2 ? Bb.x : Bb.y, q & 1);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int r = 8 * nt + g;
-          uint4 v[2] = {};
-          if (r < p.t) {
-            v[0] = *reinterpret_cast<const uint4*>(xsm + (size_t)r * x_pitch + gr * 128 + 32 * j);
-            v[1] = *reinterpret_cast<const uint4*>(xsm + (size_t)r * x_pitch + gr * 128 + 32 * j + 16);
-          }
-          const float2 X = *reinterpret_cast<const float2*>(xsum + (gr * NT + nt) * 8 + 2 * j);
+          const unsigned char* xr = xrow[nt] + gr * 128;
+          const uint4 v[2] = {*reinterpret_cast<const uint4*>(xr), *reinterpret_cast<const uint4*>(xr + 16)};
+          const float* xg = xsum + (gr * NT + nt) * (F16 ? 16 : 8) + 2 * j;
+          const float2 X = *reinterpret_cast<const float2*>(xg);
           const uint32_t xo[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
           float P[4];
 #pragma unroll
@@ -440,20 +506,14 @@ __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(Q
               mma_16816(P, a, xo[2 * s], xo[2 * s + 1], F16);
           }
           float(&d)[4] = acc[nt];
-          if (F16) {  // the rows' scales of this group
-            const int c = 8 * nt + 2 * j;
-            const float f0 = c < p.t ? __ldg(p.xs + (size_t)c * groups + gr) : 0.f;
-            const float f1 = c + 1 < p.t ? __ldg(p.xs + (size_t)(c + 1) * groups + gr) : 0.f;
-            d[0] = fmaf(f0, fmaf(s0, P[0], b0 * X.x), d[0]);
-            d[1] = fmaf(f1, fmaf(s0, P[1], b0 * X.y), d[1]);
-            d[2] = fmaf(f0, fmaf(s1, P[2], b1 * X.x), d[2]);
-            d[3] = fmaf(f1, fmaf(s1, P[3], b1 * X.y), d[3]);
-          } else {
-            d[0] = fmaf(s0, P[0], fmaf(b0, X.x, d[0]));
-            d[1] = fmaf(s0, P[1], fmaf(b0, X.y, d[1]));
-            d[2] = fmaf(s1, P[2], fmaf(b1, X.x, d[2]));
-            d[3] = fmaf(s1, P[3], fmaf(b1, X.y, d[3]));
+          if (F16) {
+            const float2 f = *reinterpret_cast<const float2*>(xg + 8);
+            P[0] *= f.x, P[1] *= f.y, P[2] *= f.x, P[3] *= f.y;
           }
+          d[0] = fmaf(s0, P[0], fmaf(b0, X.x, d[0]));
+          d[1] = fmaf(s0, P[1], fmaf(b0, X.y, d[1]));
+          d[2] = fmaf(s1, P[2], fmaf(b1, X.x, d[2]));
+          d[3] = fmaf(s1, P[3], fmaf(b1, X.y, d[3]));
         }
       }
     }
@@ -467,8 +527,9 @@ __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(Q
       q[8] = acc[nt][2];
       q[24] = acc[nt][3];
     }
+    store_scales(buf ^ 1);  // read since the last barrier but one by nobody
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(QMV_WARPS * 32) : "memory");
-    for (int i = threadIdx.x % (QMV_WARPS * 32); i < p.t * 16; i += QMV_WARPS * 32) {
+    for (int i = tt; i < p.t * 16; i += QMV_WARPS * 32) {
       const int c = i & 15, r = i >> 4, col = tile * 16 + c;
       if (col >= p.n) continue;
       float v = 0.f;
@@ -496,9 +557,9 @@ constexpr size_t QS_MAX_SMEM = 227 * 1024;
 template <int NT, int TEAMS, int S, bool F16>
 bool try_config(const QmvParams& p, bool out32, cudaStream_t s, cudaError_t& e) {
   const size_t smem = qs_smem(p, NT, TEAMS, S);
-  if (smem > QS_MAX_SMEM) return false;
+  if (smem > QS_MAX_SMEM || p.k > QS_MAX_K) return false;
   const int tiles = (p.n + 15) / 16, ctas = (tiles + TEAMS - 1) / TEAMS;
-  auto* kern = p.k % 256 == 0 ? qmv_stream_kernel<NT, TEAMS, S, F16, true> : qmv_stream_kernel<NT, TEAMS, S, F16, false>;
+  auto* kern = p.k % 512 == 0 ? qmv_stream_kernel<NT, TEAMS, S, F16, true> : qmv_stream_kernel<NT, TEAMS, S, F16, false>;
   if ((e = set_smem_limit_once(kern, (int)smem)) != cudaSuccess) return true;
   const dim3 grid(ctas < sm_count() ? ctas : sm_count()), block(TEAMS * QMV_WARPS * 32);
   MOE_LAUNCH("qmv_stream", s, { e = launch_k(kern, grid, block, smem, s, p, out32); });
@@ -552,8 +613,8 @@ extern "C" int moe_qmv(const uint16_t* x, int64_t x_stride, const int8_t* x_code
   TRY(check_ptr(x_codes, "x_codes", 16, true));
   TRY(check_ptr(x_scales, "x_scales", 4, true));
   TRY(check_ptr(w->codes, "w->codes", 16));
-  TRY(check_ptr(w->scales, "w->scales", 2));
-  TRY(check_ptr(w->biases, "w->biases", 2));
+  TRY(check_ptr(w->scales, "w->scales", 16));
+  TRY(check_ptr(w->biases, "w->biases", 16));
   TRY(check_ptr(y, "y", y_fp32 ? 4 : 2));
   const QmvParams p{x, x_stride, x_codes, x_scales, w->codes, w->scales, w->biases, t, n, k, y};
   cudaStream_t s = (cudaStream_t)stream;
