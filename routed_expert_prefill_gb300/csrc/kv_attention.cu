@@ -11,6 +11,37 @@ constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = AT_WARPS * 32;
 constexpr int WARP_TOKENS = 32;                      // tokens of one warp step
 constexpr int UNIT = AT_WARPS * WARP_TOKENS;         // tokens of one CTA step
+constexpr int STAGES = 3;                            // steps of a warp in its ring
+
+__host__ __device__ constexpr int at_smem(int d) {
+  const int ring = AT_WARPS * STAGES * 2 * WARP_TOKENS * d, sums = AT_WARPS * KV_ROWS * (d + 4) * 4;
+  return ring > sums ? ring : sums;
+}
+
+// Where the 16-byte piece c of token t's key or value goes among a step's 32,
+// so that the lanes of one shared-memory pass read different banks: pieces
+// j of two tokens for the keys, piece g of four tokens 2 j apart by two for
+// the values.
+template <int D>
+__device__ __forceinline__ int k_at(int t, int c) {
+  return D == 128 ? t * 128 + ((c ^ (t & 1) << 2) << 4) : t * 64 + (c << 4);
+}
+template <int D>
+__device__ __forceinline__ int v_at(int t, int c) {
+  if (D == 128) return t * 128 + ((c ^ (t & 7)) << 4);
+  const int r = (t >> 1 & 15) | (t & 1) << 4;
+  return r * 64 + ((c ^ (r & 2)) << 4);
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 struct AttnParams {
   const uint16_t* q;
@@ -83,12 +114,11 @@ __device__ __forceinline__ int64_t seq_units(const AttnParams& p, const Seq& q) 
 // joins them in CTA order.
 //
 // Within an item the CTA's four warps take 32 tokens each per step and hold
-// all 16 query rows.  Keys and values go from global memory into the
-// fragment layout of m16n8k16 without passing through shared memory: the
-// order of the channels inside a product of q and k is free (both operands
-// use the same), and so is the order of the output channels, so a lane reads
-// 16 bytes in a row of a key and of a value.  Codes become exact fp16
-// numbers; the key scale multiplies the fp32 scores and the value scale
+// all 16 query rows.  Each warp keeps two steps in flight by asynchronous
+// copies into a ring of its own.  The order of the channels inside a product
+// of q and k is free (both operands use the same), and so is the order of the
+// output channels, so a lane reads 16 bytes in a row of a key and of a value
+// as its part of the m16n8k16 fragments.  Codes become exact fp16 numbers; the key scale multiplies the fp32 scores and the value scale
 // enters the weights, p_j = exp2(s_j - m) vs_j, through its logarithm with a
 // running maximum M of its own, so that the fp16 weights are at most 1
 // whatever the scales are.
@@ -97,7 +127,10 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
   constexpr int KL = D / 64;   // 16-byte loads of a key per lane
   constexpr int VW = D / 32;   // 4-byte words of a value per lane
   constexpr int NO = D / 8;    // output tiles of 8 channels
-  __shared__ float osum[AT_WARPS][KV_ROWS][D + 4];
+  constexpr int STAGE = 2 * WARP_TOKENS * D;
+  extern __shared__ __align__(128) unsigned char smem[];
+  unsigned char* ring = smem + (threadIdx.x >> 5) * STAGES * STAGE;
+  float(*osum)[KV_ROWS][D + 4] = reinterpret_cast<float(*)[KV_ROWS][D + 4]>(smem);  // after an item's steps
   __shared__ float sm[AT_WARPS][KV_ROWS], sM[AT_WARPS][KV_ROWS], sl[AT_WARPS][KV_ROWS];
   __shared__ int64_t scan[AT_WARPS];
   __shared__ int64_t found_at;
@@ -204,64 +237,86 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
     }
     float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[NO][4] = {};
-    const int64_t vstep = (int64_t)p.c.n_pages * hkv * p.c.block * D;
 
-    for (int u = u0; u < u1; ++u) {
-      const int pos0 = u * UNIT + warp * WARP_TOKENS;
-      if (pos0 >= seen) continue;  // whole warp
-      // two runs of 16 tokens, each inside one page
-      const int8_t* kp[2];
+    const int64_t vstep = (int64_t)p.c.n_pages * hkv * p.c.block * D;
+    // this warp's steps: 32 tokens each, UNIT apart
+    const int first = u0 * UNIT + warp * WARP_TOKENS, stop = min(u1 * UNIT, seen);
+    const int steps = first < stop ? (stop - first + UNIT - 1) / UNIT : 0;
+    // Page and scales of the runs of 16 tokens, two a step, run r in lane
+    // r % 32, fetched a chunk of 16 steps ahead.
+    auto page_of = [&](int chunk) {
+      const int step = chunk * 16 + (lane >> 1), pos = first + step * UNIT + 16 * (lane & 1);
+      if (step >= steps || pos >= seen) return -1;
+      const int page = __ldg(p.c.table + (size_t)s * p.c.max_blocks + pos / p.c.block);
+      if (page >= 0 && page < p.c.n_pages) return page;
+      raise_flag(p.st, FLAG_BAD_CACHE);
+      return -1;
+    };
+    auto scale_of = [&](int page, int isv) {
+      return page < 0 ? 1.f : __ldg(p.c.scales + ((size_t)isv * p.c.n_pages + page) * hkv + h);
+    };
+    int chunk_now = 0;
+    int page = page_of(0), next_page = page_of(1);
+    float kscale = scale_of(page, 0), vscale = scale_of(page, 1), next_k = 0.f, next_v = 0.f;
+    auto issue = [&](int step) {
+      if (step < steps) {
+        unsigned char* dst = ring + (step % STAGES) * STAGE;
+        const int ahead = (step >> 4) != chunk_now;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int src_lane = (2 * step + r) & 31;
+          const int pg = __shfl_sync(~0u, ahead ? next_page : page, src_lane);
+          if (pg < 0) continue;
+          const int pos = first + step * UNIT + 16 * r;
+          const int8_t* src = p.c.codes + (((size_t)pg * hkv + h) * p.c.block + pos % p.c.block) * D;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const int c = lane % (D / 16), tok = lane / (D / 16) + i * (512 / D);
+            const int8_t* from = src + tok * D + 16 * c;
+            cp_async16(dst + k_at<D>(16 * r + tok, c), from);
+            cp_async16(dst + 32 * D + v_at<D>(16 * r + tok, c), from + vstep);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+    issue(0);
+    issue(1);
+
+    for (int i = 0; i < steps; ++i) {
+      if ((i & 15) == 0 && i) {  // the next chunk's runs
+        page = next_page;
+        kscale = next_k;
+        vscale = next_v;
+        ++chunk_now;
+        next_page = page_of(chunk_now + 1);
+      }
+      if ((i & 15) == 8) {
+        next_k = scale_of(next_page, 0);
+        next_v = scale_of(next_page, 1);
+      }
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();  // this step's codes are there, and the last step's are read by every lane
+      issue(i + STAGES - 1);
+      const unsigned char* src = ring + (i % STAGES) * STAGE;
+      const int pos0 = first + i * UNIT;
       float ksc[2], vlog[2];
       bool live[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int pos = pos0 + 16 * r;
-        live[r] = pos < seen;
-        int page = 0;
-        if (live[r]) page = p.c.table[(size_t)s * p.c.max_blocks + pos / p.c.block];
-        if (page < 0 || page >= p.c.n_pages) {
-          raise_flag(p.st, FLAG_BAD_CACHE);
-          live[r] = false;
-          page = 0;
-        }
-        const size_t blk = (size_t)page * hkv + h;
-        kp[r] = p.c.codes + (blk * p.c.block + pos % p.c.block) * D;
-        ksc[r] = live[r] ? p.c.scales[blk] : 0.f;
-        vlog[r] = live[r] ? log2f(p.c.scales[(size_t)p.c.n_pages * hkv + blk]) : 0.f;
+        const int run = (2 * i + r) & 31;
+        live[r] = __shfl_sync(~0u, page, run) >= 0;
+        ksc[r] = __shfl_sync(~0u, kscale, run);
+        vlog[r] = __log2f(__shfl_sync(~0u, vscale, run));
       }
-      uint4 kv[4][KL];
-      uint32_t vv[2][4][VW];
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int e = 0; e < KL; ++e) {
-          kv[a][e] = make_uint4(0, 0, 0, 0);
-          if (live[a >> 1])
-            kv[a][e] = *reinterpret_cast<const uint4*>(kp[a >> 1] + (8 * (a & 1) + g) * D + 64 * e + 16 * j);
-        }
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int8_t* vp = kp[r] + vstep + ((e >> 1) * 8 + 2 * j + (e & 1)) * D + (D / 8) * g;
-          if (VW == 4) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (live[r]) w = *reinterpret_cast<const uint4*>(vp);
-            vv[r][e][0] = w.x, vv[r][e][1] = w.y, vv[r][e][VW - 2] = w.z, vv[r][e][VW - 1] = w.w;
-          } else {
-            uint2 w = make_uint2(0, 0);
-            if (live[r]) w = *reinterpret_cast<const uint2*>(vp);
-            vv[r][e][0] = w.x, vv[r][e][1] = w.y;
-          }
-        }
       // ---- scores
       float sc[4][4] = {};
 #pragma unroll
       for (int a = 0; a < 4; ++a)
 #pragma unroll
         for (int e = 0; e < KL; ++e) {
-          const uint32_t w[4] = {kv[a][e].x ^ 0x80808080u, kv[a][e].y ^ 0x80808080u, kv[a][e].z ^ 0x80808080u,
-                                 kv[a][e].w ^ 0x80808080u};
+          const uint4 c = *reinterpret_cast<const uint4*>(src + k_at<D>(8 * a + g, 4 * e + j));
+          const uint32_t w[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
 #pragma unroll
           for (int i = 0; i < 4; ++i) mma_f16(sc[a], qa[4 * e + i], codes_f16<0x4140>(w[i]), codes_f16<0x4342>(w[i]));
         }
@@ -289,11 +344,12 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
         const float drop = ex2(M[e] - uM[e]);
         m[e] = nm[e];
         M[e] = nM[e];
+        if (__any_sync(~0u, drop != 1.f))
 #pragma unroll
-        for (int i = 0; i < NO; ++i) {
-          o[i][2 * e] *= drop;
-          o[i][2 * e + 1] *= drop;
-        }
+          for (int t = 0; t < NO; ++t) {
+            o[t][2 * e] *= drop;
+            o[t][2 * e + 1] *= drop;
+          }
       }
       // ---- weights, and their products with the values
 #pragma unroll
@@ -308,13 +364,26 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
             const __half2 w = __floats2half2_rn(ex2(z0 + vlog[r] - uM[e]), ex2(z1 + vlog[r] - uM[e]));
             pa[2 * a + e] = *reinterpret_cast<const uint32_t*>(&w);
           }
+        // values of tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of the run, D / 8 channels from (D / 8) g on
+        uint32_t vv[4][VW];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const unsigned char* vp = src + 32 * D + v_at<D>(16 * r + (e >> 1) * 8 + 2 * j + (e & 1), (D / 8) * g >> 4);
+          if (VW == 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(vp);
+            vv[e][0] = w.x, vv[e][1] = w.y, vv[e][VW - 2] = w.z, vv[e][VW - 1] = w.w;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(vp + 8 * (g & 1));
+            vv[e][0] = w.x, vv[e][1] = w.y;
+          }
+        }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           uint32_t lo[2], hi[2];  // bytes of two tokens side by side
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            lo[e] = __byte_perm(vv[r][2 * e][w], vv[r][2 * e + 1][w], 0x5140) ^ 0x80808080u;
-            hi[e] = __byte_perm(vv[r][2 * e][w], vv[r][2 * e + 1][w], 0x7362) ^ 0x80808080u;
+            lo[e] = __byte_perm(vv[2 * e][w], vv[2 * e + 1][w], 0x5140) ^ 0x80808080u;
+            hi[e] = __byte_perm(vv[2 * e][w], vv[2 * e + 1][w], 0x7362) ^ 0x80808080u;
           }
           mma_f16(o[4 * w + 0], pa, codes_f16<0x4140>(lo[0]), codes_f16<0x4140>(lo[1]));
           mma_f16(o[4 * w + 1], pa, codes_f16<0x4342>(lo[0]), codes_f16<0x4342>(lo[1]));
@@ -323,6 +392,8 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
         }
       }
     }
+
+    cp_async_wait<0>();
 
     // ---- the four warps' results
 #pragma unroll
@@ -335,7 +406,7 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
         sl[warp][g + 8 * e] = l[e];
       }
     }
-    __syncthreads();
+    __syncthreads();  // also: every warp is done with its ring
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = g + 8 * e;
@@ -457,9 +528,10 @@ cudaError_t launch_kv_attention(const uint16_t* q, int64_t q_stride, const int32
   p.counters = reinterpret_cast<uint32_t*>(ws + kv_counter_off());
   p.partials = reinterpret_cast<float*>(ws + kv_partial_off());
   const dim3 grid(kv_grid_max()), block(AT_THREADS);
-  cudaError_t e;
   auto* kern = c.d == 64 ? kv_attention_kernel<64> : kv_attention_kernel<128>;
-  MOE_LAUNCH("kv_attention", s, { e = launch_k(kern, grid, block, 0, s, p); });
+  cudaError_t e = set_smem_limit_once(kern, at_smem(c.d));
+  if (e != cudaSuccess) return e;
+  MOE_LAUNCH("kv_attention", s, { e = launch_k(kern, grid, block, at_smem(c.d), s, p); });
   return e;
 }
 
