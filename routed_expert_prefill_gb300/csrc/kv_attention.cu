@@ -1,4 +1,5 @@
 // Causal attention over the paged 8-bit key/value cache (moe_kv_attention).
+#include <limits.h>
 #include <math.h>
 
 #include "kv_common.cuh"
@@ -11,10 +12,17 @@ constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = AT_WARPS * 32;
 constexpr int WARP_TOKENS = 32;                      // tokens of one warp step
 constexpr int UNIT = AT_WARPS * WARP_TOKENS;         // tokens of one CTA step
-constexpr int STAGES = 3;                            // steps of a warp in its ring
 
-__host__ __device__ constexpr int at_smem(int d) {
-  const int ring = AT_WARPS * STAGES * 2 * WARP_TOKENS * d, sums = AT_WARPS * KV_ROWS * (d + 4) * 4;
+// Variants by the rows of a query tile, 8 NT: how many CTAs an SM holds and
+// how many steps a warp's ring.
+template <int NT>
+struct Shape {
+  static constexpr int ROWS = 8 * NT, CTAS = NT == 1 ? 3 : 2, STAGES = NT == 1 ? 2 : 3;
+};
+
+template <int D, int NT>
+constexpr int at_smem() {
+  const int ring = AT_WARPS * Shape<NT>::STAGES * 2 * WARP_TOKENS * D, sums = AT_WARPS * 8 * NT * (D + 4) * 4;
   return ring > sums ? ring : sums;
 }
 
@@ -49,6 +57,7 @@ struct AttnParams {
   const int32_t* starts;
   int t, hq, G;       // G query heads read one key/value head
   float scale_log2;   // scale * log2(e)
+  int block_log2;
   moe_kv_cache c;
   uint16_t* out;
   DeviceStatus* st;
@@ -69,14 +78,25 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two biased codes (code + 128, in bytes SEL selects) as exact fp16 numbers:
-// under the exponent of 1024 a byte b is 1024 + b.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
-  uint32_t v;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(v) : "r"(w), "r"(0x64646464u), "n"(SEL));
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v), __floats2half2_rn(1152.f, 1152.f));
-  return *reinterpret_cast<const uint32_t*>(&r);
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+// Codes c of bytes 0 and 2, and of bytes 1 and 3, as the fp16 numbers
+// (c + 128) * 2^-24: below fp16's normal range the bits are the value.
+__device__ __forceinline__ uint32_t codes_even(uint32_t w) { return (w ^ 0x80808080u) & 0x00FF00FFu; }
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return ((w >> 8) ^ 0x00808080u) & 0x00FF00FFu; }
+
+// Byte B of two words as exact fp16 numbers: under the exponent of 1024 the
+// byte c ^ 0x80 is 1024 + 128 + c.
+template <int B>
+__device__ __forceinline__ uint32_t codes_pair(uint32_t a, uint32_t b) {
+  const uint32_t v = (__byte_perm(a, b, B | (4 + B) << 8) & 0x00FF00FFu) ^ 0x64806480u;
+  return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&v), __floats2half2_rn(1152.f, 1152.f)));
 }
 
 struct Seq {
@@ -90,20 +110,24 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int s) {
   if (!q.ok) q.n = 0;
   return q;
 }
+template <int ROWS>
 __device__ __forceinline__ int q_tiles(const AttnParams& p, const Seq& q) {
-  return (int)(((int64_t)q.n * p.G + KV_ROWS - 1) / KV_ROWS);
+  return (int)(((int64_t)q.n * p.G + ROWS - 1) / ROWS);
 }
 // CTA steps of query tile qt: up to the last position its last row sees.
+template <int ROWS>
 __device__ __forceinline__ int tile_seen(const AttnParams& p, const Seq& q, int qt) {
-  const int64_t rows = min((int64_t)q.n * p.G, (int64_t)KV_ROWS * (qt + 1));
+  const int64_t rows = min((int64_t)q.n * p.G, (int64_t)ROWS * (qt + 1));
   return q.len - q.n + (int)((rows - 1) / p.G) + 1;
 }
+template <int ROWS>
 __device__ __forceinline__ int tile_units(const AttnParams& p, const Seq& q, int qt) {
-  return (tile_seen(p, q, qt) + UNIT - 1) / UNIT;
+  return (tile_seen<ROWS>(p, q, qt) + UNIT - 1) / UNIT;
 }
+template <int ROWS>
 __device__ __forceinline__ int64_t seq_units(const AttnParams& p, const Seq& q) {
   int64_t w = 0;
-  for (int qt = 0, m = q_tiles(p, q); qt < m; ++qt) w += tile_units(p, q, qt);
+  for (int qt = 0, m = q_tiles<ROWS>(p, q); qt < m; ++qt) w += tile_units<ROWS>(p, q, qt);
   return w * p.c.hkv;
 }
 
@@ -114,24 +138,33 @@ __device__ __forceinline__ int64_t seq_units(const AttnParams& p, const Seq& q) 
 // joins them in CTA order.
 //
 // Within an item the CTA's four warps take 32 tokens each per step and hold
-// all 16 query rows.  Each warp keeps two steps in flight by asynchronous
-// copies into a ring of its own.  The order of the channels inside a product
-// of q and k is free (both operands use the same), and so is the order of the
-// output channels, so a lane reads 16 bytes in a row of a key and of a value
-// as its part of the m16n8k16 fragments.  Codes become exact fp16 numbers; the key scale multiplies the fp32 scores and the value scale
-// enters the weights, p_j = exp2(s_j - m) vs_j, through its logarithm with a
-// running maximum M of its own, so that the fp16 weights are at most 1
+// all 8 NT query rows.  Each warp keeps its next step or two in flight by
+// asynchronous copies into a ring of its own.  The products are taken
+// transposed, S^T = K Q^T and O^T = V^T P^T in m16n8k16, so that tokens and
+// channels fill the 16 rows and eight query rows, a common group of heads,
+// the eight columns; S^T's fragments become P^T's by 8 x 8 transposes.  The
+// order of the channels inside a product of q and k is free (both operands
+// use the same), and so is the order of the output channels, so a lane reads
+// 16 bytes in a row of a key and of a value as its part of the fragments.
+//
+// Codes enter exactly.  A key's code is read as (c + 128) 2^-24, and 128 2^-24
+// times the query row's sum is taken off the score (8 products deep, so the
+// difference loses nothing that matters); values, summed over all tokens, are
+// converted to c itself.  The key scale multiplies the fp32 scores; the value
+// scale enters the weights, p_j = exp2(s_j - m) vs_j, through its logarithm
+// with a running maximum M of its own, so that the fp16 weights are at most 1
 // whatever the scales are.
-template <int D>
-__global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kernel(AttnParams p) {
+template <int D, int NT>
+__global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kernel(AttnParams p) {
+  constexpr int ROWS = Shape<NT>::ROWS, STAGES = Shape<NT>::STAGES;
   constexpr int KL = D / 64;   // 16-byte loads of a key per lane
   constexpr int VW = D / 32;   // 4-byte words of a value per lane
-  constexpr int NO = D / 8;    // output tiles of 8 channels
+  constexpr int NO = D / 16;   // output tiles of 16 channels
   constexpr int STAGE = 2 * WARP_TOKENS * D;
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* ring = smem + (threadIdx.x >> 5) * STAGES * STAGE;
-  float(*osum)[KV_ROWS][D + 4] = reinterpret_cast<float(*)[KV_ROWS][D + 4]>(smem);  // after an item's steps
-  __shared__ float sm[AT_WARPS][KV_ROWS], sM[AT_WARPS][KV_ROWS], sl[AT_WARPS][KV_ROWS];
+  float(*osum)[ROWS][D + 4] = reinterpret_cast<float(*)[ROWS][D + 4]>(smem);  // after an item's steps
+  __shared__ float sm[AT_WARPS][ROWS], sM[AT_WARPS][ROWS], sl[AT_WARPS][ROWS];
   __shared__ int64_t scan[AT_WARPS];
   __shared__ int64_t found_at;
   __shared__ int found_s;
@@ -142,11 +175,13 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
   const int hkv = p.c.hkv;
 
   // total steps, then the sequence that holds this CTA's first step
-  int64_t total = 0;
+  int64_t total = 0, w0 = 0;
   for (int s = tid; s < p.c.n_seq; s += AT_THREADS) {
     const Seq q = load_seq(p, s);
     if (!q.ok && blockIdx.x == 0) raise_flag(p.st, FLAG_BAD_CACHE);
-    total += seq_units(p, q);
+    const int64_t w = seq_units<ROWS>(p, q);
+    if (s == tid) w0 = w;
+    total += w;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
@@ -159,7 +194,8 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
   const int64_t x0 = total * cta / ctas, x1 = total * (cta + 1) / ctas;
   int64_t base = 0;
   for (int sb = 0; sb < p.c.n_seq; sb += AT_THREADS) {
-    const int64_t w = sb + tid < p.c.n_seq ? seq_units(p, load_seq(p, sb + tid)) : 0;
+    int64_t w = w0;
+    if (sb) w = sb + tid < p.c.n_seq ? seq_units<ROWS>(p, load_seq(p, sb + tid)) : 0;
     int64_t incl = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -186,7 +222,7 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
   int qt = 0, h = 0, u0 = 0;
   int64_t off = x0 - found_at;
   for (;; ++qt) {
-    const int units = tile_units(p, q, qt);
+    const int units = tile_units<ROWS>(p, q, qt);
     if (off < (int64_t)units * hkv) {
       h = (int)(off / units);
       u0 = (int)(off % units);
@@ -197,21 +233,21 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
 
   int64_t x = x0;
   while (x < x1) {
-    const int units = tile_units(p, q, qt), seen = tile_seen(p, q, qt);
+    const int units = tile_units<ROWS>(p, q, qt), seen = tile_seen<ROWS>(p, q, qt);
     const int u1 = (int)min((int64_t)units, u0 + (x1 - x));
-    const int rows = (int)min((int64_t)q.n * p.G - (int64_t)qt * KV_ROWS, (int64_t)KV_ROWS);
+    const int rows = (int)min((int64_t)q.n * p.G - (int64_t)qt * ROWS, (int64_t)ROWS);
     // ---- query fragments, each row scaled by a power of two into fp16
-    uint32_t qa[KL * 4][4];
-    float f[2];
-    int limit[2];
+    uint32_t qb[NT][KL * 4][2];
+    float F[NT][2], off_q[NT][2];  // of rows 2 j, 2 j + 1: score per product, 128 2^-24 times the row's sum
+    int limit[NT][2];              // last position seen
+    int all_see = INT_MAX;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = g + 8 * e;
-      uint2 raw[KL * 4];
-      float m = 0.f;
-      const int64_t rr = (int64_t)qt * KV_ROWS + r;
+    for (int t = 0; t < NT; ++t) {
+      const int r = 8 * t + g;
+      const int64_t rr = (int64_t)qt * ROWS + r;
       const int i = (int)(rr / p.G), head = h * p.G + (int)(rr % p.G);
-      limit[e] = r < rows ? q.len - q.n + i : -1;
+      uint2 raw[KL * 4];
+      float m = 0.f, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < KL * 4; ++w) {
         raw[w] = make_uint2(0, 0);
@@ -226,19 +262,42 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
       // the row's largest magnitude goes to [256, 512)
       const int ex = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
       const float up = __uint_as_float((uint32_t)(127 + 8 - ex) << 23);
-      f[e] = __uint_as_float((uint32_t)(max(127 - 8 + ex, 1)) << 23) * p.scale_log2;
 #pragma unroll
       for (int w = 0; w < KL * 4; ++w) {
-        const __half2 a = __floats2half2_rn(bf16lo(raw[w].x) * up, bf16hi(raw[w].x) * up);
-        const __half2 b = __floats2half2_rn(bf16lo(raw[w].y) * up, bf16hi(raw[w].y) * up);
-        qa[w][e] = *reinterpret_cast<const uint32_t*>(&a);
-        qa[w][2 + e] = *reinterpret_cast<const uint32_t*>(&b);
+        // with the keys' bytes 0 and 2, then 1 and 3
+        const __half2 a = __floats2half2_rn(bf16lo(raw[w].x) * up, bf16lo(raw[w].y) * up);
+        const __half2 b = __floats2half2_rn(bf16hi(raw[w].x) * up, bf16hi(raw[w].y) * up);
+        qb[t][w][0] = half2_bits(a);
+        qb[t][w][1] = half2_bits(b);
+        sum += (__low2float(a) + __high2float(a)) + (__low2float(b) + __high2float(b));
+      }
+      sum += __shfl_xor_sync(~0u, sum, 1);
+      sum += __shfl_xor_sync(~0u, sum, 2);
+      const float f = __uint_as_float((uint32_t)(max(127 - 8 + ex, 1)) << 23) * p.scale_log2 * 0x1p24f;
+      // rows past the last: nothing of theirs is stored, so they may see all
+      const int lim = r < rows ? q.len - q.n + i : INT_MAX;
+      all_see = min(all_see, lim);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        F[t][c] = __shfl_sync(~0u, f, 4 * (2 * j + c));
+        off_q[t][c] = __shfl_sync(~0u, sum, 4 * (2 * j + c)) * 0x1p-17f;
+        limit[t][c] = __shfl_sync(~0u, lim, 4 * (2 * j + c));
       }
     }
-    float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[NO][4] = {};
+    all_see = __reduce_min_sync(~0u, all_see);
+    float m[NT][2], M[NT][2], l[NT][2], o[NT][NO][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = M[t][0] = M[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NO; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+    }
 
-    const int64_t vstep = (int64_t)p.c.n_pages * hkv * p.c.block * D;
+    // a lane copies 16 bytes, piece lane_c of every (512 / D)-th token from lane_tok on
+    const int lane_c = lane % (D / 16), lane_tok = lane / (D / 16);
+    const int64_t page_bytes = (int64_t)hkv * p.c.block * D, vstep = p.c.n_pages * page_bytes;
+    const int8_t* lane_k = p.c.codes + (int64_t)h * p.c.block * D + lane_tok * D + 16 * lane_c;
     // this warp's steps: 32 tokens each, UNIT apart
     const int first = u0 * UNIT + warp * WARP_TOKENS, stop = min(u1 * UNIT, seen);
     const int steps = first < stop ? (stop - first + UNIT - 1) / UNIT : 0;
@@ -247,7 +306,7 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
     auto page_of = [&](int chunk) {
       const int step = chunk * 16 + (lane >> 1), pos = first + step * UNIT + 16 * (lane & 1);
       if (step >= steps || pos >= seen) return -1;
-      const int page = __ldg(p.c.table + (size_t)s * p.c.max_blocks + pos / p.c.block);
+      const int page = __ldg(p.c.table + (size_t)s * p.c.max_blocks + (pos >> p.block_log2));
       if (page >= 0 && page < p.c.n_pages) return page;
       raise_flag(p.st, FLAG_BAD_CACHE);
       return -1;
@@ -261,27 +320,24 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
     auto issue = [&](int step) {
       if (step < steps) {
         unsigned char* dst = ring + (step % STAGES) * STAGE;
-        const int ahead = (step >> 4) != chunk_now;
+        const int pg_lane = (step >> 4) != chunk_now ? next_page : page;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int src_lane = (2 * step + r) & 31;
-          const int pg = __shfl_sync(~0u, ahead ? next_page : page, src_lane);
+          const int pg = __shfl_sync(~0u, pg_lane, (2 * step + r) & 31);
           if (pg < 0) continue;
-          const int pos = first + step * UNIT + 16 * r;
-          const int8_t* src = p.c.codes + (((size_t)pg * hkv + h) * p.c.block + pos % p.c.block) * D;
+          const int8_t* k = lane_k + pg * page_bytes + ((first + step * UNIT + 16 * r) & (p.c.block - 1)) * D;
+          const int8_t* v = k + vstep;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
-            const int c = lane % (D / 16), tok = lane / (D / 16) + i * (512 / D);
-            const int8_t* from = src + tok * D + 16 * c;
-            cp_async16(dst + k_at<D>(16 * r + tok, c), from);
-            cp_async16(dst + 32 * D + v_at<D>(16 * r + tok, c), from + vstep);
+            cp_async16(dst + k_at<D>(16 * r + lane_tok + i * (512 / D), lane_c), k + 512 * i);
+            cp_async16(dst + 32 * D + v_at<D>(16 * r + lane_tok + i * (512 / D), lane_c), v + 512 * i);
           }
         }
       }
       cp_async_commit();
     };
-    issue(0);
-    issue(1);
+#pragma unroll
+    for (int i = 0; i < (STAGES > 2 ? STAGES - 1 : 2); ++i) issue(i);
 
     for (int i = 0; i < steps; ++i) {
       if ((i & 15) == 0 && i) {  // the next chunk's runs
@@ -295,9 +351,9 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
         next_k = scale_of(next_page, 0);
         next_v = scale_of(next_page, 1);
       }
-      cp_async_wait<STAGES - 2>();
+      cp_async_wait<(STAGES > 2 ? STAGES - 2 : 1)>();
       __syncwarp();  // this step's codes are there, and the last step's are read by every lane
-      issue(i + STAGES - 1);
+      if (STAGES > 2) issue(i + STAGES - 1);
       const unsigned char* src = ring + (i % STAGES) * STAGE;
       const int pos0 = first + i * UNIT;
       float ksc[2], vlog[2];
@@ -309,66 +365,90 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
         ksc[r] = __shfl_sync(~0u, kscale, run);
         vlog[r] = __log2f(__shfl_sync(~0u, vscale, run));
       }
-      // ---- scores
-      float sc[4][4] = {};
+      // ---- scores: row g of tile a is token 16 a + g, column c query row c
+      float sc[NT][2][4] = {};
 #pragma unroll
-      for (int a = 0; a < 4; ++a)
+      for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int e = 0; e < KL; ++e) {
-          const uint4 c = *reinterpret_cast<const uint4*>(src + k_at<D>(8 * a + g, 4 * e + j));
-          const uint32_t w[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
+          const uint4 lo = *reinterpret_cast<const uint4*>(src + k_at<D>(16 * a + g, 4 * e + j));
+          const uint4 hi = *reinterpret_cast<const uint4*>(src + k_at<D>(16 * a + 8 + g, 4 * e + j));
+          const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_f16(sc[a], qa[4 * e + i], codes_f16<0x4140>(w[i]), codes_f16<0x4342>(w[i]));
-        }
-      float nm[2] = {m[0], m[1]}, nM[2] = {M[0], M[1]};
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t k[4] = {codes_even(lw[i]), codes_even(hw[i]), codes_odd(lw[i]), codes_odd(hw[i])};
 #pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = a >> 1, pos = pos0 + 8 * a + 2 * j + (e & 1);
-          sc[a][e] = live[r] && pos <= limit[e >> 1] ? sc[a][e] * (ksc[r] * f[e >> 1]) : -INFINITY;
-          nm[e >> 1] = fmaxf(nm[e >> 1], sc[a][e]);
-          nM[e >> 1] = fmaxf(nM[e >> 1], sc[a][e] + vlog[r]);
-        }
-      float um[2], uM[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        nm[e] = fmaxf(nm[e], __shfl_xor_sync(~0u, nm[e], 1));
-        nm[e] = fmaxf(nm[e], __shfl_xor_sync(~0u, nm[e], 2));
-        nM[e] = fmaxf(nM[e], __shfl_xor_sync(~0u, nM[e], 1));
-        nM[e] = fmaxf(nM[e], __shfl_xor_sync(~0u, nM[e], 2));
-        // rows that have seen nothing yet: any finite reference does
-        um[e] = nm[e] == -INFINITY ? 0.f : nm[e];
-        uM[e] = nM[e] == -INFINITY ? 0.f : nM[e];
-        l[e] *= ex2(m[e] - um[e]);
-        const float drop = ex2(M[e] - uM[e]);
-        m[e] = nm[e];
-        M[e] = nM[e];
-        if (__any_sync(~0u, drop != 1.f))
-#pragma unroll
-          for (int t = 0; t < NO; ++t) {
-            o[t][2 * e] *= drop;
-            o[t][2 * e + 1] *= drop;
+            for (int t = 0; t < NT; ++t) mma_f16(sc[t][a], k, qb[t][4 * e + i][0], qb[t][4 * e + i][1]);
           }
-      }
-      // ---- weights, and their products with the values
+        }
+      const bool whole = live[0] && live[1] && pos0 + WARP_TOKENS - 1 <= all_see;
+      uint32_t pb[NT][2][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t pa[4];
+      for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float z0 = sc[2 * r + a][2 * e], z1 = sc[2 * r + a][2 * e + 1];
-            l[e] += ex2(z0 - um[e]) + ex2(z1 - um[e]);
-            const __half2 w = __floats2half2_rn(ex2(z0 + vlog[r] - uM[e]), ex2(z1 + vlog[r] - uM[e]));
-            pa[2 * a + e] = *reinterpret_cast<const uint32_t*>(&w);
+          for (int c = 0; c < 2; ++c) {
+            const float f = F[t][c] * ksc[a], d = -off_q[t][c] * f;
+            sc[t][a][c] = fmaf(sc[t][a][c], f, d);
+            sc[t][a][2 + c] = fmaf(sc[t][a][2 + c], f, d);
           }
-        // values of tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of the run, D / 8 channels from (D / 8) g on
+        if (!whole) {
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!live[a] || pos0 + 16 * a + 8 * (e >> 1) + g > limit[t][e & 1]) sc[t][a][e] = -INFINITY;
+        }
+        float um[2], uM[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float x0 = fmaxf(sc[t][0][c], sc[t][0][2 + c]), x1 = fmaxf(sc[t][1][c], sc[t][1][2 + c]);
+          float nm = fmaxf(x0, x1), nM = fmaxf(x0 + vlog[0], x1 + vlog[1]);
+#pragma unroll
+          for (int s = 4; s < 32; s *= 2) {
+            nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, s));
+            nM = fmaxf(nM, __shfl_xor_sync(~0u, nM, s));
+          }
+          nm = fmaxf(nm, m[t][c]);
+          nM = fmaxf(nM, M[t][c]);
+          // rows that have seen nothing yet: any finite reference does
+          um[c] = nm == -INFINITY ? 0.f : nm;
+          uM[c] = nM == -INFINITY ? 0.f : nM;
+          if (__any_sync(~0u, nm != m[t][c])) l[t][c] *= ex2(m[t][c] - um[c]);
+          if (__any_sync(~0u, nM != M[t][c])) {
+            const float drop = ex2(M[t][c] - uM[c]);
+#pragma unroll
+            for (int i = 0; i < NO; ++i) {
+              o[t][i][c] *= drop;
+              o[t][i][2 + c] *= drop;
+            }
+          }
+          m[t][c] = nm;
+          M[t][c] = nM;
+        }
+        // ---- weights, transposed into the second product's operand
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const float v0 = vlog[a] - uM[0], v1 = vlog[a] - uM[1];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float z0 = sc[t][a][2 * e], z1 = sc[t][a][2 * e + 1];
+            l[t][0] += ex2(z0 - um[0]);
+            l[t][1] += ex2(z1 - um[1]);
+            pb[t][a][e] = transpose8x8(half2_bits(__floats2half2_rn(ex2(z0 + v0), ex2(z1 + v1))));
+          }
+        }
+      }
+      // ---- values: tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of run a, channels
+      // (D / 8) g on; row g of output tile i is channel (D / 8) g + 2 i, row
+      // g + 8 the next one
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
         uint32_t vv[4][VW];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const unsigned char* vp = src + 32 * D + v_at<D>(16 * r + (e >> 1) * 8 + 2 * j + (e & 1), (D / 8) * g >> 4);
+          const unsigned char* vp = src + 32 * D + v_at<D>(16 * a + (e >> 1) * 8 + 2 * j + (e & 1), (D / 8) * g >> 4);
           if (VW == 4) {
             const uint4 w = *reinterpret_cast<const uint4*>(vp);
             vv[e][0] = w.x, vv[e][1] = w.y, vv[e][VW - 2] = w.z, vv[e][VW - 1] = w.w;
@@ -379,49 +459,56 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
         }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
-          uint32_t lo[2], hi[2];  // bytes of two tokens side by side
+          const uint32_t c0[4] = {codes_pair<0>(vv[0][w], vv[1][w]), codes_pair<1>(vv[0][w], vv[1][w]),
+                                  codes_pair<0>(vv[2][w], vv[3][w]), codes_pair<1>(vv[2][w], vv[3][w])};
+          const uint32_t c1[4] = {codes_pair<2>(vv[0][w], vv[1][w]), codes_pair<3>(vv[0][w], vv[1][w]),
+                                  codes_pair<2>(vv[2][w], vv[3][w]), codes_pair<3>(vv[2][w], vv[3][w])};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            lo[e] = __byte_perm(vv[2 * e][w], vv[2 * e + 1][w], 0x5140) ^ 0x80808080u;
-            hi[e] = __byte_perm(vv[2 * e][w], vv[2 * e + 1][w], 0x7362) ^ 0x80808080u;
+          for (int t = 0; t < NT; ++t) {
+            mma_f16(o[t][2 * w], c0, pb[t][a][0], pb[t][a][1]);
+            mma_f16(o[t][2 * w + 1], c1, pb[t][a][0], pb[t][a][1]);
           }
-          mma_f16(o[4 * w + 0], pa, codes_f16<0x4140>(lo[0]), codes_f16<0x4140>(lo[1]));
-          mma_f16(o[4 * w + 1], pa, codes_f16<0x4342>(lo[0]), codes_f16<0x4342>(lo[1]));
-          mma_f16(o[4 * w + 2], pa, codes_f16<0x4140>(hi[0]), codes_f16<0x4140>(hi[1]));
-          mma_f16(o[4 * w + 3], pa, codes_f16<0x4342>(hi[0]), codes_f16<0x4342>(hi[1]));
         }
       }
+      if (STAGES == 2) {
+        __syncwarp();
+        issue(i + 2);
+      }
     }
-
     cp_async_wait<0>();
 
     // ---- the four warps' results
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(~0u, l[e], 1);
-      l[e] += __shfl_xor_sync(~0u, l[e], 2);
-      if (j == 0) {
-        sm[warp][g + 8 * e] = m[e];
-        sM[warp][g + 8 * e] = M[e];
-        sl[warp][g + 8 * e] = l[e];
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int s = 4; s < 32; s *= 2) l[t][c] += __shfl_xor_sync(~0u, l[t][c], s);
+        if (g == 0) {
+          const int r = 8 * t + 2 * j + c;
+          sm[warp][r] = m[t][c];
+          sM[warp][r] = M[t][c];
+          sl[warp][r] = l[t][c];
+        }
       }
-    }
     __syncthreads();  // also: every warp is done with its ring
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = g + 8 * e;
-      float top = fmaxf(fmaxf(sM[0][r], sM[1][r]), fmaxf(sM[2][r], sM[3][r]));
-      if (top == -INFINITY) top = 0.f;
-      const float drop = ex2(M[e] - top);
-      // output tile i, column c stands for channel (D / 8) c + i
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < 2; ++c) {
+        const int r = 8 * t + 2 * j + c;
+        float top = fmaxf(fmaxf(sM[0][r], sM[1][r]), fmaxf(sM[2][r], sM[3][r]));
+        if (top == -INFINITY) top = 0.f;
+        const float drop = ex2(M[t][c] - top);
 #pragma unroll
-        for (int i = 0; i < NO; ++i) osum[warp][r][(D / 8) * (2 * j + c) + i] = o[i][2 * e + c] * drop;
-    }
+        for (int i = 0; i < NO; ++i)
+          *reinterpret_cast<float2*>(&osum[warp][r][(D / 8) * g + 2 * i]) =
+              make_float2(o[t][i][c] * drop, o[t][i][2 + c] * drop);
+      }
     __syncthreads();
-    const int r = tid >> 3, d0 = (tid & 7) * (D / 8);  // 8 threads a row
-    float cm = -INFINITY, cM = -INFINITY, cl = 0.f, acc[D / 8];
+    constexpr int TPR = AT_THREADS / ROWS, DPT = D / TPR;  // threads of a row, channels of a thread
+    const int r = tid / TPR, d0 = (tid % TPR) * DPT;
+    float cm = -INFINITY, cM = -INFINITY, cl = 0.f, acc[DPT];
 #pragma unroll
     for (int w = 0; w < AT_WARPS; ++w) {
       cm = fmaxf(cm, sm[w][r]);
@@ -430,7 +517,7 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
 #pragma unroll
     for (int w = 0; w < AT_WARPS; ++w) cl += sl[w][r] * ex2(sm[w][r] - (cm == -INFINITY ? 0.f : cm));
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < DPT; ++i)
       acc[i] = osum[0][r][d0 + i] + osum[1][r][d0 + i] + osum[2][r][d0 + i] + osum[3][r][d0 + i];
 
     const int64_t item = x - u0;  // the item's first step
@@ -441,9 +528,9 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
       float* mine = p.partials + (size_t)(2 * cta + (cta == c0)) * pf;
       if (r < rows) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) mine[r * D + d0 + i] = acc[i];
-        if ((tid & 7) == 0) {
-          float* sp = mine + KV_ROWS * D + 4 * r;
+        for (int i = 0; i < DPT; ++i) mine[r * D + d0 + i] = acc[i];
+        if (tid % TPR == 0) {
+          float* sp = mine + ROWS * D + 4 * r;
           sp[0] = cm, sp[1] = cM, sp[2] = cl;
         }
       }
@@ -458,20 +545,20 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
         cm = cM = -INFINITY;
         cl = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) acc[i] = 0.f;
+        for (int i = 0; i < DPT; ++i) acc[i] = 0.f;
         if (r < rows) {
           for (int c = c0; c <= c1; ++c) {
-            const float* sp = p.partials + (size_t)(2 * c + (c == c0)) * pf + KV_ROWS * D + 4 * r;
+            const float* sp = p.partials + (size_t)(2 * c + (c == c0)) * pf + ROWS * D + 4 * r;
             cm = fmaxf(cm, __ldcg(sp));
             cM = fmaxf(cM, __ldcg(sp + 1));
           }
           for (int c = c0; c <= c1; ++c) {
             const float* part = p.partials + (size_t)(2 * c + (c == c0)) * pf;
-            const float* sp = part + KV_ROWS * D + 4 * r;
+            const float* sp = part + ROWS * D + 4 * r;
             cl += __ldcg(sp + 2) * ex2(__ldcg(sp) - (cm == -INFINITY ? 0.f : cm));
             const float drop = ex2(__ldcg(sp + 1) - (cM == -INFINITY ? 0.f : cM));
 #pragma unroll
-            for (int i = 0; i < D / 8; i += 4) {
+            for (int i = 0; i < DPT; i += 4) {
               const float4 v = __ldcg(reinterpret_cast<const float4*>(part + r * D + d0 + i));
               acc[i] = fmaf(v.x, drop, acc[i]);
               acc[i + 1] = fmaf(v.y, drop, acc[i + 1]);
@@ -486,13 +573,12 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
       // sum p vs v = 2^(M - m) of what was accumulated; nothing seen, or all
       // values zero: 0
       const float k = cl == 0.f ? 0.f : (cM == -INFINITY ? 0.f : exp2f(cM - cm)) / cl;
-      const int64_t rr = (int64_t)qt * KV_ROWS + r;
+      const int64_t rr = (int64_t)qt * ROWS + r;
       uint16_t* dst = p.out + ((size_t)(q.row + rr / p.G) * p.hq + (size_t)h * p.G + rr % p.G) * D + d0;
 #pragma unroll
-      for (int i = 0; i < D / 8; i += 8)
-        *reinterpret_cast<uint4*>(dst + i) =
-            make_uint4(pack_bf16x2(acc[i] * k, acc[i + 1] * k), pack_bf16x2(acc[i + 2] * k, acc[i + 3] * k),
-                       pack_bf16x2(acc[i + 4] * k, acc[i + 5] * k), pack_bf16x2(acc[i + 6] * k, acc[i + 7] * k));
+      for (int i = 0; i < DPT; i += 4)
+        *reinterpret_cast<uint2*>(dst + i) = make_uint2(pack_bf16x2(acc[i] * k, acc[i + 1] * k),
+                                                        pack_bf16x2(acc[i + 2] * k, acc[i + 3] * k));
     }
     __syncthreads();  // the shared sums are free again
     // ---- next item
@@ -500,13 +586,23 @@ __global__ void __launch_bounds__(AT_THREADS, KV_CTAS_PER_SM) kv_attention_kerne
     u0 = 0;
     if (x < x1 && ++h == hkv) {
       h = 0;
-      if (++qt == q_tiles(p, q)) {
+      if (++qt == q_tiles<ROWS>(p, q)) {
         qt = 0;
         do q = load_seq(p, ++s);
         while (q.n == 0);  // x < x1 <= total: a later sequence has rows
       }
     }
   }
+}
+
+template <int D, int NT>
+cudaError_t launch_stream(const AttnParams& p, cudaStream_t s) {
+  auto* kern = kv_attention_kernel<D, NT>;
+  cudaError_t e = set_smem_limit_once(kern, at_smem<D, NT>());
+  if (e != cudaSuccess) return e;
+  const dim3 grid(sm_count() * Shape<NT>::CTAS), block(AT_THREADS);
+  MOE_LAUNCH("kv_attention", s, { e = launch_k(kern, grid, block, at_smem<D, NT>(), s, p); });
+  return e;
 }
 
 }  // namespace
@@ -522,17 +618,17 @@ cudaError_t launch_kv_attention(const uint16_t* q, int64_t q_stride, const int32
   p.hq = hq;
   p.G = hq / c.hkv;
   p.scale_log2 = scale * 1.44269504088896340736f;
+  p.block_log2 = c.block == 16 ? 4 : c.block == 32 ? 5 : c.block == 64 ? 6 : 7;
   p.c = c;
   p.out = out;
   p.st = reinterpret_cast<DeviceStatus*>(ws);
   p.counters = reinterpret_cast<uint32_t*>(ws + kv_counter_off());
   p.partials = reinterpret_cast<float*>(ws + kv_partial_off());
-  const dim3 grid(kv_grid_max()), block(AT_THREADS);
-  auto* kern = c.d == 64 ? kv_attention_kernel<64> : kv_attention_kernel<128>;
-  cudaError_t e = set_smem_limit_once(kern, at_smem(c.d));
-  if (e != cudaSuccess) return e;
-  MOE_LAUNCH("kv_attention", s, { e = launch_k(kern, grid, block, at_smem(c.d), s, p); });
-  return e;
+  // Eight rows a tile where they hold a token's group of heads and no
+  // sequence has more than one token on average, else sixteen.
+  const bool small = p.G <= 8 && t <= c.n_seq;
+  return c.d == 64 ? (small ? launch_stream<64, 1>(p, s) : launch_stream<64, 2>(p, s))
+                   : (small ? launch_stream<128, 1>(p, s) : launch_stream<128, 2>(p, s));
 }
 
 }  // namespace moe

@@ -6,8 +6,8 @@ namespace moe {
 
 // Workspace of both calls: the status block, the completion counters of the
 // split attention items, their partial results.
-constexpr int KV_CTAS_PER_SM = 2;
-constexpr int KV_ROWS = 16;  // rows of a query tile of the streaming kernel
+constexpr int KV_CTAS_PER_SM = 3;  // at most, of the streaming kernels
+constexpr int KV_ROWS = 16;        // rows of a query tile, at most
 
 inline int kv_grid_max() { return sm_count() * KV_CTAS_PER_SM; }
 inline size_t kv_counter_off() { return sizeof(DeviceStatus); }
