@@ -2,7 +2,7 @@
 #include <limits.h>
 #include <math.h>
 
-#include "kv_common.cuh"
+#include "kv_attention.cuh"
 
 namespace moe {
 
@@ -11,7 +11,7 @@ namespace {
 constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = AT_WARPS * 32;
 constexpr int WARP_TOKENS = 32;                      // tokens of one warp step
-constexpr int UNIT = AT_WARPS * WARP_TOKENS;         // tokens of one CTA step
+static_assert(UNIT == AT_WARPS * WARP_TOKENS, "a CTA step is a unit");
 
 // Variants by the rows of a query tile, 8 NT: how many CTAs an SM holds and
 // how many steps a warp's ring.
@@ -51,26 +51,6 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-struct AttnParams {
-  const uint16_t* q;
-  int64_t q_stride;
-  const int32_t* starts;
-  int t, hq, G;       // G query heads read one key/value head
-  float scale_log2;   // scale * log2(e)
-  int block_log2;
-  moe_kv_cache c;
-  uint16_t* out;
-  DeviceStatus* st;
-  uint32_t* counters;
-  float* partials;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -84,8 +64,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-
 // Codes c of bytes 0 and 2, and of bytes 1 and 3, as the fp16 numbers
 // (c + 128) * 2^-24: below fp16's normal range the bits are the value.
 __device__ __forceinline__ uint32_t codes_even(uint32_t w) { return (w ^ 0x80808080u) & 0x00FF00FFu; }
@@ -97,38 +75,6 @@ template <int B>
 __device__ __forceinline__ uint32_t codes_pair(uint32_t a, uint32_t b) {
   const uint32_t v = (__byte_perm(a, b, B | (4 + B) << 8) & 0x00FF00FFu) ^ 0x64806480u;
   return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&v), __floats2half2_rn(1152.f, 1152.f)));
-}
-
-struct Seq {
-  int row, n, len;
-  bool ok;
-};
-
-__device__ __forceinline__ Seq load_seq(const AttnParams& p, int s) {
-  Seq q;
-  q.ok = kv_sequence(p.c, p.starts, p.t, s, q.row, q.n, q.len);
-  if (!q.ok) q.n = 0;
-  return q;
-}
-template <int ROWS>
-__device__ __forceinline__ int q_tiles(const AttnParams& p, const Seq& q) {
-  return (int)(((int64_t)q.n * p.G + ROWS - 1) / ROWS);
-}
-// CTA steps of query tile qt: up to the last position its last row sees.
-template <int ROWS>
-__device__ __forceinline__ int tile_seen(const AttnParams& p, const Seq& q, int qt) {
-  const int64_t rows = min((int64_t)q.n * p.G, (int64_t)ROWS * (qt + 1));
-  return q.len - q.n + (int)((rows - 1) / p.G) + 1;
-}
-template <int ROWS>
-__device__ __forceinline__ int tile_units(const AttnParams& p, const Seq& q, int qt) {
-  return (tile_seen<ROWS>(p, q, qt) + UNIT - 1) / UNIT;
-}
-template <int ROWS>
-__device__ __forceinline__ int64_t seq_units(const AttnParams& p, const Seq& q) {
-  int64_t w = 0;
-  for (int qt = 0, m = q_tiles<ROWS>(p, q); qt < m; ++qt) w += tile_units<ROWS>(p, q, qt);
-  return w * p.c.hkv;
 }
 
 // The work is the list of all (sequence, query tile, key/value head) items,
@@ -165,73 +111,21 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
   unsigned char* ring = smem + (threadIdx.x >> 5) * STAGES * STAGE;
   float(*osum)[ROWS][D + 4] = reinterpret_cast<float(*)[ROWS][D + 4]>(smem);  // after an item's steps
   __shared__ float sm[AT_WARPS][ROWS], sM[AT_WARPS][ROWS], sl[AT_WARPS][ROWS];
-  __shared__ int64_t scan[AT_WARPS];
-  __shared__ int64_t found_at;
-  __shared__ int found_s;
+  __shared__ int64_t scan[AT_WARPS + 2];
   __shared__ uint32_t arrived;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, j = lane & 3;
   const int hkv = p.c.hkv;
 
-  // total steps, then the sequence that holds this CTA's first step
-  int64_t total = 0, w0 = 0;
-  for (int s = tid; s < p.c.n_seq; s += AT_THREADS) {
-    const Seq q = load_seq(p, s);
-    if (!q.ok && blockIdx.x == 0) raise_flag(p.st, FLAG_BAD_CACHE);
-    const int64_t w = seq_units<ROWS>(p, q);
-    if (s == tid) w0 = w;
-    total += w;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-  if (lane == 0) scan[warp] = total;
-  __syncthreads();
-  total = scan[0] + scan[1] + scan[2] + scan[3];
-  const int64_t ctas = min((int64_t)gridDim.x, total);
+  Work wk;
+  if (!find_work<ROWS, AT_THREADS>(p, scan, wk)) return;
+  const int64_t total = wk.total, ctas = wk.ctas, x1 = wk.x1;
   const int cta = blockIdx.x;
-  if (cta >= ctas) return;
-  const int64_t x0 = total * cta / ctas, x1 = total * (cta + 1) / ctas;
-  int64_t base = 0;
-  for (int sb = 0; sb < p.c.n_seq; sb += AT_THREADS) {
-    int64_t w = w0;
-    if (sb) w = sb + tid < p.c.n_seq ? seq_units<ROWS>(p, load_seq(p, sb + tid)) : 0;
-    int64_t incl = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(~0u, incl, o);
-      if (lane >= o) incl += u;
-    }
-    __syncthreads();
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    for (int i = 0; i < warp; ++i) incl += scan[i];
-    const int64_t all = scan[0] + scan[1] + scan[2] + scan[3];
-    if (x0 < base + all) {
-      if (base + incl - w <= x0 && x0 < base + incl) {
-        found_s = sb + tid;
-        found_at = base + incl - w;
-      }
-      break;
-    }
-    base += all;
-  }
-  __syncthreads();
-  int s = found_s;
+  int s = wk.s, qt = wk.qt, h = wk.h, u0 = wk.u;
   Seq q = load_seq(p, s);
-  int qt = 0, h = 0, u0 = 0;
-  int64_t off = x0 - found_at;
-  for (;; ++qt) {
-    const int units = tile_units<ROWS>(p, q, qt);
-    if (off < (int64_t)units * hkv) {
-      h = (int)(off / units);
-      u0 = (int)(off % units);
-      break;
-    }
-    off -= (int64_t)units * hkv;
-  }
 
-  int64_t x = x0;
+  int64_t x = wk.x0;
   while (x < x1) {
     const int units = tile_units<ROWS>(p, q, qt), seen = tile_seen<ROWS>(p, q, qt);
     const int u1 = (int)min((int64_t)units, u0 + (x1 - x));
@@ -595,6 +489,8 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
   }
 }
 
+constexpr int TILE_ROWS = 32;  // more rows a sequence, on average: the tile kernel
+
 template <int D, int NT>
 cudaError_t launch_stream(const AttnParams& p, cudaStream_t s) {
   auto* kern = kv_attention_kernel<D, NT>;
@@ -624,6 +520,7 @@ cudaError_t launch_kv_attention(const uint16_t* q, int64_t q_stride, const int32
   p.st = reinterpret_cast<DeviceStatus*>(ws);
   p.counters = reinterpret_cast<uint32_t*>(ws + kv_counter_off());
   p.partials = reinterpret_cast<float*>(ws + kv_partial_off());
+  if ((int64_t)t * p.G > (int64_t)TILE_ROWS * c.n_seq) return launch_tile(p, s);
   // Eight rows a tile where they hold a token's group of heads and no
   // sequence has more than one token on average, else sixteen.
   const bool small = p.G <= 8 && t <= c.n_seq;

@@ -1,0 +1,635 @@
+// Causal attention over the paged 8-bit cache on the tensor cores' own path
+// (tcgen05, accumulators in TMEM): sequences with many new rows.
+#include <limits.h>
+#include <math.h>
+
+#include "kv_attention.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace tc;
+
+constexpr int T_ROWS = 256;  // query rows of an item: two tiles of 128
+constexpr int T_WARPS = 13;  // 0-3 softmax of tile 0, 4-7 of tile 1, 8-11 conversion, 12 products
+constexpr int T_THREADS = T_WARPS * 32;
+constexpr int W_CVT = 8, W_MMA = 12;
+constexpr int SC_RING = 4;   // tiles whose scales are kept
+constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr float GROWTH = 8.f;  // how far (log2) a row's weights may outgrow 1 before its sums are rescaled
+
+struct TileShared {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], q_full[2], o_full[2];
+  uint64_t sc_full[SC_RING], drain;
+  float sc_k[SC_RING][8], sc_log[SC_RING][8], sc_inv[SC_RING][8], sc_ref[SC_RING];
+  float red[4];
+  uint32_t arrived[2];
+  uint32_t tmem;
+  int abort;
+  int64_t scratch[T_WARPS + 2];
+};
+
+template <int D>
+struct Smem {
+  static constexpr int Q = 128 * D * 2, K = UNIT * D * 2, V = D * UNIT * 2;
+  static constexpr int TOTAL = 2 * Q + 2 * K + 2 * V + 1024 + (int)sizeof(TileShared);
+};
+template <int D>
+constexpr size_t partial_floats() { return (size_t)128 * (D + 2); }  // accumulators, maximum, sum of a tile's rows
+
+// One CTA's part of an item: units u0 .. u1 - 1 of its `units`.
+struct Piece {
+  Seq q;
+  int s, qt, h, u0, u1, units;
+  int64_t item;  // the item's first unit
+  int n[2];      // units that the rows of either tile see
+};
+
+// The pieces of a CTA in order; every warp walks them by itself.
+struct Walk {
+  const AttnParams& p;
+  Work w;
+  int64_t x;
+  int s, qt, h, u;
+  Seq q;
+  __device__ Walk(const AttnParams& p_, const Work& w_) : p(p_), w(w_), x(w_.x0), s(w_.s), qt(w_.qt), h(w_.h), u(w_.u) {
+    q = load_seq(p, s);
+  }
+  __device__ bool next(Piece& P) {
+    if (x >= w.x1) return false;
+    const int64_t rows = (int64_t)q.n * p.G;
+    P.q = q;
+    P.s = s, P.qt = qt, P.h = h;
+    P.units = tile_units<T_ROWS>(p, q, qt);
+    P.u0 = u;
+    P.u1 = (int)min((int64_t)P.units, u + (w.x1 - x));
+    P.item = x - u;
+    P.n[0] = tile_units<128>(p, q, 2 * qt);
+    P.n[1] = rows > (int64_t)T_ROWS * qt + 128 ? P.units : 0;
+    x += P.u1 - u;
+    u = 0;
+    if (x < w.x1 && ++h == p.c.hkv) {
+      h = 0;
+      if (++qt == q_tiles<T_ROWS>(p, q)) {
+        qt = 0;
+        do q = load_seq(p, ++s);
+        while (q.n == 0);  // x < x1 <= total: a later sequence has rows
+      }
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Ties the registers of a load to this point, after tmem_ld_wait.
+__device__ __forceinline__ void ld32_fence(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                      "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+// Instruction descriptor, kind::f16: D fp32, A and B fp16, both K-major.
+constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t minus_1152(uint32_t v) {
+  return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&v), __floats2half2_rn(1152.f, 1152.f)));
+}
+// Bytes 0 and 2, bytes 1 and 3 of a word of codes; byte B of two words: exact fp16 numbers.
+__device__ __forceinline__ uint32_t f16_even(uint32_t w) { return minus_1152((w & 0x00FF00FFu) ^ 0x64806480u); }
+__device__ __forceinline__ uint32_t f16_odd(uint32_t w) { return minus_1152(((w >> 8) & 0x00FF00FFu) ^ 0x64806480u); }
+template <int B>
+__device__ __forceinline__ uint32_t f16_pair(uint32_t a, uint32_t b) {
+  return minus_1152((__byte_perm(a, b, B | (4 + B) << 8) & 0x00FF00FFu) ^ 0x64806480u);
+}
+
+__device__ __forceinline__ void named_barrier(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// The work is cut as in the streaming kernel, over items of 256 query rows
+// (a position's heads next to each other) and units of 128 tokens.
+//
+// Per unit the four conversion warps bring the keys and values, one unit
+// ahead in registers, and store them as exact fp16 codes in the swizzled
+// operand layout, the values transposed; one thread issues S = Q K^T and
+// O += P V for two tiles of 128 rows, so that while one tile's weights are
+// being taken the tensor cores work for the other.  A softmax thread owns a
+// row: S comes from TMEM and P goes back over it as fp16, the second
+// product's A operand, while O stays in TMEM for all units.  O and the sums
+// are rescaled only when a row's maximum grew by more than 2^8.
+//
+// Scales: the key scale of a run of 16 tokens multiplies the fp32 scores.  The
+// value scale vs, relative to the item's largest, enters the weights through
+// its logarithm: P = 2^(s + log2 vs - M), at most 2^8 whatever the scales
+// are, and the softmax's sum takes each run's sum of P back by 1 / vs.
+template <int D>
+__global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+  unsigned char* sq = smem;
+  unsigned char* sk = sq + 2 * Smem<D>::Q;
+  unsigned char* sv = sk + 2 * Smem<D>::K;
+  TileShared& S = *reinterpret_cast<TileShared*>(sv + 2 * Smem<D>::V);
+  constexpr uint32_t S_COL = 0, O_COL = 256;  // tile x: S at 128 x, O at 256 + D x
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hkv = p.c.hkv;
+  Work wk;
+  if (!find_work<T_ROWS, T_THREADS>(p, S.scratch, wk)) return;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.k_full[i], 128);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_full[i], 128);
+      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 128);
+      mbar_init(&S.q_full[i], 128);
+      mbar_init(&S.o_full[i], 1);
+    }
+    for (int i = 0; i < SC_RING; ++i) mbar_init(&S.sc_full[i], 8);
+    mbar_init(&S.drain, 1);
+    S.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) tmem_alloc(&S.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+
+  volatile int* abort = &S.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (mbar_wait(bar, parity, abort, WAIT_NS)) return true;
+    if (!*abort) {
+      if (atomicOr(&p.st->flags, FLAG_TIMEOUT) == 0) p.st->timeout_site = site;
+      *abort = 1;
+    }
+    return false;
+  };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+    return __all_sync(~0u, wait(bar, parity, site)) != 0;
+  };
+
+  Walk walk(p, wk);
+  Piece P;
+  if (warp < W_CVT) {
+    // ------------------------------------------------------------- softmax
+    const int X = warp >> 2, r = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the lanes
+    const uint32_t s_addr = lanes + S_COL + 128 * X, o_addr = lanes + O_COL + D * X;
+    unsigned char* q_tile = sq + X * Smem<D>::Q;
+    uint32_t units_done = 0, tiles = 0, pieces = 0;  // of the CTA; of this tile
+    bool ok = true;
+    while (ok && walk.next(P)) {
+      const int last = min(P.u1, P.n[X]);
+      if (P.u0 >= last) {
+        units_done += P.u1 - P.u0;
+        continue;
+      }
+      const int64_t rr = (int64_t)T_ROWS * P.qt + 128 * X + r, rows = (int64_t)P.q.n * p.G;
+      const bool live_row = rr < rows;
+      const int qi = live_row ? (int)(rr / p.G) : 0, head = live_row ? P.h * p.G + (int)(rr % p.G) : 0;
+      const int before = P.q.len - P.q.n;
+      // rows past the last store nothing, so they may see all
+      const int limit = live_row ? before + qi : INT_MAX;
+      const int first_limit = before + (int)(((int64_t)T_ROWS * P.qt + 128 * X) / p.G);
+      // ---- the query row, scaled by a power of two into fp16
+      float f;
+      {
+        const uint16_t* src = p.q + (int64_t)(P.q.row + qi) * p.q_stride + (size_t)head * D;
+        uint4 v[D / 8];
+        float m = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          v[c] = live_row ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
+        }
+        const int ex = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
+        // a negative scale goes into the row, so that f is not
+        const float up = copysignf(__uint_as_float((uint32_t)(127 + 8 - ex) << 23), p.scale_log2);
+        f = __uint_as_float((uint32_t)(max(127 - 8 + ex, 1)) << 23) * fabsf(p.scale_log2);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          auto two = [&](uint32_t a, uint32_t b, bool hi) {
+            return half2_bits(__floats2half2_rn((hi ? bf16hi(a) : bf16lo(a)) * up, (hi ? bf16hi(b) : bf16lo(b)) * up));
+          };
+          // channels in the keys' order: 0 2 1 3 of every four
+          *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (128 * 128) + sw128_off(r, c & 7)) =
+              make_uint4(two(v[c].x, v[c].y, false), two(v[c].x, v[c].y, true), two(v[c].z, v[c].w, false),
+                         two(v[c].z, v[c].w, true));
+        }
+        fence_async_smem();
+        mbar_arrive(&S.q_full[X]);
+      }
+      float M = -INFINITY, l = 0.f, ref = 1.f;
+      for (int u = P.u0; u < last; ++u) {
+        const uint32_t slot = (units_done + u - P.u0) % SC_RING, turn = (units_done + u - P.u0) / SC_RING;
+        // the scales' barrier second: scores imply that its phase is this
+        // unit's, not one of an earlier turn
+        if (!(ok = wait_warp(&S.s_full[X], tiles & 1, 51))) break;
+        if (!(ok = wait_warp(&S.sc_full[slot], turn & 1, 52))) break;
+        ++tiles;
+        tc_fence_after();
+        const bool masked = u * UNIT + UNIT - 1 > first_limit;
+        const int see = limit - u * UNIT;  // the last token of the unit that this row sees
+        ref = S.sc_ref[slot];
+        // ---- the row's maximum of score + log2 vs
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(s_addr + 32 * c, v);
+          tmem_ld_wait();
+          ld32_fence(v);
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 16 * h2; i < 16 * h2 + 16; ++i) {
+              float z = __uint_as_float(v[i]);
+              if (masked) z = 32 * c + i <= see ? z : -INFINITY;
+              mx = fmaxf(mx, z);
+            }
+            const float a = f * S.sc_k[slot][2 * c + h2];
+            // nothing seen: -inf, also where a = 0
+            top = fmaxf(top, mx == -INFINITY ? mx : fmaf(mx, a, S.sc_log[slot][2 * c + h2]));
+          }
+        }
+        const bool grows = top > M + GROWTH || (M == -INFINITY && top > M);
+        if (__any_sync(~0u, grows)) {
+          const float to = fmaxf(M, top);
+          const float drop = M == -INFINITY ? 1.f : ex2(M - to);  // nothing summed yet: nothing to scale
+          l *= drop;
+          if (u > P.u0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(o_addr + 32 * c, v);
+              tmem_ld_wait();
+              ld32_fence(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * drop);
+              tmem_st<32>(o_addr + 32 * c, v);
+            }
+          }
+          M = to;
+        }
+        const float at = M == -INFINITY ? 0.f : M;
+        // ---- the weights
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32], w[16];
+          tmem_ld32(s_addr + 32 * c, v);
+          tmem_ld_wait();
+          ld32_fence(v);
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2) {
+            const float a = f * S.sc_k[slot][2 * c + h2], b = S.sc_log[slot][2 * c + h2] - at;
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
+              float z0 = fmaf(__uint_as_float(v[i]), a, b), z1 = fmaf(__uint_as_float(v[i + 1]), a, b);
+              if (masked) {
+                z0 = 32 * c + i <= see ? z0 : -INFINITY;
+                z1 = 32 * c + i + 1 <= see ? z1 : -INFINITY;
+              }
+              z0 = ex2(z0);
+              z1 = ex2(z1);
+              sum0 += z0;
+              sum1 += z1;
+              w[i >> 1] = half2_bits(__floats2half2_rn(z0, z1));
+            }
+            l = fmaf(sum0 + sum1, S.sc_inv[slot][2 * c + h2], l);
+          }
+          tmem_st<16>(s_addr + 16 * c, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&S.p_full[X]);
+      }
+      if (!ok) break;
+      units_done += P.u1 - P.u0;
+      // ---- the piece's sums
+      if (!(ok = wait_warp(&S.o_full[X], pieces & 1, 53))) break;
+      ++pieces;
+      tc_fence_after();
+      const int c0 = cta_of(wk, P.item), c1 = cta_of(wk, P.item + P.n[X] - 1);
+      const int cta = blockIdx.x;
+      uint16_t* dst = p.out + ((size_t)(P.q.row + qi) * p.hq + head) * D;
+      if (c0 == c1) {
+        const float k = l == 0.f ? 0.f : ref / l;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(o_addr + 32 * c, v);
+          tmem_ld_wait();
+          ld32_fence(v);
+          if (live_row)
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(v[i + 2 * e]) * k, __uint_as_float(v[i + 2 * e + 1]) * k);
+              *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        tc_fence_before();
+      } else {
+        // a tile that spans CTAs: the last one to finish joins the parts in order
+        auto part = [&](int c) { return p.partials + (size_t)((2 * c + (c == c0)) * 2 + X) * partial_floats<D>(); };
+        float* mine = part(cta);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(o_addr + 32 * c, v);
+          tmem_ld_wait();
+          ld32_fence(v);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4*>(mine + ((8 * c + i / 4) * 128 + r) * 4) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+        tc_fence_before();
+        mine[128 * D + r] = M;
+        mine[128 * D + 128 + r] = l;
+        __threadfence();
+        named_barrier(2 + X);
+        if (r == 0) S.arrived[X] = atomicAdd(p.counters + 2 * c0 + X, 1u);
+        named_barrier(2 + X);
+        if (S.arrived[X] == (uint32_t)(c1 - c0)) {
+          __threadfence();
+          if (r == 0) p.counters[2 * c0 + X] = 0;
+          float top = -INFINITY, sum = 0.f;
+          for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(part(c) + 128 * D + r));
+          if (top == -INFINITY) top = 0.f;
+          for (int c = c0; c <= c1; ++c) sum += __ldcg(part(c) + 128 * D + 128 + r) * ex2(__ldcg(part(c) + 128 * D + r) - top);
+          const float k = sum == 0.f ? 0.f : ref / sum;
+          for (int d = 0; d < D; d += 8) {
+            float acc[8] = {};
+            for (int c = c0; c <= c1; ++c) {
+              const float drop = ex2(__ldcg(part(c) + 128 * D + r) - top) * k;
+              const float4 a = __ldcg(reinterpret_cast<const float4*>(part(c) + ((d / 4) * 128 + r) * 4));
+              const float4 b = __ldcg(reinterpret_cast<const float4*>(part(c) + ((d / 4 + 1) * 128 + r) * 4));
+              acc[0] = fmaf(a.x, drop, acc[0]), acc[1] = fmaf(a.y, drop, acc[1]);
+              acc[2] = fmaf(a.z, drop, acc[2]), acc[3] = fmaf(a.w, drop, acc[3]);
+              acc[4] = fmaf(b.x, drop, acc[4]), acc[5] = fmaf(b.y, drop, acc[5]);
+              acc[6] = fmaf(b.z, drop, acc[6]), acc[7] = fmaf(b.w, drop, acc[7]);
+            }
+            if (live_row)
+              *reinterpret_cast<uint4*>(dst + d) = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                                              pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+          }
+        }
+      }
+    }
+  } else if (warp < W_MMA) {
+    // ---------------------------------------------------------- conversion
+    const int w = warp - W_CVT, ct = tid - 32 * W_CVT;
+    constexpr int NK = D / 16;  // 16-byte pieces of keys a thread converts
+    // keys: tokens 32 w + 8 (i & 3) + lane % 8, piece lane / 8 + 4 (i >> 2);
+    // values: tokens 8 vo .. 8 vo + 7, piece vc
+    const int vo = D == 128 ? (lane & 7) + 8 * (w >> 1) : (lane & 7) + 8 * (w & 1);
+    const int vc = D == 128 ? (lane >> 3) + 4 * (w & 1) : lane >> 3;
+    const bool has_v = D == 128 || w < 2;
+    const int64_t page_bytes = (int64_t)hkv * p.c.block * D, vstep = p.c.n_pages * page_bytes;
+    struct Tile {
+      int s, h, u, seen;
+      bool first, any;
+    };
+    Piece cur;
+    cur.u0 = cur.u1 = 0;
+    int cu = 0;
+    auto next_tile = [&](Tile& t) {
+      t.any = true;
+      t.first = false;
+      if (cu >= cur.u1) {
+        if (!walk.next(cur)) {
+          t.any = false;
+          return;
+        }
+        cu = cur.u0;
+        t.first = true;
+      }
+      t.s = cur.s, t.h = cur.h, t.u = cu++;
+      t.seen = tile_seen<T_ROWS>(p, cur.q, cur.qt);
+    };
+    auto page_id = [&](const Tile& t, int pos) {
+      if (!t.any || pos >= t.seen) return -1;
+      const int page = __ldg(p.c.table + (size_t)t.s * p.c.max_blocks + (pos >> p.block_log2));
+      if (page >= 0 && page < p.c.n_pages) return page;
+      raise_flag(p.st, FLAG_BAD_CACHE);
+      return -1;
+    };
+    // run lane % 8 of a unit
+    auto pages_of = [&](const Tile& t) { return page_id(t, t.u * UNIT + 16 * (lane & 7)); };
+    uint4 kr[NK], vr[8];
+    auto load_k = [&](const Tile& t, int pages) {
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        const int tok = 32 * w + 8 * (i & 3) + (lane & 7), c = (lane >> 3) + 4 * (i >> 2);
+        const int page = __shfl_sync(~0u, pages, 2 * w + ((i & 3) >> 1));
+        kr[i] = make_uint4(0, 0, 0, 0);
+        if (page >= 0)
+          kr[i] = __ldg(reinterpret_cast<const uint4*>(p.c.codes + page * page_bytes +
+                                                       ((int64_t)t.h * p.c.block + ((t.u * UNIT + tok) & (p.c.block - 1))) * D +
+                                                       16 * c));
+      }
+    };
+    auto load_v = [&](const Tile& t, int pages) {
+      const int page = __shfl_sync(~0u, pages, vo >> 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        vr[i] = make_uint4(0, 0, 0, 0);
+        if (page >= 0 && has_v)
+          vr[i] = __ldg(reinterpret_cast<const uint4*>(
+              p.c.codes + vstep + page * page_bytes +
+              ((int64_t)t.h * p.c.block + ((t.u * UNIT + 8 * vo + i) & (p.c.block - 1))) * D + 16 * vc));
+      }
+    };
+    Tile t, n;
+    next_tile(t);
+    int pages = pages_of(t);
+    load_k(t, pages);
+    load_v(t, pages);
+    next_tile(n);
+    int next_pages = pages_of(n);
+    float vref = 1.f;
+    bool ok = true;
+    for (uint32_t it = 0; t.any; ++it) {
+      const uint32_t st = it & 1, par = ((it >> 1) & 1) ^ 1;
+      if (t.first) {  // the largest value scale of the item
+        float m = 0.f;
+        for (int b = ct; b * p.c.block < t.seen; b += 128) {
+          const int page = page_id(t, b * p.c.block);
+          if (page >= 0) m = fmaxf(m, __ldg(p.c.scales + ((size_t)p.c.n_pages + page) * hkv + t.h));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        named_barrier(1);  // the last item's values are read
+        if (lane == 0) S.red[w] = m;
+        named_barrier(1);
+        m = fmaxf(fmaxf(S.red[0], S.red[1]), fmaxf(S.red[2], S.red[3]));
+        vref = m;  // 0: every value is 0, and so is the result
+      }
+      // the slot's last unit, SC_RING back, is past every softmax thread: the
+      // products that freed this K stage came after its weights
+      float ks = 0.f, lg = -INFINITY, inv = 0.f;
+      if (w == 0 && lane < 8 && pages >= 0) {
+        ks = __ldg(p.c.scales + (size_t)pages * hkv + t.h);
+        lg = fmaxf(log2f(__ldg(p.c.scales + ((size_t)p.c.n_pages + pages) * hkv + t.h) / (vref > 0.f ? vref : 1.f)), -60.f);
+        inv = exp2f(-lg);
+      }
+      if (!(ok = wait_warp(&S.k_empty[st], par, 54))) break;
+      if (w == 0 && lane < 8) {
+        const uint32_t slot = it % SC_RING;
+        S.sc_k[slot][lane] = ks;
+        S.sc_log[slot][lane] = lg;
+        S.sc_inv[slot][lane] = inv;
+        if (lane == 0) S.sc_ref[slot] = vref;
+        __syncwarp(0xFF);
+        mbar_arrive(&S.sc_full[slot]);
+      }
+      {
+        unsigned char* dst = sk + st * Smem<D>::K;
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+          const int tok = 32 * w + 8 * (i & 3) + (lane & 7), c = (lane >> 3) + 4 * (i >> 2);
+          unsigned char* panel = dst + (c >> 2) * (128 * 128);
+          *reinterpret_cast<uint4*>(panel + sw128_off(tok, 2 * c & 7)) =
+              make_uint4(f16_even(kr[i].x), f16_odd(kr[i].x), f16_even(kr[i].y), f16_odd(kr[i].y));
+          *reinterpret_cast<uint4*>(panel + sw128_off(tok, (2 * c & 7) + 1)) =
+              make_uint4(f16_even(kr[i].z), f16_odd(kr[i].z), f16_even(kr[i].w), f16_odd(kr[i].w));
+        }
+        fence_async_smem();
+        mbar_arrive(&S.k_full[st]);
+      }
+      if (n.any) load_k(n, next_pages);
+      if (!(ok = wait_warp(&S.v_empty[st], par, 55))) break;
+      {
+        unsigned char* dst = sv + st * Smem<D>::V + (vo >> 3) * (D * 128);
+        if (has_v) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = q == 0 ? vr[i].x : q == 1 ? vr[i].y : q == 2 ? vr[i].z : vr[i].w;
+            auto put = [&](int ch, uint4 v) {
+              *reinterpret_cast<uint4*>(dst + sw128_off(16 * vc + 4 * q + ch, vo & 7)) = v;
+            };
+            put(0, make_uint4(f16_pair<0>(x[0], x[1]), f16_pair<0>(x[2], x[3]), f16_pair<0>(x[4], x[5]), f16_pair<0>(x[6], x[7])));
+            put(1, make_uint4(f16_pair<1>(x[0], x[1]), f16_pair<1>(x[2], x[3]), f16_pair<1>(x[4], x[5]), f16_pair<1>(x[6], x[7])));
+            put(2, make_uint4(f16_pair<2>(x[0], x[1]), f16_pair<2>(x[2], x[3]), f16_pair<2>(x[4], x[5]), f16_pair<2>(x[6], x[7])));
+            put(3, make_uint4(f16_pair<3>(x[0], x[1]), f16_pair<3>(x[2], x[3]), f16_pair<3>(x[4], x[5]), f16_pair<3>(x[6], x[7])));
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(&S.v_full[st]);
+      }
+      if (n.any) load_v(n, next_pages);
+      t = n;
+      pages = next_pages;
+      next_tile(n);
+      next_pages = pages_of(n);
+    }
+  } else if (elect_one()) {
+    // ------------------------------------------------------------ products
+    constexpr uint32_t ID_S = idesc_f16(128, UNIT), ID_O = idesc_f16(128, D);
+    uint32_t it = 0, q_turn[2] = {0, 0}, p_turn[2] = {0, 0};
+    bool ok = true;
+    auto scores = [&](int X, uint32_t unit) {
+      const uint32_t q0 = smem_u32(sq + X * Smem<D>::Q), k0 = smem_u32(sk + (unit & 1) * Smem<D>::K);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
+        mma_bf16(tmem + S_COL + 128 * X, desc_sw128(q0 + off), desc_sw128(k0 + off), ID_S, k > 0);
+      }
+      mma_commit(&S.s_full[X]);
+    };
+    auto outputs = [&](int X, uint32_t unit, bool first) {
+      const uint32_t v0 = smem_u32(sv + (unit & 1) * Smem<D>::V);
+#pragma unroll
+      for (int k = 0; k < UNIT / 16; ++k)
+        mma_bf16_ta(tmem + O_COL + D * X, tmem + S_COL + 128 * X + 8 * k, desc_sw128(v0 + (k >> 2) * (D * 128) + (k & 3) * 32),
+                    ID_O, !first || k > 0);
+    };
+    while (ok && walk.next(P)) {
+      const int last[2] = {min(P.u1, P.n[0]), min(P.u1, P.n[1])};
+      // unit `it` is this piece's first
+      for (int X = 0; X < 2; ++X)
+        if (ok && P.u0 < last[X]) ok = wait(&S.q_full[X], q_turn[X]++ & 1, 56);
+      if (!ok || !(ok = wait(&S.k_full[it & 1], (it >> 1) & 1, 57))) break;
+      tc_fence_after();
+      for (int X = 0; X < 2; ++X)
+        if (P.u0 < last[X]) scores(X, it);
+      mma_commit(&S.k_empty[it & 1]);
+      for (int u = P.u0; u < P.u1 && ok; ++u, ++it) {
+        if (!(ok = wait(&S.v_full[it & 1], (it >> 1) & 1, 58))) break;
+        const bool more = u + 1 < P.u1;
+        bool have_k = false;
+        for (int X = 0; X < 2 && ok; ++X) {
+          if (u < last[X]) {
+            if (!(ok = wait(&S.p_full[X], p_turn[X]++ & 1, 59))) break;
+            tc_fence_after();
+            outputs(X, it, u == P.u0);
+            if (u + 1 == last[X]) mma_commit(&S.o_full[X]);
+          }
+          if (X == 1) mma_commit(&S.v_empty[it & 1]);
+          if (more && !have_k) {
+            if (!(ok = wait(&S.k_full[(it + 1) & 1], ((it + 1) >> 1) & 1, 57))) break;
+            tc_fence_after();
+            have_k = true;
+          }
+          if (u + 1 < last[X]) scores(X, it + 1);
+        }
+        if (ok && more) mma_commit(&S.k_empty[(it + 1) & 1]);
+      }
+    }
+    // after a wait that gave up: the products in flight end before TMEM goes
+    if (!ok) {
+      int never = 0;
+      mma_commit(&S.drain);
+      mbar_wait(&S.drain, 0, &never, WAIT_NS);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == W_MMA) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const AttnParams& p, cudaStream_t s) {
+  auto* kern = kv_attention_tile_kernel<D>;
+  cudaError_t e = set_smem_limit_once(kern, Smem<D>::TOTAL);
+  if (e != cudaSuccess) return e;
+  MOE_LAUNCH("kv_attention_tile", s,
+             { e = launch_k(kern, dim3(sm_count()), dim3(T_THREADS), (size_t)Smem<D>::TOTAL, s, p); });
+  return e;
+}
+
+}  // namespace
+
+size_t kv_tile_partial_bytes(int d) {
+  return (size_t)sm_count() * 4 * (d == 64 ? partial_floats<64>() : partial_floats<128>()) * 4;
+}
+
+cudaError_t launch_tile(const AttnParams& p, cudaStream_t s) { return p.c.d == 64 ? launch<64>(p, s) : launch<128>(p, s); }
+
+}  // namespace moe

@@ -15,8 +15,10 @@ inline size_t kv_partial_off() { return align_up(kv_counter_off() + (size_t)kv_g
 // A partial result: for each row its score maximum, its maximum of score +
 // log2(value scale), its sum and d accumulators.
 __host__ __device__ constexpr size_t kv_partial_floats(int d) { return (size_t)KV_ROWS * (d + 4); }
+size_t kv_tile_partial_bytes(int d);  // kv_attention_tile.cu
 inline size_t kv_ws_bytes(int d) {
-  return kv_partial_off() + (size_t)kv_grid_max() * 2 * kv_partial_floats(d) * 4;
+  const size_t stream = (size_t)kv_grid_max() * 2 * kv_partial_floats(d) * 4, tile = kv_tile_partial_bytes(d);
+  return kv_partial_off() + (stream > tile ? stream : tile);
 }
 
 // One sequence's part of a call, checked: n new rows from `row`, `len` tokens
