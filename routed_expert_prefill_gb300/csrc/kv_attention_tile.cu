@@ -13,17 +13,17 @@ namespace {
 using namespace tc;
 
 constexpr int T_ROWS = 256;  // query rows of an item: two tiles of 128
-constexpr int T_WARPS = 13;  // 0-3 softmax of tile 0, 4-7 of tile 1, 8-11 conversion, 12 products
+constexpr int T_WARPS = 12;  // 0-3 softmax and products of tile 0, 4-7 of tile 1, 8-11 conversion
 constexpr int T_THREADS = T_WARPS * 32;
-constexpr int W_CVT = 8, W_MMA = 12;
+constexpr int W_CVT = 8;
 constexpr int SC_RING = 4;   // tiles whose scales are kept
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float GROWTH = 8.f;  // how far (log2) a row's weights may outgrow 1 before its sums are rescaled
 
 struct TileShared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], q_full[2], o_full[2];
-  uint64_t sc_full[SC_RING], drain;
+  uint64_t s_full[2], o_full[2], drain[2];
+  uint64_t sc_full[SC_RING];
   float sc_k[SC_RING][8], sc_log[SC_RING][8], sc_inv[SC_RING][8], sc_ref[SC_RING];
   float red[4];
   uint32_t arrived[2];
@@ -117,6 +117,23 @@ __device__ __forceinline__ uint32_t f16_pair(uint32_t a, uint32_t b) {
   return minus_1152((__byte_perm(a, b, B | (4 + B) << 8) & 0x00FF00FFu) ^ 0x64806480u);
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, z, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 r, x, y, z;\nmov.b64 {%0, %1}, r;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 r, x, y;\nmov.b64 {%0, %1}, r;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 __device__ __forceinline__ void named_barrier(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // The work is cut as in the streaming kernel, over items of 256 query rows
@@ -124,12 +141,13 @@ __device__ __forceinline__ void named_barrier(int id) { asm volatile("bar.sync %
 //
 // Per unit the four conversion warps bring the keys and values, one unit
 // ahead in registers, and store them as exact fp16 codes in the swizzled
-// operand layout, the values transposed; one thread issues S = Q K^T and
-// O += P V for two tiles of 128 rows, so that while one tile's weights are
-// being taken the tensor cores work for the other.  A softmax thread owns a
-// row: S comes from TMEM and P goes back over it as fp16, the second
-// product's A operand, while O stays in TMEM for all units.  O and the sums
-// are rescaled only when a row's maximum grew by more than 2^8.
+// operand layout, the values transposed.  Two groups of four warps own a tile
+// of 128 rows each: one thread issues S = Q K^T and O += P V, and while one
+// tile's weights are being taken the tensor cores work for the other.  A
+// thread owns a row: S comes from TMEM and P goes back over it as fp16, the
+// second product's A operand, while O stays in TMEM for all units.  Weights
+// are taken against the maximum so far, in one pass over S; only if one would
+// outgrow 2^8 are O and the sums rescaled and the pass repeated.
 //
 // Scales: the key scale of a run of 16 tokens multiplies the fp32 scores.  The
 // value scale vs, relative to the item's largest, enters the weights through
@@ -153,20 +171,18 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.k_full[i], 128);
-      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.k_empty[i], 2);  // released for either tile
       mbar_init(&S.v_full[i], 128);
-      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.v_empty[i], 2);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i], 128);
-      mbar_init(&S.q_full[i], 128);
       mbar_init(&S.o_full[i], 1);
+      mbar_init(&S.drain[i], 1);
     }
     for (int i = 0; i < SC_RING; ++i) mbar_init(&S.sc_full[i], 8);
-    mbar_init(&S.drain, 1);
     S.abort = 0;
     fence_mbar_init();
   }
-  if (warp == W_MMA) tmem_alloc(&S.tmem, 512);
+  if (warp == W_CVT) tmem_alloc(&S.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -188,16 +204,47 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
   Walk walk(p, wk);
   Piece P;
   if (warp < W_CVT) {
-    // ------------------------------------------------------------- softmax
+    // ------------------------------------------------- softmax and products
     const int X = warp >> 2, r = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the lanes
     const uint32_t s_addr = lanes + S_COL + 128 * X, o_addr = lanes + O_COL + D * X;
     unsigned char* q_tile = sq + X * Smem<D>::Q;
     uint32_t units_done = 0, tiles = 0, pieces = 0;  // of the CTA; of this tile
     bool ok = true;
+    constexpr uint32_t ID_S = idesc_f16(128, UNIT), ID_O = idesc_f16(128, D);
+    // S of unit `it`, by one thread
+    auto issue_scores = [&](uint32_t it) {
+      if (!wait(&S.k_full[it & 1], (it >> 1) & 1, 57)) return;
+      tc_fence_after();
+      const uint32_t q0 = smem_u32(q_tile), k0 = smem_u32(sk + (it & 1) * Smem<D>::K);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
+        mma_bf16(tmem + S_COL + 128 * X, desc_sw128(q0 + off), desc_sw128(k0 + off), ID_S, k > 0);
+      }
+      mma_commit(&S.s_full[X]);
+      mma_commit(&S.k_empty[it & 1]);
+    };
+    auto issue_outputs = [&](uint32_t it, bool first) {
+      if (!wait(&S.v_full[it & 1], (it >> 1) & 1, 58)) return;
+      tc_fence_after();
+      const uint32_t v0 = smem_u32(sv + (it & 1) * Smem<D>::V);
+#pragma unroll
+      for (int k = 0; k < UNIT / 16; ++k)
+        mma_bf16_ta(tmem + O_COL + D * X, tmem + S_COL + 128 * X + 8 * k, desc_sw128(v0 + (k >> 2) * (D * 128) + (k & 3) * 32),
+                    ID_O, !first || k > 0);
+      mma_commit(&S.v_empty[it & 1]);
+    };
+    // units that this tile's rows do not see are given back as they come
+    auto release = [&](uint32_t it) {
+      if (wait(&S.k_full[it & 1], (it >> 1) & 1, 59)) mbar_arrive(&S.k_empty[it & 1]);
+      if (wait(&S.v_full[it & 1], (it >> 1) & 1, 60)) mbar_arrive(&S.v_empty[it & 1]);
+    };
     while (ok && walk.next(P)) {
       const int last = min(P.u1, P.n[X]);
       if (P.u0 >= last) {
+        if (r == 0)
+          for (int u = P.u0; u < P.u1; ++u) release(units_done + u - P.u0);
         units_done += P.u1 - P.u0;
         continue;
       }
@@ -236,94 +283,119 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
                          two(v[c].z, v[c].w, true));
         }
         fence_async_smem();
-        mbar_arrive(&S.q_full[X]);
+        named_barrier(2 + X);
+        if (r == 0) issue_scores(units_done);
       }
       float M = -INFINITY, l = 0.f, ref = 1.f;
       for (int u = P.u0; u < last; ++u) {
-        const uint32_t slot = (units_done + u - P.u0) % SC_RING, turn = (units_done + u - P.u0) / SC_RING;
+        const uint32_t it = units_done + u - P.u0, slot = it % SC_RING;
         // the scales' barrier second: scores imply that its phase is this
         // unit's, not one of an earlier turn
         if (!(ok = wait_warp(&S.s_full[X], tiles & 1, 51))) break;
-        if (!(ok = wait_warp(&S.sc_full[slot], turn & 1, 52))) break;
+        if (!(ok = wait_warp(&S.sc_full[slot], (it / SC_RING) & 1, 52))) break;
         ++tiles;
         tc_fence_after();
         const bool masked = u * UNIT + UNIT - 1 > first_limit;
         const int see = limit - u * UNIT;  // the last token of the unit that this row sees
         ref = S.sc_ref[slot];
-        // ---- the row's maximum of score + log2 vs
-        float top = -INFINITY;
+        if (__any_sync(~0u, M == -INFINITY)) {
+          // ---- a first unit: the row's maximum of score + log2 vs
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32(s_addr + 32 * c, v);
+            tmem_ld_wait();
+            ld32_fence(v);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32(s_addr + 32 * c, v);
-          tmem_ld_wait();
-          ld32_fence(v);
+            for (int h2 = 0; h2 < 2; ++h2) {
+              float mx = -INFINITY;
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int i = 16 * h2; i < 16 * h2 + 16; ++i) {
-              float z = __uint_as_float(v[i]);
-              if (masked) z = 32 * c + i <= see ? z : -INFINITY;
-              mx = fmaxf(mx, z);
+              for (int i = 16 * h2; i < 16 * h2 + 16; ++i) mx = fmaxf(mx, 32 * c + i <= see ? __uint_as_float(v[i]) : -INFINITY);
+              // nothing seen: -inf, also where the factor is 0
+              top = fmaxf(top, mx == -INFINITY ? mx : fmaf(mx, f * S.sc_k[slot][2 * c + h2], S.sc_log[slot][2 * c + h2]));
             }
-            const float a = f * S.sc_k[slot][2 * c + h2];
-            // nothing seen: -inf, also where a = 0
-            top = fmaxf(top, mx == -INFINITY ? mx : fmaf(mx, a, S.sc_log[slot][2 * c + h2]));
           }
+          if (M == -INFINITY) M = top;  // nothing summed yet: nothing to rescale
         }
-        const bool grows = top > M + GROWTH || (M == -INFINITY && top > M);
-        if (__any_sync(~0u, grows)) {
-          const float to = fmaxf(M, top);
-          const float drop = M == -INFINITY ? 1.f : ex2(M - to);  // nothing summed yet: nothing to scale
+        // ---- the weights against the maximum so far; again, with the sums
+        // rescaled, if a row's outgrow 2^GROWTH (twice at most: scores beyond
+        // 2^24, whose units are above 1, may leave more than that)
+        uint32_t w[2][32];
+        float add;
+        for (int again = 0;; ++again) {
+          const float at = M == -INFINITY ? 0.f : M;
+          float most = -INFINITY;
+          add = 0.f;
+          uint32_t v[2][32];
+          tmem_ld32(s_addr, v[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            ld32_fence(v[c & 1]);
+            if (c < 3) tmem_ld32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2) {
+              const float a = f * S.sc_k[slot][2 * c + h2], b = S.sc_log[slot][2 * c + h2] - at;
+              float2 sum = make_float2(0.f, 0.f);
+              if (!masked) {
+#pragma unroll
+                for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
+                  float2 z = fma2(make_float2(__uint_as_float(v[c & 1][i]), __uint_as_float(v[c & 1][i + 1])), make_float2(a, a),
+                                  make_float2(b, b));
+                  most = fmaxf(fmaxf(most, z.x), z.y);
+                  z = make_float2(ex2(z.x), ex2(z.y));
+                  sum = add2(sum, z);
+                  w[c >> 1][16 * (c & 1) + (i >> 1)] = half2_bits(__float22half2_rn(z));
+                }
+              } else {
+#pragma unroll
+                for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
+                  float2 z = make_float2(fmaf(__uint_as_float(v[c & 1][i]), a, b), fmaf(__uint_as_float(v[c & 1][i + 1]), a, b));
+                  z.x = 32 * c + i <= see ? z.x : -INFINITY;
+                  z.y = 32 * c + i + 1 <= see ? z.y : -INFINITY;
+                  most = fmaxf(fmaxf(most, z.x), z.y);
+                  z = make_float2(ex2(z.x), ex2(z.y));
+                  sum = add2(sum, z);
+                  w[c >> 1][16 * (c & 1) + (i >> 1)] = half2_bits(__float22half2_rn(z));
+                }
+              }
+              add = fmaf(sum.x + sum.y, S.sc_inv[slot][2 * c + h2], add);
+            }
+          }
+          if (again == 2 || !__any_sync(~0u, most > GROWTH)) break;
+          const float by = fmaxf(most, 0.f), drop = ex2(-by);
+          M += by;
           l *= drop;
           if (u > P.u0) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tmem_ld32(o_addr + 32 * c, v);
+              tmem_ld32(o_addr + 32 * c, v[0]);
               tmem_ld_wait();
-              ld32_fence(v);
+              ld32_fence(v[0]);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * drop);
-              tmem_st<32>(o_addr + 32 * c, v);
+              for (int i = 0; i < 32; ++i) v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * drop);
+              tmem_st<32>(o_addr + 32 * c, v[0]);
             }
           }
-          M = to;
         }
-        const float at = M == -INFINITY ? 0.f : M;
-        // ---- the weights
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32], w[16];
-          tmem_ld32(s_addr + 32 * c, v);
-          tmem_ld_wait();
-          ld32_fence(v);
-#pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
-            const float a = f * S.sc_k[slot][2 * c + h2], b = S.sc_log[slot][2 * c + h2] - at;
-            float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-            for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
-              float z0 = fmaf(__uint_as_float(v[i]), a, b), z1 = fmaf(__uint_as_float(v[i + 1]), a, b);
-              if (masked) {
-                z0 = 32 * c + i <= see ? z0 : -INFINITY;
-                z1 = 32 * c + i + 1 <= see ? z1 : -INFINITY;
-              }
-              z0 = ex2(z0);
-              z1 = ex2(z1);
-              sum0 += z0;
-              sum1 += z1;
-              w[i >> 1] = half2_bits(__floats2half2_rn(z0, z1));
-            }
-            l = fmaf(sum0 + sum1, S.sc_inv[slot][2 * c + h2], l);
-          }
-          tmem_st<16>(s_addr + 16 * c, w);
-        }
+        l += add;
+        tmem_st<32>(s_addr, w[0]);
+        tmem_st<32>(s_addr + 32, w[1]);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&S.p_full[X]);
+        named_barrier(2 + X);  // every row's weights are there
+        if (r == 0) {
+          tc_fence_after();
+          issue_outputs(it, u == P.u0);
+          if (u + 1 < last)
+            issue_scores(it + 1);
+          else
+            mma_commit(&S.o_full[X]);
+        }
       }
+      if (ok && r == 0)
+        for (int u = last; u < P.u1; ++u) release(units_done + u - P.u0);
       if (!ok) break;
       units_done += P.u1 - P.u0;
       // ---- the piece's sums
@@ -399,7 +471,13 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         }
       }
     }
-  } else if (warp < W_MMA) {
+    // after a wait that gave up: the products in flight end before TMEM goes
+    if (*abort && r == 0) {
+      int never = 0;
+      mma_commit(&S.drain[X]);
+      mbar_wait(&S.drain[X], 0, &never, WAIT_NS);
+    }
+  } else {
     // ---------------------------------------------------------- conversion
     const int w = warp - W_CVT, ct = tid - 32 * W_CVT;
     constexpr int NK = D / 16;  // 16-byte pieces of keys a thread converts
@@ -548,70 +626,11 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       next_tile(n);
       next_pages = pages_of(n);
     }
-  } else if (elect_one()) {
-    // ------------------------------------------------------------ products
-    constexpr uint32_t ID_S = idesc_f16(128, UNIT), ID_O = idesc_f16(128, D);
-    uint32_t it = 0, q_turn[2] = {0, 0}, p_turn[2] = {0, 0};
-    bool ok = true;
-    auto scores = [&](int X, uint32_t unit) {
-      const uint32_t q0 = smem_u32(sq + X * Smem<D>::Q), k0 = smem_u32(sk + (unit & 1) * Smem<D>::K);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
-        mma_bf16(tmem + S_COL + 128 * X, desc_sw128(q0 + off), desc_sw128(k0 + off), ID_S, k > 0);
-      }
-      mma_commit(&S.s_full[X]);
-    };
-    auto outputs = [&](int X, uint32_t unit, bool first) {
-      const uint32_t v0 = smem_u32(sv + (unit & 1) * Smem<D>::V);
-#pragma unroll
-      for (int k = 0; k < UNIT / 16; ++k)
-        mma_bf16_ta(tmem + O_COL + D * X, tmem + S_COL + 128 * X + 8 * k, desc_sw128(v0 + (k >> 2) * (D * 128) + (k & 3) * 32),
-                    ID_O, !first || k > 0);
-    };
-    while (ok && walk.next(P)) {
-      const int last[2] = {min(P.u1, P.n[0]), min(P.u1, P.n[1])};
-      // unit `it` is this piece's first
-      for (int X = 0; X < 2; ++X)
-        if (ok && P.u0 < last[X]) ok = wait(&S.q_full[X], q_turn[X]++ & 1, 56);
-      if (!ok || !(ok = wait(&S.k_full[it & 1], (it >> 1) & 1, 57))) break;
-      tc_fence_after();
-      for (int X = 0; X < 2; ++X)
-        if (P.u0 < last[X]) scores(X, it);
-      mma_commit(&S.k_empty[it & 1]);
-      for (int u = P.u0; u < P.u1 && ok; ++u, ++it) {
-        if (!(ok = wait(&S.v_full[it & 1], (it >> 1) & 1, 58))) break;
-        const bool more = u + 1 < P.u1;
-        bool have_k = false;
-        for (int X = 0; X < 2 && ok; ++X) {
-          if (u < last[X]) {
-            if (!(ok = wait(&S.p_full[X], p_turn[X]++ & 1, 59))) break;
-            tc_fence_after();
-            outputs(X, it, u == P.u0);
-            if (u + 1 == last[X]) mma_commit(&S.o_full[X]);
-          }
-          if (X == 1) mma_commit(&S.v_empty[it & 1]);
-          if (more && !have_k) {
-            if (!(ok = wait(&S.k_full[(it + 1) & 1], ((it + 1) >> 1) & 1, 57))) break;
-            tc_fence_after();
-            have_k = true;
-          }
-          if (u + 1 < last[X]) scores(X, it + 1);
-        }
-        if (ok && more) mma_commit(&S.k_empty[(it + 1) & 1]);
-      }
-    }
-    // after a wait that gave up: the products in flight end before TMEM goes
-    if (!ok) {
-      int never = 0;
-      mma_commit(&S.drain);
-      mbar_wait(&S.drain, 0, &never, WAIT_NS);
-    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == W_MMA) tmem_dealloc(tmem, 512);
+  if (warp == W_CVT) tmem_dealloc(tmem, 512);
 }
 
 template <int D>
