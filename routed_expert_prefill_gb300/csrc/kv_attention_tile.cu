@@ -298,6 +298,21 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         const bool masked = u * UNIT + UNIT - 1 > first_limit;
         const int see = limit - u * UNIT;  // the last token of the unit that this row sees
         ref = S.sc_ref[slot];
+        if (masked) {  // the causal edge: what a row does not see becomes -inf in place
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32(s_addr + 32 * c, v);
+            tmem_ld_wait();
+            ld32_fence(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 32 * c + i <= see ? v[i] : 0xFF800000u;
+            tmem_st<32>(s_addr + 32 * c, v);
+          }
+          tmem_st_wait();
+        }
+        // a score's factor; never 0, so that -inf stays what it is
+        auto factor = [&](int run) { return fmaxf(f * S.sc_k[slot][run], 1e-30f); };
         if (__any_sync(~0u, M == -INFINITY)) {
           // ---- a first unit: the row's maximum of score + log2 vs
           float top = -INFINITY;
@@ -311,9 +326,8 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
             for (int h2 = 0; h2 < 2; ++h2) {
               float mx = -INFINITY;
 #pragma unroll
-              for (int i = 16 * h2; i < 16 * h2 + 16; ++i) mx = fmaxf(mx, 32 * c + i <= see ? __uint_as_float(v[i]) : -INFINITY);
-              // nothing seen: -inf, also where the factor is 0
-              top = fmaxf(top, mx == -INFINITY ? mx : fmaf(mx, f * S.sc_k[slot][2 * c + h2], S.sc_log[slot][2 * c + h2]));
+              for (int i = 16 * h2; i < 16 * h2 + 16; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+              top = fmaxf(top, fmaf(mx, factor(2 * c + h2), S.sc_log[slot][2 * c + h2]));
             }
           }
           if (M == -INFINITY) M = top;  // nothing summed yet: nothing to rescale
@@ -336,29 +350,16 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
             if (c < 3) tmem_ld32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
             for (int h2 = 0; h2 < 2; ++h2) {
-              const float a = f * S.sc_k[slot][2 * c + h2], b = S.sc_log[slot][2 * c + h2] - at;
+              const float a = factor(2 * c + h2), b = S.sc_log[slot][2 * c + h2] - at;
               float2 sum = make_float2(0.f, 0.f);
-              if (!masked) {
 #pragma unroll
-                for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
-                  float2 z = fma2(make_float2(__uint_as_float(v[c & 1][i]), __uint_as_float(v[c & 1][i + 1])), make_float2(a, a),
-                                  make_float2(b, b));
-                  most = fmaxf(fmaxf(most, z.x), z.y);
-                  z = make_float2(ex2(z.x), ex2(z.y));
-                  sum = add2(sum, z);
-                  w[c >> 1][16 * (c & 1) + (i >> 1)] = half2_bits(__float22half2_rn(z));
-                }
-              } else {
-#pragma unroll
-                for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
-                  float2 z = make_float2(fmaf(__uint_as_float(v[c & 1][i]), a, b), fmaf(__uint_as_float(v[c & 1][i + 1]), a, b));
-                  z.x = 32 * c + i <= see ? z.x : -INFINITY;
-                  z.y = 32 * c + i + 1 <= see ? z.y : -INFINITY;
-                  most = fmaxf(fmaxf(most, z.x), z.y);
-                  z = make_float2(ex2(z.x), ex2(z.y));
-                  sum = add2(sum, z);
-                  w[c >> 1][16 * (c & 1) + (i >> 1)] = half2_bits(__float22half2_rn(z));
-                }
+              for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
+                float2 z = fma2(make_float2(__uint_as_float(v[c & 1][i]), __uint_as_float(v[c & 1][i + 1])), make_float2(a, a),
+                                make_float2(b, b));
+                most = fmaxf(fmaxf(most, z.x), z.y);
+                z = make_float2(ex2(z.x), ex2(z.y));
+                sum = add2(sum, z);
+                w[c >> 1][16 * (c & 1) + (i >> 1)] = half2_bits(__float22half2_rn(z));
               }
               add = fmaf(sum.x + sum.y, S.sc_inv[slot][2 * c + h2], add);
             }
@@ -518,29 +519,34 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     // run lane % 8 of a unit
     auto pages_of = [&](const Tile& t) { return page_id(t, t.u * UNIT + 16 * (lane & 7)); };
     uint4 kr[NK], vr[8];
+    // where run `run` of a unit starts in its page
+    auto run_at = [&](const Tile& t, int page, int run) {
+      return p.c.codes + page * page_bytes + (t.h * p.c.block + ((t.u * UNIT + 16 * run) & (p.c.block - 1))) * D;
+    };
+    const int k_lane = (lane & 7) * D + 16 * (lane >> 3), v_lane = (vo & 1) * 8 * D + 16 * vc;
     auto load_k = [&](const Tile& t, int pages) {
 #pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        const int tok = 32 * w + 8 * (i & 3) + (lane & 7), c = (lane >> 3) + 4 * (i >> 2);
-        const int page = __shfl_sync(~0u, pages, 2 * w + ((i & 3) >> 1));
-        kr[i] = make_uint4(0, 0, 0, 0);
-        if (page >= 0)
-          kr[i] = __ldg(reinterpret_cast<const uint4*>(p.c.codes + page * page_bytes +
-                                                       ((int64_t)t.h * p.c.block + ((t.u * UNIT + tok) & (p.c.block - 1))) * D +
-                                                       16 * c));
+      for (int e = 0; e < 2; ++e) {  // the warp's two runs
+        const int page = __shfl_sync(~0u, pages, 2 * w + e);
+        const int8_t* src = run_at(t, page, 2 * w + e) + k_lane;
+#pragma unroll
+        for (int c = 0; c < NK / 4; ++c)
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+            kr[4 * c + 2 * e + o] = page >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + 8 * o * D + 64 * c))
+                                              : make_uint4(0, 0, 0, 0);
       }
     };
     auto load_v = [&](const Tile& t, int pages) {
       const int page = __shfl_sync(~0u, pages, vo >> 1);
+      const int8_t* src = run_at(t, page, vo >> 1) + vstep + v_lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        vr[i] = make_uint4(0, 0, 0, 0);
-        if (page >= 0 && has_v)
-          vr[i] = __ldg(reinterpret_cast<const uint4*>(
-              p.c.codes + vstep + page * page_bytes +
-              ((int64_t)t.h * p.c.block + ((t.u * UNIT + 8 * vo + i) & (p.c.block - 1))) * D + 16 * vc));
-      }
+      for (int i = 0; i < 8; ++i)
+        vr[i] = page >= 0 && has_v ? __ldg(reinterpret_cast<const uint4*>(src + i * D)) : make_uint4(0, 0, 0, 0);
     };
+    // where this thread's pieces go: keys in row lane % 8 of an 8-row group,
+    // 16-byte chunks 2 c and 2 c + 1; values in chunk vo % 8 of their rows
+    const uint32_t k_to[2] = {sw128_off(lane & 7, 2 * (lane >> 3)), sw128_off(lane & 7, 2 * (lane >> 3) + 1)};
     Tile t, n;
     next_tile(t);
     int pages = pages_of(t);
@@ -585,14 +591,13 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         mbar_arrive(&S.sc_full[slot]);
       }
       {
-        unsigned char* dst = sk + st * Smem<D>::K;
+        unsigned char* dst = sk + st * Smem<D>::K + 4 * w * 1024;
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-          const int tok = 32 * w + 8 * (i & 3) + (lane & 7), c = (lane >> 3) + 4 * (i >> 2);
-          unsigned char* panel = dst + (c >> 2) * (128 * 128);
-          *reinterpret_cast<uint4*>(panel + sw128_off(tok, 2 * c & 7)) =
+          unsigned char* rows = dst + (i & 3) * 1024 + (i >> 2) * (128 * 128);
+          *reinterpret_cast<uint4*>(rows + k_to[0]) =
               make_uint4(f16_even(kr[i].x), f16_odd(kr[i].x), f16_even(kr[i].y), f16_odd(kr[i].y));
-          *reinterpret_cast<uint4*>(panel + sw128_off(tok, (2 * c & 7) + 1)) =
+          *reinterpret_cast<uint4*>(rows + k_to[1]) =
               make_uint4(f16_even(kr[i].z), f16_odd(kr[i].z), f16_even(kr[i].w), f16_odd(kr[i].w));
         }
         fence_async_smem();
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       if (n.any) load_k(n, next_pages);
       if (!(ok = wait_warp(&S.v_empty[st], par, 55))) break;
       {
-        unsigned char* dst = sv + st * Smem<D>::V + (vo >> 3) * (D * 128);
+        unsigned char* dst = sv + st * Smem<D>::V + (vo >> 3) * (D * 128) + 2 * vc * 1024;
         if (has_v) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = q == 0 ? vr[i].x : q == 1 ? vr[i].y : q == 2 ? vr[i].z : vr[i].w;
             auto put = [&](int ch, uint4 v) {
-              *reinterpret_cast<uint4*>(dst + sw128_off(16 * vc + 4 * q + ch, vo & 7)) = v;
+              *reinterpret_cast<uint4*>(dst + sw128_off(4 * q + ch, vo & 7)) = v;
             };
             put(0, make_uint4(f16_pair<0>(x[0], x[1]), f16_pair<0>(x[2], x[3]), f16_pair<0>(x[4], x[5]), f16_pair<0>(x[6], x[7])));
             put(1, make_uint4(f16_pair<1>(x[0], x[1]), f16_pair<1>(x[2], x[3]), f16_pair<1>(x[4], x[5]), f16_pair<1>(x[6], x[7])));
