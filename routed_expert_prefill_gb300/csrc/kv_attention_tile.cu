@@ -29,13 +29,15 @@ struct TileShared {
   uint32_t arrived[2];
   uint32_t tmem;
   int abort;
+  int issuing;  // 1 while one tile's thread hands its products over
   int64_t scratch[T_WARPS + 2];
 };
 
 template <int D>
 struct Smem {
   static constexpr int Q = 128 * D * 2, K = UNIT * D * 2, V = D * UNIT * 2;
-  static constexpr int TOTAL = 2 * Q + 2 * K + 2 * V + 1024 + (int)sizeof(TileShared);
+  static constexpr int RAW = 2 * UNIT * D;  // codes of a unit as they come
+  static constexpr int TOTAL = 2 * Q + 2 * K + 2 * V + RAW + 1024 + (int)sizeof(TileShared);
 };
 template <int D>
 constexpr size_t partial_floats() { return (size_t)128 * (D + 2); }  // accumulators, maximum, sum of a tile's rows
@@ -46,6 +48,7 @@ struct Piece {
   int s, qt, h, u0, u1, units;
   int64_t item;  // the item's first unit
   int n[2];      // units that the rows of either tile see
+  int seen;      // positions that the item's rows see
 };
 
 // The pieces of a CTA in order; every warp walks them by itself.
@@ -63,7 +66,8 @@ struct Walk {
     const int64_t rows = (int64_t)q.n * p.G;
     P.q = q;
     P.s = s, P.qt = qt, P.h = h;
-    P.units = tile_units<T_ROWS>(p, q, qt);
+    P.seen = tile_seen<T_ROWS>(p, q, qt);
+    P.units = (P.seen + UNIT - 1) / UNIT;
     P.u0 = u;
     P.u1 = (int)min((int64_t)P.units, u + (w.x1 - x));
     P.item = x - u;
@@ -160,7 +164,8 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
   unsigned char* sq = smem;
   unsigned char* sk = sq + 2 * Smem<D>::Q;
   unsigned char* sv = sk + 2 * Smem<D>::K;
-  TileShared& S = *reinterpret_cast<TileShared*>(sv + 2 * Smem<D>::V);
+  unsigned char* raw = sv + 2 * Smem<D>::V;
+  TileShared& S = *reinterpret_cast<TileShared*>(raw + Smem<D>::RAW);
   constexpr uint32_t S_COL = 0, O_COL = 256;  // tile x: S at 128 x, O at 256 + D x
   pdl_wait();
   pdl_trigger();
@@ -180,6 +185,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     }
     for (int i = 0; i < SC_RING; ++i) mbar_init(&S.sc_full[i], 8);
     S.abort = 0;
+    S.issuing = 0;
     fence_mbar_init();
   }
   if (warp == W_CVT) tmem_alloc(&S.tmem, 512);
@@ -212,10 +218,20 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     uint32_t units_done = 0, tiles = 0, pieces = 0;  // of the CTA; of this tile
     bool ok = true;
     constexpr uint32_t ID_S = idesc_f16(128, UNIT), ID_O = idesc_f16(128, D);
-    // S of unit `it`, by one thread
+    // The products, by one thread a tile, elected in its first warp.  A tile hands over all it has at
+    // once, O += P V of its unit and S of the next, and the other waits: taken
+    // in turns product by product, both tiles' would end at the same time, and
+    // both softmaxes run while the tensor cores idle.
+    auto lock = [&]() {
+      const uint64_t t0 = globaltimer();
+      while (atomicCAS(&S.issuing, 0, 1) != 0) {
+        if (*abort || globaltimer() - t0 > WAIT_NS) return false;
+        __nanosleep(32);
+      }
+      return true;
+    };
+    auto unlock = [&]() { atomicExch(&S.issuing, 0); };
     auto issue_scores = [&](uint32_t it) {
-      if (!wait(&S.k_full[it & 1], (it >> 1) & 1, 57)) return;
-      tc_fence_after();
       const uint32_t q0 = smem_u32(q_tile), k0 = smem_u32(sk + (it & 1) * Smem<D>::K);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -226,8 +242,6 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       mma_commit(&S.k_empty[it & 1]);
     };
     auto issue_outputs = [&](uint32_t it, bool first) {
-      if (!wait(&S.v_full[it & 1], (it >> 1) & 1, 58)) return;
-      tc_fence_after();
       const uint32_t v0 = smem_u32(sv + (it & 1) * Smem<D>::V);
 #pragma unroll
       for (int k = 0; k < UNIT / 16; ++k)
@@ -284,7 +298,15 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         }
         fence_async_smem();
         named_barrier(2 + X);
-        if (r == 0) issue_scores(units_done);
+        if ((warp & 3) == 0) {
+          if (!(ok = wait_warp(&S.k_full[units_done & 1], (units_done >> 1) & 1, 57))) break;
+          tc_fence_after();
+          if (elect_one() && lock()) {
+            issue_scores(units_done);
+            unlock();
+          }
+          __syncwarp();
+        }
       }
       float M = -INFINITY, l = 0.f, ref = 1.f;
       for (int u = P.u0; u < last; ++u) {
@@ -386,13 +408,20 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         tmem_st_wait();
         tc_fence_before();
         named_barrier(2 + X);  // every row's weights are there
-        if (r == 0) {
+        if ((warp & 3) == 0) {
+          const bool more = u + 1 < last;
+          if (!(ok = wait_warp(&S.v_full[it & 1], (it >> 1) & 1, 58))) break;
+          if (more && !(ok = wait_warp(&S.k_full[(it + 1) & 1], ((it + 1) >> 1) & 1, 57))) break;
           tc_fence_after();
-          issue_outputs(it, u == P.u0);
-          if (u + 1 < last)
-            issue_scores(it + 1);
-          else
-            mma_commit(&S.o_full[X]);
+          if (elect_one() && lock()) {
+            issue_outputs(it, u == P.u0);
+            if (more)
+              issue_scores(it + 1);
+            else
+              mma_commit(&S.o_full[X]);
+            unlock();
+          }
+          __syncwarp();
         }
       }
       if (ok && r == 0)
@@ -507,7 +536,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         t.first = true;
       }
       t.s = cur.s, t.h = cur.h, t.u = cu++;
-      t.seen = tile_seen<T_ROWS>(p, cur.q, cur.qt);
+      t.seen = cur.seen;
     };
     auto page_id = [&](const Tile& t, int pos) {
       if (!t.any || pos >= t.seen) return -1;
@@ -518,68 +547,74 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     };
     // run lane % 8 of a unit
     auto pages_of = [&](const Tile& t) { return page_id(t, t.u * UNIT + 16 * (lane & 7)); };
-    uint4 kr[NK], vr[8];
     // where run `run` of a unit starts in its page
     auto run_at = [&](const Tile& t, int page, int run) {
       return p.c.codes + page * page_bytes + (t.h * p.c.block + ((t.u * UNIT + 16 * run) & (p.c.block - 1))) * D;
     };
+    // Pieces wait in shared memory, each read by the thread that copied it:
+    // keys' piece i at (i * 128 + ct) * 16, values' likewise behind them.
+    unsigned char* raw_k = raw + ct * 16;
+    unsigned char* raw_v = raw + UNIT * D + (D == 128 ? ct : ct & 63) * 16;
+    constexpr int V_STEP = D == 128 ? 2048 : 1024;
     const int k_lane = (lane & 7) * D + 16 * (lane >> 3), v_lane = (vo & 1) * 8 * D + 16 * vc;
     auto load_k = [&](const Tile& t, int pages) {
+      if (t.any)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {  // the warp's two runs
-        const int page = __shfl_sync(~0u, pages, 2 * w + e);
-        const int8_t* src = run_at(t, page, 2 * w + e) + k_lane;
+        for (int e = 0; e < 2; ++e) {  // the warp's two runs
+          const int page = __shfl_sync(~0u, pages, 2 * w + e);
+          const int8_t* src = run_at(t, max(page, 0), 2 * w + e) + k_lane;
 #pragma unroll
-        for (int c = 0; c < NK / 4; ++c)
+          for (int c = 0; c < NK / 4; ++c)
 #pragma unroll
-          for (int o = 0; o < 2; ++o)
-            kr[4 * c + 2 * e + o] = page >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + 8 * o * D + 64 * c))
-                                              : make_uint4(0, 0, 0, 0);
-      }
+            for (int o = 0; o < 2; ++o) cp_async16(raw_k + (4 * c + 2 * e + o) * 2048, src + 8 * o * D + 64 * c);
+        }
+      cp_async_commit();
     };
     auto load_v = [&](const Tile& t, int pages) {
-      const int page = __shfl_sync(~0u, pages, vo >> 1);
-      const int8_t* src = run_at(t, page, vo >> 1) + vstep + v_lane;
+      if (t.any) {
+        const int page = __shfl_sync(~0u, pages, vo >> 1);
+        const int8_t* src = run_at(t, max(page, 0), vo >> 1) + vstep + v_lane;
+        if (has_v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        vr[i] = page >= 0 && has_v ? __ldg(reinterpret_cast<const uint4*>(src + i * D)) : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 8; ++i) cp_async16(raw_v + i * V_STEP, src + i * D);
+      }
+      cp_async_commit();
     };
     // where this thread's pieces go: keys in row lane % 8 of an 8-row group,
     // 16-byte chunks 2 c and 2 c + 1; values in chunk vo % 8 of their rows
     const uint32_t k_to[2] = {sw128_off(lane & 7, 2 * (lane >> 3)), sw128_off(lane & 7, 2 * (lane >> 3) + 1)};
-    Tile t, n;
+    // scales of run lane % 8; the pages come two units ahead, codes and scales one
+    auto scale_of = [&](const Tile& t, int page, int isv) {
+      return page < 0 ? 0.f : __ldg(p.c.scales + ((size_t)isv * p.c.n_pages + page) * hkv + t.h);
+    };
+    Tile t, n, m;
     next_tile(t);
     int pages = pages_of(t);
     load_k(t, pages);
     load_v(t, pages);
+    float ks = scale_of(t, pages, 0), vs = scale_of(t, pages, 1);
     next_tile(n);
     int next_pages = pages_of(n);
+    next_tile(m);
+    int after_pages = pages_of(m);
     float vref = 1.f;
     bool ok = true;
     for (uint32_t it = 0; t.any; ++it) {
       const uint32_t st = it & 1, par = ((it >> 1) & 1) ^ 1;
       if (t.first) {  // the largest value scale of the item
-        float m = 0.f;
-        for (int b = ct; b * p.c.block < t.seen; b += 128) {
-          const int page = page_id(t, b * p.c.block);
-          if (page >= 0) m = fmaxf(m, __ldg(p.c.scales + ((size_t)p.c.n_pages + page) * hkv + t.h));
-        }
+        float top = 0.f;
+        for (int b = ct; b * p.c.block < t.seen; b += 128) top = fmaxf(top, scale_of(t, page_id(t, b * p.c.block), 1));
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
         named_barrier(1);  // the last item's values are read
-        if (lane == 0) S.red[w] = m;
+        if (lane == 0) S.red[w] = top;
         named_barrier(1);
-        m = fmaxf(fmaxf(S.red[0], S.red[1]), fmaxf(S.red[2], S.red[3]));
-        vref = m;  // 0: every value is 0, and so is the result
+        vref = fmaxf(fmaxf(S.red[0], S.red[1]), fmaxf(S.red[2], S.red[3]));  // 0: every value is 0, and so is the result
       }
       // the slot's last unit, SC_RING back, is past every softmax thread: the
       // products that freed this K stage came after its weights
-      float ks = 0.f, lg = -INFINITY, inv = 0.f;
-      if (w == 0 && lane < 8 && pages >= 0) {
-        ks = __ldg(p.c.scales + (size_t)pages * hkv + t.h);
-        lg = fmaxf(log2f(__ldg(p.c.scales + ((size_t)p.c.n_pages + pages) * hkv + t.h) / (vref > 0.f ? vref : 1.f)), -60.f);
-        inv = exp2f(-lg);
-      }
+      const float lg = pages < 0 ? -INFINITY : fmaxf(__log2f(vs / (vref > 0.f ? vref : 1.f)), -60.f);
+      const float inv = pages < 0 ? 0.f : ex2(-lg);
       if (!(ok = wait_warp(&S.k_empty[st], par, 54))) break;
       if (w == 0 && lane < 8) {
         const uint32_t slot = it % SC_RING;
@@ -591,30 +626,35 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         mbar_arrive(&S.sc_full[slot]);
       }
       {
+        cp_async_wait<1>();
         unsigned char* dst = sk + st * Smem<D>::K + 4 * w * 1024;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < NK; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(raw_k + i * 2048);
           unsigned char* rows = dst + (i & 3) * 1024 + (i >> 2) * (128 * 128);
-          *reinterpret_cast<uint4*>(rows + k_to[0]) =
-              make_uint4(f16_even(kr[i].x), f16_odd(kr[i].x), f16_even(kr[i].y), f16_odd(kr[i].y));
-          *reinterpret_cast<uint4*>(rows + k_to[1]) =
-              make_uint4(f16_even(kr[i].z), f16_odd(kr[i].z), f16_even(kr[i].w), f16_odd(kr[i].w));
+          *reinterpret_cast<uint4*>(rows + k_to[0]) = make_uint4(f16_even(v.x), f16_odd(v.x), f16_even(v.y), f16_odd(v.y));
+          *reinterpret_cast<uint4*>(rows + k_to[1]) = make_uint4(f16_even(v.z), f16_odd(v.z), f16_even(v.w), f16_odd(v.w));
         }
         fence_async_smem();
         mbar_arrive(&S.k_full[st]);
       }
-      if (n.any) load_k(n, next_pages);
+      load_k(n, next_pages);
+      ks = scale_of(n, next_pages, 0);
+      vs = scale_of(n, next_pages, 1);
       if (!(ok = wait_warp(&S.v_empty[st], par, 55))) break;
       {
         unsigned char* dst = sv + st * Smem<D>::V + (vo >> 3) * (D * 128) + 2 * vc * 1024;
+        cp_async_wait<1>();
         if (has_v) {
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = q == 0 ? vr[i].x : q == 1 ? vr[i].y : q == 2 ? vr[i].z : vr[i].w;
+            for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint32_t*>(raw_v + i * V_STEP + 4 * q);
+            // channel 4 q + ch of the piece; its row's 8-row group and place in it
+            unsigned char* rows = dst + (q >> 1) * 1024 + (q & 1) * 512;
             auto put = [&](int ch, uint4 v) {
-              *reinterpret_cast<uint4*>(dst + sw128_off(4 * q + ch, vo & 7)) = v;
+              *reinterpret_cast<uint4*>(rows + ch * 128 + (((vo & 7) ^ (4 * (q & 1) + ch)) << 4)) = v;
             };
             put(0, make_uint4(f16_pair<0>(x[0], x[1]), f16_pair<0>(x[2], x[3]), f16_pair<0>(x[4], x[5]), f16_pair<0>(x[6], x[7])));
             put(1, make_uint4(f16_pair<1>(x[0], x[1]), f16_pair<1>(x[2], x[3]), f16_pair<1>(x[4], x[5]), f16_pair<1>(x[6], x[7])));
@@ -625,12 +665,15 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         fence_async_smem();
         mbar_arrive(&S.v_full[st]);
       }
-      if (n.any) load_v(n, next_pages);
+      load_v(n, next_pages);
       t = n;
       pages = next_pages;
-      next_tile(n);
-      next_pages = pages_of(n);
+      n = m;
+      next_pages = after_pages;
+      next_tile(m);
+      after_pages = pages_of(m);
     }
+    cp_async_wait<0>();
   }
   tc_fence_before();
   __syncthreads();
