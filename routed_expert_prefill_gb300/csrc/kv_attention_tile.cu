@@ -13,12 +13,31 @@ namespace {
 using namespace tc;
 
 constexpr int T_ROWS = 256;  // query rows of an item: two tiles of 128
-constexpr int T_WARPS = 12;  // 0-3 softmax and products of tile 0, 4-7 of tile 1, 8-11 conversion
+// Warps: 0-3 softmax and products of tile 0, 4-7 of tile 1, 8-11 bring the
+// keys and values.  Twelve, so that a thread may hold 168 registers.
+constexpr int T_WARPS = 12, W_KEYS = 8;
 constexpr int T_THREADS = T_WARPS * 32;
-constexpr int W_CVT = 8;
 constexpr int SC_RING = 4;   // tiles whose scales are kept
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float GROWTH = 8.f;  // how far (log2) a row's weights may outgrow 1 before its sums are rescaled
+
+// One CTA's part of an item: units u0 .. u1 - 1 of it.
+struct Piece {
+  int row, new_rows, len;  // of the sequence
+  int s, qt, h, u0, u1;
+  int n[2];                // units that the rows of either tile see
+  int seen;                // positions that the item's rows see
+  int64_t item;            // the item's first unit
+};
+
+// A warp's walk over the CTA's pieces.  It lives in shared memory and one lane
+// advances it, which leaves the unit loops their registers (no spills).
+struct Walk {
+  int64_t x;
+  int s, qt, h, u;
+  Piece P;
+  int more;
+};
 
 struct TileShared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
@@ -31,61 +50,53 @@ struct TileShared {
   int abort;
   int issuing;  // 1 while one tile's thread hands its products over
   int64_t scratch[T_WARPS + 2];
+  Work work;
+  Walk walk[T_WARPS];
 };
+
+
+// The next piece of the warp's walk into W.P; false at the end.
+__device__ __forceinline__ bool next_piece(const AttnParams& p, const Work& w, Walk& W) {
+  __syncwarp();  // every lane is done with the last piece
+  if ((threadIdx.x & 31) == 0) {
+    W.more = W.x < w.x1;
+    if (W.more) {
+      Piece& P = W.P;
+      const Seq q = load_seq(p, W.s);
+      P.row = q.row, P.new_rows = q.n, P.len = q.len;
+      P.s = W.s, P.qt = W.qt, P.h = W.h;
+      P.seen = tile_seen<T_ROWS>(p, q, W.qt);
+      const int units = (P.seen + UNIT - 1) / UNIT;
+      P.u0 = W.u;
+      P.u1 = (int)min((int64_t)units, W.u + (w.x1 - W.x));
+      P.item = W.x - W.u;
+      P.n[0] = tile_units<128>(p, q, 2 * W.qt);
+      P.n[1] = (int64_t)q.n * p.G > (int64_t)T_ROWS * W.qt + 128 ? units : 0;
+      W.x += P.u1 - P.u0;
+      W.u = 0;
+      if (W.x < w.x1 && ++W.h == p.c.hkv) {
+        W.h = 0;
+        if (++W.qt == q_tiles<T_ROWS>(p, q)) {
+          W.qt = 0;
+          do ++W.s;
+          while (load_seq(p, W.s).n == 0);  // x < x1 <= total: a later sequence has rows
+        }
+      }
+    }
+  }
+  __syncwarp();
+  return W.more != 0;
+}
 
 template <int D>
 struct Smem {
   static constexpr int Q = 128 * D * 2, K = UNIT * D * 2, V = D * UNIT * 2;
   static constexpr int RAW = 2 * UNIT * D;  // codes of a unit as they come
-  static constexpr int TOTAL = 2 * Q + 2 * K + 2 * V + RAW + 1024 + (int)sizeof(TileShared);
+  static constexpr int TOTAL = 2 * Q + 2 * K + 2 * V + RAW + (int)sizeof(TileShared);
+  static_assert(TOTAL <= 227 * 1024, "shared memory of a CTA");
 };
 template <int D>
 constexpr size_t partial_floats() { return (size_t)128 * (D + 2); }  // accumulators, maximum, sum of a tile's rows
-
-// One CTA's part of an item: units u0 .. u1 - 1 of its `units`.
-struct Piece {
-  Seq q;
-  int s, qt, h, u0, u1, units;
-  int64_t item;  // the item's first unit
-  int n[2];      // units that the rows of either tile see
-  int seen;      // positions that the item's rows see
-};
-
-// The pieces of a CTA in order; every warp walks them by itself.
-struct Walk {
-  const AttnParams& p;
-  Work w;
-  int64_t x;
-  int s, qt, h, u;
-  Seq q;
-  __device__ Walk(const AttnParams& p_, const Work& w_) : p(p_), w(w_), x(w_.x0), s(w_.s), qt(w_.qt), h(w_.h), u(w_.u) {
-    q = load_seq(p, s);
-  }
-  __device__ bool next(Piece& P) {
-    if (x >= w.x1) return false;
-    const int64_t rows = (int64_t)q.n * p.G;
-    P.q = q;
-    P.s = s, P.qt = qt, P.h = h;
-    P.seen = tile_seen<T_ROWS>(p, q, qt);
-    P.units = (P.seen + UNIT - 1) / UNIT;
-    P.u0 = u;
-    P.u1 = (int)min((int64_t)P.units, u + (w.x1 - x));
-    P.item = x - u;
-    P.n[0] = tile_units<128>(p, q, 2 * qt);
-    P.n[1] = rows > (int64_t)T_ROWS * qt + 128 ? P.units : 0;
-    x += P.u1 - u;
-    u = 0;
-    if (x < w.x1 && ++h == p.c.hkv) {
-      h = 0;
-      if (++qt == q_tiles<T_ROWS>(p, q)) {
-        qt = 0;
-        do q = load_seq(p, ++s);
-        while (q.n == 0);  // x < x1 <= total: a later sequence has rows
-      }
-    }
-    return true;
-  }
-};
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -110,15 +121,16 @@ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ uint32_t minus_1152(uint32_t v) {
-  return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&v), __floats2half2_rn(1152.f, 1152.f)));
-}
-// Bytes 0 and 2, bytes 1 and 3 of a word of codes; byte B of two words: exact fp16 numbers.
-__device__ __forceinline__ uint32_t f16_even(uint32_t w) { return minus_1152((w & 0x00FF00FFu) ^ 0x64806480u); }
-__device__ __forceinline__ uint32_t f16_odd(uint32_t w) { return minus_1152(((w >> 8) & 0x00FF00FFu) ^ 0x64806480u); }
+// Codes c of bytes 0 and 2, and of bytes 1 and 3, as the fp16 numbers
+// (c + 128) * 2^-24: below fp16's normal range the bits are the value.
+__device__ __forceinline__ uint32_t codes_even(uint32_t w) { return (w ^ 0x80808080u) & 0x00FF00FFu; }
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return ((w >> 8) ^ 0x00808080u) & 0x00FF00FFu; }
+// Byte B of two words as exact fp16 numbers: under the exponent of 1024 the
+// byte c ^ 0x80 is 1024 + 128 + c.
 template <int B>
 __device__ __forceinline__ uint32_t f16_pair(uint32_t a, uint32_t b) {
-  return minus_1152((__byte_perm(a, b, B | (4 + B) << 8) & 0x00FF00FFu) ^ 0x64806480u);
+  const uint32_t v = (__byte_perm(a, b, B | (4 + B) << 8) & 0x00FF00FFu) ^ 0x64806480u;
+  return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&v), __floats2half2_rn(1152.f, 1152.f)));
 }
 
 // Two fp32 operations in one instruction.
@@ -143,15 +155,17 @@ __device__ __forceinline__ void named_barrier(int id) { asm volatile("bar.sync %
 // The work is cut as in the streaming kernel, over items of 256 query rows
 // (a position's heads next to each other) and units of 128 tokens.
 //
-// Per unit the four conversion warps bring the keys and values, one unit
-// ahead in registers, and store them as exact fp16 codes in the swizzled
-// operand layout, the values transposed.  Two groups of four warps own a tile
-// of 128 rows each: one thread issues S = Q K^T and O += P V, and while one
-// tile's weights are being taken the tensor cores work for the other.  A
-// thread owns a row: S comes from TMEM and P goes back over it as fp16, the
-// second product's A operand, while O stays in TMEM for all units.  Weights
-// are taken against the maximum so far, in one pass over S; only if one would
-// outgrow 2^8 are O and the sums rescaled and the pass repeated.
+// Four warps bring the keys and values of each unit, copied one unit ahead,
+// and store them as fp16 numbers in the swizzled operand layout: the
+// keys' codes raw, as (c + 128) 2^-24 (128 2^-24 times the query row's sum
+// comes off the score), the values' as c itself, transposed.  Two groups of
+// four warps own a tile of 128 rows each: one thread issues S = Q K^T and
+// O += P V, and while one tile's weights are being taken the tensor cores
+// work for the other.  A thread owns a row: S comes from TMEM and P goes back
+// over it as fp16, the second product's A operand, while O stays in TMEM for
+// all units.  Weights are taken against the maximum so far, in one pass over
+// S; only if one would outgrow 2^8 are O and the sums rescaled and the pass
+// repeated.
 //
 // Scales: the key scale of a run of 16 tokens multiplies the fp32 scores.  The
 // value scale vs, relative to the item's largest, enters the weights through
@@ -159,9 +173,8 @@ __device__ __forceinline__ void named_barrier(int id) { asm volatile("bar.sync %
 // are, and the softmax's sum takes each run's sum of P back by 1 / vs.
 template <int D>
 __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnParams p) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-  unsigned char* sq = smem;
+  extern __shared__ __align__(1024) unsigned char smem_tile[];  // operand tiles: 1024-byte aligned
+  unsigned char* sq = smem_tile;
   unsigned char* sk = sq + 2 * Smem<D>::Q;
   unsigned char* sv = sk + 2 * Smem<D>::K;
   unsigned char* raw = sv + 2 * Smem<D>::V;
@@ -171,24 +184,31 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hkv = p.c.hkv;
-  Work wk;
-  if (!find_work<T_ROWS, T_THREADS>(p, S.scratch, wk)) return;
+  {
+    Work found;
+    if (!find_work<T_ROWS, T_THREADS>(p, S.scratch, found)) return;
+    if (tid == 0) S.work = found;
+    if (lane == 0) {
+      Walk& W = S.walk[warp];
+      W.x = found.x0, W.s = found.s, W.qt = found.qt, W.h = found.h, W.u = found.u;
+    }
+  }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.k_full[i], 128);
+      mbar_init(&S.k_full[i], 4);  // one arrival a warp
       mbar_init(&S.k_empty[i], 2);  // released for either tile
-      mbar_init(&S.v_full[i], 128);
+      mbar_init(&S.v_full[i], 4);
       mbar_init(&S.v_empty[i], 2);
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.o_full[i], 1);
       mbar_init(&S.drain[i], 1);
     }
-    for (int i = 0; i < SC_RING; ++i) mbar_init(&S.sc_full[i], 8);
+    for (int i = 0; i < SC_RING; ++i) mbar_init(&S.sc_full[i], 1);
     S.abort = 0;
     S.issuing = 0;
     fence_mbar_init();
   }
-  if (warp == W_CVT) tmem_alloc(&S.tmem, 512);
+  if (warp == W_KEYS) tmem_alloc(&S.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -207,9 +227,8 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     return __all_sync(~0u, wait(bar, parity, site)) != 0;
   };
 
-  Walk walk(p, wk);
-  Piece P;
-  if (warp < W_CVT) {
+  const Piece& P = S.walk[warp].P;
+  if (warp < W_KEYS) {
     // ------------------------------------------------- softmax and products
     const int X = warp >> 2, r = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the lanes
@@ -223,10 +242,12 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     // in turns product by product, both tiles' would end at the same time, and
     // both softmaxes run while the tensor cores idle.
     auto lock = [&]() {
-      const uint64_t t0 = globaltimer();
-      while (atomicCAS(&S.issuing, 0, 1) != 0) {
-        if (*abort || globaltimer() - t0 > WAIT_NS) return false;
-        __nanosleep(32);
+      uint64_t t0 = 0;
+      for (uint32_t i = 1; atomicCAS(&S.issuing, 0, 1) != 0; ++i) {
+        if (i & 63) continue;
+        const uint64_t now = globaltimer();
+        if (t0 == 0) t0 = now;
+        if (*abort || now - t0 > WAIT_NS) return false;
       }
       return true;
     };
@@ -254,7 +275,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       if (wait(&S.k_full[it & 1], (it >> 1) & 1, 59)) mbar_arrive(&S.k_empty[it & 1]);
       if (wait(&S.v_full[it & 1], (it >> 1) & 1, 60)) mbar_arrive(&S.v_empty[it & 1]);
     };
-    while (ok && walk.next(P)) {
+    while (ok && next_piece(p, S.work, S.walk[warp])) {
       const int last = min(P.u1, P.n[X]);
       if (P.u0 >= last) {
         if (r == 0)
@@ -262,40 +283,43 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         units_done += P.u1 - P.u0;
         continue;
       }
-      const int64_t rr = (int64_t)T_ROWS * P.qt + 128 * X + r, rows = (int64_t)P.q.n * p.G;
+      const int64_t rr = (int64_t)T_ROWS * P.qt + 128 * X + r, rows = (int64_t)P.new_rows * p.G;
       const bool live_row = rr < rows;
       const int qi = live_row ? (int)(rr / p.G) : 0, head = live_row ? P.h * p.G + (int)(rr % p.G) : 0;
-      const int before = P.q.len - P.q.n;
+      const int before = P.len - P.new_rows;
       // rows past the last store nothing, so they may see all
       const int limit = live_row ? before + qi : INT_MAX;
       const int first_limit = before + (int)(((int64_t)T_ROWS * P.qt + 128 * X) / p.G);
       // ---- the query row, scaled by a power of two into fp16
-      float f;
+      float f, off;  // score per product; what the keys' 128s add to a product
       {
-        const uint16_t* src = p.q + (int64_t)(P.q.row + qi) * p.q_stride + (size_t)head * D;
-        uint4 v[D / 8];
-        float m = 0.f;
-#pragma unroll
+        const uint16_t* src = p.q + (int64_t)(P.row + qi) * p.q_stride + (size_t)head * D;
+        float m = 0.f, sum = 0.f;
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
-          v[c] = live_row ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+          const uint4 v = live_row ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16lo(w[e])), fabsf(bf16hi(w[e]))));
+          for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16lo(x[e])), fabsf(bf16hi(x[e]))));
         }
+        // its largest magnitude goes to [2^14, 2^15); a negative scale goes
+        // into the row, so that f is not
         const int ex = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
-        // a negative scale goes into the row, so that f is not
-        const float up = copysignf(__uint_as_float((uint32_t)(127 + 8 - ex) << 23), p.scale_log2);
-        f = __uint_as_float((uint32_t)(max(127 - 8 + ex, 1)) << 23) * fabsf(p.scale_log2);
-#pragma unroll
+        const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), p.scale_log2);
+        f = __uint_as_float((uint32_t)(127 - 14 + ex) << 23) * fabsf(p.scale_log2) * 0x1p24f;
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = live_row ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
           auto two = [&](uint32_t a, uint32_t b, bool hi) {
-            return half2_bits(__floats2half2_rn((hi ? bf16hi(a) : bf16lo(a)) * up, (hi ? bf16hi(b) : bf16lo(b)) * up));
+            const __half2 h = __floats2half2_rn((hi ? bf16hi(a) : bf16lo(a)) * up, (hi ? bf16hi(b) : bf16lo(b)) * up);
+            sum += __low2float(h) + __high2float(h);
+            return half2_bits(h);
           };
           // channels in the keys' order: 0 2 1 3 of every four
           *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (128 * 128) + sw128_off(r, c & 7)) =
-              make_uint4(two(v[c].x, v[c].y, false), two(v[c].x, v[c].y, true), two(v[c].z, v[c].w, false),
-                         two(v[c].z, v[c].w, true));
+              make_uint4(two(v.x, v.y, false), two(v.x, v.y, true), two(v.z, v.w, false), two(v.z, v.w, true));
         }
+        off = sum * 0x1p-17f;  // 128 * 2^-24
         fence_async_smem();
         named_barrier(2 + X);
         if ((warp & 3) == 0) {
@@ -333,10 +357,9 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
           }
           tmem_st_wait();
         }
-        // a score's factor; never 0, so that -inf stays what it is
-        auto factor = [&](int run) { return fmaxf(f * S.sc_k[slot][run], 1e-30f); };
-        if (__any_sync(~0u, M == -INFINITY)) {
-          // ---- a first unit: the row's maximum of score + log2 vs
+        // Scores are S a + log2 vs - off a, a >= 1e-30 so that -inf stays what
+        // it is.
+        if (__any_sync(~0u, M == -INFINITY)) {  // a first unit: the row's maximum
           float top = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -349,7 +372,8 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
               float mx = -INFINITY;
 #pragma unroll
               for (int i = 16 * h2; i < 16 * h2 + 16; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
-              top = fmaxf(top, fmaf(mx, factor(2 * c + h2), S.sc_log[slot][2 * c + h2]));
+              const float a = fmaxf(f * S.sc_k[slot][2 * c + h2], 1e-30f);
+              top = fmaxf(top, fmaf(mx, a, fmaf(-off, a, S.sc_log[slot][2 * c + h2])));
             }
           }
           if (M == -INFINITY) M = top;  // nothing summed yet: nothing to rescale
@@ -357,31 +381,33 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         // ---- the weights against the maximum so far; again, with the sums
         // rescaled, if a row's outgrow 2^GROWTH (twice at most: scores beyond
         // 2^24, whose units are above 1, may leave more than that)
-        uint32_t w[2][32];
+        uint32_t w[4][16];
         float add;
         for (int again = 0;; ++again) {
           const float at = M == -INFINITY ? 0.f : M;
           float most = -INFINITY;
           add = 0.f;
-          uint32_t v[2][32];
-          tmem_ld32(s_addr, v[0]);
+          uint32_t vb[2][32];
+          tmem_ld32(s_addr, vb[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
+            uint32_t(&v)[32] = vb[c & 1];
             tmem_ld_wait();
-            ld32_fence(v[c & 1]);
-            if (c < 3) tmem_ld32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
+            ld32_fence(v);
+            if (c < 3) tmem_ld32(s_addr + 32 * (c + 1), vb[(c + 1) & 1]);
 #pragma unroll
             for (int h2 = 0; h2 < 2; ++h2) {
-              const float a = factor(2 * c + h2), b = S.sc_log[slot][2 * c + h2] - at;
+              const float a = fmaxf(f * S.sc_k[slot][2 * c + h2], 1e-30f);
+              const float b = fmaf(-off, a, S.sc_log[slot][2 * c + h2] - at);
               float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
               for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
-                float2 z = fma2(make_float2(__uint_as_float(v[c & 1][i]), __uint_as_float(v[c & 1][i + 1])), make_float2(a, a),
+                float2 z = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), make_float2(a, a),
                                 make_float2(b, b));
                 most = fmaxf(fmaxf(most, z.x), z.y);
                 z = make_float2(ex2(z.x), ex2(z.y));
                 sum = add2(sum, z);
-                w[c >> 1][16 * (c & 1) + (i >> 1)] = half2_bits(__float22half2_rn(z));
+                w[c][i >> 1] = half2_bits(__float22half2_rn(z));
               }
               add = fmaf(sum.x + sum.y, S.sc_inv[slot][2 * c + h2], add);
             }
@@ -393,18 +419,19 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
           if (u > P.u0) {
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-              tmem_ld32(o_addr + 32 * c, v[0]);
+              uint32_t v[32];
+              tmem_ld32(o_addr + 32 * c, v);
               tmem_ld_wait();
-              ld32_fence(v[0]);
+              ld32_fence(v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * drop);
-              tmem_st<32>(o_addr + 32 * c, v[0]);
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * drop);
+              tmem_st<32>(o_addr + 32 * c, v);
             }
           }
         }
         l += add;
-        tmem_st<32>(s_addr, w[0]);
-        tmem_st<32>(s_addr + 32, w[1]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_st<16>(s_addr + 16 * c, w[c]);
         tmem_st_wait();
         tc_fence_before();
         named_barrier(2 + X);  // every row's weights are there
@@ -432,9 +459,9 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       if (!(ok = wait_warp(&S.o_full[X], pieces & 1, 53))) break;
       ++pieces;
       tc_fence_after();
-      const int c0 = cta_of(wk, P.item), c1 = cta_of(wk, P.item + P.n[X] - 1);
+      const int c0 = cta_of(S.work, P.item), c1 = cta_of(S.work, P.item + P.n[X] - 1);
       const int cta = blockIdx.x;
-      uint16_t* dst = p.out + ((size_t)(P.q.row + qi) * p.hq + head) * D;
+      uint16_t* dst = p.out + ((size_t)(P.row + qi) * p.hq + head) * D;
       if (c0 == c1) {
         const float k = l == 0.f ? 0.f : ref / l;
 #pragma unroll
@@ -508,150 +535,132 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       mbar_wait(&S.drain[X], 0, &never, WAIT_NS);
     }
   } else {
-    // ---------------------------------------------------------- conversion
-    const int w = warp - W_CVT, ct = tid - 32 * W_CVT;
-    constexpr int NK = D / 16;  // 16-byte pieces of keys a thread converts
+    // ------------------------------------------------------ keys and values
+    // A thread copies and converts the same pieces of 16 codes, one unit
+    // ahead, through its own places in `raw`.
+    const int w = warp & 3, ct = tid & 127;
     // keys: tokens 32 w + 8 (i & 3) + lane % 8, piece lane / 8 + 4 (i >> 2);
-    // values: tokens 8 vo .. 8 vo + 7, piece vc
+    // values: tokens 8 vo + i, piece vc
+    constexpr int NK = D / 16;
     const int vo = D == 128 ? (lane & 7) + 8 * (w >> 1) : (lane & 7) + 8 * (w & 1);
     const int vc = D == 128 ? (lane >> 3) + 4 * (w & 1) : lane >> 3;
     const bool has_v = D == 128 || w < 2;
     const int64_t page_bytes = (int64_t)hkv * p.c.block * D, vstep = p.c.n_pages * page_bytes;
-    struct Tile {
-      int s, h, u, seen;
-      bool first, any;
-    };
-    Piece cur;
-    cur.u0 = cur.u1 = 0;
-    int cu = 0;
-    auto next_tile = [&](Tile& t) {
-      t.any = true;
-      t.first = false;
-      if (cu >= cur.u1) {
-        if (!walk.next(cur)) {
-          t.any = false;
-          return;
-        }
-        cu = cur.u0;
-        t.first = true;
-      }
-      t.s = cur.s, t.h = cur.h, t.u = cu++;
-      t.seen = cur.seen;
-    };
-    auto page_id = [&](const Tile& t, int pos) {
-      if (!t.any || pos >= t.seen) return -1;
-      const int page = __ldg(p.c.table + (size_t)t.s * p.c.max_blocks + (pos >> p.block_log2));
-      if (page >= 0 && page < p.c.n_pages) return page;
-      raise_flag(p.st, FLAG_BAD_CACHE);
-      return -1;
-    };
-    // run lane % 8 of a unit
-    auto pages_of = [&](const Tile& t) { return page_id(t, t.u * UNIT + 16 * (lane & 7)); };
-    // where run `run` of a unit starts in its page
-    auto run_at = [&](const Tile& t, int page, int run) {
-      return p.c.codes + page * page_bytes + (t.h * p.c.block + ((t.u * UNIT + 16 * run) & (p.c.block - 1))) * D;
-    };
-    // Pieces wait in shared memory, each read by the thread that copied it:
-    // keys' piece i at (i * 128 + ct) * 16, values' likewise behind them.
     unsigned char* raw_k = raw + ct * 16;
     unsigned char* raw_v = raw + UNIT * D + (D == 128 ? ct : ct & 63) * 16;
-    constexpr int V_STEP = D == 128 ? 2048 : 1024;
+    constexpr int K_STEP = 2048, V_STEP = D == 128 ? 2048 : 1024;
     const int k_lane = (lane & 7) * D + 16 * (lane >> 3), v_lane = (vo & 1) * 8 * D + 16 * vc;
-    auto load_k = [&](const Tile& t, int pages) {
-      if (t.any)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {  // the warp's two runs
-          const int page = __shfl_sync(~0u, pages, 2 * w + e);
-          const int8_t* src = run_at(t, max(page, 0), 2 * w + e) + k_lane;
-#pragma unroll
-          for (int c = 0; c < NK / 4; ++c)
-#pragma unroll
-            for (int o = 0; o < 2; ++o) cp_async16(raw_k + (4 * c + 2 * e + o) * 2048, src + 8 * o * D + 64 * c);
-        }
-      cp_async_commit();
-    };
-    auto load_v = [&](const Tile& t, int pages) {
-      if (t.any) {
-        const int page = __shfl_sync(~0u, pages, vo >> 1);
-        const int8_t* src = run_at(t, max(page, 0), vo >> 1) + vstep + v_lane;
-        if (has_v)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) cp_async16(raw_v + i * V_STEP, src + i * D);
-      }
-      cp_async_commit();
-    };
-    // where this thread's pieces go: keys in row lane % 8 of an 8-row group,
-    // 16-byte chunks 2 c and 2 c + 1; values in chunk vo % 8 of their rows
+    // where the pieces go: keys in row lane % 8 of an 8-row group, 16-byte
+    // chunks 2 c and 2 c + 1; values, transposed, in chunk vo % 8 of 16 rows
     const uint32_t k_to[2] = {sw128_off(lane & 7, 2 * (lane >> 3)), sw128_off(lane & 7, 2 * (lane >> 3) + 1)};
-    // scales of run lane % 8; the pages come two units ahead, codes and scales one
-    auto scale_of = [&](const Tile& t, int page, int isv) {
-      return page < 0 ? 0.f : __ldg(p.c.scales + ((size_t)isv * p.c.n_pages + page) * hkv + t.h);
-    };
-    Tile t, n, m;
-    next_tile(t);
-    int pages = pages_of(t);
-    load_k(t, pages);
-    load_v(t, pages);
-    float ks = scale_of(t, pages, 0), vs = scale_of(t, pages, 1);
-    next_tile(n);
-    int next_pages = pages_of(n);
-    next_tile(m);
-    int after_pages = pages_of(m);
-    float vref = 1.f;
+    uint32_t it = 0;
     bool ok = true;
-    for (uint32_t it = 0; t.any; ++it) {
-      const uint32_t st = it & 1, par = ((it >> 1) & 1) ^ 1;
-      if (t.first) {  // the largest value scale of the item
-        float top = 0.f;
-        for (int b = ct; b * p.c.block < t.seen; b += 128) top = fmaxf(top, scale_of(t, page_id(t, b * p.c.block), 1));
+    while (ok && next_piece(p, S.work, S.walk[warp])) {
+      const int32_t* table = p.c.table + (size_t)P.s * p.c.max_blocks;
+      const int8_t* codes = p.c.codes + (int64_t)P.h * p.c.block * D;
+      const float* scales = p.c.scales + P.h;
+      const int seen = P.seen, end = P.u1;
+      auto page_at = [&](int pos) {
+        const int page = __ldg(table + (pos >> p.block_log2));
+        if (page >= 0 && page < p.c.n_pages) return page;
+        raise_flag(p.st, FLAG_BAD_CACHE);
+        return -1;
+      };
+      // page of run lane % 8 of unit u; -1: no token of it is seen
+      auto pages_of = [&](int u) {
+        const int pos = u * UNIT + 16 * (lane & 7);
+        return u < end && pos < seen ? page_at(pos) : -1;
+      };
+      auto scale_of = [&](int page, int64_t isv) {
+        return page < 0 ? 0.f : __ldg(scales + (isv * p.c.n_pages + page) * hkv);
+      };
+      // a run without a page is read from page 0: its weights are 0
+      auto load_k = [&](int u, int pages) {
+        if (u < end)
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        named_barrier(1);  // the last item's values are read
-        if (lane == 0) S.red[w] = top;
-        named_barrier(1);
-        vref = fmaxf(fmaxf(S.red[0], S.red[1]), fmaxf(S.red[2], S.red[3]));  // 0: every value is 0, and so is the result
-      }
-      // the slot's last unit, SC_RING back, is past every softmax thread: the
-      // products that freed this K stage came after its weights
-      const float lg = pages < 0 ? -INFINITY : fmaxf(__log2f(vs / (vref > 0.f ? vref : 1.f)), -60.f);
-      const float inv = pages < 0 ? 0.f : ex2(-lg);
-      if (!(ok = wait_warp(&S.k_empty[st], par, 54))) break;
-      if (w == 0 && lane < 8) {
-        const uint32_t slot = it % SC_RING;
-        S.sc_k[slot][lane] = ks;
-        S.sc_log[slot][lane] = lg;
-        S.sc_inv[slot][lane] = inv;
-        if (lane == 0) S.sc_ref[slot] = vref;
-        __syncwarp(0xFF);
-        mbar_arrive(&S.sc_full[slot]);
-      }
-      {
+          for (int e = 0; e < 2; ++e) {  // the warp's two runs
+            const int page = max(__shfl_sync(~0u, pages, 2 * w + e), 0);
+            const int8_t* src = codes + page * page_bytes + ((u * UNIT + 16 * (2 * w + e)) & (p.c.block - 1)) * D + k_lane;
+#pragma unroll
+            for (int c = 0; c < NK / 4; ++c)
+#pragma unroll
+              for (int o = 0; o < 2; ++o) cp_async16(raw_k + (4 * c + 2 * e + o) * K_STEP, src + 8 * o * D + 64 * c);
+          }
+        cp_async_commit();
+      };
+      auto load_v = [&](int u, int pages) {
+        if (u < end) {
+          const int page = max(__shfl_sync(~0u, pages, vo >> 1), 0);
+          const int8_t* src = codes + vstep + page * page_bytes + ((u * UNIT + 16 * (vo >> 1)) & (p.c.block - 1)) * D + v_lane;
+          if (has_v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) cp_async16(raw_v + i * V_STEP, src + i * D);
+        }
+        cp_async_commit();
+      };
+      // pages come two units ahead, codes and scales one
+      int pages = pages_of(P.u0), next_pages = pages_of(P.u0 + 1);
+      load_k(P.u0, pages);
+      load_v(P.u0, pages);
+      float ks = scale_of(pages, 0), vs = scale_of(pages, 1);
+      // the item's largest value scale; 0 if every value is, and then so is the
+      // result
+      float vref = 0.f;
+      for (int b = ct; b << p.block_log2 < seen; b += 128) vref = fmaxf(vref, scale_of(page_at(b << p.block_log2), 1));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) vref = fmaxf(vref, __shfl_xor_sync(~0u, vref, o));
+      named_barrier(1);  // the last item's values are read
+      if (lane == 0) S.red[w] = vref;
+      named_barrier(1);
+      vref = fmaxf(fmaxf(S.red[0], S.red[1]), fmaxf(S.red[2], S.red[3]));
+      const float vref_log = vref > 0.f ? __log2f(vref) : 0.f;
+      for (int u = P.u0; u < end; ++u, ++it) {
+        const uint32_t st = it & 1, par = ((it >> 1) & 1) ^ 1;
+        if (!(ok = wait_warp(&S.k_empty[st], par, 54))) break;
+        // the slot's last unit, SC_RING back, is past every softmax thread: the
+        // products that freed this K stage came after its weights
+        if (w == 0 && lane < 8) {
+          const uint32_t slot = it % SC_RING;
+          const float lg = pages < 0 ? -INFINITY : fmaxf(__log2f(vs) - vref_log, -60.f);
+          S.sc_k[slot][lane] = ks;
+          S.sc_log[slot][lane] = lg;
+          S.sc_inv[slot][lane] = pages < 0 ? 0.f : ex2(-lg);
+          if (lane == 0) S.sc_ref[slot] = vref;
+          __syncwarp(0xFF);
+          if (lane == 0) mbar_arrive(&S.sc_full[slot]);
+        }
         cp_async_wait<1>();
-        unsigned char* dst = sk + st * Smem<D>::K + 4 * w * 1024;
-#pragma unroll 1
-        for (int i = 0; i < NK; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(raw_k + i * 2048);
-          unsigned char* rows = dst + (i & 3) * 1024 + (i >> 2) * (128 * 128);
-          *reinterpret_cast<uint4*>(rows + k_to[0]) = make_uint4(f16_even(v.x), f16_odd(v.x), f16_even(v.y), f16_odd(v.y));
-          *reinterpret_cast<uint4*>(rows + k_to[1]) = make_uint4(f16_even(v.z), f16_odd(v.z), f16_even(v.w), f16_odd(v.w));
+        {
+          unsigned char* dst = sk + st * Smem<D>::K + 4 * w * 1024;
+#pragma unroll 4
+          for (int i = 0; i < NK; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(raw_k + i * K_STEP);
+            unsigned char* rows = dst + (i & 3) * 1024 + (i >> 2) * (128 * 128);
+            *reinterpret_cast<uint4*>(rows + k_to[0]) =
+                make_uint4(codes_even(v.x), codes_odd(v.x), codes_even(v.y), codes_odd(v.y));
+            *reinterpret_cast<uint4*>(rows + k_to[1]) =
+                make_uint4(codes_even(v.z), codes_odd(v.z), codes_even(v.w), codes_odd(v.w));
+          }
         }
         fence_async_smem();
-        mbar_arrive(&S.k_full[st]);
-      }
-      load_k(n, next_pages);
-      ks = scale_of(n, next_pages, 0);
-      vs = scale_of(n, next_pages, 1);
-      if (!(ok = wait_warp(&S.v_empty[st], par, 55))) break;
-      {
-        unsigned char* dst = sv + st * Smem<D>::V + (vo >> 3) * (D * 128) + 2 * vc * 1024;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.k_full[st]);
+        load_k(u + 1, next_pages);
+        const int after_pages = pages_of(u + 2);
+        if (w == 0) {
+          ks = scale_of(next_pages, 0);
+          vs = scale_of(next_pages, 1);
+        }
+        if (!(ok = wait_warp(&S.v_empty[st], par, 55))) break;
         cp_async_wait<1>();
         if (has_v) {
-#pragma unroll 1
+          unsigned char* dst = sv + st * Smem<D>::V + (vo >> 3) * (D * 128) + 2 * vc * 1024;
+#pragma unroll 2
           for (int q = 0; q < 4; ++q) {
             uint32_t x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint32_t*>(raw_v + i * V_STEP + 4 * q);
-            // channel 4 q + ch of the piece; its row's 8-row group and place in it
+            // channel 4 q + ch of the piece; its 8-row group and its row there
             unsigned char* rows = dst + (q >> 1) * 1024 + (q & 1) * 512;
             auto put = [&](int ch, uint4 v) {
               *reinterpret_cast<uint4*>(rows + ch * 128 + (((vo & 7) ^ (4 * (q & 1) + ch)) << 4)) = v;
@@ -663,22 +672,19 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
           }
         }
         fence_async_smem();
-        mbar_arrive(&S.v_full[st]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.v_full[st]);
+        load_v(u + 1, next_pages);
+        pages = next_pages;
+        next_pages = after_pages;
       }
-      load_v(n, next_pages);
-      t = n;
-      pages = next_pages;
-      n = m;
-      next_pages = after_pages;
-      next_tile(m);
-      after_pages = pages_of(m);
     }
     cp_async_wait<0>();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == W_CVT) tmem_dealloc(tmem, 512);
+  if (warp == W_KEYS) tmem_dealloc(tmem, 512);
 }
 
 template <int D>
