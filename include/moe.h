@@ -612,7 +612,8 @@ int moe_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_
  * the sizes and lengths only, never on timing.
  *
  * q bf16 [t][hq][d], heads contiguous, rows `q_stride` elements apart (a
- * multiple of 8); out bf16 [t][hq][d].  hq a multiple of hkv.  The rows
+ * multiple of 8); out bf16 [t][hq][d].  hq a multiple of hkv, at most
+ * 32768.  The rows
  * of a sequence whose lens or starts are out of range are left unwritten, and
  * a page id out of range hides its block's tokens (a row left without any
  * becomes zero); both raise MOE_EDEVICE in moe_read_device_status.

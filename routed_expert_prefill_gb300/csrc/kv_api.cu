@@ -70,8 +70,8 @@ int moe_kv_attention(const uint16_t* q, int64_t q_stride, const int32_t* starts,
   TRY(check_cache(cache, starts, t, ws, ws_bytes));
   TRY(check_rows(q, q_stride, "q"));
   TRY(check_ptr(out, "out", 16));
-  if (hq < cache->hkv || hq % cache->hkv || hq > 65536)
-    return set_error(MOE_ESHAPE, "hq=%d must be a multiple of hkv=%d", hq, cache->hkv);
+  if (hq < cache->hkv || hq % cache->hkv || hq > 32768)
+    return set_error(MOE_ESHAPE, "hq=%d must be a multiple of hkv=%d, at most 32768", hq, cache->hkv);
   if (!isfinite(scale)) return set_error(MOE_EINVAL, "scale is not finite");
   return cuda_status(launch_kv_attention(q, q_stride, starts, t, hq, scale, *cache, out, (unsigned char*)ws,
                                          (cudaStream_t)stream),

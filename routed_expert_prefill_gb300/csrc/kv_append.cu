@@ -19,6 +19,18 @@ __device__ __forceinline__ uint4 finite_vec(uint4 u, bool& bad) {
   return make_uint4(finite_pair(u.x, bad), finite_pair(u.y, bad), finite_pair(u.z, bad), finite_pair(u.w, bad));
 }
 
+// v * 127 / m to the nearest whole number, ties to even, exactly: with an
+// approximate quotient rounded to q, the remainder x - q m is exact in one
+// fma (q and the bf16 m have 7 and 8 bits), and it says whether q is the
+// nearest.  rm = 1 / m.  A true division costs about twice the instructions.
+__device__ __forceinline__ int nearest_code(float v, float m, float rm) {
+  const float x = v * 127.f;
+  const float q = rintf(x * rm);
+  const float r = fmaf(-q, m, x), over = fabsf(r) + fabsf(r) - m;
+  const int c = (int)q;
+  return over > 0.f || (over == 0.f && (c & 1)) ? c + (r > 0.f ? 1 : -1) : c;
+}
+
 // One CTA per (touched block, head, keys or values): the block's values stay
 // in registers (VPT 16-byte vectors a thread) between the maximum and the
 // codes, so every token is read once and every code written once; the bytes
@@ -30,16 +42,21 @@ __global__ void __launch_bounds__(APPEND_THREADS)
     kv_append_kernel(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* starts,
                      int t, moe_kv_cache c, DeviceStatus* st) {
   __shared__ float part[APPEND_THREADS / 32];
+  __shared__ int owner;
   pdl_wait();
   pdl_trigger();
   const int slot = blockIdx.x, head = blockIdx.y, isv = blockIdx.z, tid = threadIdx.x;
-  // the sequence that owns the slot
-  int lo = 0, hi = c.n_seq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (starts[mid] / c.block + 2 * mid <= slot) lo = mid; else hi = mid - 1;
+  // the sequence that owns the slot: every thread looks at some, one answers
+  if (tid == 0) owner = -1;
+  __syncthreads();
+  for (int i = tid; i < c.n_seq; i += APPEND_THREADS)
+    if (starts[i] / c.block + 2 * i <= slot && slot < starts[i + 1] / c.block + 2 * (i + 1)) owner = i;
+  __syncthreads();
+  const int s = owner;
+  if (s < 0) {  // past the last sequence, or starts out of order
+    if (tid == 0 && slot < starts[c.n_seq] / c.block + 2 * c.n_seq) raise_flag(st, FLAG_BAD_CACHE);
+    return;
   }
-  const int s = lo;
   int row0, n, len;
   if (!kv_sequence(c, starts, t, s, row0, n, len)) {
     if (tid == 0) raise_flag(st, FLAG_BAD_CACHE);
@@ -49,6 +66,7 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   const int old = len - n, first = old / c.block, last = (len - 1) / c.block;
   const int b = first + slot - (row0 / c.block + 2 * s);
   if (b < first || b > last) return;
+  const int page = c.table[(size_t)s * c.max_blocks + b];
   const uint16_t* src = isv ? v : k;
   const int64_t stride = isv ? v_stride : k_stride;
   const int ring = 2 * c.block;
@@ -80,13 +98,14 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   __syncthreads();  // also: what this block reads of the tail is in registers
 #pragma unroll
   for (int i = 0; i < APPEND_THREADS / 32; ++i) m = fmaxf(m, part[i]);
-  const int page = c.table[(size_t)s * c.max_blocks + b];
   if (page < 0 || page >= c.n_pages) {
     if (tid == 0) raise_flag(st, FLAG_BAD_CACHE);
   } else {
     const size_t blk = ((size_t)isv * c.n_pages + page) * c.hkv + head;
     if (tid == 0) c.scales[blk] = m / 127.f;
     int8_t* out = c.codes + blk * c.block * c.d;
+    // a maximum whose reciprocal is not a normal number is scaled up first
+    const float up = m < 0x1p-100f ? 0x1p100f : 1.f, mu = m * up, rm = 1.f / mu;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int e = tid + i * APPEND_THREADS;
@@ -97,21 +116,37 @@ __global__ void __launch_bounds__(APPEND_THREADS)
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const float f = q & 1 ? bf16hi(w[q >> 1]) : bf16lo(w[q >> 1]);
-          o[q >> 2] |= (uint32_t)(uint8_t)(int8_t)__float2int_rn(f * 127.f / m) << (8 * (q & 3));
+          o[q >> 2] |= (uint32_t)(uint8_t)(int8_t)nearest_code(f * up, mu, rm) << (8 * (q & 3));
         }
       *reinterpret_cast<uint2*>(out + (size_t)e * 8) = make_uint2(o[0], o[1]);
     }
   }
-  // The CTA of the first touched block, the only one that reads the tail,
-  // writes the new tokens of the last two blocks to it.
-  if (b == first) {
-    const int from = max(old, (last - 1) * c.block);
-    bool again = false;
-    for (int e = tid; e < (len - from) * vd; e += APPEND_THREADS) {
-      const int pos = from + e / vd, x = e % vd;
-      const uint4 w = finite_vec(*reinterpret_cast<const uint4*>(src + (size_t)(row0 + pos - old) * stride +
-                                                                (size_t)head * c.d + 8 * x), again);
-      *reinterpret_cast<uint4*>(tail + (size_t)(pos % ring) * c.d + 8 * x) = w;
+  // The new tokens of the last two blocks go to the tail.  Only the first
+  // touched block's CTA reads the tail, in that block's half of the ring, so a
+  // block in the other half, and the first itself, is written from here; one
+  // in the same half waits for the first block's CTA, which copies it.
+  if (b >= last - 1 && (b == first || ((b - first) & 1))) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int e = tid + i * APPEND_THREADS, r = e / vd, x = e % vd, pos = b * c.block + r;
+      if (e < nv && pos >= old && pos < len) *reinterpret_cast<uint4*>(tail + (size_t)(pos % ring) * c.d + 8 * x) = u[i];
+    }
+  }
+  const int other = (last - first) & 1 ? last - 1 : last;
+  if (b == first && other > first) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int e = tid + i * APPEND_THREADS, pos = other * c.block + e / vd;
+      u[i] = make_uint4(0, 0, 0, 0);
+      if (e < nv && pos < len)
+        u[i] = *reinterpret_cast<const uint4*>(src + (size_t)(row0 + pos - old) * stride + (size_t)head * c.d + 8 * (e % vd));
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int e = tid + i * APPEND_THREADS, pos = other * c.block + e / vd;
+      bool again = false;
+      if (e < nv && pos < len)
+        *reinterpret_cast<uint4*>(tail + (size_t)(pos % ring) * c.d + 8 * (e % vd)) = finite_vec(u[i], again);
     }
   }
 }

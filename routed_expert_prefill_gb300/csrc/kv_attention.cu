@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
 
   Work wk;
   if (!find_work<ROWS, AT_THREADS>(p, scan, wk)) return;
-  const int64_t total = wk.total, ctas = wk.ctas, x1 = wk.x1;
+  const int64_t x1 = wk.x1;
   const int cta = blockIdx.x;
   int s = wk.s, qt = wk.qt, h = wk.h, u0 = wk.u;
   Seq q = load_seq(p, s);
@@ -119,56 +119,24 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
   while (x < x1) {
     const int units = tile_units<ROWS>(p, q, qt), seen = tile_seen<ROWS>(p, q, qt);
     const int u1 = (int)min((int64_t)units, u0 + (x1 - x));
-    const int rows = (int)min((int64_t)q.n * p.G - (int64_t)qt * ROWS, (int64_t)ROWS);
-    // ---- query fragments, each row scaled by a power of two into fp16
-    uint32_t qb[NT][KL * 4][2];
-    float F[NT][2], off_q[NT][2];  // of rows 2 j, 2 j + 1: score per product, 128 2^-24 times the row's sum
-    int limit[NT][2];              // last position seen
-    int all_see = INT_MAX;
+    const int rows = (int)min(seq_rows(p, q) - (uint32_t)qt * ROWS, (uint32_t)ROWS);
+    // The loads that wait for one another come first: the rows of q beside the
+    // pages, then codes and scales by the pages, and the arithmetic on q last.
+    uint2 q_raw[NT][KL * 4];
+    int q_token[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int r = 8 * t + g;
-      const int64_t rr = (int64_t)qt * ROWS + r;
-      const int i = (int)(rr / p.G), head = h * p.G + (int)(rr % p.G);
-      uint2 raw[KL * 4];
-      float m = 0.f, sum = 0.f;
+      const uint32_t rr = (uint32_t)qt * ROWS + 8 * t + g;
+      const int i = (int)(rr / (uint32_t)p.G), head = h * p.G + (int)(rr % (uint32_t)p.G);
+      q_token[t] = i;
 #pragma unroll
       for (int w = 0; w < KL * 4; ++w) {
-        raw[w] = make_uint2(0, 0);
-        if (r < rows)
-          raw[w] = *reinterpret_cast<const uint2*>(p.q + (int64_t)(q.row + i) * p.q_stride + (size_t)head * D +
-                                                   64 * (w >> 2) + 16 * j + 4 * (w & 3));
-        m = fmaxf(m, fmaxf(fmaxf(fabsf(bf16lo(raw[w].x)), fabsf(bf16hi(raw[w].x))),
-                           fmaxf(fabsf(bf16lo(raw[w].y)), fabsf(bf16hi(raw[w].y)))));
-      }
-      m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-      // the row's largest magnitude goes to [256, 512)
-      const int ex = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
-      const float up = __uint_as_float((uint32_t)(127 + 8 - ex) << 23);
-#pragma unroll
-      for (int w = 0; w < KL * 4; ++w) {
-        // with the keys' bytes 0 and 2, then 1 and 3
-        const __half2 a = __floats2half2_rn(bf16lo(raw[w].x) * up, bf16lo(raw[w].y) * up);
-        const __half2 b = __floats2half2_rn(bf16hi(raw[w].x) * up, bf16hi(raw[w].y) * up);
-        qb[t][w][0] = half2_bits(a);
-        qb[t][w][1] = half2_bits(b);
-        sum += (__low2float(a) + __high2float(a)) + (__low2float(b) + __high2float(b));
-      }
-      sum += __shfl_xor_sync(~0u, sum, 1);
-      sum += __shfl_xor_sync(~0u, sum, 2);
-      const float f = __uint_as_float((uint32_t)(max(127 - 8 + ex, 1)) << 23) * p.scale_log2 * 0x1p24f;
-      // rows past the last: nothing of theirs is stored, so they may see all
-      const int lim = r < rows ? q.len - q.n + i : INT_MAX;
-      all_see = min(all_see, lim);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        F[t][c] = __shfl_sync(~0u, f, 4 * (2 * j + c));
-        off_q[t][c] = __shfl_sync(~0u, sum, 4 * (2 * j + c)) * 0x1p-17f;
-        limit[t][c] = __shfl_sync(~0u, lim, 4 * (2 * j + c));
+        q_raw[t][w] = make_uint2(0, 0);
+        if (8 * t + g < rows)
+          q_raw[t][w] = *reinterpret_cast<const uint2*>(p.q + (int64_t)(q.row + i) * p.q_stride + (size_t)head * D +
+                                                        64 * (w >> 2) + 16 * j + 4 * (w & 3));
       }
     }
-    all_see = __reduce_min_sync(~0u, all_see);
     float m[NT][2], M[NT][2], l[NT][2], o[NT][NO][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -200,7 +168,7 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
     };
     int chunk_now = 0;
     int page = page_of(0), next_page = page_of(1);
-    float kscale = scale_of(page, 0), vscale = scale_of(page, 1), next_k = 0.f, next_v = 0.f;
+    float kscale, vscale, next_k = 0.f, next_v = 0.f;
     auto issue = [&](int step) {
       if (step < steps) {
         unsigned char* dst = ring + (step % STAGES) * STAGE;
@@ -222,6 +190,52 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
     };
 #pragma unroll
     for (int i = 0; i < (STAGES > 2 ? STAGES - 1 : 2); ++i) issue(i);
+    kscale = scale_of(page, 0), vscale = scale_of(page, 1);
+
+    // ---- query fragments, each row scaled by a power of two into fp16
+    uint32_t qb[NT][KL * 4][2];
+    float F[NT][2], off_q[NT][2];  // of rows 2 j, 2 j + 1: score per product, 128 2^-24 times the row's sum
+    int limit[NT][2];              // last position seen
+    int all_see = INT_MAX;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = 8 * t + g;
+      const int i = q_token[t];
+      const uint2(&raw)[KL * 4] = q_raw[t];
+      float m = 0.f, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < KL * 4; ++w) {
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(bf16lo(raw[w].x)), fabsf(bf16hi(raw[w].x))),
+                           fmaxf(fabsf(bf16lo(raw[w].y)), fabsf(bf16hi(raw[w].y)))));
+      }
+      m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+      // the row's largest magnitude goes to [256, 512)
+      const int ex = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
+      const float up = __uint_as_float((uint32_t)(127 + 8 - ex) << 23);
+#pragma unroll
+      for (int w = 0; w < KL * 4; ++w) {
+        // with the keys' bytes 0 and 2, then 1 and 3
+        const __half2 a = __floats2half2_rn(bf16lo(raw[w].x) * up, bf16lo(raw[w].y) * up);
+        const __half2 b = __floats2half2_rn(bf16hi(raw[w].x) * up, bf16hi(raw[w].y) * up);
+        qb[t][w][0] = half2_bits(a);
+        qb[t][w][1] = half2_bits(b);
+        sum += (__low2float(a) + __high2float(a)) + (__low2float(b) + __high2float(b));
+      }
+      sum += __shfl_xor_sync(~0u, sum, 1);
+      sum += __shfl_xor_sync(~0u, sum, 2);
+      const float f = __uint_as_float((uint32_t)(max(127 - 8 + ex, 1)) << 23) * p.scale_log2 * 0x1p24f;
+      // rows past the last: nothing of theirs is stored, so they may see all
+      const int lim = r < rows ? q.len - q.n + i : INT_MAX;
+      all_see = min(all_see, lim);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        F[t][c] = __shfl_sync(~0u, f, 4 * (2 * j + c));
+        off_q[t][c] = __shfl_sync(~0u, sum, 4 * (2 * j + c)) * 0x1p-17f;
+        limit[t][c] = __shfl_sync(~0u, lim, 4 * (2 * j + c));
+      }
+    }
+    all_see = __reduce_min_sync(~0u, all_see);
 
     for (int i = 0; i < steps; ++i) {
       if ((i & 15) == 0 && i) {  // the next chunk's runs
@@ -405,7 +419,7 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
       acc[i] = osum[0][r][d0 + i] + osum[1][r][d0 + i] + osum[2][r][d0 + i] + osum[3][r][d0 + i];
 
     const int64_t item = x - u0;  // the item's first step
-    const int c0 = (int)(((item + 1) * ctas - 1) / total), c1 = (int)(((item + units) * ctas - 1) / total);
+    const int c0 = cta_of(wk, item), c1 = cta_of(wk, item + units - 1);
     bool write = true;
     if (c0 != c1) {
       const size_t pf = kv_partial_floats(D);
@@ -457,8 +471,8 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
       // sum p vs v = 2^(M - m) of what was accumulated; nothing seen, or all
       // values zero: 0
       const float k = cl == 0.f ? 0.f : (cM == -INFINITY ? 0.f : exp2f(cM - cm)) / cl;
-      const int64_t rr = (int64_t)qt * ROWS + r;
-      uint16_t* dst = p.out + ((size_t)(q.row + rr / p.G) * p.hq + (size_t)h * p.G + rr % p.G) * D + d0;
+      const uint32_t rr = (uint32_t)qt * ROWS + r;
+      uint16_t* dst = p.out + ((size_t)(q.row + rr / (uint32_t)p.G) * p.hq + (size_t)h * p.G + rr % (uint32_t)p.G) * D + d0;
 #pragma unroll
       for (int i = 0; i < DPT; i += 4)
         *reinterpret_cast<uint2*>(dst + i) = make_uint2(pack_bf16x2(acc[i] * k, acc[i + 1] * k),

@@ -49,15 +49,18 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int s) {
   if (!q.ok) q.n = 0;
   return q;
 }
+// Rows of a sequence's new tokens: below 2^32 (t <= 65536, hq < 65536).
+__device__ __forceinline__ uint32_t seq_rows(const AttnParams& p, const Seq& q) { return (uint32_t)q.n * p.G; }
+
 template <int ROWS>
 __device__ __forceinline__ int q_tiles(const AttnParams& p, const Seq& q) {
-  return (int)(((int64_t)q.n * p.G + ROWS - 1) / ROWS);
+  return (int)((seq_rows(p, q) + (uint64_t)(ROWS - 1)) / ROWS);
 }
 // Positions that the rows of query tile qt see, and its units.
 template <int ROWS>
 __device__ __forceinline__ int tile_seen(const AttnParams& p, const Seq& q, int qt) {
-  const int64_t rows = min((int64_t)q.n * p.G, (int64_t)ROWS * (qt + 1));
-  return q.len - q.n + (int)((rows - 1) / p.G) + 1;
+  const uint32_t rows = (uint32_t)min((uint64_t)seq_rows(p, q), (uint64_t)ROWS * (qt + 1));
+  return q.len - q.n + (int)((rows - 1) / (uint32_t)p.G) + 1;
 }
 template <int ROWS>
 __device__ __forceinline__ int tile_units(const AttnParams& p, const Seq& q, int qt) {
@@ -79,8 +82,19 @@ struct Work {
   int s, qt, h, u;
 };
 
-// The CTA that takes unit x.
-__device__ __forceinline__ int cta_of(const Work& w, int64_t x) { return (int)(((x + 1) * w.ctas - 1) / w.total); }
+// a * b / c, in 32 bits where they hold the product: a 64-bit division takes
+// some hundred instructions, and a CTA needs several before its first load.
+__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
+  if (((a | b) >> 16) == 0 && (c >> 32) == 0) return (uint32_t)a * (uint32_t)b / (uint32_t)c;
+  return a * b / c;
+}
+
+// The CTA that takes unit x: the last c with total * c / ctas <= x.
+__device__ __forceinline__ int cta_of(const Work& w, int64_t x) {
+  if (((x + 1) | w.total) >> 20 == 0 && w.ctas < 4096)
+    return (int)(((uint32_t)(x + 1) * (uint32_t)w.ctas - 1) / (uint32_t)w.total);
+  return (int)(((x + 1) * w.ctas - 1) / w.total);
+}
 
 // Called by all THREADS threads; scratch: THREADS / 32 + 2 values in shared
 // memory.  False where the CTA has nothing to do.
@@ -105,8 +119,8 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, int64_t* scratch,
   wk.total = total;
   wk.ctas = min((int64_t)gridDim.x, total);
   if (blockIdx.x >= wk.ctas) return false;
-  wk.x0 = total * blockIdx.x / wk.ctas;
-  wk.x1 = total * (blockIdx.x + 1) / wk.ctas;
+  wk.x0 = mul_div(total, blockIdx.x, wk.ctas);
+  wk.x1 = mul_div(total, blockIdx.x + 1, wk.ctas);
   int64_t base = 0;
   for (int sb = 0; sb < p.c.n_seq; sb += THREADS) {
     int64_t w = w0;
@@ -141,8 +155,12 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, int64_t* scratch,
   for (wk.qt = 0;; ++wk.qt) {
     const int units = tile_units<ROWS>(p, q, wk.qt);
     if (off < (int64_t)units * p.c.hkv) {
-      wk.h = (int)(off / units);
-      wk.u = (int)(off % units);
+      if (off >> 31) {
+        wk.h = (int)(off / units);
+      } else {
+        wk.h = (int)((uint32_t)off / (uint32_t)units);
+      }
+      wk.u = (int)(off - (int64_t)wk.h * units);
       return true;
     }
     off -= (int64_t)units * p.c.hkv;

@@ -19,7 +19,6 @@ allocated for that stream.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import NamedTuple
@@ -38,13 +37,13 @@ _BF = torch.bfloat16
 _current_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: no Stream object is made
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _alloc_on(stream):
-    """Allocations made inside belong to `stream`, so that the memory is not
-    handed out again before its work is done."""
-    return _HERE if stream is None else torch.cuda.stream(stream)
+def _empty(shape, dtype, like, stream):
+    """A tensor beside `like` that belongs to `stream`, so that its memory is
+    not handed out again before that stream's work is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _raw(stream, dev: int) -> int:
@@ -123,17 +122,16 @@ def moe_add_rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tenso
     if want_y is None:
         want_y = not quantize
     y = codes = scales = None
-    with _alloc_on(stream):
-        if sum_out is None and residual is not None:
-            sum_out = torch.empty(shape, dtype=_BF, device=x.device)
-        if want_y:
-            y = torch.empty(shape, dtype=_BF, device=x.device)
-        if quantize:
-            codes = torch.empty(shape, dtype=torch.int8, device=x.device)
-            scales = torch.empty((t, h // GROUP), dtype=torch.float32, device=x.device)
+    if sum_out is None and residual is not None:
+        sum_out = _empty(shape, _BF, x, stream)
+    if want_y:
+        y = _empty(shape, _BF, x, stream)
+    if quantize:
+        codes = _empty(shape, torch.int8, x, stream)
+        scales = _empty((t, h // GROUP), torch.float32, x, stream)
     status = lib.moe_add_rms_norm(
-        x.data_ptr(), _row_stride(x), None if residual is None else residual.data_ptr(),
-        0 if residual is None else _row_stride(residual), gamma.data_ptr(), eps, t, h,
+        x.data_ptr(), x.stride(0) if t > 1 else 0, None if residual is None else residual.data_ptr(),
+        0 if residual is None or t == 1 else residual.stride(0), gamma.data_ptr(), eps, t, h,
         None if sum_out is None else sum_out.data_ptr(), None if y is None else y.data_ptr(),
         None if codes is None else codes.data_ptr(), None if scales is None else scales.data_ptr(), _raw(stream, dev))
     if status:
@@ -188,8 +186,7 @@ def moe_qmv(x, weights: tuple, out: torch.Tensor | None = None, out_dtype: torch
             raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
         _on_current_device(x=rows, x_codes=xc, x_scales=xs, codes=codes, scales=scales, biases=biases, out=out)
     if out is None:
-        with _alloc_on(stream):
-            out = torch.empty((t, n), dtype=out_dtype, device=codes.device)
+        out = _empty((t, n), out_dtype, codes, stream)
     w = MoeQWeights(codes.data_ptr(), scales.data_ptr(), biases.data_ptr())
     status = lib.moe_qmv(
         None if rows is None else rows.data_ptr(), 0 if rows is None else _row_stride(rows),
@@ -301,8 +298,7 @@ def moe_kv_attention(q: torch.Tensor, starts: torch.Tensor, cache: KvCache, scal
             _need(out, "out", _BF16, shape=(t, hq, d))
         _on_current_device(q=q, starts=starts, out=out, codes=cache.codes)
     if out is None:
-        with _alloc_on(stream):
-            out = torch.empty(shape, dtype=_BF, device=q.device)
+        out = _empty(shape, _BF, q, stream)
     status = lib.moe_kv_attention(q.data_ptr(), _row_stride(q), starts.data_ptr(), t, hq,
                                   cache._scale if scale is None else scale, cache._ref, out.data_ptr(), *cache._ws,
                                   _raw(stream, dev))
