@@ -422,47 +422,93 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
     const int c0 = cta_of(wk, item), c1 = cta_of(wk, item + units - 1);
     bool write = true;
     if (c0 != c1) {
+      // A part per CTA, joined JOIN at a time: the last CTA of a group to
+      // finish joins its parts into the group's first, the last group the
+      // item.  (By one CTA at once, an item cut into 256 parts took 55 us of
+      // 64 for that.)  The order of the sums is that of the CTAs.
+      constexpr int JOIN = 16;
       const size_t pf = kv_partial_floats(D);
-      float* mine = p.partials + (size_t)(2 * cta + (cta == c0)) * pf;
-      if (r < rows) {
+      auto part_of = [&](int c) { return p.partials + (size_t)(2 * c + (c == c0)) * pf; };
+      auto put = [&](float* to) {
+        if (r < rows) {
 #pragma unroll
-        for (int i = 0; i < DPT; ++i) mine[r * D + d0 + i] = acc[i];
-        if (tid % TPR == 0) {
-          float* sp = mine + ROWS * D + 4 * r;
-          sp[0] = cm, sp[1] = cM, sp[2] = cl;
+          for (int i = 0; i < DPT; i += 4)
+            *reinterpret_cast<float4*>(to + r * D + d0 + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+          if (tid % TPR == 0) *reinterpret_cast<float4*>(to + ROWS * D + 4 * r) = make_float4(cm, cM, cl, 0.f);
         }
-      }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) arrived = atomicAdd(p.counters + c0, 1u);
-      __syncthreads();
-      write = arrived == (uint32_t)(c1 - c0);
-      if (write) {
+      };
+      // true in the CTA that comes last of `all`
+      auto last_of = [&](uint32_t* counter, int all) {
         __threadfence();
-        if (tid == 0) p.counters[c0] = 0;
+        __syncthreads();
+        if (tid == 0) arrived = atomicAdd(counter, 1u);
+        __syncthreads();
+        if (arrived != (uint32_t)(all - 1)) return false;
+        if (tid == 0) *counter = 0;
+        __threadfence();
+        return true;
+      };
+      // parts from, from + step, ... up to `to` into acc, cm, cM, cl
+      auto join = [&](int from, int to, int step) {
         cm = cM = -INFINITY;
         cl = 0.f;
 #pragma unroll
         for (int i = 0; i < DPT; ++i) acc[i] = 0.f;
-        if (r < rows) {
-          for (int c = c0; c <= c1; ++c) {
-            const float* sp = p.partials + (size_t)(2 * c + (c == c0)) * pf + ROWS * D + 4 * r;
-            cm = fmaxf(cm, __ldcg(sp));
-            cM = fmaxf(cM, __ldcg(sp + 1));
-          }
-          for (int c = c0; c <= c1; ++c) {
-            const float* part = p.partials + (size_t)(2 * c + (c == c0)) * pf;
-            const float* sp = part + ROWS * D + 4 * r;
-            cl += __ldcg(sp + 2) * ex2(__ldcg(sp) - (cm == -INFINITY ? 0.f : cm));
-            const float drop = ex2(__ldcg(sp + 1) - (cM == -INFINITY ? 0.f : cM));
+        if (r >= rows) return;
+        float4 st[JOIN];
 #pragma unroll
-            for (int i = 0; i < DPT; i += 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(part + r * D + d0 + i));
-              acc[i] = fmaf(v.x, drop, acc[i]);
-              acc[i + 1] = fmaf(v.y, drop, acc[i + 1]);
-              acc[i + 2] = fmaf(v.z, drop, acc[i + 2]);
-              acc[i + 3] = fmaf(v.w, drop, acc[i + 3]);
+        for (int i = 0; i < JOIN; ++i) {
+          const int c = from + i * step;
+          st[i] = c <= to ? __ldcg(reinterpret_cast<const float4*>(part_of(c) + ROWS * D + 4 * r))
+                          : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+          cm = fmaxf(cm, st[i].x);
+          cM = fmaxf(cM, st[i].y);
+        }
+        const float um = cm == -INFINITY ? 0.f : cm, uM = cM == -INFINITY ? 0.f : cM;
+#pragma unroll
+        for (int i = 0; i < JOIN; ++i) {
+          const int c = from + i * step;
+          if (c > to) break;
+          cl += st[i].z * ex2(st[i].x - um);
+          const float drop = ex2(st[i].y - uM);
+#pragma unroll
+          for (int e = 0; e < DPT; e += 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(c) + r * D + d0 + e));
+            acc[e] = fmaf(v.x, drop, acc[e]);
+            acc[e + 1] = fmaf(v.y, drop, acc[e + 1]);
+            acc[e + 2] = fmaf(v.z, drop, acc[e + 2]);
+            acc[e + 3] = fmaf(v.w, drop, acc[e + 3]);
+          }
+        }
+      };
+      const int parts = c1 - c0 + 1, group = c0 + (cta - c0) / JOIN * JOIN, end = min(group + JOIN - 1, c1);
+      put(part_of(cta));
+      // Counters of a CTA: of the item that starts in it and its first group,
+      // and of the group that it leads in an item from before.
+      write = last_of(p.counters + 3 * group + (group == c0 ? 1 : 2), end - group + 1);
+      if (write) {
+        join(group, end, 1);
+        if (parts > JOIN) {
+          __syncthreads();  // every thread has read the group's first part
+          put(part_of(group));
+          const int groups = (parts + JOIN - 1) / JOIN;
+          write = last_of(p.counters + 3 * c0, groups);
+          if (write) {
+            float gm = -INFINITY, gM = -INFINITY, gl = 0.f, ga[DPT] = {};
+            // more than JOIN groups (over 256 parts): in turns
+            for (int i = 0; i < groups; i += JOIN) {
+              join(c0 + i * JOIN, min(c1, c0 + (i + JOIN) * JOIN - 1), JOIN);
+              const float nm = fmaxf(gm, cm), nM = fmaxf(gM, cM);
+              const float um = nm == -INFINITY ? 0.f : nm, uM = nM == -INFINITY ? 0.f : nM;
+              gl = gl * ex2(gm - um) + cl * ex2(cm - um);
+              const float f0 = ex2(gM - uM), f1 = ex2(cM - uM);
+#pragma unroll
+              for (int e = 0; e < DPT; ++e) ga[e] = ga[e] * f0 + acc[e] * f1;
+              gm = nm, gM = nM;
             }
+            cm = gm, cM = gM, cl = gl;
+#pragma unroll
+            for (int e = 0; e < DPT; ++e) acc[e] = ga[e];
           }
         }
       }

@@ -290,36 +290,57 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       // rows past the last store nothing, so they may see all
       const int limit = live_row ? before + qi : INT_MAX;
       const int first_limit = before + (int)(((int64_t)T_ROWS * P.qt + 128 * X) / p.G);
-      // ---- the query row, scaled by a power of two into fp16
+      // ---- the warp's 32 query rows, scaled by a power of two into fp16: a
+      // row's D / 8 pieces in neighbouring lanes, so that all loads of eight
+      // are in flight together
       float f, off;  // score per product; what the keys' 128s add to a product
       {
-        const uint16_t* src = p.q + (int64_t)(P.row + qi) * p.q_stride + (size_t)head * D;
-        float m = 0.f, sum = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = live_row ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes of a row, rows of a load
+        const int c = lane % LPR;
+        f = off = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16lo(x[e])), fabsf(bf16hi(x[e]))));
+        for (int b = 0; b < 32; b += 8 * RPL) {
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t rr = (uint32_t)T_ROWS * P.qt + 128 * X + 32 * (warp & 3) + b + i * RPL + lane / LPR;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (rr < (uint32_t)rows)
+              v[i] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(P.row + (int)(rr / (uint32_t)p.G)) * p.q_stride +
+                                                     (size_t)(P.h * p.G + (int)(rr % (uint32_t)p.G)) * D + 8 * c);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            float m = 0.f, sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16lo(x[e])), fabsf(bf16hi(x[e]))));
+#pragma unroll
+            for (int o = 1; o < LPR; o *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+            // its largest magnitude goes to [2^14, 2^15); a negative scale goes
+            // into the row, so that f is not
+            const int ex = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
+            const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), p.scale_log2);
+            auto two = [&](uint32_t a, uint32_t b, bool hi) {
+              const __half2 h = __floats2half2_rn((hi ? bf16hi(a) : bf16lo(a)) * up, (hi ? bf16hi(b) : bf16lo(b)) * up);
+              sum += __low2float(h) + __high2float(h);
+              return half2_bits(h);
+            };
+            // channels in the keys' order: 0 2 1 3 of every four
+            const int row = 32 * (warp & 3) + b + i * RPL + lane / LPR;
+            *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (128 * 128) + sw128_off(row, c & 7)) =
+                make_uint4(two(x[0], x[1], false), two(x[0], x[1], true), two(x[2], x[3], false), two(x[2], x[3], true));
+#pragma unroll
+            for (int o = 1; o < LPR; o *= 2) sum += __shfl_xor_sync(~0u, sum, o);
+            // to the lanes that own the rows
+            const int ex_of = __shfl_sync(~0u, ex, (lane % RPL) * LPR);
+            const float sum_of = __shfl_sync(~0u, sum, (lane % RPL) * LPR);
+            if (lane / RPL == b / RPL + i) {
+              f = __uint_as_float((uint32_t)(127 - 14 + ex_of) << 23) * fabsf(p.scale_log2) * 0x1p24f;
+              off = sum_of * 0x1p-17f;  // 128 * 2^-24
+            }
+          }
         }
-        // its largest magnitude goes to [2^14, 2^15); a negative scale goes
-        // into the row, so that f is not
-        const int ex = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
-        const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), p.scale_log2);
-        f = __uint_as_float((uint32_t)(127 - 14 + ex) << 23) * fabsf(p.scale_log2) * 0x1p24f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = live_row ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-          auto two = [&](uint32_t a, uint32_t b, bool hi) {
-            const __half2 h = __floats2half2_rn((hi ? bf16hi(a) : bf16lo(a)) * up, (hi ? bf16hi(b) : bf16lo(b)) * up);
-            sum += __low2float(h) + __high2float(h);
-            return half2_bits(h);
-          };
-          // channels in the keys' order: 0 2 1 3 of every four
-          *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (128 * 128) + sw128_off(r, c & 7)) =
-              make_uint4(two(v.x, v.y, false), two(v.x, v.y, true), two(v.z, v.w, false), two(v.z, v.w, true));
-        }
-        off = sum * 0x1p-17f;  // 128 * 2^-24
         fence_async_smem();
         named_barrier(2 + X);
         if ((warp & 3) == 0) {
@@ -510,20 +531,26 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
           if (top == -INFINITY) top = 0.f;
           for (int c = c0; c <= c1; ++c) sum += __ldcg(part(c) + 128 * D + 128 + r) * ex2(__ldcg(part(c) + 128 * D + r) - top);
           const float k = sum == 0.f ? 0.f : ref / sum;
-          for (int d = 0; d < D; d += 8) {
-            float acc[8] = {};
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            float acc[32] = {};
             for (int c = c0; c <= c1; ++c) {
               const float drop = ex2(__ldcg(part(c) + 128 * D + r) - top) * k;
-              const float4 a = __ldcg(reinterpret_cast<const float4*>(part(c) + ((d / 4) * 128 + r) * 4));
-              const float4 b = __ldcg(reinterpret_cast<const float4*>(part(c) + ((d / 4 + 1) * 128 + r) * 4));
-              acc[0] = fmaf(a.x, drop, acc[0]), acc[1] = fmaf(a.y, drop, acc[1]);
-              acc[2] = fmaf(a.z, drop, acc[2]), acc[3] = fmaf(a.w, drop, acc[3]);
-              acc[4] = fmaf(b.x, drop, acc[4]), acc[5] = fmaf(b.y, drop, acc[5]);
-              acc[6] = fmaf(b.z, drop, acc[6]), acc[7] = fmaf(b.w, drop, acc[7]);
+              float4 v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part(c) + ((d / 4 + i) * 128 + r) * 4));
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                acc[4 * i] = fmaf(v[i].x, drop, acc[4 * i]), acc[4 * i + 1] = fmaf(v[i].y, drop, acc[4 * i + 1]);
+                acc[4 * i + 2] = fmaf(v[i].z, drop, acc[4 * i + 2]), acc[4 * i + 3] = fmaf(v[i].w, drop, acc[4 * i + 3]);
+              }
             }
             if (live_row)
-              *reinterpret_cast<uint4*>(dst + d) = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
-                                                              pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(dst + d + i) =
+                    make_uint4(pack_bf16x2(acc[i], acc[i + 1]), pack_bf16x2(acc[i + 2], acc[i + 3]),
+                               pack_bf16x2(acc[i + 4], acc[i + 5]), pack_bf16x2(acc[i + 6], acc[i + 7]));
           }
         }
       }

@@ -5,13 +5,13 @@
 namespace moe {
 
 // Workspace of both calls: the status block, the completion counters of the
-// split attention items, their partial results.
+// split attention items (three a CTA), their partial results.
 constexpr int KV_CTAS_PER_SM = 3;  // at most, of the streaming kernels
 constexpr int KV_ROWS = 16;        // rows of a query tile, at most
 
 inline int kv_grid_max() { return sm_count() * KV_CTAS_PER_SM; }
 inline size_t kv_counter_off() { return sizeof(DeviceStatus); }
-inline size_t kv_partial_off() { return align_up(kv_counter_off() + (size_t)kv_grid_max() * 4, 256); }
+inline size_t kv_partial_off() { return align_up(kv_counter_off() + (size_t)kv_grid_max() * 3 * 4, 256); }
 // A partial result: for each row its score maximum, its maximum of score +
 // log2(value scale), its sum and d accumulators.
 __host__ __device__ constexpr size_t kv_partial_floats(int d) { return (size_t)KV_ROWS * (d + 4); }

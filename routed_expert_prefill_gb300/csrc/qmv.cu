@@ -49,145 +49,7 @@ __device__ __forceinline__ void codes_to_pairs(uint32_t w, uint32_t (&o)[4]) {
   }
 }
 
-// 16 row values k = 16 j .. 16 j + 15 of one group as the B operands of its
-// four products: o[2 s], o[2 s + 1] hold the pairs (k0 + i, k0 + i + 4) that
-// meet pairs 2 (s & 1) and 2 (s & 1) + 1 of the code word s >> 1.
-__device__ __forceinline__ void row_pairs(const uint4 (&u)[2], uint32_t (&o)[8]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    o[4 * h + 0] = __byte_perm(u[h].x, u[h].z, 0x5410);
-    o[4 * h + 1] = __byte_perm(u[h].x, u[h].z, 0x7632);
-    o[4 * h + 2] = __byte_perm(u[h].y, u[h].w, 0x5410);
-    o[4 * h + 3] = __byte_perm(u[h].y, u[h].w, 0x7632);
-  }
-}
-
-// The same from 16 signed 8-bit codes, to fp16: 1024 + (c + 128) is exact
-// under the exponent of 1024, and so is the difference to 1152.
-__device__ __forceinline__ void code_pairs(uint4 u, uint32_t (&o)[8]) {
-  const uint32_t w[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
-  const __half2 off = __floats2half2_rn(1152.f, 1152.f);
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // bytes i of both words, each in the low byte of a half
-      const uint32_t v = (__byte_perm(w[2 * h], w[2 * h + 1], i | (4 + i) << 8) & 0x00FFu) |
-                         ((w[2 * h + 1] >> (8 * i)) & 0xFFu) << 16 | 0x64006400u;
-      const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v), off);
-      o[4 * h + i] = *reinterpret_cast<const uint32_t*>(&r);
-    }
-}
-
 constexpr int QMV_WARPS = 8;
-
-// y = x W^T with W as the A operand of m16n8k16: a warp owns a tile of 16
-// weight rows and 8 NT rows of x, and walks its share of the 64-wide groups.
-// Per group a lane loads 8 bytes of codes of two weight rows (a quad covers a
-// group's 32 bytes) straight into the fragment layout -- the order of k
-// within a group is free as long as both operands agree -- so weights never
-// pass through shared memory.  With q' = 1 + q / 16 the products give
-// P = sum q' x and, from a constant operand of ones, X = sum x, and the
-// group adds 16 s P + (b - 16 s) X, exactly s sum q x + b sum x.
-// KS warps share a tile, each with a contiguous part of the groups; their
-// sums meet in shared memory in a fixed order.
-template <int NT, bool F16, bool OUT32>
-__global__ void __launch_bounds__(QMV_WARPS * 32) qmv_kernel(QmvParams p, int KS) {
-  extern __shared__ float red[];  // [warp][16][8 NT]
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
-  const int tiles = QMV_WARPS / KS, ks = warp % KS;
-  const int row0 = (blockIdx.x * tiles + warp / KS) * 16;
-  const int t0 = blockIdx.y * 8 * NT;
-  const int groups = p.k >> 6;
-  const int gb = (int)((int64_t)groups * ks / KS), ge = (int)((int64_t)groups * (ks + 1) / KS);
-  // rows past the end read the last row; their results are not stored
-  const int ra = min(row0 + g, p.n - 1), rb = min(row0 + g + 8, p.n - 1);
-  const uint8_t* ca = p.codes + (size_t)ra * (p.k >> 1) + 8 * j;
-  const uint8_t* cb = p.codes + (size_t)rb * (p.k >> 1) + 8 * j;
-  const uint16_t* sa = p.scales + (size_t)ra * groups;
-  const uint16_t* sb = p.scales + (size_t)rb * groups;
-  const uint16_t* ba = p.biases + (size_t)ra * groups;
-  const uint16_t* bb = p.biases + (size_t)rb * groups;
-  constexpr uint32_t ONES = F16 ? 0x3C003C00u : 0x3F803F80u;
-  const uint32_t ones[4] = {ONES, ONES, ONES, ONES};
-  float acc[NT][4] = {};
-  if (row0 < p.n)
-#pragma unroll 4
-    for (int gr = gb; gr < ge; ++gr) {
-      const uint2 wa = __ldg(reinterpret_cast<const uint2*>(ca + gr * 32));
-      const uint2 wb = __ldg(reinterpret_cast<const uint2*>(cb + gr * 32));
-      const float s0 = 16.f * __half2float(__ushort_as_half(__ldg(sa + gr)));
-      const float s1 = 16.f * __half2float(__ushort_as_half(__ldg(sb + gr)));
-      const float b0 = __half2float(__ushort_as_half(__ldg(ba + gr))) - s0;
-      const float b1 = __half2float(__ushort_as_half(__ldg(bb + gr))) - s1;
-      uint32_t pa[2][4], pb[2][4];
-      codes_to_pairs<F16>(wa.x, pa[0]);
-      codes_to_pairs<F16>(wa.y, pa[1]);
-      codes_to_pairs<F16>(wb.x, pb[0]);
-      codes_to_pairs<F16>(wb.y, pb[1]);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int r = t0 + 8 * nt + g;
-        uint32_t xo[8];
-        if (F16) {
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (r < p.t) u = *reinterpret_cast<const uint4*>(p.xc + (size_t)r * p.k + gr * 64 + 16 * j);
-          code_pairs(u, xo);
-        } else {
-          uint4 u[2] = {};
-          if (r < p.t) {
-            const uint4* q = reinterpret_cast<const uint4*>(p.x + (size_t)r * p.x_stride + gr * 64 + 16 * j);
-            u[0] = q[0];
-            u[1] = q[1];
-          }
-          row_pairs(u, xo);
-        }
-        float P[4] = {}, X[4] = {};
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int w = s >> 1, q = 2 * (s & 1);
-          const uint32_t a[4] = {pa[w][q], pb[w][q], pa[w][q + 1], pb[w][q + 1]};
-          mma_16816(P, a, xo[2 * s], xo[2 * s + 1], F16);
-          mma_16816(X, ones, xo[2 * s], xo[2 * s + 1], F16);
-        }
-        float f0 = 1.f, f1 = 1.f;
-        if (F16) {  // the rows' scales of this group
-          const int c = t0 + 8 * nt + 2 * j;
-          f0 = c < p.t ? p.xs[(size_t)c * groups + gr] : 0.f;
-          f1 = c + 1 < p.t ? p.xs[(size_t)(c + 1) * groups + gr] : 0.f;
-        }
-        acc[nt][0] = fmaf(f0, fmaf(s0, P[0], b0 * X[0]), acc[nt][0]);
-        acc[nt][1] = fmaf(f1, fmaf(s0, P[1], b0 * X[1]), acc[nt][1]);
-        acc[nt][2] = fmaf(f0, fmaf(s1, P[2], b1 * X[2]), acc[nt][2]);
-        acc[nt][3] = fmaf(f1, fmaf(s1, P[3], b1 * X[3]), acc[nt][3]);
-      }
-    }
-  // sums of the KS parts, rows of x outermost, weight rows contiguous
-  float* mine = red + (size_t)warp * 16 * 8 * NT;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float* q = mine + (8 * nt + 2 * j) * 16;
-    q[g] = acc[nt][0];
-    q[16 + g] = acc[nt][1];
-    q[g + 8] = acc[nt][2];
-    q[16 + g + 8] = acc[nt][3];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < tiles * 16 * 8 * NT; i += blockDim.x) {
-    const int c = i % 16, tile = i / 16 % tiles, r = i / (16 * tiles);
-    const int col = (blockIdx.x * tiles + tile) * 16 + c;
-    if (t0 + r >= p.t || col >= p.n) continue;
-    float v = 0.f;
-    for (int s = 0; s < KS; ++s) v += red[((size_t)(tile * KS + s) * 8 * NT + r) * 16 + c];
-    const size_t o = (size_t)(t0 + r) * p.n + col;
-    if (OUT32)
-      static_cast<float*>(p.y)[o] = v;
-    else
-      static_cast<uint16_t*>(p.y)[o] = f2bf(v);
-  }
-}
 
 // ---------------------------------------------------------------------------
 // Few rows: weights streamed through shared memory.
@@ -195,6 +57,10 @@ __global__ void __launch_bounds__(QMV_WARPS * 32) qmv_kernel(QmvParams p, int KS
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
                : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -259,8 +125,7 @@ size_t qs_smem(const QmvParams& p, int nt, int teams, int stages) {
          + (size_t)p.t * qs_x_pitch(p.k);                          // x
 }
 
-// The products of qmv_kernel for t <= 8 NT rows, when what counts is how
-// fast the weights come.  The CTA stages x once; then each of its TEAMS teams
+// y for t <= 8 NT rows, when what counts is how fast the weights come.  The CTA stages x once; then each of its TEAMS teams
 // of eight warps walks tiles of 16 weight rows.  A team's warps split k in
 // units of 4 groups (128 bytes of a weight row), the same units in every
 // tile, and each warp keeps S - 1 units in flight by asynchronous copies into
@@ -566,29 +431,255 @@ bool try_config(const QmvParams& p, bool out32, cudaStream_t s, cudaError_t& e) 
   return true;
 }
 
-// The streaming kernel, if the rows of x fit beside its rings: two teams a
-// CTA when there are tiles for them.
+// The streaming kernel, if the rows of x fit beside its rings.  With more
+// tiles than SMs it wants two teams a CTA; one team is then no match for the
+// tile kernel below (8 rows of 8192 with 32768 weight rows: 66.6 us against
+// 55.3), but for rows where that one pads most (9 rows of 4096 with 65536:
+// 60.7 against 68.8, 16 rows 76.7 against 69.0) and for 8-bit rows (56.5
+// against 73.2, 63.3 against 73.6).
 template <int NT, bool F16>
 bool try_stream(const QmvParams& p, bool out32, cudaStream_t s, cudaError_t& e) {
-  if ((p.n + 15) / 16 > sm_count() && (try_config<NT, 2, 4, F16>(p, out32, s, e) || try_config<NT, 2, 3, F16>(p, out32, s, e)))
-    return true;
+  if ((p.n + 15) / 16 > sm_count()) {
+    if (try_config<NT, 2, 4, F16>(p, out32, s, e) || try_config<NT, 2, 3, F16>(p, out32, s, e)) return true;
+    if (p.t <= 8 || (p.t > 12 && !F16)) return false;
+  }
   return try_config<NT, 1, 4, F16>(p, out32, s, e) || try_config<NT, 1, 3, F16>(p, out32, s, e);
 }
 
-template <int NT, bool F16>
-cudaError_t launch_qmv(const QmvParams& p, bool out32, cudaStream_t s) {
-  const int tiles = (p.n + 15) / 16, groups = p.k / 64;
-  // as few parts of k as keep every SM's warps busy
-  int KS = 1;
-  while (KS < QMV_WARPS && KS * 2 <= groups && (int64_t)tiles * KS < (int64_t)sm_count() * 16) KS *= 2;
-  const int per = QMV_WARPS / KS;
-  const dim3 grid((tiles + per - 1) / per, (p.t + 8 * NT - 1) / (8 * NT)), block(QMV_WARPS * 32);
-  const size_t smem = (size_t)QMV_WARPS * 16 * 8 * NT * 4;
-  cudaError_t e;
-  auto* kern = out32 ? qmv_kernel<NT, F16, true> : qmv_kernel<NT, F16, false>;
-  if (smem > 48 * 1024 && (e = set_smem_limit_once(kern, (int)smem)) != cudaSuccess) return e;
-  MOE_LAUNCH("qmv", s, { e = launch_k(kern, grid, block, smem, s, p, KS); });
+// ---------------------------------------------------------------------------
+// More rows.
+// ---------------------------------------------------------------------------
+
+constexpr int QM_STAGES = 3;
+template <int MT>
+constexpr int qm_stage() { return MT * 16 * (QS_ROW + 16); }  // a unit: codes, then 4 scales and 4 biases a row
+constexpr int QM_X_PITCH = 512 + 16;                           // bytes of a row's 4 groups of x, and a shift of banks
+template <int NT, int MT>
+constexpr int qm_smem() {
+  return QMV_WARPS * QM_STAGES * qm_stage<MT>() + 2 * 8 * NT * QM_X_PITCH + 2 * 4 * 8 * NT * 8;
+}
+
+// y for 8 NT rows of x (a tile of them per blockIdx.y): a CTA owns 128 MT
+// weight rows, 16 MT a warp, over all of k, in units of 4 groups.  Each warp's
+// codes and scales come through a ring of its own, as in the streaming
+// kernel; x comes unit by unit through two buffers that all warps share.
+// What costs here is what is done per row of x, so codes are converted to
+// 1 + q / 16, exact in bf16 and fp16, which needs nothing of x but the order of
+// its values; P = sum q' x and X = sum x of a group add 16 s P + (b - 16 s) X.
+// MT = 2 reads every value of x from shared memory once per 32 weight rows.
+template <int NT, int MT, bool F16, bool VEC>
+__global__ void __launch_bounds__(QMV_WARPS * 32, 1) qmv_tile_kernel(QmvParams p, bool out32) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int STAGE = qm_stage<MT>(), ROWS = 16 * MT, S = QM_STAGES;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, j = lane & 3;
+  unsigned char* ring = smem + (size_t)warp * S * STAGE;
+  unsigned char* xsm = smem + (size_t)QMV_WARPS * S * STAGE;                  // [2][8 NT rows]
+  float2* xsum = reinterpret_cast<float2*>(xsm + 2 * 8 * NT * QM_X_PITCH);    // [2][4 groups][8 NT]: X, the row's scale
+  const int groups = p.k >> 6, units = (groups + 3) >> 2;
+  const int row0 = (blockIdx.x * QMV_WARPS + warp) * ROWS, t0 = blockIdx.y * 8 * NT;
+  const size_t row_bytes = (size_t)p.k >> 1;
+  pdl_wait();
+  pdl_trigger();
+
+  auto issue = [&](int u) {
+    if (u < units && row0 < p.n) {
+      unsigned char* dst = ring + (u % S) * STAGE;
+      const int g0 = 4 * u, c = lane & 7;
+#pragma unroll
+      for (int i = 0; i < ROWS / 4; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        // rows past the end read the last row; their results are not stored
+        if (VEC || g0 + (c >> 1) < groups)
+          cp_async16(dst + r * QS_ROW + 16 * c, p.codes + min(row0 + r, p.n - 1) * row_bytes + g0 * 32 + 16 * c);
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int r = 16 * i + (lane >> 1);
+        const uint16_t* src = (lane & 1 ? p.biases : p.scales) + (size_t)min(row0 + r, p.n - 1) * groups + g0;
+        unsigned char* to = dst + ROWS * QS_ROW + r * 16 + 8 * (lane & 1);
+        if (VEC) {
+          cp_async8(to, src);
+        } else {
+          uint32_t v[4] = {};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (g0 + e < groups) v[e] = __ldg(src + e);
+          *reinterpret_cast<uint2*>(to) = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+
+  // x of a unit: vector i of a thread is 8 values of row i * 8 + warp, so that
+  // a warp reads one row's 256 and eight lanes hold a group
+  uint4 xv[NT];
+  float xf[NT];
+  auto load_x = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int r = t0 + 8 * i + warp, gr = 4 * u + (lane >> 3);
+      xv[i] = make_uint4(0, 0, 0, 0);
+      xf[i] = 0.f;
+      if (r < p.t && gr < groups) {
+        if (F16) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p.xc + (size_t)r * p.k + u * 256 + 8 * lane);
+          xv[i].x = v.x, xv[i].y = v.y;
+          xf[i] = __ldg(p.xs + (size_t)r * groups + gr);
+        } else {
+          xv[i] = *reinterpret_cast<const uint4*>(p.x + (size_t)r * p.x_stride + u * 256 + 8 * lane);
+        }
+      }
+    }
+  };
+  auto store_x = [&](int u) {
+    unsigned char* xb = xsm + (u & 1) * 8 * NT * QM_X_PITCH;
+    float2* sb = xsum + (u & 1) * 4 * 8 * NT;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      uint4 o;
+      float sum;
+      if (F16) {
+        const uint2 v = make_uint2(xv[i].x, xv[i].y);
+        const int8_t* b = reinterpret_cast<const int8_t*>(&v);
+        auto pair = [&](int e) {
+          const __half2 h = __floats2half2_rn(b[e], b[e + 4]);
+          return *reinterpret_cast<const uint32_t*>(&h);
+        };
+        o = make_uint4(pair(0), pair(1), pair(2), pair(3));
+        sum = (float)(((b[0] + b[1]) + (b[2] + b[3])) + ((b[4] + b[5]) + (b[6] + b[7])));
+      } else {
+        const uint4 v = xv[i];
+        o = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                       __byte_perm(v.y, v.w, 0x7632));
+        sum = ((bf16lo(v.x) + bf16hi(v.x)) + (bf16lo(v.y) + bf16hi(v.y))) +
+              ((bf16lo(v.z) + bf16hi(v.z)) + (bf16lo(v.w) + bf16hi(v.w)));
+      }
+#pragma unroll
+      for (int s = 1; s < 8; s *= 2) sum += __shfl_xor_sync(~0u, sum, s);
+      *reinterpret_cast<uint4*>(xb + (8 * i + warp) * QM_X_PITCH + 16 * lane) = o;
+      if ((lane & 7) == 0) sb[(lane >> 3) * 8 * NT + 8 * i + warp] = make_float2(sum, F16 ? xf[i] : 1.f);
+    }
+  };
+
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(i);
+  load_x(0);
+  store_x(0);
+  __syncthreads();
+  float acc[MT][NT][4] = {};
+  for (int u = 0; u < units; ++u) {
+    if (u + 1 < units) load_x(u + 1);
+    cp_async_wait<S - 2>();
+    __syncwarp();  // this unit is there, and the last one is read by every lane
+    issue(u + S - 1);
+    const unsigned char* src = ring + (u % S) * STAGE;
+    const unsigned char* xb = xsm + (u & 1) * 8 * NT * QM_X_PITCH;
+    const float2* sums = xsum + (u & 1) * 4 * 8 * NT;
+    uint4 sb[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        sb[m][e] = *reinterpret_cast<const uint4*>(src + ROWS * QS_ROW + (16 * m + 8 * e + g) * 16);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (!VEC && 4 * u + q >= groups) break;
+      uint32_t pa[MT][2][4], pb[MT][2][4];
+      float s[MT][2], b[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const uint2 wa = *reinterpret_cast<const uint2*>(src + (16 * m + g) * QS_ROW + 32 * q + 8 * j);
+        const uint2 wb = *reinterpret_cast<const uint2*>(src + (16 * m + 8 + g) * QS_ROW + 32 * q + 8 * j);
+        codes_to_pairs<F16>(wa.x, pa[m][0]);
+        codes_to_pairs<F16>(wa.y, pa[m][1]);
+        codes_to_pairs<F16>(wb.x, pb[m][0]);
+        codes_to_pairs<F16>(wb.y, pb[m][1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t sw = q < 2 ? sb[m][e].x : sb[m][e].y, bw = q < 2 ? sb[m][e].z : sb[m][e].w;
+          s[m][e] = 16.f * __half2float(__ushort_as_half((uint16_t)(q & 1 ? sw >> 16 : sw)));
+          b[m][e] = __half2float(__ushort_as_half((uint16_t)(q & 1 ? bw >> 16 : bw))) - s[m][e];
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const unsigned char* xr = xb + (8 * nt + g) * QM_X_PITCH + q * 128 + 32 * j;
+        const uint4 v0 = *reinterpret_cast<const uint4*>(xr), v1 = *reinterpret_cast<const uint4*>(xr + 16);
+        const uint32_t xo[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        const float4 X = *reinterpret_cast<const float4*>(sums + q * 8 * NT + 8 * nt + 2 * j);  // rows 2 j, 2 j + 1
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          float P[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int w = i >> 1, h = 2 * (i & 1);
+            const uint32_t a[4] = {pa[m][w][h], pb[m][w][h], pa[m][w][h + 1], pb[m][w][h + 1]};
+            if (i == 0)
+              mma_first<F16>(P, a, xo[0], xo[1]);
+            else
+              mma_16816(P, a, xo[2 * i], xo[2 * i + 1], F16);
+          }
+          float(&d)[4] = acc[m][nt];
+          if (F16) {
+            d[0] = fmaf(X.y, fmaf(s[m][0], P[0], b[m][0] * X.x), d[0]);
+            d[1] = fmaf(X.w, fmaf(s[m][0], P[1], b[m][0] * X.z), d[1]);
+            d[2] = fmaf(X.y, fmaf(s[m][1], P[2], b[m][1] * X.x), d[2]);
+            d[3] = fmaf(X.w, fmaf(s[m][1], P[3], b[m][1] * X.z), d[3]);
+          } else {
+            d[0] = fmaf(s[m][0], P[0], fmaf(b[m][0], X.x, d[0]));
+            d[1] = fmaf(s[m][0], P[1], fmaf(b[m][0], X.z, d[1]));
+            d[2] = fmaf(s[m][1], P[2], fmaf(b[m][1], X.x, d[2]));
+            d[3] = fmaf(s[m][1], P[3], fmaf(b[m][1], X.z, d[3]));
+          }
+        }
+      }
+    }
+    if (u + 1 < units) store_x(u + 1);  // its buffer was read up to the last barrier
+    __syncthreads();
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = row0 + 16 * m + 8 * (e >> 1) + g, r = t0 + 8 * nt + 2 * j + (e & 1);
+        if (col >= p.n || r >= p.t) continue;
+        const size_t o = (size_t)r * p.n + col;
+        if (out32)
+          static_cast<float*>(p.y)[o] = acc[m][nt][e];
+        else
+          static_cast<uint16_t*>(p.y)[o] = f2bf(acc[m][nt][e]);
+      }
+}
+
+template <int NT, int MT, bool F16>
+cudaError_t launch_tile(const QmvParams& p, bool out32, cudaStream_t s) {
+  auto* kern = p.k % 256 == 0 ? qmv_tile_kernel<NT, MT, F16, true> : qmv_tile_kernel<NT, MT, F16, false>;
+  cudaError_t e = set_smem_limit_once(kern, qm_smem<NT, MT>());
+  if (e != cudaSuccess) return e;
+  const dim3 grid((p.n + 128 * MT - 1) / (128 * MT), (p.t + 8 * NT - 1) / (8 * NT)), block(QMV_WARPS * 32);
+  MOE_LAUNCH("qmv_tile", s, { e = launch_k(kern, grid, block, (size_t)qm_smem<NT, MT>(), s, p, out32); });
   return e;
+}
+
+template <bool F16>
+cudaError_t launch_rows(const QmvParams& p, bool out32, cudaStream_t s) {
+  // 32 weight rows a warp where that still gives every SM a CTA
+  const bool wide = p.n >= 256 * sm_count();
+  // Few rows stream the weights, unless k is so short that a tile's end comes
+  // too often (4 rows with 131072 weight rows: k = 512 29.0 us streaming,
+  // 17.8 in tiles; k = 1024 32.0 and 29.9).
+  cudaError_t e;
+  if (!(wide && p.k <= 1024) &&
+      (p.t <= 8 ? try_stream<1, F16>(p, out32, s, e) : p.t <= 16 && try_stream<2, F16>(p, out32, s, e)))
+    return e;
+  if (p.t <= 8) return wide ? launch_tile<1, 2, F16>(p, out32, s) : launch_tile<1, 1, F16>(p, out32, s);
+  if (p.t <= 16) return wide ? launch_tile<2, 2, F16>(p, out32, s) : launch_tile<2, 1, F16>(p, out32, s);
+  if (p.t <= 32) return wide ? launch_tile<4, 2, F16>(p, out32, s) : launch_tile<4, 1, F16>(p, out32, s);
+  return wide ? launch_tile<8, 2, F16>(p, out32, s) : launch_tile<8, 1, F16>(p, out32, s);
 }
 
 }  // namespace
@@ -619,18 +710,5 @@ extern "C" int moe_qmv(const uint16_t* x, int64_t x_stride, const int8_t* x_code
   const QmvParams p{x, x_stride, x_codes, x_scales, w->codes, w->scales, w->biases, t, n, k, y};
   cudaStream_t s = (cudaStream_t)stream;
   const bool f = x_codes != nullptr, o = y_fp32 != 0;
-  const int nt = (t + 7) / 8;
-  cudaError_t e;
-  if (t <= 8 ? (f ? try_stream<1, true>(p, o, s, e) : try_stream<1, false>(p, o, s, e))
-             : t <= 16 && (f ? try_stream<2, true>(p, o, s, e) : try_stream<2, false>(p, o, s, e)))
-    return cuda_status(e, "moe_qmv launch");
-  if (nt <= 1)
-    e = f ? launch_qmv<1, true>(p, o, s) : launch_qmv<1, false>(p, o, s);
-  else if (nt <= 2)
-    e = f ? launch_qmv<2, true>(p, o, s) : launch_qmv<2, false>(p, o, s);
-  else if (nt <= 4)
-    e = f ? launch_qmv<4, true>(p, o, s) : launch_qmv<4, false>(p, o, s);
-  else
-    e = f ? launch_qmv<8, true>(p, o, s) : launch_qmv<8, false>(p, o, s);
-  return cuda_status(e, "moe_qmv launch");
+  return cuda_status(f ? launch_rows<true>(p, o, s) : launch_rows<false>(p, o, s), "moe_qmv launch");
 }
