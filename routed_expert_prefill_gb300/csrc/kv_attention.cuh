@@ -66,17 +66,18 @@ template <int ROWS>
 __device__ __forceinline__ int tile_units(const AttnParams& p, const Seq& q, int qt) {
   return (tile_seen<ROWS>(p, q, qt) + UNIT - 1) / UNIT;
 }
-template <int ROWS>
+template <int ROWS, int EXTRA>
 __device__ __forceinline__ int64_t seq_units(const AttnParams& p, const Seq& q) {
   int64_t w = 0;
-  for (int qt = 0, m = q_tiles<ROWS>(p, q); qt < m; ++qt) w += tile_units<ROWS>(p, q, qt);
+  for (int qt = 0, m = q_tiles<ROWS>(p, q); qt < m; ++qt) w += EXTRA + tile_units<ROWS>(p, q, qt);
   return w * p.c.hkv;
 }
 
 // A CTA's run of units.  The work is the list of all (sequence, query tile of
 // ROWS rows, key/value head) items in this order, each as many units of 128
-// tokens as its rows see; CTA c of `ctas` takes units x0 .. x1 - 1 of the
-// `total`, starting with unit u of item (s, qt, h).
+// tokens as its rows see, after EXTRA units that stand for what an item costs
+// whatever its length; CTA c of `ctas` takes units x0 .. x1 - 1 of the
+// `total`, starting with unit u (EXTRA ones counted) of item (s, qt, h).
 struct Work {
   int64_t total, ctas, x0, x1;
   int s, qt, h, u;
@@ -98,7 +99,7 @@ __device__ __forceinline__ int cta_of(const Work& w, int64_t x) {
 
 // Called by all THREADS threads; scratch: THREADS / 32 + 2 values in shared
 // memory.  False where the CTA has nothing to do.
-template <int ROWS, int THREADS>
+template <int ROWS, int THREADS, int EXTRA = 0>
 __device__ __forceinline__ bool find_work(const AttnParams& p, int64_t* scratch, Work& wk) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -106,7 +107,7 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, int64_t* scratch,
   for (int s = tid; s < p.c.n_seq; s += THREADS) {
     const Seq q = load_seq(p, s);
     if (!q.ok && blockIdx.x == 0) raise_flag(p.st, FLAG_BAD_CACHE);
-    const int64_t w = seq_units<ROWS>(p, q);
+    const int64_t w = seq_units<ROWS, EXTRA>(p, q);
     if (s == tid) w0 = w;
     total += w;
   }
@@ -124,7 +125,7 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, int64_t* scratch,
   int64_t base = 0;
   for (int sb = 0; sb < p.c.n_seq; sb += THREADS) {
     int64_t w = w0;
-    if (sb) w = sb + tid < p.c.n_seq ? seq_units<ROWS>(p, load_seq(p, sb + tid)) : 0;
+    if (sb) w = sb + tid < p.c.n_seq ? seq_units<ROWS, EXTRA>(p, load_seq(p, sb + tid)) : 0;
     int64_t incl = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -153,7 +154,7 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, int64_t* scratch,
   const Seq q = load_seq(p, wk.s);
   int64_t off = wk.x0 - scratch[WARPS + 1];
   for (wk.qt = 0;; ++wk.qt) {
-    const int units = tile_units<ROWS>(p, q, wk.qt);
+    const int units = EXTRA + tile_units<ROWS>(p, q, wk.qt);
     if (off < (int64_t)units * p.c.hkv) {
       if (off >> 31) {
         wk.h = (int)(off / units);

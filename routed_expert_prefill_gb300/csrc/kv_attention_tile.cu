@@ -17,6 +17,11 @@ constexpr int T_ROWS = 256;  // query rows of an item: two tiles of 128
 // keys and values.  Twelve, so that a thread may hold 168 registers.
 constexpr int T_WARPS = 12, W_KEYS = 8;
 constexpr int T_THREADS = T_WARPS * 32;
+// Units that an item counts for beside its own, when the work is cut: its
+// query rows, first scales and results are worth about four (one prompt of
+// 4096 tokens, 32 heads on 8: 433 us with none, 252 with two, 202 with five;
+// two prompts behind contexts 335, 324, 315, and 327 with eight).
+constexpr int ITEM_COST = 4;
 constexpr int SC_RING = 4;   // tiles whose scales are kept
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float GROWTH = 8.f;  // how far (log2) a row's weights may outgrow 1 before its sums are rescaled
@@ -27,7 +32,7 @@ struct Piece {
   int s, qt, h, u0, u1;
   int n[2];                // units that the rows of either tile see
   int seen;                // positions that the item's rows see
-  int64_t item;            // the item's first unit
+  int64_t first;           // where the item's unit 0 stands in the work
 };
 
 // A warp's walk over the CTA's pieces.  It lives in shared memory and one lane
@@ -59,20 +64,22 @@ struct TileShared {
 __device__ __forceinline__ bool next_piece(const AttnParams& p, const Work& w, Walk& W) {
   __syncwarp();  // every lane is done with the last piece
   if ((threadIdx.x & 31) == 0) {
-    W.more = W.x < w.x1;
-    if (W.more) {
-      Piece& P = W.P;
+    Piece& P = W.P;
+    W.more = 0;
+    while (W.x < w.x1 && !W.more) {
       const Seq q = load_seq(p, W.s);
       P.row = q.row, P.new_rows = q.n, P.len = q.len;
       P.s = W.s, P.qt = W.qt, P.h = W.h;
       P.seen = tile_seen<T_ROWS>(p, q, W.qt);
       const int units = (P.seen + UNIT - 1) / UNIT;
-      P.u0 = W.u;
-      P.u1 = (int)min((int64_t)units, W.u + (w.x1 - W.x));
-      P.item = W.x - W.u;
+      const int end = (int)min((int64_t)(ITEM_COST + units), W.u + (w.x1 - W.x));
+      P.u0 = max(W.u - ITEM_COST, 0);
+      P.u1 = end - ITEM_COST;
+      P.first = W.x - W.u + ITEM_COST;
       P.n[0] = tile_units<128>(p, q, 2 * W.qt);
-      P.n[1] = (int64_t)q.n * p.G > (int64_t)T_ROWS * W.qt + 128 ? units : 0;
-      W.x += P.u1 - P.u0;
+      P.n[1] = seq_rows(p, q) > (uint32_t)T_ROWS * W.qt + 128 ? units : 0;
+      W.more = P.u1 > P.u0;  // not if the run ends among the units that stand for the item's cost
+      W.x += end - W.u;
       W.u = 0;
       if (W.x < w.x1 && ++W.h == p.c.hkv) {
         W.h = 0;
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
   const int hkv = p.c.hkv;
   {
     Work found;
-    if (!find_work<T_ROWS, T_THREADS>(p, S.scratch, found)) return;
+    if (!find_work<T_ROWS, T_THREADS, ITEM_COST>(p, S.scratch, found)) return;
     if (tid == 0) S.work = found;
     if (lane == 0) {
       Walk& W = S.walk[warp];
@@ -480,7 +487,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       if (!(ok = wait_warp(&S.o_full[X], pieces & 1, 53))) break;
       ++pieces;
       tc_fence_after();
-      const int c0 = cta_of(S.work, P.item), c1 = cta_of(S.work, P.item + P.n[X] - 1);
+      const int c0 = cta_of(S.work, P.first), c1 = cta_of(S.work, P.first + P.n[X] - 1);
       const int cta = blockIdx.x;
       uint16_t* dst = p.out + ((size_t)(P.row + qi) * p.hq + head) * D;
       if (c0 == c1) {
