@@ -9,26 +9,66 @@ namespace {
 
 constexpr int APPEND_THREADS = 256;
 
-// A bf16 pair with each value whose 127-fold is not finite replaced by zero.
+// The largest magnitude, in the bits of a bf16, whose 127-fold is a finite
+// fp32 number; what is above is taken as zero.
+constexpr uint32_t MOST_BITS = 0x7C00 + 0x0001;  // 1.0078125 * 2^121: 127 times it is 2^127.99
+
 __device__ __forceinline__ uint32_t finite_pair(uint32_t u, bool& bad) {
-  if (!isfinite(bf16lo(u) * 127.f)) u &= 0xFFFF0000u, bad = true;
-  if (!isfinite(bf16hi(u) * 127.f)) u &= 0x0000FFFFu, bad = true;
+  if ((u & 0x7FFFu) > MOST_BITS) u &= 0xFFFF0000u, bad = true;
+  if ((u >> 16 & 0x7FFFu) > MOST_BITS) u &= 0x0000FFFFu, bad = true;
   return u;
 }
 __device__ __forceinline__ uint4 finite_vec(uint4 u, bool& bad) {
   return make_uint4(finite_pair(u.x, bad), finite_pair(u.y, bad), finite_pair(u.z, bad), finite_pair(u.w, bad));
 }
+// The larger of m and the magnitudes of eight values, as bits in both halves.
+__device__ __forceinline__ uint32_t most_of(uint32_t m, uint4 u) {
+  m = __vmaxu2(m, __vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu));
+  return __vmaxu2(m, __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+}
 
 // v * 127 / m to the nearest whole number, ties to even, exactly: with an
 // approximate quotient rounded to q, the remainder x - q m is exact in one
 // fma (q and the bf16 m have 7 and 8 bits), and it says whether q is the
-// nearest.  rm = 1 / m.  A true division costs about twice the instructions.
+// nearest.  rm = 1 / m.
 __device__ __forceinline__ int nearest_code(float v, float m, float rm) {
   const float x = v * 127.f;
   const float q = rintf(x * rm);
   const float r = fmaf(-q, m, x), over = fabsf(r) + fabsf(r) - m;
   const int c = (int)q;
   return over > 0.f || (over == 0.f && (c & 1)) ? c + (r > 0.f ? 1 : -1) : c;
+}
+
+// Codes of eight values.  k = 127 / m rounded, so v k is off by 2^-24 of at
+// most 127: adding 1.5 * 2^23 rounds it to the nearest whole number, which then
+// stands in the sum's low byte, and only where the remainder comes within
+// 2^-13 of a half does nearest_code decide.
+__device__ __forceinline__ uint2 codes_of(uint4 u, float up, float m, float rm, float k) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t t[8];
+  float far = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float f = (q & 1 ? bf16hi(w[q >> 1]) : bf16lo(w[q >> 1])) * up;
+    const float s = fmaf(f, k, 12582912.f);
+    far = fmaxf(far, fabsf(fmaf(f, k, 12582912.f - s)));
+    t[q] = __float_as_uint(s);
+  }
+  if (far > 0.5f - 0x1p-13f) {
+#pragma unroll 1
+    for (int q = 0; q < 8; ++q) {
+      const uint32_t x = q < 4 ? (q < 2 ? w[0] : w[1]) : (q < 6 ? w[2] : w[3]);
+      const int c = nearest_code((q & 1 ? bf16hi(x) : bf16lo(x)) * up, m, rm);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e == q) t[e] = (uint32_t)c;
+    }
+  }
+  uint32_t o[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    o[h] = __byte_perm(__byte_perm(t[4 * h], t[4 * h + 1], 0x0040), __byte_perm(t[4 * h + 2], t[4 * h + 3], 0x0040), 0x5410);
+  return make_uint2(o[0], o[1]);
 }
 
 // One CTA per (touched block, head, keys or values): the block's values stay
@@ -41,7 +81,7 @@ template <int VPT>
 __global__ void __launch_bounds__(APPEND_THREADS)
     kv_append_kernel(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* starts,
                      int t, moe_kv_cache c, DeviceStatus* st) {
-  __shared__ float part[APPEND_THREADS / 32];
+  __shared__ uint32_t part[APPEND_THREADS / 32];
   __shared__ int owner;
   pdl_wait();
   pdl_trigger();
@@ -73,31 +113,45 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   uint16_t* tail = c.tail + (((size_t)s * 2 + isv) * c.hkv + head) * ring * c.d;
   const int vd = c.d >> 3, nv = c.block * vd;  // vectors of a token and of the block
   uint4 u[VPT];
-  bool bad = false, lost = false;
-  float m = 0.f;
+  uint32_t m2 = 0;  // maxima of the low and of the high halves
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int e = tid + i * APPEND_THREADS, r = e / vd, x = e % vd;
     const int pos = b * c.block + r;
     u[i] = make_uint4(0, 0, 0, 0);
-    if (e < nv && pos < len) {
-      if (pos < old)
-        u[i] = finite_vec(*reinterpret_cast<const uint4*>(tail + (size_t)(pos % ring) * c.d + 8 * x), lost);
-      else
-        u[i] = finite_vec(*reinterpret_cast<const uint4*>(src + (size_t)(row0 + pos - old) * stride +
-                                                          (size_t)head * c.d + 8 * x), bad);
-    }
-    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) m = fmaxf(m, fmaxf(fabsf(bf16lo(w[q])), fabsf(bf16hi(w[q]))));
+    if (e < nv && pos < len)
+      u[i] = *reinterpret_cast<const uint4*>(
+          pos < old ? tail + (size_t)(pos % ring) * c.d + 8 * x
+                    : src + (size_t)(row0 + pos - old) * stride + (size_t)head * c.d + 8 * x);
   }
-  if (bad) raise_flag(st, FLAG_NOT_FINITE);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  if ((tid & 31) == 0) part[tid >> 5] = m;
-  __syncthreads();  // also: what this block reads of the tail is in registers
+  for (int i = 0; i < VPT; ++i) m2 = most_of(m2, u[i]);
+  auto block_most = [&](uint32_t v) {  // also: what this block reads of the tail is in registers
+    v = __reduce_max_sync(~0u, max(v & 0xFFFFu, v >> 16));
+    if ((tid & 31) == 0) part[tid >> 5] = v;
+    __syncthreads();
+    v = 0;
 #pragma unroll
-  for (int i = 0; i < APPEND_THREADS / 32; ++i) m = fmaxf(m, part[i]);
+    for (int i = 0; i < APPEND_THREADS / 32; ++i) v = max(v, part[i]);
+    return v;
+  };
+  uint32_t bits = block_most(m2);
+  if (bits > MOST_BITS) {  // the whole block: something in it is not finite
+    bool bad = false;
+    m2 = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      bool lost = false;
+      u[i] = finite_vec(u[i], lost);
+      const int e = tid + i * APPEND_THREADS;
+      if (lost && b * c.block + e / vd >= old) bad = true;  // older ones have been reported
+      m2 = most_of(m2, u[i]);
+    }
+    if (bad) raise_flag(st, FLAG_NOT_FINITE);
+    __syncthreads();
+    bits = block_most(m2);
+  }
+  const float m = __uint_as_float(bits << 16);
   if (page < 0 || page >= c.n_pages) {
     if (tid == 0) raise_flag(st, FLAG_BAD_CACHE);
   } else {
@@ -105,20 +159,12 @@ __global__ void __launch_bounds__(APPEND_THREADS)
     if (tid == 0) c.scales[blk] = m / 127.f;
     int8_t* out = c.codes + blk * c.block * c.d;
     // a maximum whose reciprocal is not a normal number is scaled up first
-    const float up = m < 0x1p-100f ? 0x1p100f : 1.f, mu = m * up, rm = 1.f / mu;
+    const float up = m < 0x1p-100f ? 0x1p100f : 1.f, mu = m * up, rm = 1.f / mu, k127 = 127.f / mu;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int e = tid + i * APPEND_THREADS;
       if (e >= nv) continue;
-      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-      uint32_t o[2] = {0, 0};
-      if (m > 0.f)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float f = q & 1 ? bf16hi(w[q >> 1]) : bf16lo(w[q >> 1]);
-          o[q >> 2] |= (uint32_t)(uint8_t)(int8_t)nearest_code(f * up, mu, rm) << (8 * (q & 3));
-        }
-      *reinterpret_cast<uint2*>(out + (size_t)e * 8) = make_uint2(o[0], o[1]);
+      *reinterpret_cast<uint2*>(out + (size_t)e * 8) = m > 0.f ? codes_of(u[i], up, mu, rm, k127) : make_uint2(0, 0);
     }
   }
   // The new tokens of the last two blocks go to the tail.  Only the first
