@@ -42,7 +42,7 @@ __device__ __forceinline__ int v_at(int t, int c) {
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -266,19 +266,25 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
       // ---- scores: row g of tile a is token 16 a + g, column c query row c
       float sc[NT][2][4] = {};
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+      for (int e = 0; e < KL; ++e) {
+        uint32_t kw[2][2][4];  // of either run, tokens g and g + 8
 #pragma unroll
-        for (int e = 0; e < KL; ++e) {
-          const uint4 lo = *reinterpret_cast<const uint4*>(src + k_at<D>(16 * a + g, 4 * e + j));
-          const uint4 hi = *reinterpret_cast<const uint4*>(src + k_at<D>(16 * a + 8 + g, 4 * e + j));
-          const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t k[4] = {codes_even(lw[i]), codes_even(hw[i]), codes_odd(lw[i]), codes_odd(hw[i])};
+          for (int o = 0; o < 2; ++o) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + k_at<D>(16 * a + 8 * o + g, 4 * e + j));
+            kw[a][o][0] = v.x, kw[a][o][1] = v.y, kw[a][o][2] = v.z, kw[a][o][3] = v.w;
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {  // the runs' chains side by side
+            const uint32_t k[4] = {codes_even(kw[a][0][i]), codes_even(kw[a][1][i]), codes_odd(kw[a][0][i]),
+                                   codes_odd(kw[a][1][i])};
 #pragma unroll
             for (int t = 0; t < NT; ++t) mma_f16(sc[t][a], k, qb[t][4 * e + i][0], qb[t][4 * e + i][1]);
           }
-        }
+      }
       const bool whole = live[0] && live[1] && pos0 + WARP_TOKENS - 1 <= all_see;
       uint32_t pb[NT][2][2];
 #pragma unroll
