@@ -13,18 +13,22 @@ namespace {
 using namespace tc;
 
 constexpr int T_ROWS = 256;  // query rows of an item: two tiles of 128
-// Warps: 0-3 softmax and products of tile 0, 4-7 of tile 1, 8-11 bring the
-// keys and values.  Twelve, so that a thread may hold 168 registers.
-constexpr int T_WARPS = 12, W_KEYS = 8;
+// Warps: 0-3 softmax of tile 0, 4-7 of tile 1, 8-10 bring the keys, 11 issues
+// the products, 12-15 bring the values.
+constexpr int T_WARPS = 16, W_KEYS = 8, W_MMA = 11, W_VALUES = 12;
+constexpr int KEY_WARPS = W_MMA - W_KEYS;
 constexpr int T_THREADS = T_WARPS * 32;
 // Units that an item counts for beside its own, when the work is cut: its
-// query rows, first scales and results are worth about four (one prompt of
-// 4096 tokens, 32 heads on 8: 433 us with none, 252 with two, 202 with five;
-// two prompts behind contexts 335, 324, 315, and 327 with eight).
-constexpr int ITEM_COST = 4;
+// query rows, first scales and results take as long as about three (two
+// prompts behind contexts: 285.3 us with two, 285.6 with three, 289.5 with
+// four, 293 with five; one prompt of 4096 tokens, 32 heads on 8: 183, 175, 178,
+// 180).
+constexpr int ITEM_COST = 3;
 constexpr int SC_RING = 4;   // tiles whose scales are kept
 constexpr uint64_t WAIT_NS = 2000000000ull;
-constexpr float GROWTH = 8.f;  // how far (log2) a row's weights may outgrow 1 before its sums are rescaled
+// What a row's weights of 64 tokens may add up to before its sums are rescaled:
+// none is then above it, and if they exceed it the largest is above 4.
+constexpr float LIMIT = 256.f;
 
 // One CTA's part of an item: units u0 .. u1 - 1 of it.
 struct Piece {
@@ -40,20 +44,21 @@ struct Piece {
 struct Walk {
   int64_t x;
   int s, qt, h, u;
+  Seq q;  // sequence s
   Piece P;
   int more;
 };
 
 struct TileShared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], o_full[2], drain[2];
-  uint64_t sc_full[SC_RING];
+  uint64_t s_full[2], q_full[2], drain;  // of a tile
+  uint64_t p_full[2][2], o_step[2][2];         // of its halves
+  uint64_t sc_full[SC_RING], raw_full[2][UNIT / 16];
   float sc_k[SC_RING][8], sc_log[SC_RING][8], sc_inv[SC_RING][8], sc_ref[SC_RING];
   float red[4];
   uint32_t arrived[2];
   uint32_t tmem;
   int abort;
-  int issuing;  // 1 while one tile's thread hands its products over
   int64_t scratch[T_WARPS + 2];
   Work work;
   Walk walk[T_WARPS];
@@ -61,13 +66,15 @@ struct TileShared {
 
 
 // The next piece of the warp's walk into W.P; false at the end.
+// ALONE: called by one thread of a warp.
+template <bool ALONE = false>
 __device__ __forceinline__ bool next_piece(const AttnParams& p, const Work& w, Walk& W) {
-  __syncwarp();  // every lane is done with the last piece
-  if ((threadIdx.x & 31) == 0) {
+  if (!ALONE) __syncwarp();  // every lane is done with the last piece
+  if (ALONE || (threadIdx.x & 31) == 0) {
     Piece& P = W.P;
     W.more = 0;
     while (W.x < w.x1 && !W.more) {
-      const Seq q = load_seq(p, W.s);
+      const Seq q = W.q;
       P.row = q.row, P.new_rows = q.n, P.len = q.len;
       P.s = W.s, P.qt = W.qt, P.h = W.h;
       P.seen = tile_seen<T_ROWS>(p, q, W.qt);
@@ -85,13 +92,13 @@ __device__ __forceinline__ bool next_piece(const AttnParams& p, const Work& w, W
         W.h = 0;
         if (++W.qt == q_tiles<T_ROWS>(p, q)) {
           W.qt = 0;
-          do ++W.s;
-          while (load_seq(p, W.s).n == 0);  // x < x1 <= total: a later sequence has rows
+          do W.q = load_seq(p, ++W.s);
+          while (W.q.n == 0);  // x < x1 <= total: a later sequence has rows
         }
       }
     }
   }
-  __syncwarp();
+  if (!ALONE) __syncwarp();
   return W.more != 0;
 }
 
@@ -157,26 +164,41 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-__device__ __forceinline__ void named_barrier(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+template <class T>
+__device__ __forceinline__ T* shfl_ptr(T* x, int lane) {
+  return reinterpret_cast<T*>(__shfl_sync(~0u, (unsigned long long)x, lane));
+}
+template <int THREADS>
+__device__ __forceinline__ void named_barrier(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
+}
 
 // The work is cut as in the streaming kernel, over items of 256 query rows
 // (a position's heads next to each other) and units of 128 tokens.
 //
-// Four warps bring the keys and values of each unit, copied one unit ahead,
-// and store them as fp16 numbers in the swizzled operand layout: the
-// keys' codes raw, as (c + 128) 2^-24 (128 2^-24 times the query row's sum
-// comes off the score), the values' as c itself, transposed.  Two groups of
-// four warps own a tile of 128 rows each: one thread issues S = Q K^T and
-// O += P V, and while one tile's weights are being taken the tensor cores
-// work for the other.  A thread owns a row: S comes from TMEM and P goes back
-// over it as fp16, the second product's A operand, while O stays in TMEM for
-// all units.  Weights are taken against the maximum so far, in one pass over
-// S; only if one would outgrow 2^8 are O and the sums rescaled and the pass
-// repeated.
+// Three warps bring the keys and four the values of each unit, copied one unit
+// ahead by bulk copies, and store them as fp16 numbers in the swizzled operand
+// layout: the keys' codes raw, as (c + 128) 2^-24 (128 2^-24 times the query
+// row's sum comes off the score), the values' as c itself, transposed.  One
+// thread issues S = Q K^T and O += P V for two tiles of 128 rows.  The weights
+// come in halves of 64 tokens, so that a half's O += P V runs beside the
+// softmax of the next and a softmax thread needs few registers; S is asked for
+// whole, since with 64 columns Q would be read twice as often as the tensor
+// cores allow (342 us against 305).  A softmax thread owns a row: S comes from
+// TMEM and P goes back over it as fp16, the second product's A operand, while
+// O stays in TMEM for all units.  Weights are taken against the maximum so
+// far, in one pass over S; only if a half's add up to more than LIMIT are O and
+// the sums rescaled and the pass repeated.
+//
+// Two prompts of 2600 tokens behind contexts of up to 3000, 32 heads on 8:
+// 286 us, 266 GFLOP, 0.48 of the measured bf16 rate; one prompt of 4096 tokens:
+// 175 us.  No unit is full: a unit takes some 4000 clocks, of which the tensor
+// cores work 2050; the rest is the softmax's chain and the conversion of the
+// codes, which run beside each other.
 //
 // Scales: the key scale of a run of 16 tokens multiplies the fp32 scores.  The
 // value scale vs, relative to the item's largest, enters the weights through
-// its logarithm: P = 2^(s + log2 vs - M), at most 2^8 whatever the scales
+// its logarithm: P = 2^(s + log2 vs - M), at most LIMIT whatever the scales
 // are, and the softmax's sum takes each run's sum of P back by 1 / vs.
 template <int D>
 __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnParams p) {
@@ -198,24 +220,29 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     if (lane == 0) {
       Walk& W = S.walk[warp];
       W.x = found.x0, W.s = found.s, W.qt = found.qt, W.h = found.h, W.u = found.u;
+      W.q = load_seq(p, found.s);
     }
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.k_full[i], 4);  // one arrival a warp
-      mbar_init(&S.k_empty[i], 2);  // released for either tile
+      mbar_init(&S.k_full[i], KEY_WARPS);  // one arrival a warp
+      mbar_init(&S.k_empty[i], 1);
       mbar_init(&S.v_full[i], 4);
-      mbar_init(&S.v_empty[i], 2);
+      mbar_init(&S.v_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.o_full[i], 1);
-      mbar_init(&S.drain[i], 1);
+      mbar_init(&S.p_full[i][0], 4);
+      mbar_init(&S.p_full[i][1], 4);
+      mbar_init(&S.q_full[i], 4);
+      mbar_init(&S.o_step[i][0], 1);
+      mbar_init(&S.o_step[i][1], 1);
     }
     for (int i = 0; i < SC_RING; ++i) mbar_init(&S.sc_full[i], 1);
+    for (int i = 0; i < 2 * UNIT / 16; ++i) mbar_init(&S.raw_full[0][i], 1);
+    mbar_init(&S.drain, 1);
     S.abort = 0;
-    S.issuing = 0;
     fence_mbar_init();
   }
-  if (warp == W_KEYS) tmem_alloc(&S.tmem, 512);
+  if (warp == W_MMA) tmem_alloc(&S.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -236,107 +263,81 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
 
   const Piece& P = S.walk[warp].P;
   if (warp < W_KEYS) {
-    // ------------------------------------------------- softmax and products
+    // ------------------------------------------------------------- softmax
     const int X = warp >> 2, r = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the lanes
     const uint32_t s_addr = lanes + S_COL + 128 * X, o_addr = lanes + O_COL + D * X;
     unsigned char* q_tile = sq + X * Smem<D>::Q;
-    uint32_t units_done = 0, tiles = 0, pieces = 0;  // of the CTA; of this tile
+    uint32_t units_done = 0, tiles = 0;  // of the CTA; of this tile
     bool ok = true;
-    constexpr uint32_t ID_S = idesc_f16(128, UNIT), ID_O = idesc_f16(128, D);
-    // The products, by one thread a tile, elected in its first warp.  A tile hands over all it has at
-    // once, O += P V of its unit and S of the next, and the other waits: taken
-    // in turns product by product, both tiles' would end at the same time, and
-    // both softmaxes run while the tensor cores idle.
-    auto lock = [&]() {
-      uint64_t t0 = 0;
-      for (uint32_t i = 1; atomicCAS(&S.issuing, 0, 1) != 0; ++i) {
-        if (i & 63) continue;
-        const uint64_t now = globaltimer();
-        if (t0 == 0) t0 = now;
-        if (*abort || now - t0 > WAIT_NS) return false;
-      }
-      return true;
-    };
-    auto unlock = [&]() { atomicExch(&S.issuing, 0); };
-    auto issue_scores = [&](uint32_t it) {
-      const uint32_t q0 = smem_u32(q_tile), k0 = smem_u32(sk + (it & 1) * Smem<D>::K);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
-        mma_bf16(tmem + S_COL + 128 * X, desc_sw128(q0 + off), desc_sw128(k0 + off), ID_S, k > 0);
-      }
-      mma_commit(&S.s_full[X]);
-      mma_commit(&S.k_empty[it & 1]);
-    };
-    auto issue_outputs = [&](uint32_t it, bool first) {
-      const uint32_t v0 = smem_u32(sv + (it & 1) * Smem<D>::V);
-#pragma unroll
-      for (int k = 0; k < UNIT / 16; ++k)
-        mma_bf16_ta(tmem + O_COL + D * X, tmem + S_COL + 128 * X + 8 * k, desc_sw128(v0 + (k >> 2) * (D * 128) + (k & 3) * 32),
-                    ID_O, !first || k > 0);
-      mma_commit(&S.v_empty[it & 1]);
-    };
-    // units that this tile's rows do not see are given back as they come
-    auto release = [&](uint32_t it) {
-      if (wait(&S.k_full[it & 1], (it >> 1) & 1, 59)) mbar_arrive(&S.k_empty[it & 1]);
-      if (wait(&S.v_full[it & 1], (it >> 1) & 1, 60)) mbar_arrive(&S.v_empty[it & 1]);
-    };
     while (ok && next_piece(p, S.work, S.walk[warp])) {
       const int last = min(P.u1, P.n[X]);
       if (P.u0 >= last) {
-        if (r == 0)
-          for (int u = P.u0; u < P.u1; ++u) release(units_done + u - P.u0);
         units_done += P.u1 - P.u0;
         continue;
       }
-      const int64_t rr = (int64_t)T_ROWS * P.qt + 128 * X + r, rows = (int64_t)P.new_rows * p.G;
-      const bool live_row = rr < rows;
-      const int qi = live_row ? (int)(rr / p.G) : 0, head = live_row ? P.h * p.G + (int)(rr % p.G) : 0;
+      // The thread's row is a token and a head.
+      const uint32_t first_row = (uint32_t)T_ROWS * P.qt + 128 * X, G = p.G;
+      const int token0 = first_row / G, token = (first_row + r) / G, head = P.h * (int)G + (first_row + r) % G;
+      const bool live_row = token < P.new_rows;
       const int before = P.len - P.new_rows;
       // rows past the last store nothing, so they may see all
-      const int limit = live_row ? before + qi : INT_MAX;
-      const int first_limit = before + (int)(((int64_t)T_ROWS * P.qt + 128 * X) / p.G);
-      // ---- the warp's 32 query rows, scaled by a power of two into fp16: a
-      // row's D / 8 pieces in neighbouring lanes, so that all loads of eight
-      // are in flight together
-      float f, off;  // score per product; what the keys' 128s add to a product
+      const int limit = live_row ? before + token : INT_MAX;
+      const int first_limit = before + token0;
+      // ---- the warp's 32 query rows, scaled by a power of two into fp16, in
+      // their places in the tile; D / 8 neighbouring lanes take a row, whose
+      // address its own thread has.
+      constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes of a row, rows of a turn
+      const int c8 = lane % LPR, k8 = 32 * (warp & 3) + lane / LPR;
+      auto q_place = [&](int k) { return q_tile + (c8 >> 3) * (128 * 128) + sw128_off(k, c8 & 7); };
+      float f = 0.f, off = 0.f;  // score per product; what the keys' 128s add to a product
       {
-        constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes of a row, rows of a load
-        const int c = lane % LPR;
-        f = off = 0.f;
+        const uint16_t* row = live_row ? p.q + (int64_t)(P.row + token) * p.q_stride + head * D : nullptr;
+#pragma unroll 1
+        for (int b = 0; b < 32; b += 8 * RPL) {
+          const uint16_t* src[8];
 #pragma unroll
+          for (int i = 0; i < 8; ++i) src[i] = shfl_ptr(row, b + i * RPL + lane / LPR);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (src[i])
+              cp_async16(q_place(k8 + b + i * RPL), src[i] + 8 * c8);
+            else
+              *reinterpret_cast<uint4*>(q_place(k8 + b + i * RPL)) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();  // a lane converts what it copied
+#pragma unroll 1
         for (int b = 0; b < 32; b += 8 * RPL) {
           uint4 v[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t rr = (uint32_t)T_ROWS * P.qt + 128 * X + 32 * (warp & 3) + b + i * RPL + lane / LPR;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (rr < (uint32_t)rows)
-              v[i] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(P.row + (int)(rr / (uint32_t)p.G)) * p.q_stride +
-                                                     (size_t)(P.h * p.G + (int)(rr % (uint32_t)p.G)) * D + 8 * c);
-          }
+          for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(q_place(k8 + b + i * RPL));
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            float m = 0.f, sum = 0.f;
+            uint32_t m = 0;  // magnitudes, as whole numbers
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16lo(x[e])), fabsf(bf16hi(x[e]))));
+            for (int e = 0; e < 4; ++e) m = __vmaxu2(m, x[e] & 0x7FFF7FFFu);
 #pragma unroll
-            for (int o = 1; o < LPR; o *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-            // its largest magnitude goes to [2^14, 2^15); a negative scale goes
-            // into the row, so that f is not
-            const int ex = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
+            for (int o = 1; o < LPR; o *= 2) m = __vmaxu2(m, __shfl_xor_sync(~0u, m, o));
+            // the largest goes to [2^14, 2^15); a negative scale goes into the
+            // row, so that f is not
+            const int ex = min(max((int)(max(m >> 16, m & 0xFFFF) >> 7) - 127, -100), 127);
             const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), p.scale_log2);
-            auto two = [&](uint32_t a, uint32_t b, bool hi) {
-              const __half2 h = __floats2half2_rn((hi ? bf16hi(a) : bf16lo(a)) * up, (hi ? bf16hi(b) : bf16lo(b)) * up);
-              sum += __low2float(h) + __high2float(h);
-              return half2_bits(h);
+            // the sum is that of the rows before they are rounded: only what
+            // is 2^-29 of the largest and less is
+            float2 part = make_float2(0.f, 0.f);
+            auto two = [&](float a, float b) {
+              const float2 y = make_float2(a * up, b * up);
+              part = add2(part, y);
+              return half2_bits(__float22half2_rn(y));
             };
             // channels in the keys' order: 0 2 1 3 of every four
-            const int row = 32 * (warp & 3) + b + i * RPL + lane / LPR;
-            *reinterpret_cast<uint4*>(q_tile + (c >> 3) * (128 * 128) + sw128_off(row, c & 7)) =
-                make_uint4(two(x[0], x[1], false), two(x[0], x[1], true), two(x[2], x[3], false), two(x[2], x[3], true));
+            *reinterpret_cast<uint4*>(q_place(k8 + b + i * RPL)) =
+                make_uint4(two(bf16lo(x[0]), bf16lo(x[1])), two(bf16hi(x[0]), bf16hi(x[1])), two(bf16lo(x[2]), bf16lo(x[3])),
+                           two(bf16hi(x[2]), bf16hi(x[3])));
+            float sum = part.x + part.y;
 #pragma unroll
             for (int o = 1; o < LPR; o *= 2) sum += __shfl_xor_sync(~0u, sum, o);
             // to the lanes that own the rows
@@ -349,171 +350,182 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
           }
         }
         fence_async_smem();
-        named_barrier(2 + X);
-        if ((warp & 3) == 0) {
-          if (!(ok = wait_warp(&S.k_full[units_done & 1], (units_done >> 1) & 1, 57))) break;
-          tc_fence_after();
-          if (elect_one() && lock()) {
-            issue_scores(units_done);
-            unlock();
-          }
-          __syncwarp();
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.q_full[X]);
       }
       float M = -INFINITY, l = 0.f, ref = 1.f;
-      for (int u = P.u0; u < last; ++u) {
+      for (int u = P.u0; u < last && ok; ++u, ++tiles) {
         const uint32_t it = units_done + u - P.u0, slot = it % SC_RING;
+        if (!(ok = wait_warp(&S.s_full[X], tiles & 1, 51))) break;
         // the scales' barrier second: scores imply that its phase is this
         // unit's, not one of an earlier turn
-        if (!(ok = wait_warp(&S.s_full[X], tiles & 1, 51))) break;
         if (!(ok = wait_warp(&S.sc_full[slot], (it / SC_RING) & 1, 52))) break;
-        ++tiles;
         tc_fence_after();
-        const bool masked = u * UNIT + UNIT - 1 > first_limit;
-        const int see = limit - u * UNIT;  // the last token of the unit that this row sees
-        ref = S.sc_ref[slot];
-        if (masked) {  // the causal edge: what a row does not see becomes -inf in place
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(s_addr + 32 * c, v);
-            tmem_ld_wait();
-            ld32_fence(v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 32 * c + i <= see ? v[i] : 0xFF800000u;
-            tmem_st<32>(s_addr + 32 * c, v);
-          }
-          tmem_st_wait();
-        }
-        // Scores are S a + log2 vs - off a, a >= 1e-30 so that -inf stays what
-        // it is.
-        if (__any_sync(~0u, M == -INFINITY)) {  // a first unit: the row's maximum
-          float top = -INFINITY;
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t sh = s_addr + 64 * half;
+          const float *sck = S.sc_k[slot] + 4 * half, *scl = S.sc_log[slot] + 4 * half, *sci = S.sc_inv[slot] + 4 * half;
+          const int pos0 = u * UNIT + 64 * half;
+          const int see = limit - pos0;  // the last token of the half that this row sees
+          ref = S.sc_ref[slot];
+          if (pos0 + 63 > first_limit) {  // the causal edge: what a row does not see becomes -inf in place
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(s_addr + 32 * c, v);
-            tmem_ld_wait();
-            ld32_fence(v);
-#pragma unroll
-            for (int h2 = 0; h2 < 2; ++h2) {
-              float mx = -INFINITY;
-#pragma unroll
-              for (int i = 16 * h2; i < 16 * h2 + 16; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
-              const float a = fmaxf(f * S.sc_k[slot][2 * c + h2], 1e-30f);
-              top = fmaxf(top, fmaf(mx, a, fmaf(-off, a, S.sc_log[slot][2 * c + h2])));
-            }
-          }
-          if (M == -INFINITY) M = top;  // nothing summed yet: nothing to rescale
-        }
-        // ---- the weights against the maximum so far; again, with the sums
-        // rescaled, if a row's outgrow 2^GROWTH (twice at most: scores beyond
-        // 2^24, whose units are above 1, may leave more than that)
-        uint32_t w[4][16];
-        float add;
-        for (int again = 0;; ++again) {
-          const float at = M == -INFINITY ? 0.f : M;
-          float most = -INFINITY;
-          add = 0.f;
-          uint32_t vb[2][32];
-          tmem_ld32(s_addr, vb[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&v)[32] = vb[c & 1];
-            tmem_ld_wait();
-            ld32_fence(v);
-            if (c < 3) tmem_ld32(s_addr + 32 * (c + 1), vb[(c + 1) & 1]);
-#pragma unroll
-            for (int h2 = 0; h2 < 2; ++h2) {
-              const float a = fmaxf(f * S.sc_k[slot][2 * c + h2], 1e-30f);
-              const float b = fmaf(-off, a, S.sc_log[slot][2 * c + h2] - at);
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
-                float2 z = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), make_float2(a, a),
-                                make_float2(b, b));
-                most = fmaxf(fmaxf(most, z.x), z.y);
-                z = make_float2(ex2(z.x), ex2(z.y));
-                sum = add2(sum, z);
-                w[c][i >> 1] = half2_bits(__float22half2_rn(z));
-              }
-              add = fmaf(sum.x + sum.y, S.sc_inv[slot][2 * c + h2], add);
-            }
-          }
-          if (again == 2 || !__any_sync(~0u, most > GROWTH)) break;
-          const float by = fmaxf(most, 0.f), drop = ex2(-by);
-          M += by;
-          l *= drop;
-          if (u > P.u0) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < 2; ++c) {
               uint32_t v[32];
-              tmem_ld32(o_addr + 32 * c, v);
+              tmem_ld32(sh + 32 * c, v);
               tmem_ld_wait();
               ld32_fence(v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * drop);
-              tmem_st<32>(o_addr + 32 * c, v);
+              for (int i = 0; i < 32; ++i) v[i] = 32 * c + i <= see ? v[i] : 0xFF800000u;
+              tmem_st<32>(sh + 32 * c, v);
+            }
+            tmem_st_wait();
+          }
+          // Scores are S a + log2 vs - off a, a >= 1e-30 so that -inf stays
+          // what it is.
+          auto largest = [&]() {
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[32];
+              tmem_ld32(sh + 32 * c, v);
+              tmem_ld_wait();
+              ld32_fence(v);
+#pragma unroll
+              for (int h2 = 0; h2 < 2; ++h2) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int i = 16 * h2; i < 16 * h2 + 16; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+                const float a = fmaxf(f * sck[2 * c + h2], 1e-30f);
+                top = fmaxf(top, fmaf(mx, a, fmaf(-off, a, scl[2 * c + h2])));
+              }
+            }
+            return top;
+          };
+          if (__any_sync(~0u, M == -INFINITY)) {  // nothing seen so far: the row's maximum
+            const float top = largest();
+            if (M == -INFINITY) M = top;  // nothing summed yet: nothing to rescale
+          }
+          // ---- the weights against the maximum so far; again, with the sums
+          // rescaled, if a row's outgrow LIMIT (twice at most: scores beyond
+          // 2^24, whose units are above 1, may leave more than that)
+          uint32_t w[2][16];
+          float add;
+          for (int again = 0;; ++again) {
+            const float at = M == -INFINITY ? 0.f : M;
+            add = 0.f;
+            float all = 0.f;
+            uint32_t vb[2][32];
+            tmem_ld32(sh, vb[0]);
+            tmem_ld32(sh + 32, vb[1]);
+            tmem_ld_wait();
+            ld32_fence(vb[0]);
+            ld32_fence(vb[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int h2 = 0; h2 < 2; ++h2) {
+                const float a = fmaxf(f * sck[2 * c + h2], 1e-30f);
+                const float b = fmaf(-off, a, scl[2 * c + h2] - at);
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
+                  float2 z = fma2(make_float2(__uint_as_float(vb[c][i]), __uint_as_float(vb[c][i + 1])),
+                                  make_float2(a, a), make_float2(b, b));
+                  z = make_float2(ex2(z.x), ex2(z.y));
+                  sum = add2(sum, z);
+                  w[c][i >> 1] = half2_bits(__float22half2_rn(z));
+                }
+                add = fmaf(sum.x + sum.y, sci[2 * c + h2], add);
+                all += sum.x + sum.y;
+              }
+            // no weight above the limit if their sum is not
+            if (again == 2 || !__any_sync(~0u, all > LIMIT)) break;
+            const float top = largest();  // by the whole warp
+            const float by = all > LIMIT ? fmaxf(top - at, 0.f) : 0.f, drop = ex2(-by);
+            M += by;
+            l *= drop;
+            if (u > P.u0 || half) {
+              // O is the first half's until its product has ended (the products
+              // before have: the unit's scores came after them)
+              if (half && !(ok = wait_warp(&S.o_step[X][0], tiles & 1, 53))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld32(o_addr + 32 * c, v);
+                tmem_ld_wait();
+                ld32_fence(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * drop);
+                tmem_st<32>(o_addr + 32 * c, v);
+              }
             }
           }
-        }
-        l += add;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_st<16>(s_addr + 16 * c, w[c]);
-        tmem_st_wait();
-        tc_fence_before();
-        named_barrier(2 + X);  // every row's weights are there
-        if ((warp & 3) == 0) {
-          const bool more = u + 1 < last;
-          if (!(ok = wait_warp(&S.v_full[it & 1], (it >> 1) & 1, 58))) break;
-          if (more && !(ok = wait_warp(&S.k_full[(it + 1) & 1], ((it + 1) >> 1) & 1, 57))) break;
-          tc_fence_after();
-          if (elect_one() && lock()) {
-            issue_outputs(it, u == P.u0);
-            if (more)
-              issue_scores(it + 1);
-            else
-              mma_commit(&S.o_full[X]);
-            unlock();
-          }
+          if (!ok) break;
+          l += add;
+          tmem_st<16>(sh, w[0]);
+          tmem_st<16>(sh + 16, w[1]);
+          tmem_st_wait();
+          tc_fence_before();
           __syncwarp();
+          if (lane == 0) mbar_arrive(&S.p_full[X][half]);
         }
       }
-      if (ok && r == 0)
-        for (int u = last; u < P.u1; ++u) release(units_done + u - P.u0);
       if (!ok) break;
       units_done += P.u1 - P.u0;
       // ---- the piece's sums
-      if (!(ok = wait_warp(&S.o_full[X], pieces & 1, 53))) break;
-      ++pieces;
+      if (!(ok = wait_warp(&S.o_step[X][1], (tiles - 1) & 1, 53))) break;
       tc_fence_after();
-      const int c0 = cta_of(S.work, P.first), c1 = cta_of(S.work, P.first + P.n[X] - 1);
-      const int cta = blockIdx.x;
-      uint16_t* dst = p.out + ((size_t)(P.row + qi) * p.hq + head) * D;
-      if (c0 == c1) {
-        const float k = l == 0.f ? 0.f : ref / l;
+      // Results go out through the rows' places in the query tile, which no
+      // product reads any more: whole rows a store instead of 32 pieces of 16
+      // bytes.
+      auto put = [&](int chunk, uint4 v) {
+        *reinterpret_cast<uint4*>(q_tile + (chunk >> 3) * (128 * 128) + sw128_off(r, chunk & 7)) = v;
+      };
+      auto write_out = [&]() {
+        __syncwarp();
+        uint16_t* row = live_row ? p.out + ((size_t)(P.row + token) * p.hq + head) * D : nullptr;
+#pragma unroll 1
+        for (int b = 0; b < 32; b += 8 * RPL) {
+          uint16_t* dst[8];
+          uint4 v[8];
 #pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dst[i] = shfl_ptr(row, b + i * RPL + lane / LPR);
+            v[i] = *reinterpret_cast<const uint4*>(q_place(k8 + b + i * RPL));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + 8 * c8) = v[i];
+        }
+        __syncwarp();
+      };
+      if (P.u0 == 0 && last == P.n[X]) {  // all of the tile's units
+        const float k = l == 0.f ? 0.f : ref / l;
+#pragma unroll 2
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
           tmem_ld32(o_addr + 32 * c, v);
           tmem_ld_wait();
           ld32_fence(v);
-          if (live_row)
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w[4];
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t w[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(v[i + 2 * e]) * k, __uint_as_float(v[i + 2 * e + 1]) * k);
-              *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(v[i + 2 * e]) * k, __uint_as_float(v[i + 2 * e + 1]) * k);
+            put(4 * c + i / 8, make_uint4(w[0], w[1], w[2], w[3]));
+          }
         }
         tc_fence_before();
+        write_out();
       } else {
         // a tile that spans CTAs: the last one to finish joins the parts in order
+        const int c0 = cta_of(S.work, P.first), c1 = cta_of(S.work, P.first + P.n[X] - 1);
         auto part = [&](int c) { return p.partials + (size_t)((2 * c + (c == c0)) * 2 + X) * partial_floats<D>(); };
-        float* mine = part(cta);
-#pragma unroll
+        float* mine = part(blockIdx.x);
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
           tmem_ld32(o_addr + 32 * c, v);
@@ -527,9 +539,9 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         mine[128 * D + r] = M;
         mine[128 * D + 128 + r] = l;
         __threadfence();
-        named_barrier(2 + X);
+        named_barrier<128>(2 + X);
         if (r == 0) S.arrived[X] = atomicAdd(p.counters + 2 * c0 + X, 1u);
-        named_barrier(2 + X);
+        named_barrier<128>(2 + X);
         if (S.arrived[X] == (uint32_t)(c1 - c0)) {
           __threadfence();
           if (r == 0) p.counters[2 * c0 + X] = 0;
@@ -552,46 +564,112 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
                 acc[4 * i + 2] = fmaf(v[i].z, drop, acc[4 * i + 2]), acc[4 * i + 3] = fmaf(v[i].w, drop, acc[4 * i + 3]);
               }
             }
-            if (live_row)
 #pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4*>(dst + d + i) =
-                    make_uint4(pack_bf16x2(acc[i], acc[i + 1]), pack_bf16x2(acc[i + 2], acc[i + 3]),
-                               pack_bf16x2(acc[i + 4], acc[i + 5]), pack_bf16x2(acc[i + 6], acc[i + 7]));
+            for (int i = 0; i < 32; i += 8)
+              put((d + i) / 8, make_uint4(pack_bf16x2(acc[i], acc[i + 1]), pack_bf16x2(acc[i + 2], acc[i + 3]),
+                                          pack_bf16x2(acc[i + 4], acc[i + 5]), pack_bf16x2(acc[i + 6], acc[i + 7])));
           }
+          write_out();
         }
       }
     }
-    // after a wait that gave up: the products in flight end before TMEM goes
-    if (*abort && r == 0) {
-      int never = 0;
-      mma_commit(&S.drain[X]);
-      mbar_wait(&S.drain[X], 0, &never, WAIT_NS);
+  } else if (warp == W_MMA) {
+    // ------------------------------------------------------------ products
+    if (elect_one()) {
+      constexpr uint32_t ID_S = idesc_f16(128, UNIT), ID_O = idesc_f16(128, D);
+      uint32_t it = 0, q_turn[2] = {0, 0}, p_turn[2] = {0, 0};
+      bool ok = true;
+      auto scores = [&](int X, uint32_t unit) {
+        const uint32_t q0 = smem_u32(sq + X * Smem<D>::Q), k0 = smem_u32(sk + (unit & 1) * Smem<D>::K);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = (k >> 2) * (128 * 128) + (k & 3) * 32;
+          mma_bf16(tmem + S_COL + 128 * X, desc_sw128(q0 + o), desc_sw128(k0 + o), ID_S, k > 0);
+        }
+        mma_commit(&S.s_full[X]);
+      };
+      auto outputs = [&](int X, uint32_t unit, int half, bool first) {
+        const uint32_t v0 = smem_u32(sv + (unit & 1) * Smem<D>::V) + half * (D * 128);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_bf16_ta(tmem + O_COL + D * X, tmem + S_COL + 128 * X + 64 * half + 8 * k, desc_sw128(v0 + k * 32), ID_O,
+                      !first || k > 0);
+        mma_commit(&S.o_step[X][half]);
+      };
+      while (ok && next_piece<true>(p, S.work, S.walk[warp])) {
+        const int last[2] = {min(P.u1, P.n[0]), min(P.u1, P.n[1])};
+        // unit `it` is the piece's first
+#pragma unroll
+        for (int X = 0; X < 2; ++X)
+          if (ok && P.u0 < last[X]) ok = wait(&S.q_full[X], q_turn[X]++ & 1, 56);
+        if (!ok || !(ok = wait(&S.k_full[it & 1], (it >> 1) & 1, 57))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int X = 0; X < 2; ++X)
+          if (P.u0 < last[X]) scores(X, it);
+        mma_commit(&S.k_empty[it & 1]);
+        for (int u = P.u0; u < P.u1 && ok; ++u, ++it) {
+          if (!(ok = wait(&S.v_full[it & 1], (it >> 1) & 1, 58))) break;
+          const bool more = u + 1 < P.u1;
+          bool have_k = false;
+#pragma unroll
+          for (int X = 0; X < 2; ++X)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (!ok || u >= last[X]) continue;
+              // one barrier a half: the softmax may be a half ahead
+              if (!(ok = wait(&S.p_full[X][half], p_turn[X] & 1, 59))) continue;
+              p_turn[X] += half;
+              tc_fence_after();
+              outputs(X, it, half, u == P.u0 && half == 0);
+              if (half && u + 1 < last[X]) {
+                if (!have_k && !(ok = wait(&S.k_full[(it + 1) & 1], ((it + 1) >> 1) & 1, 60))) continue;
+                have_k = true;
+                tc_fence_after();
+                scores(X, it + 1);
+              }
+            }
+          mma_commit(&S.v_empty[it & 1]);
+          if (more) {
+            if (!have_k && ok) ok = wait(&S.k_full[(it + 1) & 1], ((it + 1) >> 1) & 1, 60);
+            mma_commit(&S.k_empty[(it + 1) & 1]);
+          }
+        }
+      }
+      if (!ok) {  // after a wait that gave up: the products in flight end before TMEM goes
+        int never = 0;
+        mma_commit(&S.drain);
+        mbar_wait(&S.drain, 0, &never, WAIT_NS);
+      }
     }
   } else {
-    // ------------------------------------------------------ keys and values
-    // A thread copies and converts the same pieces of 16 codes, one unit
-    // ahead, through its own places in `raw`.
-    const int w = warp & 3, ct = tid & 127;
-    // keys: tokens 32 w + 8 (i & 3) + lane % 8, piece lane / 8 + 4 (i >> 2);
-    // values: tokens 8 vo + i, piece vc
-    constexpr int NK = D / 16;
-    const int vo = D == 128 ? (lane & 7) + 8 * (w >> 1) : (lane & 7) + 8 * (w & 1);
-    const int vc = D == 128 ? (lane >> 3) + 4 * (w & 1) : lane >> 3;
-    const bool has_v = D == 128 || w < 2;
-    const int64_t page_bytes = (int64_t)hkv * p.c.block * D, vstep = p.c.n_pages * page_bytes;
-    unsigned char* raw_k = raw + ct * 16;
-    unsigned char* raw_v = raw + UNIT * D + (D == 128 ? ct : ct & 63) * 16;
-    constexpr int K_STEP = 2048, V_STEP = D == 128 ? 2048 : 1024;
-    const int k_lane = (lane & 7) * D + 16 * (lane >> 3), v_lane = (vo & 1) * 8 * D + 16 * vc;
-    // where the pieces go: keys in row lane % 8 of an 8-row group, 16-byte
-    // chunks 2 c and 2 c + 1; values, transposed, in chunk vo % 8 of 16 rows
-    const uint32_t k_to[2] = {sw128_off(lane & 7, 2 * (lane >> 3)), sw128_off(lane & 7, 2 * (lane >> 3) + 1)};
+    // ------------------------------------------------------- keys or values
+    // The codes come in runs of 16 tokens, one bulk copy each, a unit ahead:
+    // a warp waits for its own runs, converts them and asks for the next
+    // unit's into the same places.
+    const bool keys = warp < W_VALUES;
+    const int w = keys ? warp - W_KEYS : warp - W_VALUES;
+    // keys: runs w, w + KEY_WARPS, ..; values: runs 2 w and 2 w + 1
+    constexpr int RUN = 16 * D, RUNS = UNIT / 16;
+    const int run0 = keys ? w : 2 * w, run_step = keys ? KEY_WARPS : 1, run1 = keys ? RUNS : 2 * w + 2;
+    const int64_t page_bytes = (int64_t)hkv * p.c.block * D;
+    unsigned char* mine = raw + (keys ? 0 : UNIT * D);
+    uint64_t* came = S.raw_full[keys ? 0 : 1];
+    // keys: D / 16 neighbouring lanes take a token's pieces of 16 codes, one
+    // half (k_flip) before the other, which keeps loads and stores of eight
+    // lanes in different banks
+    constexpr int PIECES = D / 16, ROWS = 32 / PIECES;
+    const int kc = lane % PIECES, kr = lane / PIECES;
+    const int k_flip = D == 128 ? ((kc >> 2) ^ kr) & 1 : (kr >> 1) & 1;
+    // values: 8 tokens vo of the warp's 32, piece vc; words (q + v_turn) % 4 of
+    // it, again for the banks
+    const int vo = 4 * w + (lane & 3), vc = (lane >> 2) % PIECES;
+    const int v_turn = (lane & 3) + vc + (D == 128 ? 0 : 2 * (lane >> 4));
     uint32_t it = 0;
     bool ok = true;
     while (ok && next_piece(p, S.work, S.walk[warp])) {
       const int32_t* table = p.c.table + (size_t)P.s * p.c.max_blocks;
-      const int8_t* codes = p.c.codes + (int64_t)P.h * p.c.block * D;
+      const int8_t* codes = p.c.codes + (keys ? 0 : p.c.n_pages * page_bytes) + (int64_t)P.h * p.c.block * D;
       const float* scales = p.c.scales + P.h;
       const int seen = P.seen, end = P.u1;
       auto page_at = [&](int pos) {
@@ -608,52 +686,39 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       auto scale_of = [&](int page, int64_t isv) {
         return page < 0 ? 0.f : __ldg(scales + (isv * p.c.n_pages + page) * hkv);
       };
-      // a run without a page is read from page 0: its weights are 0
-      auto load_k = [&](int u, int pages) {
-        if (u < end)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // the warp's two runs
-            const int page = max(__shfl_sync(~0u, pages, 2 * w + e), 0);
-            const int8_t* src = codes + page * page_bytes + ((u * UNIT + 16 * (2 * w + e)) & (p.c.block - 1)) * D + k_lane;
-#pragma unroll
-            for (int c = 0; c < NK / 4; ++c)
-#pragma unroll
-              for (int o = 0; o < 2; ++o) cp_async16(raw_k + (4 * c + 2 * e + o) * K_STEP, src + 8 * o * D + 64 * c);
-          }
-        cp_async_commit();
-      };
-      auto load_v = [&](int u, int pages) {
-        if (u < end) {
-          const int page = max(__shfl_sync(~0u, pages, vo >> 1), 0);
-          const int8_t* src = codes + vstep + page * page_bytes + ((u * UNIT + 16 * (vo >> 1)) & (p.c.block - 1)) * D + v_lane;
-          if (has_v)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) cp_async16(raw_v + i * V_STEP, src + i * D);
-        }
-        cp_async_commit();
+      // one run of unit u < end, by one lane; a run without a page is read from
+      // page 0: its weights are 0
+      auto fetch = [&](int u, int run, int page) {
+        mbar_arrive_expect_tx(&came[run], RUN);
+        bulk_copy_g2s(mine + run * RUN, codes + max(page, 0) * page_bytes + ((u * UNIT + 16 * run) & (p.c.block - 1)) * D, RUN,
+                      &came[run]);
       };
       // pages come two units ahead, codes and scales one
       int pages = pages_of(P.u0), next_pages = pages_of(P.u0 + 1);
-      load_k(P.u0, pages);
-      load_v(P.u0, pages);
-      float ks = scale_of(pages, 0), vs = scale_of(pages, 1);
-      // the item's largest value scale; 0 if every value is, and then so is the
-      // result
-      float vref = 0.f;
-      for (int b = ct; b << p.block_log2 < seen; b += 128) vref = fmaxf(vref, scale_of(page_at(b << p.block_log2), 1));
+      if (lane >= run0 && lane < run1 && (lane - run0) % run_step == 0) fetch(P.u0, lane, pages);
+      float ks = 0.f, vs = 0.f, vref = 0.f, vref_log = 0.f;
+      if (keys) {
+        ks = scale_of(pages, 0);
+        vs = scale_of(pages, 1);
+        // the item's largest value scale; 0 if every value is, and then so is
+        // the result
+        for (int b = 32 * w + lane; b << p.block_log2 < seen; b += 32 * KEY_WARPS)
+          vref = fmaxf(vref, scale_of(page_at(b << p.block_log2), 1));
 #pragma unroll
-      for (int o = 16; o; o >>= 1) vref = fmaxf(vref, __shfl_xor_sync(~0u, vref, o));
-      named_barrier(1);  // the last item's values are read
-      if (lane == 0) S.red[w] = vref;
-      named_barrier(1);
-      vref = fmaxf(fmaxf(S.red[0], S.red[1]), fmaxf(S.red[2], S.red[3]));
-      const float vref_log = vref > 0.f ? __log2f(vref) : 0.f;
+        for (int o = 16; o; o >>= 1) vref = fmaxf(vref, __shfl_xor_sync(~0u, vref, o));
+        named_barrier<32 * KEY_WARPS>(1);  // the last item's values are read
+        if (lane == 0) S.red[w] = vref;
+        named_barrier<32 * KEY_WARPS>(1);
+        vref = fmaxf(fmaxf(S.red[0], S.red[1]), S.red[2]);
+        vref_log = vref > 0.f ? __log2f(vref) : 0.f;
+      }
       for (int u = P.u0; u < end; ++u, ++it) {
         const uint32_t st = it & 1, par = ((it >> 1) & 1) ^ 1;
-        if (!(ok = wait_warp(&S.k_empty[st], par, 54))) break;
-        // the slot's last unit, SC_RING back, is past every softmax thread: the
-        // products that freed this K stage came after its weights
-        if (w == 0 && lane < 8) {
+        int run = run0;
+        ok = wait_warp(keys ? &S.k_empty[st] : &S.v_empty[st], par, 54);
+        if (ok && keys && w == 0 && lane < 8) {
+          // the slot's last unit, SC_RING back, is past every softmax thread:
+          // the products that freed this K stage came after its weights
           const uint32_t slot = it % SC_RING;
           const float lg = pages < 0 ? -INFINITY : fmaxf(__log2f(vs) - vref_log, -60.f);
           S.sc_k[slot][lane] = ks;
@@ -663,62 +728,77 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
           __syncwarp(0xFF);
           if (lane == 0) mbar_arrive(&S.sc_full[slot]);
         }
-        cp_async_wait<1>();
-        {
-          unsigned char* dst = sk + st * Smem<D>::K + 4 * w * 1024;
-#pragma unroll 4
-          for (int i = 0; i < NK; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(raw_k + i * K_STEP);
-            unsigned char* rows = dst + (i & 3) * 1024 + (i >> 2) * (128 * 128);
-            *reinterpret_cast<uint4*>(rows + k_to[0]) =
-                make_uint4(codes_even(v.x), codes_odd(v.x), codes_even(v.y), codes_odd(v.y));
-            *reinterpret_cast<uint4*>(rows + k_to[1]) =
-                make_uint4(codes_even(v.z), codes_odd(v.z), codes_even(v.w), codes_odd(v.w));
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.k_full[st]);
-        load_k(u + 1, next_pages);
-        const int after_pages = pages_of(u + 2);
-        if (w == 0) {
-          ks = scale_of(next_pages, 0);
-          vs = scale_of(next_pages, 1);
-        }
-        if (!(ok = wait_warp(&S.v_empty[st], par, 55))) break;
-        cp_async_wait<1>();
-        if (has_v) {
-          unsigned char* dst = sv + st * Smem<D>::V + (vo >> 3) * (D * 128) + 2 * vc * 1024;
-#pragma unroll 2
-          for (int q = 0; q < 4; ++q) {
-            uint32_t x[8];
+        for (; ok && run < run1; run += run_step) {
+          if (!(ok = wait_warp(&came[run], it & 1, 55))) break;
+          if (keys) {
+            unsigned char* dst = sk + st * Smem<D>::K + (kc >> 2) * (128 * 128);
+            // all loads of the run first: with each before its store the run
+            // took three times as long
+            uint2 v[16 / ROWS][2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint32_t*>(raw_v + i * V_STEP + 4 * q);
-            // channel 4 q + ch of the piece; its 8-row group and its row there
-            unsigned char* rows = dst + (q >> 1) * 1024 + (q & 1) * 512;
-            auto put = [&](int ch, uint4 v) {
-              *reinterpret_cast<uint4*>(rows + ch * 128 + (((vo & 7) ^ (4 * (q & 1) + ch)) << 4)) = v;
-            };
-            put(0, make_uint4(f16_pair<0>(x[0], x[1]), f16_pair<0>(x[2], x[3]), f16_pair<0>(x[4], x[5]), f16_pair<0>(x[6], x[7])));
-            put(1, make_uint4(f16_pair<1>(x[0], x[1]), f16_pair<1>(x[2], x[3]), f16_pair<1>(x[4], x[5]), f16_pair<1>(x[6], x[7])));
-            put(2, make_uint4(f16_pair<2>(x[0], x[1]), f16_pair<2>(x[2], x[3]), f16_pair<2>(x[4], x[5]), f16_pair<2>(x[6], x[7])));
-            put(3, make_uint4(f16_pair<3>(x[0], x[1]), f16_pair<3>(x[2], x[3]), f16_pair<3>(x[4], x[5]), f16_pair<3>(x[6], x[7])));
+            for (int i = 0; i < 16 / ROWS; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                v[i][e] = *reinterpret_cast<const uint2*>(mine + (16 * run + ROWS * i + kr) * D + 16 * kc + 8 * (k_flip ^ e));
+#pragma unroll
+            for (int i = 0; i < 16 / ROWS; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<uint4*>(dst + sw128_off(16 * run + ROWS * i + kr, 2 * (kc & 3) + (k_flip ^ e))) = make_uint4(
+                    codes_even(v[i][e].x), codes_odd(v[i][e].x), codes_even(v[i][e].y), codes_odd(v[i][e].y));
+          } else if (run & 1) {  // both of the warp's runs are there
+            const unsigned char* src = mine + 8 * vo * D + 16 * vc;
+            unsigned char* dst = sv + st * Smem<D>::V + (vo >> 3) * (D * 128) + 2 * vc * 1024;
+#pragma unroll 2
+            for (int i = 0; i < D / 32; ++i) {
+              const int q = (i + v_turn) & 3;
+              uint32_t x[8];
+#pragma unroll
+              for (int t = 0; t < 8; ++t) x[t] = *reinterpret_cast<const uint32_t*>(src + t * D + 4 * q);
+              // channel 4 q + ch of the piece; its 8-row group and its row there
+              unsigned char* rows = dst + (q >> 1) * 1024 + (q & 1) * 512;
+              auto put = [&](int ch, uint4 v) {
+                *reinterpret_cast<uint4*>(rows + ch * 128 + (((vo & 7) ^ (4 * (q & 1) + ch)) << 4)) = v;
+              };
+              put(0, make_uint4(f16_pair<0>(x[0], x[1]), f16_pair<0>(x[2], x[3]), f16_pair<0>(x[4], x[5]), f16_pair<0>(x[6], x[7])));
+              put(1, make_uint4(f16_pair<1>(x[0], x[1]), f16_pair<1>(x[2], x[3]), f16_pair<1>(x[4], x[5]), f16_pair<1>(x[6], x[7])));
+              put(2, make_uint4(f16_pair<2>(x[0], x[1]), f16_pair<2>(x[2], x[3]), f16_pair<2>(x[4], x[5]), f16_pair<2>(x[6], x[7])));
+              put(3, make_uint4(f16_pair<3>(x[0], x[1]), f16_pair<3>(x[2], x[3]), f16_pair<3>(x[4], x[5]), f16_pair<3>(x[6], x[7])));
+            }
           }
+          if (u + 1 < end && (keys || (run & 1))) {
+            const int page = __shfl_sync(~0u, next_pages, run), page0 = __shfl_sync(~0u, next_pages, run & ~1);
+            __syncwarp();  // every lane has read the run
+            if (lane == 0) {
+              if (!keys) fetch(u + 1, run - 1, page0);
+              fetch(u + 1, run, page);
+            }
+          }
+        }
+        if (!ok) {  // after a wait that gave up: the copies in flight end before the block's memory goes
+          int never = 0;
+          for (int r = run0; r < run1; r += run_step) {
+            const bool ahead = keys ? r < run : false;  // asked for unit u + 1 already
+            if (!ahead || u + 1 < end) mbar_wait(&came[r], (it + ahead) & 1, &never, WAIT_NS);
+          }
+          break;
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.v_full[st]);
-        load_v(u + 1, next_pages);
+        if (lane == 0) mbar_arrive(keys ? &S.k_full[st] : &S.v_full[st]);
         pages = next_pages;
-        next_pages = after_pages;
+        next_pages = pages_of(u + 2);
+        if (keys && w == 0) {
+          ks = scale_of(pages, 0);
+          vs = scale_of(pages, 1);
+        }
       }
     }
-    cp_async_wait<0>();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == W_KEYS) tmem_dealloc(tmem, 512);
+  if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
 template <int D>
