@@ -191,7 +191,7 @@ __device__ __forceinline__ void named_barrier(int id) {
 // the sums rescaled and the pass repeated.
 //
 // Two prompts of 2600 tokens behind contexts of up to 3000, 32 heads on 8:
-// 286 us, 266 GFLOP, 0.48 of the measured bf16 rate; one prompt of 4096 tokens:
+// 279 us, 266 GFLOP, 0.49 of the measured bf16 rate; one prompt of 4096 tokens:
 // 175 us.  No unit is full: a unit takes some 4000 clocks, of which the tensor
 // cores work 2050; the rest is the softmax's chain and the conversion of the
 // codes, which run beside each other.
@@ -665,6 +665,25 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     // it, again for the banks
     const int vo = 4 * w + (lane & 3), vc = (lane >> 2) % PIECES;
     const int v_turn = (lane & 3) + vc + (D == 128 ? 0 : 2 * (lane >> 4));
+    // Where the pieces come from and go to, worked out once: a key half of the
+    // first rows of a run (an odd turn's rows lie 4 or 8 on), a value word.
+    uint32_t k_to[2][2], v_to[D / 32], v_ch[4];
+    int k_from[2], v_from[D / 32];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      k_from[e] = kr * D + 16 * kc + 8 * (k_flip ^ e);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        k_to[i][e] = (kc >> 2) * (128 * 128) + sw128_off(ROWS * i + kr, 2 * (kc & 3) + (k_flip ^ e));
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int q = (i + v_turn) & 3;
+      v_from[i] = 8 * vo * D + 16 * vc + 4 * q;
+      v_to[i] = (vo >> 3) * (D * 128) + (2 * vc + (q >> 1)) * 1024 + (q & 1) * 512 + (((vo >> 2) ^ q) & 1) * 64;
+    }
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) v_ch[ch] = ch * 128 + (((vo & 3) ^ ch) << 4);
     uint32_t it = 0;
     bool ok = true;
     while (ok && next_piece(p, S.work, S.walk[warp])) {
@@ -731,7 +750,8 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         for (; ok && run < run1; run += run_step) {
           if (!(ok = wait_warp(&came[run], it & 1, 55))) break;
           if (keys) {
-            unsigned char* dst = sk + st * Smem<D>::K + (kc >> 2) * (128 * 128);
+            unsigned char* dst = sk + st * Smem<D>::K + 2048 * run;
+            const unsigned char* src = mine + run * RUN;
             // all loads of the run first: with each before its store the run
             // took three times as long
             uint2 v[16 / ROWS][2];
@@ -739,27 +759,22 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
             for (int i = 0; i < 16 / ROWS; ++i)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                v[i][e] = *reinterpret_cast<const uint2*>(mine + (16 * run + ROWS * i + kr) * D + 16 * kc + 8 * (k_flip ^ e));
+                v[i][e] = *reinterpret_cast<const uint2*>(src + k_from[e] + ROWS * i * D);
 #pragma unroll
             for (int i = 0; i < 16 / ROWS; ++i)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<uint4*>(dst + sw128_off(16 * run + ROWS * i + kr, 2 * (kc & 3) + (k_flip ^ e))) = make_uint4(
-                    codes_even(v[i][e].x), codes_odd(v[i][e].x), codes_even(v[i][e].y), codes_odd(v[i][e].y));
+                *reinterpret_cast<uint4*>(dst + k_to[i & 1][e] + 1024 * (i >> 1)) =
+                    make_uint4(codes_even(v[i][e].x), codes_odd(v[i][e].x), codes_even(v[i][e].y), codes_odd(v[i][e].y));
           } else if (run & 1) {  // both of the warp's runs are there
-            const unsigned char* src = mine + 8 * vo * D + 16 * vc;
-            unsigned char* dst = sv + st * Smem<D>::V + (vo >> 3) * (D * 128) + 2 * vc * 1024;
-#pragma unroll 2
+            unsigned char* dst = sv + st * Smem<D>::V;
+#pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-              const int q = (i + v_turn) & 3;
               uint32_t x[8];
 #pragma unroll
-              for (int t = 0; t < 8; ++t) x[t] = *reinterpret_cast<const uint32_t*>(src + t * D + 4 * q);
-              // channel 4 q + ch of the piece; its 8-row group and its row there
-              unsigned char* rows = dst + (q >> 1) * 1024 + (q & 1) * 512;
-              auto put = [&](int ch, uint4 v) {
-                *reinterpret_cast<uint4*>(rows + ch * 128 + (((vo & 7) ^ (4 * (q & 1) + ch)) << 4)) = v;
-              };
+              for (int t = 0; t < 8; ++t) x[t] = *reinterpret_cast<const uint32_t*>(mine + v_from[i] + t * D);
+              // channel 4 q + ch of the piece: row 4 (q & 1) + ch of an 8-row group
+              auto put = [&](int ch, uint4 v) { *reinterpret_cast<uint4*>(dst + (v_to[i] + v_ch[ch])) = v; };
               put(0, make_uint4(f16_pair<0>(x[0], x[1]), f16_pair<0>(x[2], x[3]), f16_pair<0>(x[4], x[5]), f16_pair<0>(x[6], x[7])));
               put(1, make_uint4(f16_pair<1>(x[0], x[1]), f16_pair<1>(x[2], x[3]), f16_pair<1>(x[4], x[5]), f16_pair<1>(x[6], x[7])));
               put(2, make_uint4(f16_pair<2>(x[0], x[1]), f16_pair<2>(x[2], x[3]), f16_pair<2>(x[4], x[5]), f16_pair<2>(x[6], x[7])));
