@@ -90,6 +90,9 @@ __device__ __forceinline__ uint32_t codes_pair(uint32_t a, uint32_t b) {
 // scale enters the weights, p_j = exp2(s_j - m) vs_j, through its logarithm
 // with a running maximum M of its own, so that the fp16 weights are at most 1
 // whatever the scales are.
+//
+// 48 sequences of up to 20000 tokens, 32 heads on 4, one new token each: 109 us
+// for 626 MB, 0.86 of the copy rate; the unpacking (ALU pipe 0.6 full) is next.
 template <int D, int NT>
 __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kernel(AttnParams p) {
   constexpr int ROWS = Shape<NT>::ROWS, STAGES = Shape<NT>::STAGES;
@@ -545,7 +548,10 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
   }
 }
 
-constexpr int TILE_ROWS = 32;  // more rows a sequence, on average: the tile kernel
+// More query rows a sequence and key head than this, on average: the tile
+// kernel.  Sixteen sequences of 8000 tokens, 32 heads on 8: 16 rows 73 us
+// streaming, 131 in tiles; 32 rows 123 and 132; 40 rows 178 and 132.
+constexpr int TILE_ROWS = 32;
 
 template <int D, int NT>
 cudaError_t launch_stream(const AttnParams& p, cudaStream_t s) {
