@@ -19,12 +19,13 @@ constexpr int T_WARPS = 16, W_KEYS = 8, W_MMA = 11, W_VALUES = 12;
 constexpr int KEY_WARPS = W_MMA - W_KEYS;
 constexpr int T_THREADS = T_WARPS * 32;
 // Units that an item counts for beside its own, when the work is cut: its
-// query rows, first scales and results take as long as about three (two
-// prompts behind contexts: 285.3 us with two, 285.6 with three, 289.5 with
+// query rows, first scales and results take as long as about three (in
+// a form a little slower in its units, two prompts behind contexts: 285.3 us with two, 285.6 with three, 289.5 with
 // four, 293 with five; one prompt of 4096 tokens, 32 heads on 8: 183, 175, 178,
 // 180).
 constexpr int ITEM_COST = 3;
 constexpr int SC_RING = 4;   // tiles whose scales are kept
+constexpr int RED_RING = 4;  // pieces whose largest value scales are kept
 constexpr uint64_t WAIT_NS = 2000000000ull;
 // What a row's weights of 64 tokens may add up to before its sums are rescaled:
 // none is then above it, and if they exceed it the largest is above 4.
@@ -44,7 +45,8 @@ struct Piece {
 struct Walk {
   int64_t x;
   int s, qt, h, u;
-  Seq q;  // sequence s
+  Seq q;           // sequence s
+  uint32_t piece;  // number of P among the walk's
   Piece P;
   int more;
 };
@@ -55,8 +57,8 @@ struct TileShared {
   uint64_t p_full[2][2], o_step[2][2];         // of its halves
   uint64_t sc_full[SC_RING], raw_full[2][UNIT / 16];
   float sc_k[SC_RING][8], sc_log[SC_RING][8], sc_inv[SC_RING][8], sc_ref[SC_RING];
-  float red[4];
-  uint32_t arrived[2];
+  uint64_t red_full[RED_RING];
+  float red[RED_RING][KEY_WARPS];  // largest value scales of a piece, by warp
   uint32_t tmem;
   int abort;
   int64_t scratch[T_WARPS + 2];
@@ -86,6 +88,7 @@ __device__ __forceinline__ bool next_piece(const AttnParams& p, const Work& w, W
       P.n[0] = tile_units<128>(p, q, 2 * W.qt);
       P.n[1] = seq_rows(p, q) > (uint32_t)T_ROWS * W.qt + 128 ? units : 0;
       W.more = P.u1 > P.u0;  // not if the run ends among the units that stand for the item's cost
+      W.piece += W.more;
       W.x += end - W.u;
       W.u = 0;
       if (W.x < w.x1 && ++W.h == p.c.hkv) {
@@ -168,10 +171,6 @@ template <class T>
 __device__ __forceinline__ T* shfl_ptr(T* x, int lane) {
   return reinterpret_cast<T*>(__shfl_sync(~0u, (unsigned long long)x, lane));
 }
-template <int THREADS>
-__device__ __forceinline__ void named_barrier(int id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
-}
 
 // The work is cut as in the streaming kernel, over items of 256 query rows
 // (a position's heads next to each other) and units of 128 tokens.
@@ -191,8 +190,8 @@ __device__ __forceinline__ void named_barrier(int id) {
 // the sums rescaled and the pass repeated.
 //
 // Two prompts of 2600 tokens behind contexts of up to 3000, 32 heads on 8:
-// 279 us, 266 GFLOP, 0.49 of the measured bf16 rate; one prompt of 4096 tokens:
-// 175 us.  No unit is full: a unit takes some 4000 clocks, of which the tensor
+// 280 us, 266 GFLOP, 0.48 of the measured bf16 rate; one prompt of 4096 tokens:
+// 185 us.  No unit is full: a unit takes some 4000 clocks, of which the tensor
 // cores work 2050; the rest is the softmax's chain and the conversion of the
 // codes, which run beside each other.
 //
@@ -221,6 +220,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       Walk& W = S.walk[warp];
       W.x = found.x0, W.s = found.s, W.qt = found.qt, W.h = found.h, W.u = found.u;
       W.q = load_seq(p, found.s);
+      W.piece = ~0u;
     }
   }
   if (tid == 0) {
@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     }
     for (int i = 0; i < SC_RING; ++i) mbar_init(&S.sc_full[i], 1);
     for (int i = 0; i < 2 * UNIT / 16; ++i) mbar_init(&S.raw_full[0][i], 1);
+    for (int i = 0; i < RED_RING; ++i) mbar_init(&S.red_full[i], KEY_WARPS - 1);
     mbar_init(&S.drain, 1);
     S.abort = 0;
     fence_mbar_init();
@@ -539,12 +540,16 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         mine[128 * D + r] = M;
         mine[128 * D + 128 + r] = l;
         __threadfence();
-        named_barrier<128>(2 + X);
-        if (r == 0) S.arrived[X] = atomicAdd(p.counters + 2 * c0 + X, 1u);
-        named_barrier<128>(2 + X);
-        if (S.arrived[X] == (uint32_t)(c1 - c0)) {
+        __syncwarp();
+        // a count for each warp's rows: no warp waits for another here
+        static_assert(W_KEYS <= 3 * KV_CTAS_PER_SM, "counters of an SM");
+        uint32_t* counter = p.counters + W_KEYS * c0 + warp;
+        uint32_t others = 0;
+        if (lane == 0) others = atomicAdd(counter, 1u);
+        others = __shfl_sync(~0u, others, 0);
+        if (others == (uint32_t)(c1 - c0)) {
           __threadfence();
-          if (r == 0) p.counters[2 * c0 + X] = 0;
+          if (lane == 0) *counter = 0;
           float top = -INFINITY, sum = 0.f;
           for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(part(c) + 128 * D + r));
           if (top == -INFINITY) top = 0.f;
@@ -725,10 +730,23 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
           vref = fmaxf(vref, scale_of(page_at(b << p.block_log2), 1));
 #pragma unroll
         for (int o = 16; o; o >>= 1) vref = fmaxf(vref, __shfl_xor_sync(~0u, vref, o));
-        named_barrier<32 * KEY_WARPS>(1);  // the last item's values are read
-        if (lane == 0) S.red[w] = vref;
-        named_barrier<32 * KEY_WARPS>(1);
-        vref = fmaxf(fmaxf(S.red[0], S.red[1]), S.red[2]);
+        // the first warp, which writes the scales, has the others'; a warp is two
+        // pieces ahead of it at most, as the stages hold two units
+        const uint32_t piece = S.walk[warp].piece, slot = piece % RED_RING;
+        if (w && lane == 0) {
+          S.red[slot][w] = vref;
+          mbar_arrive(&S.red_full[slot]);
+        }
+        if (w == 0) {
+          if (!(ok = wait_warp(&S.red_full[slot], (piece / RED_RING) & 1, 61))) {
+            for (int run = run0; run < run1; run += run_step) {
+              int never = 0;
+              mbar_wait(&came[run], it & 1, &never, WAIT_NS);
+            }
+            break;
+          }
+          for (int i = 1; i < KEY_WARPS; ++i) vref = fmaxf(vref, S.red[slot][i]);
+        }
         vref_log = vref > 0.f ? __log2f(vref) : 0.f;
       }
       for (int u = P.u0; u < end; ++u, ++it) {

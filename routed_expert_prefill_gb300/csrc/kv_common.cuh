@@ -5,7 +5,8 @@
 namespace moe {
 
 // Workspace of both calls: the status block, the completion counters of the
-// split attention items (three a CTA), their partial results.
+// split attention items (three a CTA; of the tile kernel's one CTA an SM,
+// eight), their partial results.
 constexpr int KV_CTAS_PER_SM = 3;  // at most, of the streaming kernels
 constexpr int KV_ROWS = 16;        // rows of a query tile, at most
 
