@@ -191,7 +191,7 @@ __device__ __forceinline__ T* shfl_ptr(T* x, int lane) {
 //
 // Two prompts of 2600 tokens behind contexts of up to 3000, 32 heads on 8:
 // 280 us, 266 GFLOP, 0.48 of the measured bf16 rate; one prompt of 4096 tokens:
-// 185 us.  No unit is full: a unit takes some 4000 clocks, of which the tensor
+// 187 us.  No unit is full: a unit takes some 4000 clocks, of which the tensor
 // cores work 2050; the rest is the softmax's chain and the conversion of the
 // codes, which run beside each other.
 //
