@@ -117,10 +117,13 @@ __device__ __forceinline__ float times_pow2(float v, int e) {
   return v * __uint_as_float((uint32_t)(127 + a) << 23) * __uint_as_float((uint32_t)(127 + b) << 23);
 }
 
+// All of a CTA's shared memory: the kernel has none beside the dynamic part,
+// as the limit (227 KB) is on both together.
 size_t qs_smem(const QmvParams& p, int nt, int teams, int stages) {
   return (size_t)teams * QMV_WARPS * stages * QS_STAGE            // rings
          + (size_t)teams * 2 * QMV_WARPS * 16 * 8 * nt * 4         // sums
          + (size_t)teams * 2 * 2 * 16 * qs_s_pitch(p.k >> 6)       // scales and biases of two tiles
+         + (p.xc ? 0 : 8 * nt * 4)                                 // rows' largest magnitudes
          + (size_t)(p.k >> 6) * 8 * nt * (p.xc ? 8 : 4)            // group sums of x, scales of 8-bit rows
          + (size_t)p.t * qs_x_pitch(p.k);                          // x
 }
@@ -147,7 +150,6 @@ size_t qs_smem(const QmvParams& p, int nt, int teams, int stages) {
 template <int NT, int TEAMS, int S, bool F16, bool VEC>
 __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(QmvParams p, bool out32) {
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int rowmax[8 * NT];
   constexpr int THREADS = TEAMS * QMV_WARPS * 32;
   const int lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
   const int team = threadIdx.x / (QMV_WARPS * 32), warp = (threadIdx.x >> 5) % QMV_WARPS;
@@ -157,7 +159,8 @@ __global__ void __launch_bounds__(TEAMS * QMV_WARPS * 32, 1) qmv_stream_kernel(Q
                (size_t)team * 2 * QMV_WARPS * 8 * NT * 16;  // [2][warp][8 NT][16]
   const int s_pitch = qs_s_pitch(groups);
   unsigned char* scb = smem + (size_t)TEAMS * QMV_WARPS * (S * QS_STAGE + 2 * 8 * NT * 16 * 4);
-  float* xsum = reinterpret_cast<float*>(scb + (size_t)TEAMS * 2 * 2 * 16 * s_pitch);
+  int* rowmax = reinterpret_cast<int*>(scb + (size_t)TEAMS * 2 * 2 * 16 * s_pitch);  // [8 NT], bf16 rows only
+  float* xsum = reinterpret_cast<float*>(rowmax + (F16 ? 0 : 8 * NT));
   scb += (size_t)team * 2 * 2 * 16 * s_pitch;  // [2][scales, biases][16] rows of s_pitch bytes
   unsigned char* xsm = reinterpret_cast<unsigned char*>(xsum + groups * 8 * NT * (F16 ? 2 : 1));
   const int ub = units * warp / QMV_WARPS, ue = units * (warp + 1) / QMV_WARPS;
