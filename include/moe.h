@@ -583,9 +583,15 @@ typedef struct {
  * tokens and channels of one head, scale = m / 127, code = v * 127 / m to
  * the nearest whole number, ties to even; the places past the length become
  * zero.  So the cache depends on its tokens alone, not on how many came per
- * call, and a sequence may be cut back by up to `block` tokens (smaller
- * lens) and continued.  `tail` then holds the new tokens of the last two
- * blocks.
+ * call.  `tail` then holds the new tokens of the last two blocks.
+ *
+ * A sequence may be cut back (smaller lens) and continued: from any length at
+ * a block's start, where nothing before the call is read, and inside a block
+ * while `tail` still holds that block.  It holds the last two that were
+ * written, so cutting back twice counts from the longest length in between,
+ * not from the last one.  Behind a part of a block that `tail` does not hold
+ * (cut back too far, or lens grown by more than the new tokens) the block is
+ * quantised from whatever stands there; moe_kv_append_held reports that.
  *
  * k, v: bf16 [t][hkv][d], heads contiguous, rows `k_stride`, `v_stride`
  * elements apart (multiples of 8).  A key or value whose 127-fold is not
@@ -597,6 +603,18 @@ typedef struct {
  */
 int moe_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* starts,
                   int32_t t, const moe_kv_cache* cache, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_kv_append that also keeps account of the tail: held int32 [n_seq][2],
+ * device, says up to which token each half of a sequence's tail is filled, 0
+ * where that is not known (all zero at first).  New tokens behind a part of a
+ * block that the tail is known not to hold raise MOE_EDEVICE in
+ * moe_read_device_status; what is written is the same.  `held` goes along
+ * where a sequence's tail is copied, and is set to 0 where one is filled by
+ * hand.  Errors: as moe_kv_append.
+ */
+int moe_kv_append_held(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* starts,
+                       int32_t t, const moe_kv_cache* cache, int32_t* held, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Causal attention of the new rows over the cache (after moe_kv_append of

@@ -23,6 +23,7 @@ enum : uint32_t {
   FLAG_ROUTE_BOUND = 1u << 3, // a router score left its error bound
   FLAG_BAD_CACHE = 1u << 4,   // cache lengths, starts or page ids out of range
   FLAG_NOT_FINITE = 1u << 5,  // a key or value that is not finite reached the cache
+  FLAG_BAD_TAIL = 1u << 6,    // a cache's tail does not hold the tokens before a call's
   FLAG_TIMEOUT = 1u << 8,     // a bounded device wait gave up
 };
 

@@ -7,7 +7,8 @@
 namespace moe {
 
 cudaError_t launch_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
-                             const int32_t* starts, int t, const moe_kv_cache& c, DeviceStatus* st, cudaStream_t s);
+                             const int32_t* starts, int t, const moe_kv_cache& c, int32_t* held, DeviceStatus* st,
+                             cudaStream_t s);
 cudaError_t launch_kv_attention(const uint16_t* q, int64_t q_stride, const int32_t* starts, int t, int hq,
                                 float scale, const moe_kv_cache& c, uint16_t* out, unsigned char* ws,
                                 cudaStream_t s);
@@ -55,14 +56,20 @@ extern "C" {
 
 size_t moe_kv_workspace_bytes(int32_t d) { return d == 64 || d == 128 ? kv_ws_bytes(d) : 0; }
 
-int moe_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* starts,
-                  int32_t t, const moe_kv_cache* cache, void* ws, size_t ws_bytes, void* stream) {
+int moe_kv_append_held(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* starts,
+                       int32_t t, const moe_kv_cache* cache, int32_t* held, void* ws, size_t ws_bytes, void* stream) {
   TRY(check_cache(cache, starts, t, ws, ws_bytes));
   TRY(check_rows(k, k_stride, "k"));
   TRY(check_rows(v, v_stride, "v"));
-  return cuda_status(launch_kv_append(k, k_stride, v, v_stride, starts, t, *cache, (DeviceStatus*)ws,
+  TRY(check_ptr(held, "held", 4, true));
+  return cuda_status(launch_kv_append(k, k_stride, v, v_stride, starts, t, *cache, held, (DeviceStatus*)ws,
                                       (cudaStream_t)stream),
                      "moe_kv_append launch");
+}
+
+int moe_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* starts,
+                  int32_t t, const moe_kv_cache* cache, void* ws, size_t ws_bytes, void* stream) {
+  return moe_kv_append_held(k, k_stride, v, v_stride, starts, t, cache, nullptr, ws, ws_bytes, stream);
 }
 
 int moe_kv_attention(const uint16_t* q, int64_t q_stride, const int32_t* starts, int32_t t, int32_t hq, float scale,

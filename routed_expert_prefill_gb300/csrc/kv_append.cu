@@ -82,7 +82,7 @@ __device__ __forceinline__ uint2 codes_of(uint4 u, float up, float m, float rm, 
 template <int VPT>
 __global__ void __launch_bounds__(APPEND_THREADS)
     kv_append_kernel(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* starts,
-                     int t, moe_kv_cache c, DeviceStatus* st) {
+                     int t, moe_kv_cache c, int32_t* held, DeviceStatus* st) {
   __shared__ uint32_t part[APPEND_THREADS / 32];
   __shared__ int owner;
   pdl_wait();
@@ -108,6 +108,16 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   const int old = len - n, first = old / c.block, last = (len - 1) / c.block;
   const int b = first + slot - (row0 / c.block + 2 * s);
   if (b < first || b > last) return;
+  // Whether the tail holds what this call reads of it, and what it holds
+  // afterwards: by one thread a sequence.
+  if (held && b == first && head == 0 && isv == 0 && tid == 0) {
+    int32_t* filled = held + 2 * (size_t)s;
+    if (old > first * c.block) {
+      const int end = filled[first & 1];
+      if (end && (end < old || (end - 1) / c.block != first)) raise_flag(st, FLAG_BAD_TAIL);
+    }
+    for (int e = max(first, last - 1); e <= last; ++e) filled[e & 1] = min(len, (e + 1) * c.block);
+  }
   const int page = c.table[(size_t)s * c.max_blocks + b];
   const uint16_t* src = isv ? v : k;
   const int64_t stride = isv ? v_stride : k_stride;
@@ -202,15 +212,16 @@ __global__ void __launch_bounds__(APPEND_THREADS)
 }  // namespace
 
 cudaError_t launch_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
-                             const int32_t* starts, int t, const moe_kv_cache& c, DeviceStatus* st,
+                             const int32_t* starts, int t, const moe_kv_cache& c, int32_t* held, DeviceStatus* st,
                              cudaStream_t s) {
   const dim3 grid(t / c.block + 2 * c.n_seq, c.hkv, 2);
   const int vpt = (c.block * c.d / 8 + APPEND_THREADS - 1) / APPEND_THREADS;
   cudaError_t e;
   auto* kern = vpt <= 1 ? kv_append_kernel<1> : vpt <= 2 ? kv_append_kernel<2> : vpt <= 4 ? kv_append_kernel<4>
                                                                                       : kv_append_kernel<8>;
-  MOE_LAUNCH("kv_append", s,
-             { e = launch_k(kern, grid, dim3(APPEND_THREADS), 0, s, k, k_stride, v, v_stride, starts, t, c, st); });
+  MOE_LAUNCH("kv_append", s, {
+    e = launch_k(kern, grid, dim3(APPEND_THREADS), 0, s, k, k_stride, v, v_stride, starts, t, c, held, st);
+  });
   return e;
 }
 

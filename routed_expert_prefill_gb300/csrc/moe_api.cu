@@ -643,14 +643,15 @@ int moe_read_device_status(void* ws, void* stream) {
   if (st.flags & FLAG_TIMEOUT)
     return set_error(MOE_ETIMEOUT, "a bounded device wait gave up (site %u)", st.timeout_site);
   if (st.flags & (FLAG_BAD_EXPERT | FLAG_BAD_ROW | FLAG_BAD_OFFSETS | FLAG_ROUTE_BOUND | FLAG_BAD_CACHE |
-                  FLAG_NOT_FINITE))
-    return set_error(MOE_EDEVICE, "device-side check failed (flags 0x%x: %s%s%s%s%s%s)", st.flags,
+                  FLAG_NOT_FINITE | FLAG_BAD_TAIL))
+    return set_error(MOE_EDEVICE, "device-side check failed (flags 0x%x: %s%s%s%s%s%s%s)", st.flags,
                      (st.flags & FLAG_BAD_EXPERT) ? "expert id out of range " : "",
                      (st.flags & FLAG_BAD_ROW) ? "row out of range " : "",
                      (st.flags & FLAG_BAD_OFFSETS) ? "bad offsets " : "",
                      (st.flags & FLAG_ROUTE_BOUND) ? "router score outside its error bound " : "",
                      (st.flags & FLAG_BAD_CACHE) ? "cache lengths, starts or pages out of range " : "",
-                     (st.flags & FLAG_NOT_FINITE) ? "a key or value that is not finite" : "");
+                     (st.flags & FLAG_NOT_FINITE) ? "a key or value that is not finite " : "",
+                     (st.flags & FLAG_BAD_TAIL) ? "tokens before the new ones that the cache's tail does not hold" : "");
   return MOE_OK;
 }
 

@@ -207,6 +207,12 @@ class KvCache:
     sets ``lens`` (the new tokens included) before moe_kv_append; both are
     read on the device.  The tensors are kept, not copied: calls that use one
     cache are ordered on one stream.
+
+    held int32 [n_seq, 2], made here, says up to which token each half of a
+    sequence's tail is filled (0: not known); moe_kv_append keeps it, and
+    reports a sequence that was cut back to where its tail does not reach.
+    Copy it along with a sequence's tail, or set it to 0 where a tail is
+    filled by hand.
     """
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, tail: torch.Tensor, table: torch.Tensor,
@@ -229,9 +235,11 @@ class KvCache:
         self.codes, self.scales, self.tail, self.table, self.lens = codes, scales, tail, table, lens
         self.n_seq, self.hkv, self.block, self.d = n_seq, hkv, block, d
         self.ws = torch.zeros(n, dtype=torch.uint8, device=codes.device)
+        self.held = torch.zeros(n_seq, 2, dtype=torch.int32, device=codes.device)
         self._dev = codes.get_device()
         self._starts, self._kv, self._scale = (n_seq + 1,), (hkv, d), 1 / math.sqrt(d)
         self._ws = self.ws.data_ptr(), n
+        self._held = self.held.data_ptr()
         self._c = MoeKvCache(codes.data_ptr(), scales.data_ptr(), tail.data_ptr(), table.data_ptr(), lens.data_ptr(),
                              n_seq, n_pages, max_blocks, block, hkv, d)
         self._ref = ctypes.byref(self._c)
@@ -273,8 +281,8 @@ def moe_kv_append(k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, cache:
         if v.shape[0] != t:
             raise ValueError(f"v must have {t} rows, got {v.shape[0]}")
         _on_current_device(k=k, v=v, starts=starts, codes=cache.codes)
-    status = lib.moe_kv_append(k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), starts.data_ptr(), t,
-                               cache._ref, *cache._ws, _raw(stream, dev))
+    status = lib.moe_kv_append_held(k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), starts.data_ptr(), t,
+                                    cache._ref, cache._held, *cache._ws, _raw(stream, dev))
     if status:
         _check(status)
 

@@ -60,6 +60,7 @@ EXPORTS = (
     "moe_add_rms_norm",
     "moe_qmv",
     "moe_kv_append",
+    "moe_kv_append_held",
     "moe_kv_attention",
     "moe_kv_workspace_bytes",
 )
@@ -191,6 +192,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_qmv.argtypes = [vp, i64, vp, vp, ctypes.POINTER(MoeQWeights), i32, i32, i32, vp, i32, vp]
     lib.moe_kv_append.restype = ctypes.c_int
     lib.moe_kv_append.argtypes = [vp, i64, vp, i64, vp, i32, ctypes.POINTER(MoeKvCache), vp, sz, vp]
+    lib.moe_kv_append_held.restype = ctypes.c_int
+    lib.moe_kv_append_held.argtypes = [vp, i64, vp, i64, vp, i32, ctypes.POINTER(MoeKvCache), vp, vp, sz, vp]
     lib.moe_kv_attention.restype = ctypes.c_int
     lib.moe_kv_attention.argtypes = [vp, i64, vp, i32, i32, f32, ctypes.POINTER(MoeKvCache), vp, vp, sz, vp]
     lib.moe_kv_workspace_bytes.restype = sz

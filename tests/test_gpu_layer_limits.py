@@ -8,7 +8,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_layer import BF16, F64, gen, layer, randn, weights, within  # noqa: E402, F401
+from test_gpu_layer import (BF16, F64, check_cache, feed, filled, gen, i32, layer, make_kv, new_cache, randn,  # noqa: E402, F401
+                            weights, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,37 @@ def qmv_case(layer, t, n, k, q8):
                                    (5, 1000, 12864)])
 def test_qmv_rows_that_fill_shared_memory(layer, t, n, k):
     qmv_case(layer, t, n, k, False)
+
+
+# ---------------------------------------------------------------- append
+
+def test_append_cut_back_past_the_tail_is_reported(layer):
+    """Two cuts in a row that each drop at most a block: the second one goes
+    back into a block whose tokens the tail no longer holds."""
+    block, total = 16, [33]
+    kv = make_kv(gen(21), total, 2, 64)
+    cache = new_cache(layer, total, block, 2, 64)
+    feed(layer, cache, kv, [0], [33])
+    feed(layer, cache, kv, [17], [1])  # into the block before the last: the tail holds it
+    check_cache(cache, kv, [18])
+    assert cache.read_device_status() == 0
+    feed(layer, cache, kv, [2], [1])  # block 0: its places hold block 2's tokens
+    assert cache.read_device_status() == -5
+    feed(layer, cache, kv, [0], [20])  # from a block's start on nothing is read back
+    check_cache(cache, kv, [20])
+    feed(layer, cache, kv, [20], [1])
+    assert cache.read_device_status() == 0
+    feed(layer, cache, kv, [24], [1])  # tokens 21 .. 23 were never given
+    assert cache.read_device_status() == -5
+
+
+def test_append_tail_given_by_the_caller_is_taken(layer):
+    """A cache around tensors that another one has filled: what its tail holds is not known, and taken as it is."""
+    total = [45, 20]
+    kv = make_kv(gen(22), total, 2, 64)
+    a = new_cache(layer, total, 16, 2, 64)
+    lens = feed(layer, a, kv, [0, 0], [40, 3])
+    b = layer.KvCache(a.codes, a.scales, a.tail, a.table, a.lens)
+    lens = feed(layer, b, kv, lens, [5, 17])
+    check_cache(b, kv, lens)
+    assert b.read_device_status() == 0
