@@ -482,7 +482,9 @@ int moe_read_device_status(void* ws, void* stream);
  * kind of wait run out instead of completing:
  *   MOE_STALL_WEIGHT_COPIES: the weight producer of the tensor-core expert
  *     kernels (packed and row-major) and of the small-t kernels issues no
- *     copy, so their consumers' waits give up;
+ *     copy, so their consumers' waits give up; nor do the key and value
+ *     warps of moe_kv_attention's tensor-core kernel in its first CTA (the
+ *     others go on, so what is joined across CTAs is left in between);
  *   MOE_STALL_GRID_BARRIER: the grid barrier of the fused decode launch
  *     waits for one arrival more than the grid has.
  * Each such wait gives up after its limit (2 s of device time), records
@@ -634,7 +636,9 @@ int moe_kv_append_held(const uint16_t* k, int64_t k_stride, const uint16_t* v, i
  * 32768.  The rows
  * of a sequence whose lens or starts are out of range are left unwritten, and
  * a page id out of range hides its block's tokens (a row left without any
- * becomes zero); both raise MOE_EDEVICE in moe_read_device_status.
+ * becomes zero); both raise MOE_EDEVICE in moe_read_device_status.  A wait
+ * that gave up raises MOE_ETIMEOUT there; rows may then be unwritten, and the
+ * next call on the workspace runs as if that one had not been.
  * ws: moe_kv_workspace_bytes() bytes, set to zero once before its first use;
  * calls that share it are ordered on one stream.
  * Errors: MOE_EINVAL, MOE_ESHAPE, MOE_EWORKSPACE, MOE_ECUDA.

@@ -271,6 +271,25 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     unsigned char* q_tile = sq + X * Smem<D>::Q;
     uint32_t units_done = 0, tiles = 0;  // of the CTA; of this tile
     bool ok = true;
+    // A tile that spans CTAs: the parts are counted for each warp's rows (no
+    // warp waits for another here), a part that was given up with its bit in
+    // the upper half, and the last one sets the count to zero again, whatever
+    // became of the others: so the next call finds it as this one did.  True
+    // in the warp that comes last, if every part is there.
+    auto first_cta = [&]() { return cta_of(S.work, P.first); };
+    auto last_cta = [&]() { return cta_of(S.work, P.first + P.n[X] - 1); };
+    auto count_part = [&](uint32_t add) {
+      static_assert(W_KEYS <= 3 * KV_CTAS_PER_SM, "counters of an SM");
+      const int c0 = first_cta();
+      uint32_t* counter = p.counters + W_KEYS * c0 + warp;
+      uint32_t others = 0;
+      if (lane == 0) others = atomicAdd(counter, add);
+      others = __shfl_sync(~0u, others, 0);
+      if ((others & 0xFFFFu) != (uint32_t)(last_cta() - c0)) return false;
+      __threadfence();
+      if (lane == 0) *counter = 0;
+      return (others + add) >> 16 == 0;
+    };
     while (ok && next_piece(p, S.work, S.walk[warp])) {
       const int last = min(P.u1, P.n[X]);
       if (P.u0 >= last) {
@@ -523,7 +542,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         write_out();
       } else {
         // a tile that spans CTAs: the last one to finish joins the parts in order
-        const int c0 = cta_of(S.work, P.first), c1 = cta_of(S.work, P.first + P.n[X] - 1);
+        const int c0 = first_cta(), c1 = last_cta();
         auto part = [&](int c) { return p.partials + (size_t)((2 * c + (c == c0)) * 2 + X) * partial_floats<D>(); };
         float* mine = part(blockIdx.x);
 #pragma unroll 1
@@ -541,15 +560,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         mine[128 * D + 128 + r] = l;
         __threadfence();
         __syncwarp();
-        // a count for each warp's rows: no warp waits for another here
-        static_assert(W_KEYS <= 3 * KV_CTAS_PER_SM, "counters of an SM");
-        uint32_t* counter = p.counters + W_KEYS * c0 + warp;
-        uint32_t others = 0;
-        if (lane == 0) others = atomicAdd(counter, 1u);
-        others = __shfl_sync(~0u, others, 0);
-        if (others == (uint32_t)(c1 - c0)) {
-          __threadfence();
-          if (lane == 0) *counter = 0;
+        if (count_part(1)) {
           float top = -INFINITY, sum = 0.f;
           for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(part(c) + 128 * D + r));
           if (top == -INFINITY) top = 0.f;
@@ -577,6 +588,12 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
           write_out();
         }
       }
+    }
+    if (!ok) {  // a wait gave up: this piece and those that would have come
+      do {
+        const int last = min(P.u1, P.n[X]);
+        if (P.u0 < last && !(P.u0 == 0 && last == P.n[X])) count_part(0x10001u);
+      } while (next_piece(p, S.work, S.walk[warp]));
     }
   } else if (warp == W_MMA) {
     // ------------------------------------------------------------ products
@@ -652,7 +669,10 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
     // The codes come in runs of 16 tokens, one bulk copy each, a unit ahead:
     // a warp waits for its own runs, converts them and asks for the next
     // unit's into the same places.
+    // The first CTA asks for none under the MOE_STALL_WEIGHT_COPIES test hook:
+    // its waits run out.
     const bool keys = warp < W_VALUES;
+    const bool stalled = blockIdx.x == 0 && (p.st->stall & MOE_STALL_WEIGHT_COPIES);
     const int w = keys ? warp - W_KEYS : warp - W_VALUES;
     // keys: runs w, w + KEY_WARPS, ..; values: runs 2 w and 2 w + 1
     constexpr int RUN = 16 * D, RUNS = UNIT / 16;
@@ -713,6 +733,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
       // one run of unit u < end, by one lane; a run without a page is read from
       // page 0: its weights are 0
       auto fetch = [&](int u, int run, int page) {
+        if (stalled) return;
         mbar_arrive_expect_tx(&came[run], RUN);
         bulk_copy_g2s(mine + run * RUN, codes + max(page, 0) * page_bytes + ((u * UNIT + 16 * run) & (p.c.block - 1)) * D, RUN,
                       &came[run]);
@@ -739,7 +760,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         }
         if (w == 0) {
           if (!(ok = wait_warp(&S.red_full[slot], (piece / RED_RING) & 1, 61))) {
-            for (int run = run0; run < run1; run += run_step) {
+            for (int run = run0; run < run1 && !stalled; run += run_step) {
               int never = 0;
               mbar_wait(&came[run], it & 1, &never, WAIT_NS);
             }
@@ -810,7 +831,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
         }
         if (!ok) {  // after a wait that gave up: the copies in flight end before the block's memory goes
           int never = 0;
-          for (int r = run0; r < run1; r += run_step) {
+          for (int r = run0; r < run1 && !stalled; r += run_step) {
             const bool ahead = keys ? r < run : false;  // asked for unit u + 1 already
             if (!ahead || u + 1 < end) mbar_wait(&came[r], (it + ahead) & 1, &never, WAIT_NS);
           }

@@ -3,13 +3,14 @@ memory, kernel forms that only large sizes reach, caches that are cut back,
 waits that run out, very long contexts, very large scores."""
 
 import math
+import time
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_layer import (BF16, F64, check_cache, feed, filled, gen, i32, layer, make_kv, new_cache, randn,  # noqa: E402, F401
-                            weights, within)
+from test_gpu_layer import (BF16, F64, check_attention, check_cache, feed, filled, gen, i32, layer,  # noqa: E402, F401
+                            make_kv, new_cache, randn, starts_of, weights, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +74,32 @@ def test_append_tail_given_by_the_caller_is_taken(layer):
     lens = feed(layer, b, kv, lens, [5, 17])
     check_cache(b, kv, lens)
     assert b.read_device_status() == 0
+
+
+# ---------------------------------------------------------------- attention
+
+def test_attention_wait_runs_out_and_workspace_recovers(layer):
+    """The first CTA brings no codes, and gives up its part of items that all
+    CTAs share; the others count theirs.  The next calls, of either kernel,
+    find the counts as if nothing had been."""
+    from routed_expert_prefill_gb300 import moe
+
+    g = gen(25)
+    new, lens = [40], [200000]  # some eight units of 128 tokens a CTA
+    cache = filled(layer, g, new, lens, 1, 64, 64)
+    q = randn(g, 40, 4, 64).bfloat16()
+    ref = check_attention(layer, cache, q, new, lens)
+    for _ in range(2):
+        out = torch.full_like(q, 7.0)
+        moe.debug_stall(cache.ws, moe.MOE_STALL_WEIGHT_COPIES)
+        torch.cuda.synchronize()
+        t0 = time.monotonic()
+        layer.moe_kv_attention(q, starts_of(new), cache, out=out)
+        assert cache.read_device_status() == -6
+        assert time.monotonic() - t0 < 20  # waits of 2 s, side by side
+        assert (out == 7).all()  # the item was not joined
+    assert torch.equal(layer.moe_kv_attention(q, starts_of(new), cache), ref)
+    one = check_attention(layer, cache, q[39:], [1], lens)
+    assert torch.equal(layer.moe_kv_attention(q, starts_of(new), cache), ref)
+    assert torch.equal(layer.moe_kv_attention(q[39:], starts_of([1]), cache), one)
+    assert cache.read_device_status() == 0
