@@ -204,9 +204,10 @@ class KvCache:
     hold keys, then values; tail bf16 [n_seq, 2, hkv, 2 * block, d] the last
     tokens as given; table int32 [n_seq, max_blocks] each sequence's pages;
     lens int32 [n_seq] its tokens.  The caller assigns pages in ``table`` and
-    sets ``lens`` (the new tokens included) before moe_kv_append; both are
-    read on the device.  The tensors are kept, not copied: calls that use one
-    cache are ordered on one stream.
+    sets ``lens`` (the new tokens included) before moe_kv_append, in place
+    (``cache.lens.copy_(...)``, ``cache.table[s, b] = page``); both are read on
+    the device.  The tensors are kept, not copied, and cannot be replaced by
+    others: calls that use one cache are ordered on one stream.
 
     held int32 [n_seq, 2], made here, says up to which token each half of a
     sequence's tail is filled (0: not known); moe_kv_append keeps it, and
@@ -232,17 +233,28 @@ class KvCache:
         n = load_library().moe_kv_workspace_bytes(d)
         if n == 0:
             raise MoeError(-2, f"d={d} must be 64 or 128")
-        self.codes, self.scales, self.tail, self.table, self.lens = codes, scales, tail, table, lens
+        self._codes, self._scales, self._tail, self._table, self._lens = codes, scales, tail, table, lens
         self.n_seq, self.hkv, self.block, self.d = n_seq, hkv, block, d
-        self.ws = torch.zeros(n, dtype=torch.uint8, device=codes.device)
-        self.held = torch.zeros(n_seq, 2, dtype=torch.int32, device=codes.device)
+        self._workspace = torch.zeros(n, dtype=torch.uint8, device=codes.device)
+        self._filled = torch.zeros(n_seq, 2, dtype=torch.int32, device=codes.device)
         self._dev = codes.get_device()
-        self._starts, self._kv, self._scale = (n_seq + 1,), (hkv, d), 1 / math.sqrt(d)
+        self._starts, self._kv, self._softmax_scale = (n_seq + 1,), (hkv, d), 1 / math.sqrt(d)
         self._ws = self.ws.data_ptr(), n
         self._held = self.held.data_ptr()
         self._c = MoeKvCache(codes.data_ptr(), scales.data_ptr(), tail.data_ptr(), table.data_ptr(), lens.data_ptr(),
                              n_seq, n_pages, max_blocks, block, hkv, d)
         self._ref = ctypes.byref(self._c)
+
+    # Kernels read these by address, so that a tensor put in the place of one
+    # would not be seen, and the one it replaced could be handed out again
+    # while kernels still read it: assigning raises AttributeError.
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    tail = property(lambda self: self._tail)
+    table = property(lambda self: self._table)
+    lens = property(lambda self: self._lens)
+    held = property(lambda self: self._filled)
+    ws = property(lambda self: self._workspace)
 
     @classmethod
     def new(cls, n_seq: int, n_pages: int, max_blocks: int, hkv: int, d: int, block: int = 64, device="cuda"):
@@ -308,7 +320,7 @@ def moe_kv_attention(q: torch.Tensor, starts: torch.Tensor, cache: KvCache, scal
     if out is None:
         out = _empty(shape, _BF, q, stream)
     status = lib.moe_kv_attention(q.data_ptr(), _row_stride(q), starts.data_ptr(), t, hq,
-                                  cache._scale if scale is None else scale, cache._ref, out.data_ptr(), *cache._ws,
+                                  cache._softmax_scale if scale is None else scale, cache._ref, out.data_ptr(), *cache._ws,
                                   _raw(stream, dev))
     if status:
         _check(status)

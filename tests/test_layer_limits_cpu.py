@@ -17,3 +17,11 @@ def test_append_held_refuses(moe, kw, status):  # noqa: F811
     a = dict(k=OK, ks=256, v=OK, vs=256, starts=OK, t=3, c=ctypes.byref(_cache(moe)), held=OK, ws=OK, n=1 << 30)
     a.update(kw)
     assert moe.load_library().moe_kv_append_held(*a.values(), None) == status
+
+
+@pytest.mark.parametrize("name", ["codes", "scales", "tail", "table", "lens", "held", "ws"])
+def test_cache_tensors_cannot_be_replaced(layer, name):  # noqa: F811
+    """The kernels keep the addresses of the first ones."""
+    cache = object.__new__(layer.KvCache)
+    with pytest.raises(AttributeError):
+        setattr(cache, name, torch.zeros(1))
