@@ -91,8 +91,11 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   // the sequence that owns the slot: every thread looks at some, one answers
   if (tid == 0) owner = -1;
   __syncthreads();
-  for (int i = tid; i < c.n_seq; i += APPEND_THREADS)
-    if (starts[i] / c.block + 2 * i <= slot && slot < starts[i + 1] / c.block + 2 * (i + 1)) owner = i;
+  for (int i = tid; i < c.n_seq; i += APPEND_THREADS) {
+    const int from = starts[i], to = starts[i + 1];
+    if (from / c.block + 2 * i <= slot && slot < to / c.block + 2 * (i + 1)) owner = i;
+    if (to < from && slot == 0) raise_flag(st, FLAG_BAD_CACHE);  // may own no slot that would say so
+  }
   __syncthreads();
   const int s = owner;
   if (s < 0) {  // past the last sequence, or starts out of order

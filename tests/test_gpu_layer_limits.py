@@ -76,6 +76,16 @@ def test_append_tail_given_by_the_caller_is_taken(layer):
     assert b.read_device_status() == 0
 
 
+def test_append_reports_starts_out_of_order(layer):
+    """A sequence whose rows end before they begin, between two whose rows are in range."""
+    total = [200, 64, 295]
+    kv = make_kv(gen(23), [300], 1, 64)[0]
+    cache = new_cache(layer, total, 64, 1, 64)
+    cache.lens.copy_(i32(total))
+    layer.moe_kv_append(kv[:, 0], kv[:, 1], i32([0, 200, 5, 300]), cache)
+    assert cache.read_device_status() == -5
+
+
 # ---------------------------------------------------------------- attention
 
 def test_attention_wait_runs_out_and_workspace_recovers(layer):
