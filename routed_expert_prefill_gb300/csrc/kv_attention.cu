@@ -10,6 +10,7 @@ namespace {
 
 constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = AT_WARPS * 32;
+constexpr float ABOVE = 14.f;                        // the largest fp16 weight is 2^ABOVE
 constexpr int WARP_TOKENS = 32;                      // tokens of one warp step
 static_assert(UNIT == AT_WARPS * WARP_TOKENS, "a CTA step is a unit");
 
@@ -88,8 +89,10 @@ __device__ __forceinline__ uint32_t codes_pair(uint32_t a, uint32_t b) {
 // difference loses nothing that matters); values, summed over all tokens, are
 // converted to c itself.  The key scale multiplies the fp32 scores; the value
 // scale enters the weights, p_j = exp2(s_j - m) vs_j, through its logarithm
-// with a running maximum M of its own, so that the fp16 weights are at most 1
-// whatever the scales are.
+// with a running maximum M of its own, so that the fp16 weights are at most
+// 2^ABOVE whatever the scales are; that far up, those that fp16 rounds to
+// nothing are below 2^-39 of the largest (2^-25 without it: what the small
+// weights of a long context add up to was lost).
 //
 // 48 sequences of up to 20000 tokens, 32 heads on 4, one new token each: 109 us
 // for 626 MB, 0.86 of the copy rate; the unpacking (ALU pipe 0.6 full) is next.
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
         // ---- weights, transposed into the second product's operand
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-          const float v0 = vlog[a] - uM[0], v1 = vlog[a] - uM[1];
+          const float v0 = vlog[a] + ABOVE - uM[0], v1 = vlog[a] + ABOVE - uM[1];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float z0 = sc[t][a][2 * e], z1 = sc[t][a][2 * e + 1];
@@ -523,11 +526,13 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
       }
     }
     if (write && r < rows) {
-      // sum p vs v = 2^(M - m) of what was accumulated; nothing seen, or all
-      // values zero: 0
+      // sum p vs v = 2^(M - m - ABOVE) of what was accumulated; nothing seen, or
+      // all values zero: 0
       const float k = cl == 0.f ? 0.f : (cM == -INFINITY ? 0.f : exp2f(cM - cm)) / cl;
       const uint32_t rr = (uint32_t)qt * ROWS + r;
       uint16_t* dst = p.out + ((size_t)(q.row + rr / (uint32_t)p.G) * p.hq + (size_t)h * p.G + rr % (uint32_t)p.G) * D + d0;
+#pragma unroll
+      for (int i = 0; i < DPT; ++i) acc[i] *= 1.f / (1 << (int)ABOVE);
 #pragma unroll
       for (int i = 0; i < DPT; i += 4)
         *reinterpret_cast<uint2*>(dst + i) = make_uint2(pack_bf16x2(acc[i] * k, acc[i + 1] * k),

@@ -27,9 +27,13 @@ constexpr int ITEM_COST = 3;
 constexpr int SC_RING = 4;   // tiles whose scales are kept
 constexpr int RED_RING = 4;  // pieces whose largest value scales are kept
 constexpr uint64_t WAIT_NS = 2000000000ull;
-// What a row's weights of 64 tokens may add up to before its sums are rescaled:
-// none is then above it, and if they exceed it the largest is above 4.
-constexpr float LIMIT = 256.f;
+// A row's weights are taken against a reference 2^ABOVE below its largest, so
+// that those fp16 rounds to nothing are below 2^-32 of that: taken against the
+// largest itself, a long context's small weights were lost from 2^-25 on, and
+// with them what they add up to.  LIMIT: what the weights of 64 tokens may add
+// up to before the row's sums are rescaled; none is then above it, which fp16
+// holds, and if they exceed it the largest is above 4 * 2^ABOVE.
+constexpr float ABOVE = 7.f, LIMIT = 32768.f;
 
 // One CTA's part of an item: units u0 .. u1 - 1 of it.
 struct Piece {
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
           };
           if (__any_sync(~0u, M == -INFINITY)) {  // nothing seen so far: the row's maximum
             const float top = largest();
-            if (M == -INFINITY) M = top;  // nothing summed yet: nothing to rescale
+            if (M == -INFINITY) M = top - ABOVE;  // nothing summed yet: nothing to rescale
           }
           // ---- the weights against the maximum so far; again, with the sums
           // rescaled, if a row's outgrow LIMIT (twice at most: scores beyond
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
             // no weight above the limit if their sum is not
             if (again == 2 || !__any_sync(~0u, all > LIMIT)) break;
             const float top = largest();  // by the whole warp
-            const float by = all > LIMIT ? fmaxf(top - at, 0.f) : 0.f, drop = ex2(-by);
+            const float by = all > LIMIT ? fmaxf(top - ABOVE - at, 0.f) : 0.f, drop = ex2(-by);
             M += by;
             l *= drop;
             if (u > P.u0 || half) {

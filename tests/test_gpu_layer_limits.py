@@ -113,3 +113,31 @@ def test_attention_wait_runs_out_and_workspace_recovers(layer):
     assert torch.equal(layer.moe_kv_attention(q, starts_of(new), cache), ref)
     assert torch.equal(layer.moe_kv_attention(q[39:], starts_of([1]), cache), one)
     assert cache.read_device_status() == 0
+
+
+@pytest.mark.parametrize("n_seq,new,bits", [(500, 1, 39), (200, 40, 32)])
+def test_attention_small_weights_of_a_long_context(layer, n_seq, new, bits):
+    """One token with nearly all of the weight and no value, before 2^18 with
+    2^-26.25 of its weight each: what they add up to is the result.  A weight
+    may be off by 2^-11 and by 2^-bits of the row's largest.  All sequences
+    share their pages; there are enough for most to stay within one CTA."""
+    ln, d, block = 2 ** 18, 64, 64
+    pages = ln // block
+    cache = layer.KvCache.new(n_seq, pages, pages, 1, d, block)
+    cache.table[:] = torch.randperm(pages, generator=torch.Generator().manual_seed(0)).to(torch.int32).cuda()
+    place = torch.arange(ln, device="cuda")
+    v = (32 + (place[:, None] * 7 + torch.arange(d, device="cuda")) % 64).to(torch.int8)
+    v[0] = 0
+    cache.codes[1, cache.table[0].long(), 0] = v.view(pages, block, d)
+    cache.codes[0, int(cache.table[0, 0]), 0, 0, 0] = 64  # the first token's key: 1 in channel 0
+    cache.scales.fill_(1 / 64)
+    cache.lens.fill_(ln)
+    q = torch.zeros(n_seq * new, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = 1
+    got = layer.moe_kv_attention(q, starts_of([new] * n_seq), cache, scale=26.25 * math.log(2))
+    w = 2.0 ** -26.25
+    sums = v.to(F64).cumsum(0)[ln - new:] / 64  # of what each row sees
+    seen = torch.arange(ln - new, ln, device="cuda", dtype=F64)[:, None]  # tokens beside the first
+    ref = (w * sums / (1 + w * seen)).repeat(n_seq, 1)[:, None]
+    tol = (2.0 ** -11 + 2.0 ** -14) * ref + ln * 2.0 ** -bits * 95 / 64
+    within(got, ref, tol + BF16 * (ref + tol))
