@@ -431,8 +431,10 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
             if (M == -INFINITY) M = top - ABOVE;  // nothing summed yet: nothing to rescale
           }
           // ---- the weights against the maximum so far; again, with the sums
-          // rescaled, if a row's outgrow LIMIT (twice at most: scores beyond
-          // 2^24, whose units are above 1, may leave more than that)
+          // rescaled, if a row's outgrow LIMIT.  Scores and their maximum are
+          // rounded alike before M comes off, so that the largest weight is
+          // 2^ABOVE but for the rounding of M, 4 times at most, however large
+          // the scores are
           uint32_t w[2][16];
           float add;
           for (int again = 0;; ++again) {
@@ -450,12 +452,14 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
 #pragma unroll
               for (int h2 = 0; h2 < 2; ++h2) {
                 const float a = fmaxf(f * sck[2 * c + h2], 1e-30f);
-                const float b = fmaf(-off, a, scl[2 * c + h2] - at);
+                const float b = fmaf(-off, a, scl[2 * c + h2]);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 16 * h2; i < 16 * h2 + 16; i += 2) {
+                  // rounded as `largest` rounds, and only then taken off M
                   float2 z = fma2(make_float2(__uint_as_float(vb[c][i]), __uint_as_float(vb[c][i + 1])),
                                   make_float2(a, a), make_float2(b, b));
+                  z = add2(z, make_float2(-at, -at));
                   z = make_float2(ex2(z.x), ex2(z.y));
                   sum = add2(sum, z);
                   w[c][i >> 1] = half2_bits(__float22half2_rn(z));
@@ -464,10 +468,10 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
                 all += sum.x + sum.y;
               }
             // no weight above the limit if their sum is not
-            if (again == 2 || !__any_sync(~0u, all > LIMIT)) break;
+            if (again || !__any_sync(~0u, all > LIMIT)) break;
             const float top = largest();  // by the whole warp
-            const float by = all > LIMIT ? fmaxf(top - ABOVE - at, 0.f) : 0.f, drop = ex2(-by);
-            M += by;
+            const float to = all > LIMIT ? fmaxf(top - ABOVE, at) : at, drop = ex2(at - to);
+            if (all > LIMIT) M = to;
             l *= drop;
             if (u > P.u0 || half) {
               // O is the first half's until its product has ended (the products

@@ -141,3 +141,41 @@ def test_attention_small_weights_of_a_long_context(layer, n_seq, new, bits):
     ref = (w * sums / (1 + w * seen)).repeat(n_seq, 1)[:, None]
     tol = (2.0 ** -11 + 2.0 ** -14) * ref + ln * 2.0 ** -bits * 95 / 64
     within(got, ref, tol + BF16 * (ref + tol))
+
+def one_hot_case(layer, new, exponent, q_exponent, scale):
+    """Scores so large that each row's best token has all of the weight, with
+    value scales that differ: the result is that token's value."""
+    g = gen(24 + new)
+    ln, hq, d, block = 300, 4, 64, 16
+    cache = filled(layer, g, [new], [ln], 2, d, block)
+    pages = cache.table[0, :-(-ln // block)].long()
+    cache.scales[1, pages] *= 10 ** (2 * torch.rand(len(pages), 2, generator=g, device="cuda") - 1)
+    q = (randn(g, new, hq, d) * 2.0 ** q_exponent).bfloat16()
+    got = layer.moe_kv_attention(q, i32([0, new]), cache, scale=scale)
+    checked = 0
+    for h in range(hq):
+        k, v = ((cache.codes[i, pages, h // 2].to(F64) * cache.scales[i, pages, h // 2].to(F64)[:, None, None])
+                .reshape(-1, d)[:ln] for i in range(2))
+        z = q[:, h].to(F64) @ k.t() * scale
+        size = (q[:, h].to(F64).abs() @ k.abs().t() * scale).amax(-1)
+        see = torch.arange(ln, device="cuda")[None, :] <= torch.arange(ln - new, ln, device="cuda")[:, None]
+        two = z.masked_fill(~see, -math.inf).topk(2, -1)
+        gap = two.values[:, 0] - two.values[:, 1]
+        # scores are off by less than 2^-18 of `size`; beside a token 200 ahead nothing counts
+        clear = gap > 200 + 2.0 ** -16 * size
+        assert float(size.max()) > 2.0 ** exponent
+        checked += int(clear.sum())
+        ref = v[two.indices[:, 0]][clear]
+        # one weight rounded to fp16, the value scale's logarithm and power
+        tol = (2.0 ** -11 + 2.0 ** -16) * ref.abs()
+        within(got[clear, h], ref, tol + BF16 * (ref.abs() + tol))
+    assert checked >= max(2, new)  # of 4 * new rows
+
+
+@pytest.mark.parametrize("exponent", [12, 17, 21, 25, 28, 40])
+def test_attention_large_scores_of_many_rows(layer, exponent):
+    one_hot_case(layer, 40, exponent, 0, 2.0 ** (exponent - 3))
+
+
+def test_attention_large_queries_of_many_rows(layer):
+    one_hot_case(layer, 40, 110, 116, 2.0 ** -3)
