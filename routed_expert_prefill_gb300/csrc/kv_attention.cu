@@ -89,10 +89,12 @@ __device__ __forceinline__ uint32_t codes_pair(uint32_t a, uint32_t b) {
 // difference loses nothing that matters); values, summed over all tokens, are
 // converted to c itself.  The key scale multiplies the fp32 scores; the value
 // scale enters the weights, p_j = exp2(s_j - m) vs_j, through its logarithm
-// with a running maximum M of its own, so that the fp16 weights are at most
+// with a running maximum of its own, so that the fp16 weights are at most
 // 2^ABOVE whatever the scales are; that far up, those that fp16 rounds to
 // nothing are below 2^-39 of the largest (2^-25 without it: what the small
-// weights of a long context add up to was lost).
+// weights of a long context add up to was lost).  That maximum, V, is of
+// s_j - m + log2 vs_j: beside large scores the logarithm would lose its bits
+// (a value 4% off at scores of 2^20, in powers of two).
 //
 // 48 sequences of up to 20000 tokens, 32 heads on 4, one new token each: 109 us
 // for 626 MB, 0.86 of the copy rate; the unpacking (ALU pipe 0.6 full) is next.
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* ring = smem + (threadIdx.x >> 5) * STAGES * STAGE;
   float(*osum)[ROWS][D + 4] = reinterpret_cast<float(*)[ROWS][D + 4]>(smem);  // after an item's steps
-  __shared__ float sm[AT_WARPS][ROWS], sM[AT_WARPS][ROWS], sl[AT_WARPS][ROWS];
+  __shared__ float sm[AT_WARPS][ROWS], sV[AT_WARPS][ROWS], sl[AT_WARPS][ROWS];
   __shared__ int64_t scan[AT_WARPS + 2];
   __shared__ uint32_t arrived;
   pdl_wait();
@@ -143,10 +145,10 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
                                                         64 * (w >> 2) + 16 * j + 4 * (w & 3));
       }
     }
-    float m[NT][2], M[NT][2], l[NT][2], o[NT][NO][4];
+    float m[NT][2], V[NT][2], l[NT][2], o[NT][NO][4];  // o: in units of 2^(m + V - ABOVE)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t][0] = m[t][1] = M[t][0] = M[t][1] = -INFINITY;
+      m[t][0] = m[t][1] = V[t][0] = V[t][1] = -INFINITY;
       l[t][0] = l[t][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < NO; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
@@ -310,42 +312,63 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
             for (int e = 0; e < 4; ++e)
               if (!live[a] || pos0 + 16 * a + 8 * (e >> 1) + g > limit[t][e & 1]) sc[t][a][e] = -INFINITY;
         }
-        float um[2], uM[2];
+        // ---- the running maxima; V at first against the old m, so that both
+        // go through the lanes side by side
+        float um[2], uV[2], nV[2], down[2];
+        bool far = false;
+        auto top_V = [&](int c, float ref) {
+          return fmaxf(fmaxf(sc[t][0][c], sc[t][0][2 + c]) - ref + vlog[0],
+                       fmaxf(sc[t][1][c], sc[t][1][2 + c]) - ref + vlog[1]);
+        };
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float x0 = fmaxf(sc[t][0][c], sc[t][0][2 + c]), x1 = fmaxf(sc[t][1][c], sc[t][1][2 + c]);
-          float nm = fmaxf(x0, x1), nM = fmaxf(x0 + vlog[0], x1 + vlog[1]);
+          const float old = m[t][c];
+          float nm = fmaxf(fmaxf(sc[t][0][c], sc[t][0][2 + c]), fmaxf(sc[t][1][c], sc[t][1][2 + c]));
+          nV[c] = top_V(c, old);
 #pragma unroll
           for (int s = 4; s < 32; s *= 2) {
             nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, s));
-            nM = fmaxf(nM, __shfl_xor_sync(~0u, nM, s));
+            nV[c] = fmaxf(nV[c], __shfl_xor_sync(~0u, nV[c], s));
           }
-          nm = fmaxf(nm, m[t][c]);
-          nM = fmaxf(nM, M[t][c]);
+          m[t][c] = nm = fmaxf(nm, old);
           // rows that have seen nothing yet: any finite reference does
           um[c] = nm == -INFINITY ? 0.f : nm;
-          uM[c] = nM == -INFINITY ? 0.f : nM;
-          if (__any_sync(~0u, nm != m[t][c])) l[t][c] *= ex2(m[t][c] - um[c]);
-          if (__any_sync(~0u, nM != M[t][c])) {
-            const float drop = ex2(M[t][c] - uM[c]);
+          down[c] = old - um[c];
+          nV[c] += down[c];
+          l[t][c] *= ex2(down[c]);
+          far |= nm != old && !(down[c] > -1024.f);
+        }
+        if (__any_sync(~0u, far)) {  // an old maximum far off, or none
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            nV[c] = top_V(c, um[c]);
+#pragma unroll
+            for (int s = 4; s < 32; s *= 2) nV[c] = fmaxf(nV[c], __shfl_xor_sync(~0u, nV[c], s));
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float was = V[t][c] + down[c];  // what was, against the new m
+          V[t][c] = nV[c] = fmaxf(nV[c], was);  // (-inf in all places gives no number: then that of `was`)
+          uV[c] = nV[c] == -INFINITY ? 0.f : nV[c];
+          if (__any_sync(~0u, nV[c] != was)) {
+            const float drop = ex2(was - uV[c]);
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
               o[t][i][c] *= drop;
               o[t][i][2 + c] *= drop;
             }
           }
-          m[t][c] = nm;
-          M[t][c] = nM;
         }
         // ---- weights, transposed into the second product's operand
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-          const float v0 = vlog[a] + ABOVE - uM[0], v1 = vlog[a] + ABOVE - uM[1];
+          const float v0 = vlog[a] + ABOVE - uV[0], v1 = vlog[a] + ABOVE - uV[1];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float z0 = sc[t][a][2 * e], z1 = sc[t][a][2 * e + 1];
-            l[t][0] += ex2(z0 - um[0]);
-            l[t][1] += ex2(z1 - um[1]);
+            const float z0 = sc[t][a][2 * e] - um[0], z1 = sc[t][a][2 * e + 1] - um[1];
+            l[t][0] += ex2(z0);
+            l[t][1] += ex2(z1);
             pb[t][a][e] = transpose8x8(half2_bits(__floats2half2_rn(ex2(z0 + v0), ex2(z1 + v1))));
           }
         }
@@ -397,7 +420,7 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
         if (g == 0) {
           const int r = 8 * t + 2 * j + c;
           sm[warp][r] = m[t][c];
-          sM[warp][r] = M[t][c];
+          sV[warp][r] = V[t][c];
           sl[warp][r] = l[t][c];
         }
       }
@@ -407,9 +430,12 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int r = 8 * t + 2 * j + c;
-        float top = fmaxf(fmaxf(sM[0][r], sM[1][r]), fmaxf(sM[2][r], sM[3][r]));
+        float um = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r])), top = -INFINITY;
+        if (um == -INFINITY) um = 0.f;
+#pragma unroll
+        for (int w = 0; w < AT_WARPS; ++w) top = fmaxf(top, sV[w][r] + (sm[w][r] - um));
         if (top == -INFINITY) top = 0.f;
-        const float drop = ex2(M[t][c] - top);
+        const float drop = ex2(V[t][c] + (m[t][c] - um) - top);
 #pragma unroll
         for (int i = 0; i < NO; ++i)
           *reinterpret_cast<float2*>(&osum[warp][r][(D / 8) * g + 2 * i]) =
@@ -418,14 +444,15 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
     __syncthreads();
     constexpr int TPR = AT_THREADS / ROWS, DPT = D / TPR;  // threads of a row, channels of a thread
     const int r = tid / TPR, d0 = (tid % TPR) * DPT;
-    float cm = -INFINITY, cM = -INFINITY, cl = 0.f, acc[DPT];
+    float cm = -INFINITY, cV = -INFINITY, cl = 0.f, acc[DPT];
+#pragma unroll
+    for (int w = 0; w < AT_WARPS; ++w) cm = fmaxf(cm, sm[w][r]);
 #pragma unroll
     for (int w = 0; w < AT_WARPS; ++w) {
-      cm = fmaxf(cm, sm[w][r]);
-      cM = fmaxf(cM, sM[w][r]);
+      const float down = sm[w][r] - (cm == -INFINITY ? 0.f : cm);
+      cV = fmaxf(cV, sV[w][r] + down);
+      cl += sl[w][r] * ex2(down);
     }
-#pragma unroll
-    for (int w = 0; w < AT_WARPS; ++w) cl += sl[w][r] * ex2(sm[w][r] - (cm == -INFINITY ? 0.f : cm));
 #pragma unroll
     for (int i = 0; i < DPT; ++i)
       acc[i] = osum[0][r][d0 + i] + osum[1][r][d0 + i] + osum[2][r][d0 + i] + osum[3][r][d0 + i];
@@ -446,7 +473,7 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
 #pragma unroll
           for (int i = 0; i < DPT; i += 4)
             *reinterpret_cast<float4*>(to + r * D + d0 + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-          if (tid % TPR == 0) *reinterpret_cast<float4*>(to + ROWS * D + 4 * r) = make_float4(cm, cM, cl, 0.f);
+          if (tid % TPR == 0) *reinterpret_cast<float4*>(to + ROWS * D + 4 * r) = make_float4(cm, cV, cl, 0.f);
         }
       };
       // true in the CTA that comes last of `all`
@@ -460,9 +487,9 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
         __threadfence();
         return true;
       };
-      // parts from, from + step, ... up to `to` into acc, cm, cM, cl
+      // parts from, from + step, ... up to `to` into acc, cm, cV, cl
       auto join = [&](int from, int to, int step) {
-        cm = cM = -INFINITY;
+        cm = cV = -INFINITY;
         cl = 0.f;
 #pragma unroll
         for (int i = 0; i < DPT; ++i) acc[i] = 0.f;
@@ -474,15 +501,21 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
           st[i] = c <= to ? __ldcg(reinterpret_cast<const float4*>(part_of(c) + ROWS * D + 4 * r))
                           : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
           cm = fmaxf(cm, st[i].x);
-          cM = fmaxf(cM, st[i].y);
         }
-        const float um = cm == -INFINITY ? 0.f : cm, uM = cM == -INFINITY ? 0.f : cM;
+        const float um = cm == -INFINITY ? 0.f : cm;
+#pragma unroll
+        for (int i = 0; i < JOIN; ++i) {
+          st[i].x -= um;
+          st[i].y += st[i].x;
+          cV = fmaxf(cV, st[i].y);
+        }
+        const float uV = cV == -INFINITY ? 0.f : cV;
 #pragma unroll
         for (int i = 0; i < JOIN; ++i) {
           const int c = from + i * step;
           if (c > to) break;
-          cl += st[i].z * ex2(st[i].x - um);
-          const float drop = ex2(st[i].y - uM);
+          cl += st[i].z * ex2(st[i].x);
+          const float drop = ex2(st[i].y - uV);
 #pragma unroll
           for (int e = 0; e < DPT; e += 4) {
             const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(c) + r * D + d0 + e));
@@ -506,19 +539,21 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
           const int groups = (parts + JOIN - 1) / JOIN;
           write = last_of(p.counters + 3 * c0, groups);
           if (write) {
-            float gm = -INFINITY, gM = -INFINITY, gl = 0.f, ga[DPT] = {};
+            float gm = -INFINITY, gV = -INFINITY, gl = 0.f, ga[DPT] = {};
             // more than JOIN groups (over 256 parts): in turns
             for (int i = 0; i < groups; i += JOIN) {
               join(c0 + i * JOIN, min(c1, c0 + (i + JOIN) * JOIN - 1), JOIN);
-              const float nm = fmaxf(gm, cm), nM = fmaxf(gM, cM);
-              const float um = nm == -INFINITY ? 0.f : nm, uM = nM == -INFINITY ? 0.f : nM;
+              const float nm = fmaxf(gm, cm), um = nm == -INFINITY ? 0.f : nm;
               gl = gl * ex2(gm - um) + cl * ex2(cm - um);
-              const float f0 = ex2(gM - uM), f1 = ex2(cM - uM);
+              gV += gm - um;
+              cV += cm - um;
+              const float nV = fmaxf(gV, cV), uV = nV == -INFINITY ? 0.f : nV;
+              const float f0 = ex2(gV - uV), f1 = ex2(cV - uV);
 #pragma unroll
               for (int e = 0; e < DPT; ++e) ga[e] = ga[e] * f0 + acc[e] * f1;
-              gm = nm, gM = nM;
+              gm = nm, gV = nV;
             }
-            cm = gm, cM = gM, cl = gl;
+            cm = gm, cV = gV, cl = gl;
 #pragma unroll
             for (int e = 0; e < DPT; ++e) acc[e] = ga[e];
           }
@@ -526,9 +561,9 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
       }
     }
     if (write && r < rows) {
-      // sum p vs v = 2^(M - m - ABOVE) of what was accumulated; nothing seen, or
-      // all values zero: 0
-      const float k = cl == 0.f ? 0.f : (cM == -INFINITY ? 0.f : exp2f(cM - cm)) / cl;
+      // sum p vs v = 2^(V - ABOVE) of what was accumulated; nothing seen, or all
+      // values zero: 0
+      const float k = cl == 0.f ? 0.f : (cV == -INFINITY ? 0.f : exp2f(cV)) / cl;
       const uint32_t rr = (uint32_t)qt * ROWS + r;
       uint16_t* dst = p.out + ((size_t)(q.row + rr / (uint32_t)p.G) * p.hq + (size_t)h * p.G + rr % (uint32_t)p.G) * D + d0;
 #pragma unroll

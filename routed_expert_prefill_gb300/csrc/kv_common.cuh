@@ -13,8 +13,8 @@ constexpr int KV_ROWS = 16;        // rows of a query tile, at most
 inline int kv_grid_max() { return sm_count() * KV_CTAS_PER_SM; }
 inline size_t kv_counter_off() { return sizeof(DeviceStatus); }
 inline size_t kv_partial_off() { return align_up(kv_counter_off() + (size_t)kv_grid_max() * 3 * 4, 256); }
-// A partial result: for each row its score maximum, its maximum of score +
-// log2(value scale), its sum and d accumulators.
+// A partial result: for each row its score maximum, its maximum of score less
+// that + log2(value scale), its sum and d accumulators.
 __host__ __device__ constexpr size_t kv_partial_floats(int d) { return (size_t)KV_ROWS * (d + 4); }
 size_t kv_tile_partial_bytes(int d);  // kv_attention_tile.cu
 inline size_t kv_ws_bytes(int d) {

@@ -179,3 +179,29 @@ def test_attention_large_scores_of_many_rows(layer, exponent):
 
 def test_attention_large_queries_of_many_rows(layer):
     one_hot_case(layer, 40, 110, 116, 2.0 ** -3)
+
+
+@pytest.mark.parametrize("exponent", [12, 17, 21, 25, 28, 40])
+def test_attention_large_scores_of_single_tokens(layer, exponent):
+    one_hot_case(layer, 1, exponent, 0, 2.0 ** (exponent - 3))
+
+
+@pytest.mark.parametrize("exponent", [12, 21, 28])
+def test_attention_large_scores_joined_across_the_gpu(layer, exponent):
+    """The same from the parts of many CTAs, in two levels: each row's best
+    token is one of three far apart, the other parts are far below it."""
+    g = gen(26)
+    ln, d, block = 70001, 64, 64
+    cache = filled(layer, g, [1], [ln], 1, d, block)
+    pages = cache.table[0, :-(-ln // block)].long()
+    cache.scales[1, pages] *= 10 ** (2 * torch.rand(len(pages), 1, generator=g, device="cuda") - 1)
+    for at in (77, 35000, ln - 1):
+        page, place = int(cache.table[0, at // block]), at % block
+        kept = cache.codes[0, page, 0, place].clone()
+        cache.codes[0, page, 0, place] = 127
+        q = torch.ones(1, 2, d, dtype=torch.bfloat16, device="cuda")
+        got = layer.moe_kv_attention(q, i32([0, 1]), cache, scale=2.0 ** (exponent - 6))
+        ref = cache.codes[1, page, 0, place].to(F64) * cache.scales[1, page, 0].to(F64)
+        tol = (2.0 ** -11 + 2.0 ** -16) * ref.abs()
+        within(got[0], ref.expand(2, d), tol + BF16 * (ref.abs() + tol))
+        cache.codes[0, page, 0, place] = kept
