@@ -218,9 +218,9 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
       }
       m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
       m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-      // the row's largest magnitude goes to [256, 512)
+      // the row's largest magnitude goes to [2^14, 2^15)
       const int ex = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
-      const float up = __uint_as_float((uint32_t)(127 + 8 - ex) << 23);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
 #pragma unroll
       for (int w = 0; w < KL * 4; ++w) {
         // with the keys' bytes 0 and 2, then 1 and 3
@@ -232,7 +232,9 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
       }
       sum += __shfl_xor_sync(~0u, sum, 1);
       sum += __shfl_xor_sync(~0u, sum, 2);
-      const float f = __uint_as_float((uint32_t)(max(127 - 8 + ex, 1)) << 23) * p.scale_log2 * 0x1p24f;
+      // 2^24 of the codes, half here and half with the key scale: neither then
+      // passes fp32's range before their product does
+      const float f = __uint_as_float((uint32_t)(127 - 14 + ex) << 23) * p.scale_log2 * 0x1p12f;
       // rows past the last: nothing of theirs is stored, so they may see all
       const int lim = r < rows ? q.len - q.n + i : INT_MAX;
       all_see = min(all_see, lim);
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
       for (int r = 0; r < 2; ++r) {
         const int run = (2 * i + r) & 31;
         live[r] = __shfl_sync(~0u, page, run) >= 0;
-        ksc[r] = __shfl_sync(~0u, kscale, run);
+        ksc[r] = __shfl_sync(~0u, kscale, run) * 0x1p12f;
         vlog[r] = __log2f(__shfl_sync(~0u, vscale, run));
       }
       // ---- scores: row g of tile a is token 16 a + g, column c query row c

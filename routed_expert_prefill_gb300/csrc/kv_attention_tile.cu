@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
             const int ex_of = __shfl_sync(~0u, ex, (lane % RPL) * LPR);
             const float sum_of = __shfl_sync(~0u, sum, (lane % RPL) * LPR);
             if (lane / RPL == b / RPL + i) {
-              f = __uint_as_float((uint32_t)(127 - 14 + ex_of) << 23) * fabsf(p.scale_log2) * 0x1p24f;
+              f = __uint_as_float((uint32_t)(127 - 14 + ex_of) << 23) * fabsf(p.scale_log2) * 0x1p12f;
               off = sum_of * 0x1p-17f;  // 128 * 2^-24
             }
           }
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_attention_tile_kernel(AttnPar
           // the products that freed this K stage came after its weights
           const uint32_t slot = it % SC_RING;
           const float lg = pages < 0 ? -INFINITY : fmaxf(__log2f(vs) - vref_log, -60.f);
-          S.sc_k[slot][lane] = ks;
+          S.sc_k[slot][lane] = ks * 0x1p12f;  // half of the codes' 2^24; the row's factor has the other half
           S.sc_log[slot][lane] = lg;
           S.sc_inv[slot][lane] = pages < 0 ? 0.f : ex2(-lg);
           if (lane == 0) S.sc_ref[slot] = vref;

@@ -205,3 +205,9 @@ def test_attention_large_scores_joined_across_the_gpu(layer, exponent):
         tol = (2.0 ** -11 + 2.0 ** -16) * ref.abs()
         within(got[0], ref.expand(2, d), tol + BF16 * (ref.abs() + tol))
         cache.codes[0, page, 0, place] = kept
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("q_exponent,scale", [(116, 2.0 ** -3), (122, 2.0 ** -6)])
+def test_attention_largest_queries(layer, new, q_exponent, scale):
+    one_hot_case(layer, new, 110, q_exponent, scale)
