@@ -42,6 +42,35 @@ def test_qmv_rows_that_fill_shared_memory(layer, t, n, k):
     qmv_case(layer, t, n, k, False)
 
 
+WIDE = 38912 + 89  # 256 weight rows for each of 152 SMs, and an odd rest
+
+
+# 32 weight rows a warp: 8, 16, 32 and 64 rows of x a tile; k of whole units and not
+@pytest.mark.parametrize("t", [5, 12, 27, 50])
+@pytest.mark.parametrize("k", [512, 448])
+@pytest.mark.parametrize("q8", [False, True])
+def test_qmv_wide_tiles(layer, t, k, q8):
+    qmv_case(layer, t, WIDE, k, q8)
+
+
+# The largest k of every form of the streaming kernel (one or two teams, three
+# or four stages, 8 or 16 rows), and sizes one step above, which take the next
+# form or the tile kernel; 152 SMs.
+@pytest.mark.parametrize("t,n,k,q8", [
+    (1, 4000, 7680, False), (1, 4000, 13824, False), (1, 4000, 13888, False), (8, 4000, 2368, False),
+    (8, 4000, 2432, False), (8, 4000, 4352, False), (8, 4000, 4416, False), (4, 4000, 7168, False),
+    (9, 4000, 1408, False), (9, 4000, 1472, False), (9, 4000, 3136, False), (9, 4000, 3200, False),
+    (12, 4000, 4864, False), (9, 4000, 7232, False), (9, 4000, 7296, False), (16, 4000, 832, False),
+    (16, 4000, 1984, False), (16, 4000, 2048, False), (4, 1000, 13312, False), (4, 1000, 15360, False),
+    (4, 1000, 15424, False), (8, 1000, 8704, False), (16, 1000, 4352, False), (16, 1000, 4416, False),
+    (1, 4000, 7104, True), (1, 4000, 12800, True), (2, 4000, 5504, True), (8, 4000, 4224, True),
+    (8, 4000, 4288, True), (10, 4000, 1216, True), (10, 4000, 2816, True), (16, 4000, 1920, True),
+    (13, 4000, 4416, True), (16, 4000, 4224, True), (16, 4000, 4288, True), (4, 1000, 14656, True),
+    (16, 1000, 3648, True), (16, 1000, 4224, True), (3, 1000, 16384, True), (3, 1000, 16448, True)])
+def test_qmv_streaming_forms(layer, t, n, k, q8):
+    qmv_case(layer, t, n, k, q8)
+
+
 # ---------------------------------------------------------------- append
 
 def test_append_cut_back_past_the_tail_is_reported(layer):
