@@ -534,9 +534,18 @@ int moe_add_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residu
  * Product of rows with 4-bit weights:  y[r][o] = sum_i x[r][i] * W[o][i],
  * W[o][i] = q[o][i] * s[o][i/64] + b[o][i/64], the records' affine kind
  * (moe_qweights, one row-major matrix): codes uint8 [n][k/2] with the low
- * nibble at the even i, scales and biases fp16 [n][k/64].  The codes, scales
- * and biases enter exactly (no rounding of W to bf16), products are summed
- * in fp32 and the result is rounded once.
+ * nibble at the even i, scales and biases fp16 [n][k/64], each array 16-byte
+ * aligned.  The codes, scales and biases enter exactly (no rounding of W to
+ * bf16), products are summed in fp32 and the result is rounded once.
+ *
+ * The fp32 sums are those of the two terms apart, s sum q x and b sum x (for
+ * more rows of x than the streaming kernel takes, s sum (q + 16) x and
+ * (b - 16 s) sum x), by tensor cores that may cut where fp32 rounds: an fp32
+ * result is within (k/64 + 32) 2^-23 of the sum of the terms' magnitudes, a
+ * few times the error of an fp32 sum over W itself.  A row that holds an
+ * infinity or NaN has no finite result and may have NaN where its sum would be
+ * infinite; so may one whose terms pass fp32's range (from |x| of 2^118 on).
+ * Other rows are not touched by it.
  *
  * Rows: x bf16 [t][k] with row stride x_stride (elements, a multiple of 8;
  * x_codes and x_scales NULL), or 8-bit rows as moe_add_rms_norm writes them
@@ -561,7 +570,9 @@ int moe_qmv(const uint16_t* x, int64_t x_stride, const int8_t* x_codes, const fl
  *   lens   int32 [n_seq]: tokens of each sequence, the new ones included
  * A call takes t new rows, sequence s owning rows starts[s] .. starts[s+1]-1
  * (starts int32 [n_seq+1], device, starts[0] = 0, starts[n_seq] = t): its
- * last starts[s+1] - starts[s] tokens.  A sequence may have none.
+ * last starts[s+1] - starts[s] tokens.  A sequence may have none.  Rows that
+ * no sequence owns (starts[0] > 0, starts[n_seq] < t) are not read, and their
+ * results are not written.
  * d is 64 or 128; block 16, 32, 64 or 128.
  */
 typedef struct {
@@ -627,9 +638,19 @@ int moe_kv_append_held(const uint16_t* k, int64_t k_stride, const uint16_t* v, i
  *   z_j = scale * (q[r][a] . k_j),   head a reading key/value head a / (hq / hkv),
  *
  * keys and values being code * scale.  Codes enter the products exactly;
- * scores, statistics and sums are fp32, the weights are rounded to fp16
- * (2^-12 of each) for the second product.  The order of the sums depends on
- * the sizes and lengths only, never on timing.
+ * scores, statistics and sums are fp32.  For the second product a weight times
+ * its value scale is rounded to fp16: by at most 2^-11 of itself, or 2^-32 of
+ * the row's largest where that is more (a long context's small weights); the
+ * sum that divides is of the weights before that.  The order of the sums
+ * depends on the sizes and lengths only, never on timing.
+ *
+ * Which kernel runs is chosen by the rows of a sequence and key/value head on
+ * average, t * (hq / hkv) / n_seq, the lengths being on the device: up to 32
+ * one that walks a context once per 8 or 16 rows, above that one of 256 rows.
+ * A call is fastest where its sequences have about as many new rows each;
+ * prompts and single tokens, or few busy sequences among many idle ones, cost
+ * less as calls of their own, on caches that name those sequences' tables and
+ * lengths.
  *
  * q bf16 [t][hq][d], heads contiguous, rows `q_stride` elements apart (a
  * multiple of 8); out bf16 [t][hq][d].  hq a multiple of hkv, at most

@@ -74,7 +74,7 @@ __device__ __forceinline__ uint2 codes_of(uint4 u, float up, float m, float rm, 
 // One CTA per (touched block, head, keys or values): the block's values stay
 // in registers (VPT 16-byte vectors a thread) between the maximum and the
 // codes, so every token is read once and every code written once.  Three
-// prompts of 2311 tokens, 8 heads: 24 us for 38 MB; what bounds it is the
+// prompts of 2311 tokens, 8 heads: 23 us for 38 MB; what bounds it is the
 // quantiser's instructions (some 12 a value, issued in 0.61 of the cycles) and
 // the barriers around the maximum, not the bytes.  Block slots are numbered without a scan: sequence s owns
 // the slots from starts[s] / block + 2 s on, which is enough for n new

@@ -96,7 +96,7 @@ __device__ __forceinline__ uint32_t codes_pair(uint32_t a, uint32_t b) {
 // s_j - m + log2 vs_j: beside large scores the logarithm would lose its bits
 // (a value 4% off at scores of 2^20, in powers of two).
 //
-// 48 sequences of up to 20000 tokens, 32 heads on 4, one new token each: 109 us
+// 48 sequences of up to 20000 tokens, 32 heads on 4, one new token each: 108 us
 // for 626 MB, 0.86 of the copy rate; the unpacking (ALU pipe 0.6 full) is next.
 template <int D, int NT>
 __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kernel(AttnParams p) {
@@ -592,7 +592,10 @@ __global__ void __launch_bounds__(AT_THREADS, Shape<NT>::CTAS) kv_attention_kern
 
 // More query rows a sequence and key head than this, on average: the tile
 // kernel.  Sixteen sequences of 8000 tokens, 32 heads on 8: 16 rows 73 us
-// streaming, 131 in tiles; 32 rows 123 and 132; 40 rows 178 and 132.
+// streaming, 131 in tiles; 32 rows 123 and 132; 40 rows 178 and 132.  An average
+// is all the host knows, and it is poor where sequences differ: a prompt of 2048
+// tokens among 31 single tokens behind 8000 takes 300 us, the two parts apart
+// 75 and 94; 512 new tokens behind 7488 in one of 64 slots 430 us, alone 87.
 constexpr int TILE_ROWS = 32;
 
 template <int D, int NT>

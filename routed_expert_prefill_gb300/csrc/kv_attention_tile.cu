@@ -19,10 +19,10 @@ constexpr int T_WARPS = 16, W_KEYS = 8, W_MMA = 11, W_VALUES = 12;
 constexpr int KEY_WARPS = W_MMA - W_KEYS;
 constexpr int T_THREADS = T_WARPS * 32;
 // Units that an item counts for beside its own, when the work is cut: its
-// query rows, first scales and results take as long as about three (in
-// a form a little slower in its units, two prompts behind contexts: 285.3 us with two, 285.6 with three, 289.5 with
-// four, 293 with five; one prompt of 4096 tokens, 32 heads on 8: 183, 175, 178,
-// 180).
+// query rows, first scales and results take as long as about three (two
+// prompts behind contexts, the kernel alone: 292 us with two, 285 with three,
+// 288 with four, 294 with five; one prompt of 4096 tokens, 32 heads on 8: 205,
+// 189, 187, 189).
 constexpr int ITEM_COST = 3;
 constexpr int SC_RING = 4;   // tiles whose scales are kept
 constexpr int RED_RING = 4;  // pieces whose largest value scales are kept
@@ -45,7 +45,8 @@ struct Piece {
 };
 
 // A warp's walk over the CTA's pieces.  It lives in shared memory and one lane
-// advances it, which leaves the unit loops their registers (no spills).
+// advances it, which leaves the unit loops their registers (some 20 bytes are
+// spilt outside of them).
 struct Walk {
   int64_t x;
   int s, qt, h, u;
@@ -194,8 +195,8 @@ __device__ __forceinline__ T* shfl_ptr(T* x, int lane) {
 // the sums rescaled and the pass repeated.
 //
 // Two prompts of 2600 tokens behind contexts of up to 3000, 32 heads on 8:
-// 280 us, 266 GFLOP, 0.48 of the measured bf16 rate; one prompt of 4096 tokens:
-// 187 us.  No unit is full: a unit takes some 4000 clocks, of which the tensor
+// 282 us, 266 GFLOP, 0.48 of the measured bf16 rate; one prompt of 4096 tokens:
+// 189 us.  No unit is full: a unit takes some 4000 clocks, of which the tensor
 // cores work 2050; the rest is the softmax's chain and the conversion of the
 // codes, which run beside each other.
 //

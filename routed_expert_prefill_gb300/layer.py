@@ -69,10 +69,11 @@ def _need_rows(t, name: str, inner: tuple):
 
 
 # Each call first asks in one expression whether its tensors are the ordinary
-# ones (their own types and shapes, contiguous, on one device); only when that
-# is false do the checks that name what is wrong run, and pass the rarer valid
-# forms (16-bit patterns, strided rows).  A decoded token's call is host time:
-# the checks by name cost 10 us of it, the expression 1 us.
+# ones (their own types and shapes, contiguous, on one device, no tensor given
+# for the result); only when that is false do the checks that name what is wrong
+# run, and pass the other valid forms (16-bit patterns, strided rows such as
+# slices of a fused projection's, sum_out, out).  A decoded token's call is host
+# time: the checks by name cost 10 us of it, the expression 1 us.
 
 def _row_stride(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else 0
