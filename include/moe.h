@@ -505,6 +505,9 @@ int moe_debug_stall(void* ws, uint32_t what, void* stream);
  * mixer reads a key/value cache.  One decoder layer over t rows runs
  *   moe_add_rms_norm -> moe_qmv (q, k, v) -> moe_kv_append ->
  *   moe_kv_attention -> moe_qmv -> moe_add_rms_norm -> moe_forward.
+ * moe_kv_plan comes before a step's layers, moe_logprobs behind them;
+ * moe_linear_attention is another mixer, and moe_gated_rms_norm takes the
+ * place of moe_add_rms_norm where a block has a norm or a gate behind it.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -529,6 +532,31 @@ int moe_debug_stall(void* ws, uint32_t what, void* stream);
 int moe_add_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, int64_t residual_stride,
                      const uint16_t* gamma, float eps, int32_t t, int32_t h, uint16_t* sum, uint16_t* y,
                      int8_t* codes, float* scales, void* stream);
+
+/*
+ * The norms behind and before a block, with the block's gate and the
+ * residual's scale between them:
+ *
+ *   b[r][i] = x[r][i] / sqrt(mean_i x[r][i]^2 + eps) * post_gamma[i]   (post_gamma NULL: b = x)
+ *   a[r][i] = residual_scale * residual[r][i] + gate[r][i] * b[r][i]   (residual NULL: the second term alone)
+ *   y[r][i] = a[r][i] / sqrt(mean_i a[r][i]^2 + eps) * gamma[i]
+ *
+ * in fp32, each output rounded once from it.  x is the block's output, bf16
+ * [t][h] with a row stride as moe_add_rms_norm takes it; residual, gamma and
+ * the outputs (sum: a) are those of moe_add_rms_norm.  gate NULL: 1.
+ * Errors: MOE_EINVAL, MOE_ESHAPE, MOE_ECUDA.
+ */
+typedef struct {
+  const uint16_t* values; /* bf16, rows row_stride elements apart (0: one row for all) */
+  int64_t row_stride;     /* per_channel: a multiple of 8 */
+  int32_t per_channel;    /* != 0: h values a row; 0: one value a row */
+  int32_t sigmoid;        /* != 0: 1 / (1 + exp(-value)) is the gate; 0: the value itself */
+} moe_gate;
+
+int moe_gated_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* post_gamma, const moe_gate* gate,
+                       const uint16_t* residual, int64_t residual_stride, float residual_scale, const uint16_t* gamma,
+                       float eps, int32_t t, int32_t h, uint16_t* sum, uint16_t* y, int8_t* codes, float* scales,
+                       void* stream);
 
 /*
  * Product of rows with 4-bit weights:  y[r][o] = sum_i x[r][i] * W[o][i],
@@ -670,6 +698,119 @@ int moe_kv_attention(const uint16_t* q, int64_t q_stride, const int32_t* starts,
 /* Workspace bytes of moe_kv_append and moe_kv_attention on the current
  * device for caches of width d (one buffer serves both); 0 on a bad d. */
 size_t moe_kv_workspace_bytes(int32_t d);
+
+/*
+ * Pages of a cache, given out and taken back on the device (all arrays
+ * device, caller-owned):
+ *   free  int32 [n_pages]: the first `count` are the free pages, taken from the end
+ *   held  int32 [n_seq]: blocks of each sequence that have a page in its row of the table
+ *   count int32 [1]
+ */
+typedef struct {
+  int32_t* free;
+  int32_t* held;
+  int32_t* count;
+} moe_kv_pages;
+
+/*
+ * What a batch's calls on a cache read, from the new tokens of each sequence
+ * (fresh int32 [n_seq]; below 0: the sequence ends):
+ *
+ *   lens[s]    lens_before[s] + fresh[s]; 0 where the sequence ends.  lens_before may be lens itself, or
+ *              lengths to which sequences are cut back
+ *   starts[s]  sum of fresh over the sequences before s (those that end count 0); starts[n_seq] over all
+ *   table      a page for each block up to lens[s] that has none; blocks held beyond it keep theirs
+ *   pages      first the pages of the sequences that end are put behind the free ones, sequence by sequence,
+ *              block by block; then the others take theirs from the end, in the same order
+ *
+ * and, for each of t rows (each array or NULL): seq int32 the sequence it
+ * belongs to, pos int32 its position in it, slot int64 page * block + place in
+ * the page; -1 for the rows behind starts[n_seq].
+ *
+ * A batch is done as a whole or not at all: where fresh, lens_before or what
+ * the pages' arrays say is out of range (more than t rows; positions behind
+ * max_blocks; tokens before the call without pages; page ids that change
+ * hands), or there are too few free pages, MOE_EDEVICE is raised in
+ * moe_read_device_status, all starts are 0, the rows' maps -1, and lens, table
+ * and pages stay as they are.  moe_kv_append and moe_kv_attention then find no
+ * rows.
+ *
+ * n_seq, max_blocks, block, t as in the calls on the cache.  ws:
+ * moe_kv_plan_workspace_bytes(n_seq) bytes, its first 256 set to zero once
+ * before its first use; calls that share it, or the pages, are ordered on one stream.
+ * Errors: MOE_EINVAL, MOE_ESHAPE, MOE_EWORKSPACE, MOE_ECUDA.
+ */
+int moe_kv_plan(const int32_t* fresh, const int32_t* lens_before, int32_t* lens, int32_t* table, const moe_kv_pages* pages,
+                int32_t n_seq, int32_t n_pages, int32_t max_blocks, int32_t block, int32_t t, int32_t* starts, int32_t* seq,
+                int32_t* pos, int64_t* slot, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moe_kv_plan; 0 on a bad n_seq. */
+size_t moe_kv_plan_workspace_bytes(int32_t n_seq);
+
+/*
+ * Linear attention with a decay for each head, over packed sequences:
+ *
+ *   S_r = exp(log_decay[r]) S_(r-1) + k_r v_r^T,   out_r = scale * S_r^T q_r,
+ *
+ * one d x d state S a sequence and value head, value head a reading query and
+ * key head a / (hv / hk).  q, k bf16 [t][hk][d], v bf16 [t][hv][d], heads
+ * contiguous, rows `*_stride` elements apart (multiples of 8); log_decay fp32
+ * [t][hv], rows decay_stride apart (0: one value a head for all rows); a value
+ * above zero counts as zero.  out bf16 [t][hv][d].  Sequence s owns rows
+ * starts[s] .. starts[s+1]-1 (starts int32 [n_seq+1], device); rows that no
+ * sequence owns are not read, and their results are not written.
+ *
+ * states fp32 [n_slots][hv][d][d], S[i][j] for key channel i and value channel
+ * j: a sequence begins from the state in slots[s] (-1: zero) and leaves its
+ * last one in slots_out[s] (-1: nowhere); without rows it is carried over.
+ * slots NULL: sequence s has slot s; slots_out NULL: the same as slots, so that
+ * states are kept in place.  A slot that is written is named once in
+ * slots_out, and no other sequence reads it in the same call.
+ *
+ * Sums and states are fp32, the result is rounded once.  An infinity or NaN in
+ * a row's q, k or v shows in that row's results and, from k or v, in those
+ * behind it and in the state; rows before it are not touched.
+ *
+ * Starts or slots out of range leave their sequence's rows and state
+ * unwritten and raise MOE_EDEVICE in moe_read_device_status.
+ * d is 64 or 128; hv a multiple of hk, at most 1024.
+ * ws: moe_linear_workspace_bytes(d) bytes, set to zero once before its first
+ * use; calls that share it are ordered on one stream.
+ * Errors: MOE_EINVAL, MOE_ESHAPE, MOE_EWORKSPACE, MOE_ECUDA.
+ */
+int moe_linear_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                         int64_t v_stride, const float* log_decay, int64_t decay_stride, const int32_t* starts, int32_t t,
+                         int32_t n_seq, int32_t hk, int32_t hv, int32_t d, float scale, float* states, int32_t n_slots,
+                         const int32_t* slots, const int32_t* slots_out, uint16_t* out, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* Workspace bytes of moe_linear_attention on the current device for heads of width d; 0 on a bad d. */
+size_t moe_linear_workspace_bytes(int32_t d);
+
+/*
+ * Log probabilities of given tokens under rows of logits, with entropy and the
+ * most likely alternatives (the logits that moe_qmv writes):
+ *
+ *   lse[r]        = log sum_i exp(x[r][i])
+ *   logprob[r][m] = x[r][ids[r][m]] - lse[r]
+ *   entropy[r]    = - sum_i p_i log p_i,  p_i = exp(x[r][i] - lse[r])
+ *   top_ids, top_logprobs [t][top]: the largest x[r][i] in order, the lower index first among equals
+ *
+ * logits fp32 (logits_fp32 != 0) or bf16 [t][n], rows `stride` elements apart
+ * (any number); ids int32 or, ids_int64 != 0, int64 [t][n_ids], 0 <= n_ids <=
+ * 256; 0 <= top <= 32, top <= n.  entropy and lse may be NULL; all results fp32,
+ * top_ids int32.  Sums are fp32 and relative to the row's largest value.
+ *
+ * A logit of -inf has probability 0; alternatives may run into them (lowest
+ * index first, log probability -inf).  A row of nothing else has lse -inf and
+ * NaN for the other values.  A row that holds NaN or +inf has NaN everywhere
+ * and -1 as alternatives.  An id outside [0, n) has NaN as its log probability.
+ * 1 <= t <= 65536, 1 <= n <= 1048576.  No workspace.
+ * Errors: MOE_EINVAL, MOE_ESHAPE, MOE_ECUDA.
+ */
+int moe_logprobs(const void* logits, int64_t stride, int32_t logits_fp32, int32_t t, int32_t n, const void* ids,
+                 int32_t ids_int64, int32_t n_ids, int32_t top, float* logprob, float* entropy, float* lse,
+                 int32_t* top_ids, float* top_logprobs, void* stream);
 
 /*
  * Launch accounting (benchmark support; no counterpart in the method).

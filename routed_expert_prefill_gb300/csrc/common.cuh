@@ -24,7 +24,9 @@ enum : uint32_t {
   FLAG_BAD_CACHE = 1u << 4,   // cache lengths, starts or page ids out of range
   FLAG_NOT_FINITE = 1u << 5,  // a key or value that is not finite reached the cache
   FLAG_BAD_TAIL = 1u << 6,    // a cache's tail does not hold the tokens before a call's
+  FLAG_NO_PAGES = 1u << 7,    // a batch needs more pages than are free
   FLAG_TIMEOUT = 1u << 8,     // a bounded device wait gave up
+  FLAG_BAD_STATE = 1u << 9,   // starts or state slots out of range
 };
 
 struct DeviceStatus {

@@ -1,0 +1,376 @@
+// Log probabilities of given tokens, entropy and top alternatives (moe_logprobs).
+#include <cooperative_groups.h>
+#include <float.h>
+#include <math.h>
+
+#include "api_checks.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+
+namespace {
+
+constexpr int LP_THREADS = 256;
+constexpr int LP_VECS = 4;        // 16-byte loads of a thread in flight
+constexpr int LP_TOP = 32;        // alternatives, at most
+constexpr int LP_CAND = 1024;     // candidates that wait to be ranked
+constexpr int LP_RANK_AT = 96;    // so many are ranked before more come
+constexpr int LP_CLUSTER = 8;     // CTAs of a row, at most
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float FAR = -1e30f;     // stands for -inf where it is multiplied by zero
+constexpr float NOT_A_NUMBER = __builtin_nanf("");
+
+struct LogprobParams {
+  const void* logits;
+  int64_t stride;
+  int t, n;
+  const void* ids;
+  int ids64, n_ids, top;
+  float* logprob;
+  float* entropy;
+  float* lse;
+  int32_t* top_ids;
+  float* top_logprobs;
+};
+
+// What is known of a set of logits: m, the largest; s = sum p and u = sum p d,
+// with d = (x - m) log2(e) and p = 2^d.
+struct Stats {
+  float m, s, u;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The same set's s and u with respect to the larger maximum m.
+__device__ __forceinline__ void rebase(Stats& a, float m) {
+  const float d = fmaxf((a.m - m) * LOG2E, FAR), f = ex2(d);
+  a.u = f * fmaf(d, a.s, a.u);
+  a.s *= f;
+  a.m = m;
+}
+
+__device__ __forceinline__ Stats join(Stats a, Stats b) {
+  const float m = fmaxf(a.m, b.m);
+  rebase(a, m);
+  rebase(b, m);
+  return {m, a.s + b.s, a.u + b.u};
+}
+
+// Larger value first, then the lower index: whole numbers in that order.
+__device__ __forceinline__ uint64_t key_of(float x, int i) {
+  const int b = __float_as_int(x + 0.f);  // -0 counts as 0
+  return ((uint64_t)(uint32_t)(b ^ ((b >> 31) | 0x80000000)) << 32) | (uint32_t)~i;
+}
+__device__ __forceinline__ float value_of(uint64_t key) {
+  const uint32_t k = (uint32_t)(key >> 32);
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(uint4 v, float* e) {
+    e[0] = __uint_as_float(v.x), e[1] = __uint_as_float(v.y), e[2] = __uint_as_float(v.z), e[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ float load(const float* p) { return *p; }
+};
+template <>
+struct Vec<uint16_t> {  // bf16
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(uint4 v, float* e) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[2 * i] = bf16lo(w[i]), e[2 * i + 1] = bf16hi(w[i]);
+  }
+  static __device__ __forceinline__ float load(const uint16_t* p) { return bf16f(*p); }
+};
+
+struct Shared {
+  uint64_t cand[LP_CAND];
+  uint64_t best[LP_TOP];
+  Stats part[LP_THREADS / 32];
+  Stats all;
+  float group[32];
+  float thr;  // the top-th largest value so far, once there are as many; -inf before
+  int count;
+  int total;
+};
+
+// The `top` largest of the candidates to their first places and to best, in
+// order.  All threads call it after a barrier; what it leaves is visible to all.
+__device__ void rank_candidates(Shared& sh, int top) {
+  const int c = sh.count;
+  for (int i = threadIdx.x; i < c; i += LP_THREADS) {
+    const uint64_t mine = sh.cand[i];
+    int rank = 0;
+    for (int j = 0; j < c; ++j) rank += sh.cand[j] > mine;
+    if (rank < top) sh.best[rank] = mine;
+  }
+  __syncthreads();
+  const int kept = min(c, top);
+  if (threadIdx.x < kept) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
+  if (threadIdx.x == 0) {
+    sh.count = kept;
+    if (kept == top) sh.thr = value_of(sh.best[top - 1]);
+  }
+  __syncthreads();
+}
+
+// One row by a cluster of CTAs, each of which walks every csize-th tile of it
+// and keeps no more than a tile in registers: memory is read once, which is
+// what bounds the kernel where there are many rows; where there are few, the
+// CTAs of a cluster share one.
+//
+// Sums: a thread rebases its sums where its part of a tile has a new maximum,
+// so that an element costs one exponential.  Alternatives: an element becomes
+// a candidate if it is above the top-th largest value so far, which a thread
+// first asks of its part's maximum.  A CTA's elements come in ascending order,
+// tile by tile, so that an equal value of a later tile takes no earlier one's
+// place.  While there are too few candidates for such a bound, the maxima of
+// 32 groups of threads give one: the top-th largest of them is reached by as
+// many elements.  -inf never becomes a candidate; a row that has too few other
+// values is filled up at the end.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(LogprobParams p, int csize) {
+  __shared__ Shared sh;
+  constexpr int N = Vec<T>::N, E = N * LP_VECS, TILE = LP_THREADS * LP_VECS;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = blockIdx.x / csize, rank = blockIdx.x % csize;
+  const T* x = reinterpret_cast<const T*>(p.logits) + (size_t)row * p.stride;
+  // elements before the first 16-byte boundary, whole vectors, the rest
+  const int head = min(p.n, (int)((16 - (uintptr_t)x % 16) % 16 / sizeof(T)));
+  const int nv = (p.n - head) / N, edge = p.n - nv * N;  // edge: head and rest together, fewer than 2 N
+  const uint4* body = reinterpret_cast<const uint4*>(x + head);
+  float given = NOT_A_NUMBER;
+  if (rank == 0 && tid < p.n_ids) {
+    const size_t at = (size_t)row * p.n_ids + tid;
+    const int64_t id = p.ids64 ? reinterpret_cast<const int64_t*>(p.ids)[at] : reinterpret_cast<const int32_t*>(p.ids)[at];
+    if (id >= 0 && id < p.n) given = Vec<T>::load(x + id);
+  }
+  Stats a{-FLT_MAX, 0.f, 0.f};
+  if (TOP) {
+    if (tid == 0) sh.count = 0, sh.thr = -INFINITY;
+    __syncthreads();
+  }
+
+  // Takes a thread's part of a tile, elements e[i] at index(i).  `ties`: an
+  // element may come after others of a higher index.
+  const auto take = [&](const float* e, auto index, bool ties) {
+    float lm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < E; ++i) lm = fmaxf(lm, e[i]);
+    if (lm > a.m) rebase(a, lm);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float d = (e[i] - a.m) * LOG2E, q = ex2(d);
+      a.s += q;
+      a.u = fmaf(q, fmaxf(d, FAR), a.u);
+    }
+    if (!TOP) return;
+    float thr = sh.thr;
+    const bool loose = thr == -INFINITY;  // the same for the whole CTA
+    if (loose) {
+      constexpr int G = LP_THREADS / 32;  // threads of a group
+      float g = lm;
+#pragma unroll
+      for (int o = G / 2; o; o >>= 1) g = fmaxf(g, __shfl_xor_sync(~0u, g, o));
+      if (tid % G == 0) sh.group[tid / G] = g;
+      __syncthreads();
+      g = sh.group[lane];
+      int above = 0;
+      for (int j = 0; j < 32; ++j) {
+        const float o = __shfl_sync(~0u, g, j);
+        above += o > g || (o == g && j < lane);
+      }
+      const uint32_t who = __ballot_sync(~0u, above == p.top - 1);
+      thr = __shfl_sync(~0u, g, __ffs(who) - 1);
+      ties = true;
+    }
+    bool full = loose;
+    uint32_t in = 0;  // elements among the first LP_RANK_AT candidates
+    if (lm > thr || (ties && lm == thr)) {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (e[i] > -INFINITY && (e[i] > thr || (ties && e[i] == thr))) {
+          const int at = atomicAdd(&sh.count, 1);
+          if (at < LP_CAND) sh.cand[at] = key_of(e[i], index(i));
+          if (at < LP_RANK_AT)
+            in |= 1u << i;
+          else
+            full = true;
+        }
+    }
+    if (!__syncthreads_or(full)) return;
+    if (sh.count > LP_CAND) {
+      // More than the list holds, all but LP_RANK_AT of them of this tile.
+      // The top-th largest key of the tile is found bit by bit; those from it
+      // on that are not among the first LP_RANK_AT take the others' places.
+      uint64_t low = 0;
+      for (int bit = 63; bit >= 0; --bit) {
+        __syncthreads();
+        if (tid == 0) sh.total = 0;
+        __syncthreads();
+        const uint64_t key = low | (uint64_t)1 << bit;
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) c += e[i] > -INFINITY && key_of(e[i], index(i)) >= key;
+        c = __reduce_add_sync(~0u, c);
+        if (lane == 0 && c) atomicAdd(&sh.total, c);
+        __syncthreads();
+        if (sh.total >= p.top) low = key;
+      }
+      if (tid == 0) sh.count = LP_RANK_AT;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const uint64_t key = key_of(e[i], index(i));
+        if (e[i] > -INFINITY && key >= low && !(in >> i & 1)) sh.cand[atomicAdd(&sh.count, 1)] = key;
+      }
+      __syncthreads();
+    }
+    rank_candidates(sh, p.top);
+  };
+
+  for (int v0 = rank * TILE; v0 < nv; v0 += csize * TILE) {
+    float e[E];
+#pragma unroll
+    for (int j = 0; j < LP_VECS; ++j) {
+      const int v = v0 + j * LP_THREADS + tid;
+      if (v < nv) {
+        Vec<T>::unpack(__ldcs(body + v), e + j * N);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[j * N + i] = -INFINITY;
+      }
+    }
+    take(e, [&](int i) { return head + (v0 + i / N * LP_THREADS + tid) * N + i % N; }, false);
+  }
+  if (rank == 0 && edge) {
+    const int at = tid < head ? tid : p.n - edge + tid;
+    float e[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) e[i] = -INFINITY;
+    if (tid < edge) e[0] = Vec<T>::load(x + at);
+    take(e, [&](int) { return at; }, true);
+  }
+
+  // the CTA's sums, then the cluster's
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    a = join(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o), __shfl_xor_sync(~0u, a.u, o)});
+  if (lane == 0) sh.part[warp] = a;
+  __syncthreads();
+  if (TOP) rank_candidates(sh, p.top);
+  a = sh.part[0];
+#pragma unroll
+  for (int i = 1; i < LP_THREADS / 32; ++i) a = join(a, sh.part[i]);
+  if (csize > 1) {
+    cg::cluster_group cluster = cg::this_cluster();
+    if (tid == 0) sh.all = a;
+    cluster.sync();
+    uint64_t far = 0;
+    if (rank == 0) {
+      for (int i = 1; i < csize; ++i) a = join(a, *cluster.map_shared_rank(&sh.all, i));
+      if (TOP && tid < csize * p.top) {
+        const int who = tid / p.top, nth = tid % p.top;
+        if (nth < *cluster.map_shared_rank(&sh.count, who)) far = cluster.map_shared_rank(sh.best, who)[nth];
+      }
+    }
+    cluster.sync();
+    if (rank != 0) return;
+    if (TOP) {
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+      if (far) sh.cand[atomicAdd(&sh.count, 1)] = far;
+      __syncthreads();
+      rank_candidates(sh, p.top);
+    }
+  }
+  const float ln_s = logf(a.s);
+  const bool whole = a.s == a.s;  // false where the row holds +inf or NaN
+  if (tid < p.n_ids) p.logprob[(size_t)row * p.n_ids + tid] = (given - a.m) - ln_s;
+  if (tid == 0) {
+    const float h = ln_s - LN2 * (a.u / a.s);
+    if (p.lse) p.lse[row] = a.m + ln_s;
+    if (p.entropy) p.entropy[row] = h < 0.f ? 0.f : h;
+  }
+  if (!TOP) return;
+  const int kept = sh.count;
+  const size_t to = (size_t)row * p.top;
+  if (!whole) {
+    if (tid < p.top) p.top_ids[to + tid] = -1, p.top_logprobs[to + tid] = NOT_A_NUMBER;
+  } else if (tid < kept) {
+    p.top_ids[to + tid] = ~(uint32_t)sh.best[tid];
+    p.top_logprobs[to + tid] = (value_of(sh.best[tid]) - a.m) - ln_s;
+  } else if (tid == kept) {  // -inf, the lowest indices first
+    for (int i = kept, id = 0; i < p.top; ++id) {
+      bool taken = false;
+      for (int j = 0; j < kept; ++j) taken |= (uint32_t)id == ~(uint32_t)sh.best[j];
+      if (taken) continue;
+      p.top_ids[to + i] = id;
+      p.top_logprobs[to + i++] = -INFINITY - ln_s;
+    }
+  }
+}
+
+template <typename T, bool TOP>
+cudaError_t launch_logprobs(const LogprobParams& p, int csize, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.t * csize);
+  cfg.blockDim = dim3(LP_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = csize;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = csize > 1 ? 2 : 1;
+  cudaError_t e = cudaSuccess;
+  MOE_LAUNCH("logprobs", s, { e = cudaLaunchKernelEx(&cfg, logprobs_kernel<T, TOP>, p, csize); });
+  return e;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_logprobs(const void* logits, int64_t stride, int32_t logits_fp32, int32_t t, int32_t n, const void* ids,
+                            int32_t ids_int64, int32_t n_ids, int32_t top, float* logprob, float* entropy, float* lse,
+                            int32_t* top_ids, float* top_logprobs, void* stream) {
+  if (t < 1 || t > 65536) return set_error(MOE_ESHAPE, "t=%d outside [1, 65536]", t);
+  if (n < 1 || n > 1048576) return set_error(MOE_ESHAPE, "n=%d outside [1, 1048576]", n);
+  if (stride < 0) return set_error(MOE_ESHAPE, "the row stride must not be negative");
+  if (n_ids < 0 || n_ids > LP_THREADS) return set_error(MOE_ESHAPE, "n_ids=%d outside [0, %d]", n_ids, LP_THREADS);
+  if (top < 0 || top > LP_TOP || top > n)
+    return set_error(MOE_ESHAPE, "top=%d outside [0, %d]", top, n < LP_TOP ? n : LP_TOP);
+  TRY(check_ptr(logits, "logits", logits_fp32 ? 4 : 2));
+  TRY(check_ptr(ids, "ids", ids_int64 ? 8 : 4, n_ids == 0));
+  TRY(check_ptr(logprob, "logprob", 4, n_ids == 0));
+  TRY(check_ptr(entropy, "entropy", 4, true));
+  TRY(check_ptr(lse, "lse", 4, true));
+  TRY(check_ptr(top_ids, "top_ids", 4, top == 0));
+  TRY(check_ptr(top_logprobs, "top_logprobs", 4, top == 0));
+  const LogprobParams p{logits, stride, t, n, ids, ids_int64, n_ids, top, logprob, entropy, lse, top_ids, top_logprobs};
+  // CTAs of a row: as many as leave every SM two, while each has a tile
+  const int tile = LP_THREADS * LP_VECS * (logits_fp32 ? 4 : 8);
+  int csize = 1;
+  while (csize < LP_CLUSTER && (int64_t)t * csize * 2 <= 2 * sm_count() && (int64_t)n >= 2 * csize * tile) csize *= 2;
+  cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = logits_fp32 ? (top ? launch_logprobs<float, true>(p, csize, s) : launch_logprobs<float, false>(p, csize, s))
+                                    : (top ? launch_logprobs<uint16_t, true>(p, csize, s)
+                                           : launch_logprobs<uint16_t, false>(p, csize, s));
+  return cuda_status(e, "moe_logprobs launch");
+}

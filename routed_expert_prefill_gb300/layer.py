@@ -5,6 +5,8 @@ One decoder layer over t rows of a residual stream runs
     moe_add_rms_norm -> moe_qmv (q, k, v) -> moe_kv_append -> moe_kv_attention
     -> moe_qmv -> moe_add_rms_norm -> moe.moe_forward
 
+with moe_kv_plan before a step's layers and moe_logprobs behind them.
+
 Argument checks and marshalling only, as in :mod:`.moe`: every step runs in the
 library's CUDA kernels, and there is no fallback.
 
@@ -12,6 +14,14 @@ library's CUDA kernels, and there is no fallback.
 * ``moe_qmv(x, (codes, scales, biases))`` -> ``y``
 * ``KvCache`` (the paged 8-bit cache), ``moe_kv_append(k, v, starts, cache)``,
   ``moe_kv_attention(q, starts, cache)`` -> ``out``
+* ``moe_gated_rms_norm(x, gamma, residual, post_gamma, gate)`` -> ``NormOut``:
+  the norms behind and before a block, with its gate and residual scale
+* ``KvPages`` (a cache's free pages), ``moe_kv_plan(fresh, cache, pages, t)`` ->
+  ``KvPlan(starts, seq, pos, slot)``
+* ``LinearState`` (a pool of states), ``moe_linear_attention(q, k, v, log_decay,
+  starts, state)`` -> ``out``
+* ``moe_logprobs(logits, ids, top)`` -> ``Logprobs(logprob, entropy, lse,
+  top_ids, top_logprobs)``
 
 Every call takes ``stream`` (default: the current stream); what it allocates is
 allocated for that stream.
@@ -25,10 +35,12 @@ from typing import NamedTuple
 
 import torch
 
-from .moe import (_BF16, _F16, MoeError, MoeKvCache, MoeQWeights, _check, _need, _on_current_device,
-                  load_library, read_device_status)
+from .moe import (_BF16, _F16, MoeError, MoeGate, MoeKvCache, MoeKvPages, MoeQWeights, _check, _need,
+                  _on_current_device, load_library, read_device_status)
 
-__all__ = ["NormOut", "moe_add_rms_norm", "moe_qmv", "KvCache", "moe_kv_append", "moe_kv_attention"]
+__all__ = ["NormOut", "moe_add_rms_norm", "moe_gated_rms_norm", "moe_qmv", "KvCache", "moe_kv_append",
+           "moe_kv_attention", "KvPages", "KvPlan", "moe_kv_plan", "LinearState", "moe_linear_attention", "Logprobs",
+           "moe_logprobs"]
 
 GROUP = 64  # weights per scale, and channels per scale of an 8-bit row
 
@@ -135,6 +147,87 @@ def moe_add_rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tenso
         0 if residual is None or t == 1 else residual.stride(0), gamma.data_ptr(), eps, t, h,
         None if sum_out is None else sum_out.data_ptr(), None if y is None else y.data_ptr(),
         None if codes is None else codes.data_ptr(), None if scales is None else scales.data_ptr(), _raw(stream, dev))
+    if status:
+        _check(status)
+    return NormOut(sum_out, y, codes, scales)
+
+
+def _gate_of(gate, sigmoid: bool, t: int, h: int):
+    """The gate as the C ABI takes it: values for each channel ([h] or [t, h]), or one a row ([t, 1])."""
+    if not isinstance(gate, torch.Tensor):
+        raise TypeError(f"gate must be a torch.Tensor, got {type(gate).__name__}")
+    if gate.dtype not in _BF16:
+        raise TypeError(f"gate must have dtype {' or '.join(str(d) for d in _BF16)}, got {gate.dtype}")
+    if gate.shape == (h,):
+        _need(gate, "gate", _BF16)
+        return MoeGate(gate.data_ptr(), 0, 1, sigmoid)
+    if gate.shape == (t, h) and h > 1:
+        _need_rows(gate, "gate", (h,))
+        return MoeGate(gate.data_ptr(), _row_stride(gate), 1, sigmoid)
+    if gate.shape == (t, 1):
+        return MoeGate(gate.data_ptr(), _row_stride(gate), 0, sigmoid)
+    raise ValueError(f"gate must have shape ({h},), ({t}, {h}) or ({t}, 1), got {tuple(gate.shape)}")
+
+
+def moe_gated_rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: torch.Tensor | None = None,
+                       post_gamma: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                       gate_sigmoid: bool = False, residual_scale: float = 1.0, eps: float = 1e-6,
+                       quantize: bool = False, want_y: bool | None = None, sum_out: torch.Tensor | None = None,
+                       stream=None) -> NormOut:
+    """b = norm(x) * post_gamma; a = residual_scale * residual + gate * b; y = norm(a) * gamma, per row.
+
+    x bf16 [t, h] is a block's output (rows may be strided); without
+    ``post_gamma`` (bf16 [h]) b = x.  gate bf16: [h] (one value a channel),
+    [t, 1] (one a row) or [t, h]; with ``gate_sigmoid`` 1 / (1 + exp(-gate))
+    takes its place.  residual, gamma, ``sum`` (a), ``y``, ``codes`` and
+    ``scales`` as in moe_add_rms_norm; ``sum`` is given unless there is neither a
+    residual nor a ``sum_out``.
+    """
+    lib = load_library()
+    if x.dim() != 2:
+        raise ValueError("x must be [t, h]")
+    t, h = shape = x.shape
+    dev = x.get_device()
+    if not (dev >= 0 and dev == torch.cuda.current_device() == gamma.get_device()
+            and x.dtype is _BF and x.is_contiguous() and gamma.dtype is _BF and gamma.shape == (h,) and gamma.is_contiguous()
+            and (residual is None or (residual.dtype is _BF and residual.shape == shape and residual.is_contiguous()
+                                      and residual.get_device() == dev))
+            and (post_gamma is None or (post_gamma.dtype is _BF and post_gamma.shape == (h,) and post_gamma.is_contiguous()
+                                        and post_gamma.get_device() == dev))
+            and (gate is None or gate.get_device() == dev)
+            and sum_out is None and not (quantize and h % GROUP)):
+        _need_rows(x, "x", (h,))
+        _need(gamma, "gamma", _BF16, shape=(h,))
+        if post_gamma is not None:
+            _need(post_gamma, "post_gamma", _BF16, shape=(h,))
+        if residual is not None:
+            _need_rows(residual, "residual", (h,))
+            if residual.shape[0] != t:
+                raise ValueError(f"residual must have {t} rows, got {residual.shape[0]}")
+        if sum_out is not None:
+            _need(sum_out, "sum_out", _BF16, shape=(t, h))
+        if gate is not None:
+            _gate_of(gate, gate_sigmoid, t, h)
+        if quantize and h % GROUP:
+            raise ValueError(f"h={h} must be a multiple of {GROUP} for 8-bit rows")
+        _on_current_device(x=x, gamma=gamma, residual=residual, post_gamma=post_gamma, gate=gate, sum_out=sum_out)
+    g = None if gate is None else ctypes.byref(_gate_of(gate, gate_sigmoid, t, h))
+    if want_y is None:
+        want_y = not quantize
+    y = codes = scales = None
+    if sum_out is None and residual is not None:
+        sum_out = _empty(shape, _BF, x, stream)
+    if want_y:
+        y = _empty(shape, _BF, x, stream)
+    if quantize:
+        codes = _empty(shape, torch.int8, x, stream)
+        scales = _empty((t, h // GROUP), torch.float32, x, stream)
+    status = lib.moe_gated_rms_norm(
+        x.data_ptr(), x.stride(0) if t > 1 else 0, None if post_gamma is None else post_gamma.data_ptr(), g,
+        None if residual is None else residual.data_ptr(), 0 if residual is None or t == 1 else residual.stride(0),
+        residual_scale, gamma.data_ptr(), eps, t, h, None if sum_out is None else sum_out.data_ptr(),
+        None if y is None else y.data_ptr(), None if codes is None else codes.data_ptr(),
+        None if scales is None else scales.data_ptr(), _raw(stream, dev))
     if status:
         _check(status)
     return NormOut(sum_out, y, codes, scales)
@@ -326,3 +419,258 @@ def moe_kv_attention(q: torch.Tensor, starts: torch.Tensor, cache: KvCache, scal
     if status:
         _check(status)
     return out
+
+
+class KvPages:
+    """The pages of a KvCache that are free (moe_kv_pages), with the plan's workspace.
+
+    free int32 [n_pages], whose first ``count`` entries are the free pages,
+    taken from the end; account int32 [n_seq + 1]: the blocks that each
+    sequence holds pages for in the cache's table, then ``count``.  Both are
+    kept, not copied, read and written on the device; a copy of both brings the
+    pages back to where they stood.  Without them every page is free, the
+    lowest one taken first.
+    """
+
+    def __init__(self, cache: KvCache, free: torch.Tensor | None = None, account: torch.Tensor | None = None):
+        if not isinstance(cache, KvCache):
+            raise TypeError(f"cache must be a KvCache, got {type(cache).__name__}")
+        n_seq, n_pages = cache.n_seq, cache.codes.shape[1]
+        if (free is None) != (account is None):
+            raise ValueError("free and account come together")
+        if free is None:
+            free = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=cache.codes.device)
+            account = torch.zeros(n_seq + 1, dtype=torch.int32, device=cache.codes.device)
+            account[n_seq] = n_pages
+        _need(free, "free", (torch.int32,), shape=(n_pages,))
+        _need(account, "account", (torch.int32,), shape=(n_seq + 1,))
+        _on_current_device(free=free, account=account, codes=cache.codes)
+        self._cache, self._free, self._account = cache, free, account
+        n = load_library().moe_kv_plan_workspace_bytes(n_seq)
+        if n == 0:
+            raise MoeError(-2, f"n_seq={n_seq} outside [1, 65536]")
+        self._workspace = torch.zeros(n, dtype=torch.uint8, device=free.device)
+        self._ws = self._workspace.data_ptr(), n
+        self._c = MoeKvPages(free.data_ptr(), account.data_ptr(), account.data_ptr() + 4 * n_seq)
+        self._ref = ctypes.byref(self._c)
+        c = cache._c
+        self._table, self._sizes = cache.table.data_ptr(), (c.n_seq, c.n_pages, c.max_blocks, c.block)
+
+    # read by address, as the cache's tensors
+    cache = property(lambda self: self._cache)
+    free = property(lambda self: self._free)
+    account = property(lambda self: self._account)
+    held = property(lambda self: self._account[:-1])
+    count = property(lambda self: self._account[-1:])
+    ws = property(lambda self: self._workspace)
+
+    def read_device_status(self, stream=None) -> int:
+        """Synchronise and return the device-side status (0 = clean); clears it."""
+        return read_device_status(self.ws, stream)
+
+
+class KvPlan(NamedTuple):
+    """Outputs of moe_kv_plan: starts int32 [n_seq + 1]; of each row its sequence and position (int32 [t]) and its
+    slot page * block + place (int64 [t]), -1 behind the last sequence."""
+
+    starts: torch.Tensor
+    seq: torch.Tensor
+    pos: torch.Tensor
+    slot: torch.Tensor
+
+
+def moe_kv_plan(fresh: torch.Tensor, cache: KvCache, pages: KvPages, t: int, lens: torch.Tensor | None = None,
+                stream=None) -> KvPlan:
+    """Starts, lengths, page table and row maps of a batch of t rows.
+
+    fresh int32 [n_seq]: the new tokens of each sequence (0: idle; below 0: it
+    ends and its pages become free).  ``cache.lens`` becomes the lengths with
+    the new tokens, from those before the call: its own, or ``lens`` (int32
+    [n_seq]), to which sequences are cut back.  ``cache.table`` gets pages for
+    the blocks that have none.  A batch that does not fit changes nothing, and
+    is reported by ``pages.read_device_status()``.
+    """
+    lib = load_library()
+    if not isinstance(pages, KvPages):
+        raise TypeError(f"pages must be a KvPages, got {type(pages).__name__}")
+    if pages._cache is not cache:
+        raise ValueError("pages belong to another cache")
+    before = cache._lens if lens is None else lens
+    dev = fresh.get_device()
+    shape = (cache.n_seq,)
+    if not (dev >= 0 and dev == torch.cuda.current_device() == cache._dev == before.get_device()
+            and fresh.dtype is torch.int32 and fresh.shape == shape and fresh.is_contiguous()
+            and before.dtype is torch.int32 and before.shape == shape and before.is_contiguous()):
+        _need(fresh, "fresh", (torch.int32,), shape=shape)
+        _need(before, "lens", (torch.int32,), shape=shape)
+        _on_current_device(fresh=fresh, lens=before, codes=cache.codes)
+    if not 1 <= t <= 65536:  # before memory is asked for
+        raise MoeError(-2, f"t={t} outside [1, 65536]")
+    # one allocation: the maps of 8 bytes a row, then those of 4, then the starts
+    whole = _empty((4 * t + cache.n_seq + 1,), torch.int32, fresh, stream)
+    slot = whole[:2 * t].view(torch.int64)
+    seq, pos, starts = whole[2 * t:3 * t], whole[3 * t:4 * t], whole[4 * t:]
+    at = whole.data_ptr()
+    n_seq, n_pages, max_blocks, block = pages._sizes
+    status = lib.moe_kv_plan(fresh.data_ptr(), before.data_ptr(), cache._c.lens, pages._table, pages._ref, n_seq, n_pages,
+                             max_blocks, block, t, at + 16 * t, at + 8 * t, at + 12 * t, at, *pages._ws, _raw(stream, dev))
+    if status:
+        _check(status)
+    return KvPlan(starts, seq, pos, slot)
+
+
+class LinearState:
+    """A pool of states of linear attention, fp32 [n_slots, heads, d, d] (key channel, value channel), with its
+    workspace.  The tensor is kept, not copied: calls that use one pool are ordered on one stream."""
+
+    def __init__(self, states: torch.Tensor):
+        if states.dim() != 4 or states.shape[2] != states.shape[3]:
+            raise ValueError("states must be [n_slots, heads, d, d]")
+        _need(states, "states", (torch.float32,))
+        _on_current_device(states=states)
+        self.n_slots, self.heads, self.d, _ = states.shape
+        n = load_library().moe_linear_workspace_bytes(self.d)
+        if n == 0:
+            raise MoeError(-2, f"d={self.d} must be 64 or 128")
+        self._states, self._dev = states, states.get_device()
+        self._workspace = torch.zeros(n, dtype=torch.uint8, device=states.device)
+        self._ws = self._workspace.data_ptr(), n
+        self._scale = 1 / math.sqrt(self.d)
+
+    # read by address, as a cache's tensors
+    states = property(lambda self: self._states)
+    ws = property(lambda self: self._workspace)
+
+    @classmethod
+    def new(cls, n_slots: int, heads: int, d: int, device="cuda"):
+        """A pool of zero states."""
+        return cls(torch.zeros(n_slots, heads, d, d, device=device))
+
+    def read_device_status(self, stream=None) -> int:
+        """Synchronise and return the device-side status (0 = clean); clears it."""
+        return read_device_status(self.ws, stream)
+
+
+def moe_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, starts: torch.Tensor,
+                         state: LinearState, slots: torch.Tensor | None = None, slots_out: torch.Tensor | None = None,
+                         scale: float | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """S_r = exp(log_decay_r) S_(r-1) + k_r v_r^T, out_r = scale * S_r^T q_r over packed sequences.
+
+    q, k bf16 [t, hk, d], v bf16 [t, hv, d] (rows may be strided), log_decay
+    fp32 [hv] or [t, hv] (rows may be strided), starts int32 [n_seq + 1].
+    Sequence s begins from the state in slot ``slots[s]`` (int32 [n_seq]; -1:
+    zero; default: slot s) and leaves its last one in ``slots_out[s]`` (-1:
+    nowhere; default: the same slots).  ``scale`` defaults to 1 / sqrt(d).
+    Returns bf16 [t, hv, d].
+    """
+    lib = load_library()
+    if not isinstance(state, LinearState):
+        raise TypeError(f"state must be a LinearState, got {type(state).__name__}")
+    if q.dim() != 3 or v.dim() != 3 or starts.dim() != 1 or log_decay.dim() not in (1, 2):
+        raise ValueError("q, k and v must be [t, heads, d], log_decay [heads] or [t, heads], starts [n_seq + 1]")
+    t, hk, d = q.shape
+    hv, n_seq = v.shape[1], starts.shape[0] - 1
+    shape = (t, hv, d)
+    dev = q.get_device()
+    decays = log_decay.shape
+    if not (dev >= 0 and dev == torch.cuda.current_device() == state._dev and d == state.d and hv == state.heads
+            and k.get_device() == dev == v.get_device() and starts.get_device() == dev == log_decay.get_device()
+            and q.dtype is _BF and q.is_contiguous() and k.dtype is _BF and k.shape == q.shape and k.is_contiguous()
+            and v.dtype is _BF and v.shape == shape and v.is_contiguous()
+            and log_decay.dtype is torch.float32 and log_decay.is_contiguous() and (decays == (hv,) or decays == (t, hv))
+            and starts.dtype is torch.int32 and starts.is_contiguous() and n_seq > 0 and out is None
+            and (slots is None or (slots.dtype is torch.int32 and slots.shape == (n_seq,) and slots.is_contiguous()
+                                   and slots.get_device() == dev))
+            and (slots_out is None or (slots_out.dtype is torch.int32 and slots_out.shape == (n_seq,)
+                                       and slots_out.is_contiguous() and slots_out.get_device() == dev))):
+        if n_seq < 1:
+            raise ValueError("starts must hold at least one sequence")
+        _need_rows(q, "q", (hk, state.d))
+        _need_rows(k, "k", (hk, d))
+        _need_rows(v, "v", (state.heads, d))
+        for name, r in (("k", k), ("v", v)):
+            if r.shape[0] != t:
+                raise ValueError(f"{name} must have {t} rows, got {r.shape[0]}")
+        if log_decay.dtype is not torch.float32:
+            raise TypeError(f"log_decay must have dtype torch.float32, got {log_decay.dtype}")
+        if decays != (hv,) and decays != (t, hv):
+            raise ValueError(f"log_decay must have shape ({hv},) or ({t}, {hv}), got {tuple(decays)}")
+        if log_decay.stride(-1) != 1 and hv > 1:
+            raise ValueError(f"log_decay: the values of a row must be contiguous, got strides {log_decay.stride()}")
+        _need(starts, "starts", (torch.int32,))
+        for name, r in (("slots", slots), ("slots_out", slots_out)):
+            if r is not None:
+                _need(r, name, (torch.int32,), shape=(n_seq,))
+        if out is not None:
+            _need(out, "out", _BF16, shape=shape)
+        _on_current_device(q=q, k=k, v=v, log_decay=log_decay, starts=starts, slots=slots, slots_out=slots_out, out=out,
+                           states=state.states)
+    if out is None:
+        out = _empty(shape, _BF, q, stream)
+    status = lib.moe_linear_attention(
+        q.data_ptr(), _row_stride(q), k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), log_decay.data_ptr(),
+        _row_stride(log_decay) if len(decays) == 2 else 0, starts.data_ptr(), t, n_seq, hk, hv, d,
+        state._scale if scale is None else scale, state._states.data_ptr(), state.n_slots,
+        None if slots is None else slots.data_ptr(), None if slots_out is None else slots_out.data_ptr(), out.data_ptr(),
+        *state._ws, _raw(stream, dev))
+    if status:
+        _check(status)
+    return out
+
+
+class Logprobs(NamedTuple):
+    """Outputs of moe_logprobs, fp32 but for the ids (int32); what was not asked for is None."""
+
+    logprob: torch.Tensor | None
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_ids: torch.Tensor | None
+    top_logprobs: torch.Tensor | None
+
+
+def moe_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top: int = 0, stream=None) -> Logprobs:
+    """Log probabilities of given tokens under rows of logits, their entropy and top alternatives.
+
+    logits fp32 or bf16 [t, n] (rows may be strided); ids int32 or int64 [t] or
+    [t, m], m <= 256: ``logprob`` fp32 of ids' shape.  ``entropy`` and ``lse``
+    (log of the sum of exponentials) fp32 [t]; ``top_ids`` int32 and
+    ``top_logprobs`` fp32 [t, top], top <= 32, the largest logits in order, the
+    lower index first among equals.
+    """
+    lib = load_library()
+    if logits.dim() != 2:
+        raise ValueError("logits must be [t, n]")
+    t, n = logits.shape
+    dev = logits.get_device()
+    f32 = logits.dtype is torch.float32
+    if not (dev >= 0 and dev == torch.cuda.current_device() and (f32 or logits.dtype is _BF) and logits.is_contiguous()
+            and (ids is None or (ids.get_device() == dev and ids.shape == (t,) and ids.is_contiguous()
+                                 and (ids.dtype is torch.int64 or ids.dtype is torch.int32)))):
+        if logits.dtype not in (torch.float32,) + _BF16:
+            raise TypeError(f"logits must have dtype torch.float32 or torch.bfloat16, got {logits.dtype}")
+        if logits.stride(1) != 1 and n > 1:
+            raise ValueError(f"logits: the values of a row must be contiguous, got strides {logits.stride()}")
+        if ids is not None:
+            if ids.dim() not in (1, 2) or ids.shape[0] != t:
+                raise ValueError(f"ids must have shape ({t},) or ({t}, m), got {tuple(ids.shape)}")
+            _need(ids, "ids", (torch.int64, torch.int32))
+        _on_current_device(logits=logits, ids=ids)
+    if not 0 <= top <= 32:
+        raise MoeError(-2, f"top={top} outside [0, 32]")
+    logprob = top_ids = top_logprobs = None
+    m = 0
+    if ids is not None:
+        m = 1 if ids.dim() == 1 else ids.shape[1]
+        logprob = _empty(ids.shape, torch.float32, logits, stream)
+    entropy, lse = _empty((2, t), torch.float32, logits, stream).unbind(0)
+    if top:
+        top_ids = _empty((t, top), torch.int32, logits, stream)
+        top_logprobs = _empty((t, top), torch.float32, logits, stream)
+    status = lib.moe_logprobs(
+        logits.data_ptr(), _row_stride(logits), f32, t, n, None if not m else ids.data_ptr(),
+        ids is not None and ids.dtype is torch.int64, m, top, None if not m else logprob.data_ptr(), entropy.data_ptr(),
+        lse.data_ptr(), None if not top else top_ids.data_ptr(), None if not top else top_logprobs.data_ptr(),
+        _raw(stream, dev))
+    if status:
+        _check(status)
+    return Logprobs(logprob, entropy, lse, top_ids, top_logprobs)

@@ -63,6 +63,12 @@ EXPORTS = (
     "moe_kv_append_held",
     "moe_kv_attention",
     "moe_kv_workspace_bytes",
+    "moe_gated_rms_norm",
+    "moe_kv_plan",
+    "moe_kv_plan_workspace_bytes",
+    "moe_linear_attention",
+    "moe_linear_workspace_bytes",
+    "moe_logprobs",
 )
 
 
@@ -112,6 +118,15 @@ class MoeKvCache(ctypes.Structure):
                 ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("n_seq", ctypes.c_int32),
                 ("n_pages", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("block", ctypes.c_int32),
                 ("hkv", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+class MoeGate(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("per_channel", ctypes.c_int32),
+                ("sigmoid", ctypes.c_int32)]
+
+
+class MoeKvPages(ctypes.Structure):
+    _fields_ = [("free", ctypes.c_void_p), ("held", ctypes.c_void_p), ("count", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -198,6 +213,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_kv_attention.argtypes = [vp, i64, vp, i32, i32, f32, ctypes.POINTER(MoeKvCache), vp, vp, sz, vp]
     lib.moe_kv_workspace_bytes.restype = sz
     lib.moe_kv_workspace_bytes.argtypes = [i32]
+    lib.moe_gated_rms_norm.restype = ctypes.c_int
+    lib.moe_gated_rms_norm.argtypes = [vp, i64, vp, ctypes.POINTER(MoeGate), vp, i64, f32, vp, f32, i32, i32, vp, vp, vp, vp,
+                                       vp]
+    lib.moe_kv_plan.restype = ctypes.c_int
+    lib.moe_kv_plan.argtypes = [vp, vp, vp, vp, ctypes.POINTER(MoeKvPages), i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz,
+                                vp]
+    lib.moe_kv_plan_workspace_bytes.restype = sz
+    lib.moe_kv_plan_workspace_bytes.argtypes = [i32]
+    lib.moe_linear_attention.restype = ctypes.c_int
+    lib.moe_linear_attention.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, f32, vp, i32, vp,
+                                         vp, vp, vp, sz, vp]
+    lib.moe_linear_workspace_bytes.restype = sz
+    lib.moe_linear_workspace_bytes.argtypes = [i32]
+    lib.moe_logprobs.restype = ctypes.c_int
+    lib.moe_logprobs.argtypes = [vp, i64, i32, i32, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     _lib = lib
     return lib
 
