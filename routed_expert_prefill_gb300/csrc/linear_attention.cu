@@ -97,9 +97,15 @@ cudaError_t launch_linear_recurrent(const LinearParams& p, int d, cudaStream_t s
   return e;
 }
 
+size_t linear_chunk_ws_bytes(int d);  // linear_chunk.cu
+cudaError_t launch_linear_chunk(const LinearParams& p, int d, unsigned char* ws, cudaStream_t s);
+
 namespace {
 
-size_t linear_ws_bytes(int) { return sizeof(DeviceStatus); }
+size_t linear_ws_bytes(int d) { return sizeof(DeviceStatus) + linear_chunk_ws_bytes(d); }
+
+// Rows of a sequence on average, from which on the chunk kernel takes the call.
+constexpr int CHUNK_ROWS = 24;
 
 }  // namespace
 
@@ -142,7 +148,11 @@ int moe_linear_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k,
     return set_error(MOE_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, linear_ws_bytes(d));
   const LinearParams p{q, k, v, q_stride, k_stride, v_stride, log_decay, decay_stride, starts, t, n_seq, hk, hv, scale,
                        states, n_slots, slots, slots_out, out, (DeviceStatus*)ws};
-  return cuda_status(launch_linear_recurrent(p, d, (cudaStream_t)stream), "moe_linear_attention launch");
+  cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = t > (int64_t)CHUNK_ROWS * n_seq
+                            ? launch_linear_chunk(p, d, (unsigned char*)ws + sizeof(DeviceStatus), s)
+                            : launch_linear_recurrent(p, d, s);
+  return cuda_status(e, "moe_linear_attention launch");
 }
 
 }  // extern "C"
