@@ -149,7 +149,9 @@ int moe_linear_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k,
   const LinearParams p{q, k, v, q_stride, k_stride, v_stride, log_decay, decay_stride, starts, t, n_seq, hk, hv, scale,
                        states, n_slots, slots, slots_out, out, (DeviceStatus*)ws};
   cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = t > (int64_t)CHUNK_ROWS * n_seq
+  // rows that lie over one another (one row for all) are no tiles
+  const bool apart = q_stride >= (int64_t)hk * d && k_stride >= (int64_t)hk * d && v_stride >= (int64_t)hv * d;
+  const cudaError_t e = apart && t > (int64_t)CHUNK_ROWS * n_seq
                             ? launch_linear_chunk(p, d, (unsigned char*)ws + sizeof(DeviceStatus), s)
                             : launch_linear_recurrent(p, d, s);
   return cuda_status(e, "moe_linear_attention launch");

@@ -2,7 +2,10 @@
 // tensor cores' own path: chunks of 128 rows, accumulators in TMEM.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "linear_common.cuh"
+#include "tc_common.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -12,26 +15,22 @@ namespace {
 using namespace tc;
 
 constexpr int CHUNK = 128;
-constexpr int LC_THREADS = 256;
+// Warps: 0-7 compute, 8 brings the tiles and issues the products, 9 works out
+// the decays, 10 and 11 fill the warpgroup.  Registers: 384 * 168 at launch,
+// 256 * 224 + 128 * 56 after the split.
+constexpr int LC_COMPUTE = 256, LC_THREADS = 384, W_ISSUE = 8, W_GAIN = 9;
+constexpr int LC_REGS = 224, LC_REGS_REST = 56;
 constexpr uint64_t LC_WAIT_NS = 2000000000ull;
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LN2 = 0.6931471805599453f;
 // A row's log2 decay as it counts: below it the state of one row is 0 in the
-// next whatever it was (2^-512 of an fp32 number), and sums over a chunk stay
-// exact whole numbers and fractions.
-constexpr float LEAST = -512.f;
-constexpr float NOT_A_NUMBER = __builtin_nanf("");
-
-// log2 of a product of decays, n + f with a whole number n: differences of two
-// keep the fraction's 24 bits however large both are.
-struct Gain {
-  float n, f;
-};
+// next whatever it was (2^-512 of an fp32 number).
+constexpr double LEAST = -512.0;
 
 // What one CTA leaves for those that go on with its last chain: the state
 // behind its part (or, if its part does not begin the chain, what the part
 // adds) and the part's decay.
-constexpr int PUB_EXTRA = 64;  // floats behind the state: the decay
-constexpr size_t pub_floats(int d) { return (size_t)d * d + PUB_EXTRA; }
+constexpr int PUB_EXTRA = 64;  // floats behind the state: log2 of the decay, whole part and rest
+__host__ __device__ constexpr size_t pub_floats(int d) { return (size_t)d * d + PUB_EXTRA; }
 
 // Behind the status block of the workspace.
 struct LinearSync {
@@ -46,19 +45,35 @@ struct ChunkParams {
   float* pub;       // [CTAs][pub_floats]
 };
 
-// Chunks c0 .. c1 - 1 of the nc of one sequence and head.
+// Chunks c0 .. c1 - 1 of the nc of one sequence and head.  full: with its
+// results, else only what it adds to a state of zero.
 struct Part {
   int s, head, c0, c1, nc;
   int row, n, slot_in, slot_out;
+  bool full;
+};
+
+// The decays of a chunk's rows: G_i is the log2 of the product of rows 0 .. i's.
+struct Gains {
+  float rel[CHUNK];    // G_i less that of the first of its 32 rows
+  float last[CHUNK];   // 2^(G_127 - G_i)
+  float first[CHUNK];  // 2^G_i
+  float off[192];      // rows 32 q .. of q = 1, 2, 3, for i < 32 q: 2^(G_32q - G_i)
+  float n, f;          // G_127, whole part and rest
+  float keep;          // what a state is multiplied by: 2^G_127, less 1 if slow
+  int slow;
 };
 
 struct LcShared {
-  uint64_t bar[4];  // scores, state times queries, weights times values, state: done
-  Gain gain[2][CHUNK];
-  int poison[128];  // first row whose value of a channel is not finite; CHUNK: none
-  int scan[8];
-  int total, longest;
+  uint64_t qk_full[2], v_full, g_full, g_empty;
+  uint64_t qk_done, sq_done, pv_done, ds_done;  // products
+  uint64_t s_ready, p_ready, k_ready, o_ready;  // their operands, and the results
+  uint64_t drain;
+  Gains g;
+  Part first, last;
   int at[2][2];  // where the CTA's first and last chunk are: sequence, chunks before it
+  int scan[LC_THREADS / 32];
+  int total, longest;
   uint32_t tmem;
   int abort;
 };
@@ -72,10 +87,11 @@ struct Lc {
   static constexpr int Q0 = 0, K0 = 2 * TILE, V0 = 4 * TILE, X0 = 5 * TILE;
   static constexpr int TILES = 7 * TILE;
   static constexpr int TOTAL = TILES + (int)sizeof(LcShared);
-  static constexpr int NC = D * D / LC_THREADS;        // values of the state a thread holds
+  static constexpr int NC = D * D / LC_COMPUTE;        // values of the state a thread holds
   // TMEM columns: scores (then weights), state times queries, weights times values, what the chunk adds
   static constexpr int T_S = 0, T_SQ = 128, T_PV = 128 + D, T_DS = 128 + 2 * D;
 };
+static_assert(Lc<128>::TOTAL <= 227 * 1024, "shared memory of a CTA");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -95,17 +111,13 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_rows, bool b_r
   return idesc_bf16(M, N) | ((uint32_t)a_rows << 15) | ((uint32_t)b_rows << 16);
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-  const int bytes = on ? 16 : 0;  // 0: sixteen zeros, nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(tm), "r"(x), "r"(y),
+               "r"(smem_u32(src))
+               : "memory");
 }
 
-// Two fp32 values as bf16 pairs whose sum is them up to 2^-17: v becomes what is left.
+// Two fp32 values as a bf16 pair; what is left of them takes their place.
 __device__ __forceinline__ uint32_t take_bf16(float& a, float& b) {
   const uint32_t w = pack_bf16x2(a, b);
   a -= bf16lo(w);
@@ -133,428 +145,167 @@ __device__ __forceinline__ int chunks_of(const LinearParams& p, int s, bool repo
   return n ? (n + CHUNK - 1) / CHUNK : in != out && out >= 0;
 }
 
+__device__ __forceinline__ Part part_of(const LinearParams& p, int s, int head) {
+  Part t;
+  t.s = s;
+  t.head = head;
+  linear_sequence(p, s, t.row, t.n, t.slot_in, t.slot_out);
+  t.c0 = 0;
+  t.c1 = t.nc = chunks_of(p, s, false);
+  t.full = true;
+  return t;
+}
+
+// A walk over the chunks of a CTA's run, part by part: first the part that
+// other CTAs go on with, so that they need not wait long (inside a chain: what
+// it adds); then whole chains; last the part that others began.
+struct Walk {
+  Part t;
+  int c;      // the chunk, if any is left
+  int stage;  // of t; 3: none left
+  int s, head;
+  bool left;  // (s, head) has not been looked at
+
+  __device__ __forceinline__ void begin(const LinearParams& p, const LcShared& sh) {
+    s = sh.first.s;
+    head = sh.first.head;
+    left = true;
+    stage = 0;
+    if (sh.last.c1 < sh.last.nc) {
+      t = sh.last;
+      t.full = t.c0 == 0;
+      c = t.c0;
+    } else {
+      next_part(p, sh);
+    }
+  }
+  __device__ void next_part(const LinearParams& p, const LcShared& sh) {
+    while (stage < 2 && left) {
+      const bool is_last = s == sh.last.s && head == sh.last.head;
+      bool whole;
+      if (s == sh.first.s && head == sh.first.head) {
+        t = sh.first;
+        whole = t.c0 == 0 && t.c1 == t.nc;
+      } else {
+        t = is_last ? sh.last : part_of(p, s, head);
+        whole = t.c1 == t.nc;
+      }
+      if (is_last) {
+        left = false;
+      } else if (++head == p.hv) {
+        head = 0;
+        do ++s;
+        while (chunks_of(p, s, false) == 0);  // the last part's sequence has some
+      }
+      if (whole) {
+        stage = 1;
+        c = t.c0;
+        return;
+      }
+    }
+    if (stage < 2 && sh.first.c0 > 0) {
+      t = sh.first;
+      stage = 2;
+      c = t.c0;
+    } else {
+      stage = 3;
+    }
+  }
+  __device__ __forceinline__ void next(const LinearParams& p, const LcShared& sh) {
+    if (++c == t.c1) next_part(p, sh);
+  }
+  __device__ __forceinline__ bool more() const { return stage < 3; }
+  __device__ __forceinline__ int rows() const { return min(CHUNK, t.n - c * CHUNK); }
+};
+
+// sum_(j <= i) w_ij (q_i . k_j) v_j of one row and channel, for those whose
+// products over the chunk met a value that is not finite.
+__device__ __noinline__ float weighted_values(const LinearParams& p, int d, int row0, int i, int head, int channel) {
+  const int hk = head / (p.hv / p.hk);
+  const uint16_t* q = p.q + (size_t)(row0 + i) * p.q_stride + hk * d;
+  float sum = 0.f, w = 1.f;
+  for (int j = i; j >= 0; --j) {
+    const uint16_t* k = p.k + (size_t)(row0 + j) * p.k_stride + hk * d;
+    float z = 0.f;
+    for (int c = 0; c < d; ++c) z = fmaf(bf16f(q[c]), bf16f(k[c]), z);
+    sum = fmaf(z * w, bf16f(p.v[(size_t)(row0 + j) * p.v_stride + head * d + channel]), sum);
+    if (!isfinite(sum)) break;
+    w *= expf(decay_of(p.log_decay[(size_t)(row0 + j) * p.decay_stride + head]));
+  }
+  return sum;
+}
+
+// The list of all chunks (sequence by sequence, head by head) is cut into
+// equal runs, one a CTA.  Over a chunk of 128 rows, with G_i as in Gains,
+//
+//   out_i = scale * (2^G_i q_i S + sum_(j <= i) 2^(G_i - G_j) (q_i . k_j) v_j)
+//   S <- 2^G_127 S + sum_j 2^(G_127 - G_j) k_j v_j^T,
+//
+// four products of 128 rows.  Operands that are not bf16 to begin with are
+// taken in parts: the weights and the state, for results that are rounded to
+// bf16, in two (2^-17 of each); the keys times their decays, which enter the
+// state, in three (2^-25).  The state stays in fp32 registers and is added to
+// there, since the tensor cores' sums may cut where fp32 rounds.
+//
+// A chain that is cut is joined through L2: each CTA works out the part that
+// others go on with first, and the part that others began last.  Where a
+// whole run lies inside a chain, what it adds is worked out first, without
+// results.
+//
+// What bounds it: of a chunk's some 4100 clocks of products (D = 128), all but
+// the state's own chain (sum, conversion, products with the keys) run beside
+// the conversions.
 template <int D>
-__global__ void __launch_bounds__(LC_THREADS, 1) linear_chunk_kernel(ChunkParams cp) {
+__global__ void __launch_bounds__(LC_THREADS, 1)
+    linear_chunk_kernel(const __grid_constant__ ChunkParams cp, const __grid_constant__ CUtensorMap tm_q,
+                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_o) {
   using L = Lc<D>;
   constexpr int NC = L::NC;
   extern __shared__ __align__(1024) unsigned char smem[];
   LcShared& sh = *reinterpret_cast<LcShared*>(smem + L::TILES);
   const LinearParams& p = cp.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int quarter = warp & 3, group = warp >> 2;
   pdl_wait();
   pdl_trigger();
 
-  if (warp == 0) {
+  if (warp == W_ISSUE) {
     tmem_alloc(&sh.tmem, 512);
     if (lane == 0) {
-      for (int i = 0; i < 4; ++i) mbar_init(&sh.bar[i], 1);
+      for (uint64_t* b : {&sh.qk_full[0], &sh.qk_full[1], &sh.v_full, &sh.g_full, &sh.qk_done, &sh.sq_done, &sh.pv_done,
+                          &sh.ds_done, &sh.drain})
+        mbar_init(b, 1);
+      for (uint64_t* b : {&sh.g_empty, &sh.s_ready, &sh.p_ready, &sh.k_ready, &sh.o_ready}) mbar_init(b, LC_COMPUTE / 32);
       fence_mbar_init();
       sh.abort = 0;
     }
   }
-  if (tid < 128) sh.poison[tid] = CHUNK;
 
-  // ---- the CTA's run of the list of all chunks: sequences, their heads, their chunks
-  int total = 0, longest = 0;
-  for (int s = tid; s < p.n_seq; s += LC_THREADS) {
-    const int c = chunks_of(p, s, blockIdx.x == 0);
-    total += c;
-    longest = max(longest, c);
+  // ---- the CTA's run
+  {
+    int total = 0, longest = 0;
+    for (int s = tid; s < p.n_seq; s += LC_THREADS) {
+      const int c = chunks_of(p, s, blockIdx.x == 0);
+      total += c;
+      longest = max(longest, c);
+    }
+    total = __reduce_add_sync(~0u, total);
+    longest = __reduce_max_sync(~0u, longest);
+    if (tid == 0) sh.total = sh.longest = 0;
+    __syncthreads();
+    if (lane == 0) {
+      atomicAdd(&sh.total, total);
+      atomicMax(&sh.longest, longest);
+    }
+    __syncthreads();
   }
-  total = __reduce_add_sync(~0u, total);
-  longest = __reduce_max_sync(~0u, longest);
-  if (tid == 0) sh.total = sh.longest = 0;
-  __syncthreads();
-  if (lane == 0) {
-    atomicAdd(&sh.total, total);
-    atomicMax(&sh.longest, longest);
-  }
-  __syncthreads();
   const int64_t all = (int64_t)sh.total * p.hv;
-  longest = sh.longest;
   // Equal runs, but none so short that joining a chain's runs (a state from L2
   // each) takes longer than the runs do.
-  const int64_t run = max((all + gridDim.x - 1) / gridDim.x, (int64_t)ceilf(sqrtf(longest / 12.f)));
+  const int64_t run = max((all + gridDim.x - 1) / gridDim.x, (int64_t)ceilf(sqrtf(sh.longest / 12.f)));
   const int64_t a = run * blockIdx.x, b = min(a + run, all);
   const uint32_t tmem = sh.tmem;
-  uint32_t phase[4] = {};
-  const int never = 0;
-
-  const auto wait_bar = [&](int i) {
-    if (!mbar_wait(&sh.bar[i], phase[i], (volatile int*)&sh.abort, LC_WAIT_NS) && !sh.abort) {
-      if (atomicOr(&p.st->flags, FLAG_TIMEOUT) == 0) p.st->timeout_site = 60 + i;
-      sh.abort = 1;
-    }
-    phase[i] ^= 1;
-  };
-
-  float S[NC];
-  // rows of the state in TMEM: lanes, the upper 64 a copy of the lower with D = 64
-  const int s_row = (32 * quarter + lane) % D;
-  const int s_col = D == 128 ? 64 * group : 16 * ((quarter >> 1) + 2 * group);
-
-  // ---- one part; full: with its results, else only what it adds to a state of zero
-  const auto load_tile = [&](const uint16_t* x, int64_t stride, size_t row0, int col, int rows, int at) {
-    const uint32_t base = smem_u32(smem) + at;
-#pragma unroll
-    for (int i = 0; i < CHUNK * D / 8 / LC_THREADS; ++i) {
-      const int e = tid + i * LC_THREADS, r = e / (D / 8), c = e % (D / 8);
-      const bool on = r < rows;
-      cp16(base + (c >> 3) * L::HALF + sw128_off(r, c & 7), on ? x + (row0 + r) * stride + col + c * 8 : x, on);
-    }
-  };
-  const auto write_state = [&]() {  // both bf16 parts, as the operand of the products with the queries
-#pragma unroll
-    for (int c = 0; c < NC; c += 8) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float u = S[c + 2 * i], v = S[c + 2 * i + 1];
-        hi[i] = take_bf16(u, v);
-        lo[i] = pack_bf16x2(u, v);
-      }
-      const int col = s_col + c;
-      unsigned char* to = smem + L::X0 + (col >> 6) * L::S_HALF + sw128_off(s_row, (col & 63) >> 3);
-      *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(to + L::S_PART) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-  };
-
-  // Runs the part's chunks on S; returns the log2 of its decays' product.
-  const auto run_part = [&](const Part& t, bool full) -> double {
-    const int hk = t.head / (p.hv / p.hk);
-    const int rows_all = t.n;
-    const auto rows_of = [&](int c) { return min(CHUNK, rows_all - c * CHUNK); };
-    const auto row_of = [&](int c) { return (size_t)(t.row + c * CHUNK); };
-    float g[4] = {};
-    const auto load_gains = [&](int c) {  // warp 7: four rows a lane
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * lane + i;
-        g[i] = r < rows_of(c) ? p.log_decay[(row_of(c) + r) * p.decay_stride + t.head] : 0.f;
-      }
-    };
-    double decay = 0.0;
-    const auto scan_gains = [&](int to) {
-      double sum[4], at = 0.0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float l = decay_of(g[i]) * LOG2E;
-        at += l < LEAST ? (double)LEAST : (double)decay_of(g[i]) * 1.4426950408889634;
-        sum[i] = at;
-      }
-      double in = at;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double u = __shfl_up_sync(~0u, in, o);
-        if (lane >= o) in += u;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const double v = in - at + sum[i], n = rint(v);
-        sh.gain[to][4 * lane + i] = Gain{(float)n, (float)(v - n)};
-      }
-    };
-    const auto load_qk = [&](int c) {
-      if (full) load_tile(p.q, p.q_stride, row_of(c), hk * D, rows_of(c), L::Q0 + (c & 1) * L::TILE);
-      load_tile(p.k, p.k_stride, row_of(c), hk * D, rows_of(c), L::K0 + (c & 1) * L::TILE);
-      cp_commit();
-    };
-    const auto load_v = [&](int c) {
-      load_tile(p.v, p.v_stride, row_of(c), t.head * D, rows_of(c), L::V0);
-      cp_commit();
-    };
-    __syncthreads();  // the decays of the part before are still read
-    load_qk(t.c0);
-    load_v(t.c0);
-    if (warp == 7) {
-      load_gains(t.c0);
-      scan_gains(t.c0 & 1);
-    }
-    if (full) write_state();
-
-    for (int c = t.c0; c < t.c1; ++c) {
-      const bool more = c + 1 < t.c1;
-      const uint32_t sb = smem_u32(smem), q0 = sb + L::Q0 + (c & 1) * L::TILE, k0 = sb + L::K0 + (c & 1) * L::TILE,
-                     v0 = sb + L::V0, x0 = sb + L::X0;
-      const Gain* gain = sh.gain[c & 1];
-      cp_wait<1>();  // queries and keys
-      fence_async_smem();
-      tc_fence_before();
-      __syncthreads();
-      if (sh.abort) break;
-      if (full && warp == 0) {
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = (k >> 2) * L::HALF + (k & 3) * 32;
-            mma_bf16(tmem + L::T_S, desc_sw128(q0 + o), desc_sw128(k0 + o), idesc(128, 128, false, false), k > 0);
-          }
-          mma_commit(&sh.bar[0]);
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_bf16(tmem + L::T_SQ, desc_sw128(q0 + (k >> 2) * L::HALF + (k & 3) * 32),
-                       desc_rows(x0 + part * L::S_PART + k * 2048, L::S_HALF), idesc(128, D, false, true), part + k > 0);
-          mma_commit(&sh.bar[1]);
-        }
-        __syncwarp();
-      }
-      if (more)
-        load_qk(c + 1);
-      else
-        cp_commit();  // an empty group keeps the count
-      if (warp == 7 && more) load_gains(c + 1);
-      const Gain end = gain[CHUNK - 1];
-      const int row = 32 * quarter + lane;  // of the chunk, in the products whose rows are the queries'
-      if (full) {
-        // weights: scores times the decays between key and query, in two bf16 parts over the scores' own columns
-        wait_bar(0);
-        tc_fence_after();
-        const Gain mine = gain[row];
-        const uint32_t at = tmem + ((uint32_t)(32 * quarter) << 16) + L::T_S + 64 * group;
-        uint32_t hi[32], lo[32];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int j0 = 64 * group + 16 * j;
-          if (j0 > 32 * quarter + 31) {  // behind all of the warp's rows
-#pragma unroll
-            for (int i = 0; i < 8; ++i) hi[8 * j + i] = lo[8 * j + i] = 0;
-            continue;
-          }
-          uint32_t r[16];
-          tmem_ld16(at + 16 * j, r);
-          tmem_ld_wait();
-          tmem_ld_fence(r);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 two = *reinterpret_cast<const float4*>(&gain[j0 + 2 * i]);
-            float u = __uint_as_float(r[2 * i]) * ex2((mine.n - two.x) + (mine.f - two.y));
-            float v = __uint_as_float(r[2 * i + 1]) * ex2((mine.n - two.z) + (mine.f - two.w));
-            u = j0 + 2 * i <= row ? u : 0.f;
-            v = j0 + 2 * i + 1 <= row ? v : 0.f;
-            hi[8 * j + i] = take_bf16(u, v);
-            lo[8 * j + i] = pack_bf16x2(u, v);
-          }
-        }
-        tmem_st<32>(at, hi);
-        tmem_st<32>(at + 32, lo);
-        tmem_st_wait();
-      }
-      // values: one that is not finite would reach the rows before it (0 times
-      // it is NaN), so it is taken out and its channel's rows are marked
-      cp_wait<1>();
-      bool odd = false;
-#pragma unroll
-      for (int i = 0; i < CHUNK * D / 8 / LC_THREADS; ++i) {
-        const int e = tid + i * LC_THREADS, r = e / (D / 8), ch = e % (D / 8);
-        uint4* at = reinterpret_cast<uint4*>(smem + L::V0 + (ch >> 3) * L::HALF + sw128_off(r, ch & 7));
-        const uint4 v = *at;
-        const uint32_t any = ((v.x & 0x7F807F80u) + 0x00800080u) | ((v.y & 0x7F807F80u) + 0x00800080u) |
-                             ((v.z & 0x7F807F80u) + 0x00800080u) | ((v.w & 0x7F807F80u) + 0x00800080u);
-        if (any & 0x80008000u) {
-          odd = true;
-          uint16_t* el = reinterpret_cast<uint16_t*>(at);
-          for (int j = 0; j < 8; ++j)
-            if ((el[j] & 0x7F80) == 0x7F80) {
-              el[j] = 0;
-              atomicMin(&sh.poison[8 * ch + j], r);
-            }
-        }
-      }
-      fence_async_smem();
-      tc_fence_before();
-      const bool poisoned = __syncthreads_or(odd);
-      if (sh.abort) {  // the products in flight end before their memory goes
-        if (full) mbar_wait(&sh.bar[1], phase[1], &never, LC_WAIT_NS);
-        break;
-      }
-      if (full) {
-        if (warp == 0) {
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-              for (int k = 0; k < CHUNK / 16; ++k)
-                mma_bf16_ta(tmem + L::T_PV, tmem + L::T_S + 64 * (k >> 2) + 32 * part + 8 * (k & 3),
-                            desc_rows(v0 + k * 2048, L::HALF), idesc(128, D, false, true), part + k > 0);
-            mma_commit(&sh.bar[2]);
-          }
-          __syncwarp();
-        }
-        wait_bar(1);  // the state's operand is free
-      }
-      // keys times the decays behind them, in three bf16 parts (2^-25): one in
-      // the keys' place, two in that of the state's
-      {
-        const int r = tid >> 1, half = tid & 1;
-        const float w = ex2((end.n - gain[r].n) + (end.f - gain[r].f));
-        unsigned char* kp = smem + L::K0 + (c & 1) * L::TILE;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int ch = half * (D / 16) + i;
-          const uint32_t off = (ch >> 3) * L::HALF + sw128_off(r, ch & 7);
-          const uint4 v = *reinterpret_cast<const uint4*>(kp + off);
-          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[3][4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x = bf16lo(in[j]) * w, y = bf16hi(in[j]) * w;
-            o[0][j] = take_bf16(x, y);
-            o[1][j] = take_bf16(x, y);
-            o[2][j] = pack_bf16x2(x, y);
-          }
-          *reinterpret_cast<uint4*>(kp + off) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-          *reinterpret_cast<uint4*>(smem + L::X0 + off) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
-          *reinterpret_cast<uint4*>(smem + L::X0 + L::TILE + off) = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
-        }
-      }
-      fence_async_smem();
-      __syncthreads();
-      if (warp == 0) {
-        if (elect_one()) {
-          // with D = 64 the keys' 64 channels count twice, as the product's 128 rows
-          constexpr uint32_t outer = D == 128 ? L::HALF : 0;
-#pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            const uint32_t from = part == 0 ? k0 : x0 + (part - 1) * L::TILE;
-#pragma unroll
-            for (int k = 0; k < CHUNK / 16; ++k)
-              mma_bf16(tmem + L::T_DS, desc_rows(from + k * 2048, outer), desc_rows(v0 + k * 2048, L::HALF),
-                       idesc(128, D, true, true), part + k > 0);
-          }
-          mma_commit(&sh.bar[3]);
-        }
-        __syncwarp();
-      }
-      if (full) {
-        wait_bar(2);
-        tc_fence_after();
-        const float before = ex2(gain[row].n + gain[row].f);
-        const uint32_t at = tmem + ((uint32_t)(32 * quarter) << 16) + group * (D / 2);
-        uint16_t* out = p.out + ((row_of(c) + row) * p.hv + t.head) * D + group * (D / 2);
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          uint32_t x[16], y[16];
-          tmem_ld16(at + L::T_SQ + 16 * j, x);
-          tmem_ld16(at + L::T_PV + 16 * j, y);
-          tmem_ld_wait();
-          tmem_ld_fence(x);
-          tmem_ld_fence(y);
-          float o[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            o[i] = p.scale * fmaf(before, __uint_as_float(x[i]), __uint_as_float(y[i]));
-            if (poisoned && sh.poison[group * (D / 2) + 16 * j + i] <= row) o[i] = NOT_A_NUMBER;
-          }
-          if (row < rows_of(c)) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 8)
-              *reinterpret_cast<uint4*>(out + 16 * j + i) =
-                  make_uint4(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]), pack_bf16x2(o[i + 4], o[i + 5]),
-                             pack_bf16x2(o[i + 6], o[i + 7]));
-          }
-        }
-      }
-      wait_bar(3);
-      tc_fence_after();
-      if (more)
-        load_v(c + 1);
-      else
-        cp_commit();
-      if (warp == 7 && more) scan_gains((c + 1) & 1);
-      // S times the chunk's decay, plus what it adds; a slow decay as in the recurrent kernel
-      const float whole = end.n + end.f;
-      const bool slow = whole > -0.5f;
-      const float f = slow ? expm1f(whole * LN2) : exp2f(whole);
-      decay += (double)end.n + (double)end.f;
-#pragma unroll
-      for (int j = 0; j < NC / 16; ++j) {
-        uint32_t x[16];
-        tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + L::T_DS + s_col + 16 * j, x);
-        tmem_ld_wait();
-        tmem_ld_fence(x);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float& s = S[16 * j + i];
-          s = fmaf(s, f, slow ? s + __uint_as_float(x[i]) : __uint_as_float(x[i]));
-          if (poisoned && sh.poison[s_col + 16 * j + i] < CHUNK) s = NOT_A_NUMBER;
-        }
-      }
-      if (poisoned) {
-        __syncthreads();
-        if (tid < 128) sh.poison[tid] = CHUNK;
-      }
-      if (full && more) write_state();
-    }
-    cp_wait<0>();
-    return decay;
-  };
-
-  const auto state_at = [&](int slot, int head) { return p.states + ((size_t)slot * p.hv + head) * D * D + s_row * D + s_col; };
-  const auto begin_chain = [&](const Part& t, bool full) {
-#pragma unroll
-    for (int i = 0; i < NC; i += 4) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (full && t.slot_in >= 0) v = *reinterpret_cast<const float4*>(state_at(t.slot_in, t.head) + i);
-      S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
-    }
-  };
-  const auto end_chain = [&](const Part& t) {
-    if (t.slot_out < 0 || sh.abort) return;
-#pragma unroll
-    for (int i = 0; i < NC; i += 4)
-      *reinterpret_cast<float4*>(state_at(t.slot_out, t.head) + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-  };
-  const auto publish = [&](double decay) {
-    float* to = cp.pub + blockIdx.x * pub_floats(D);
-#pragma unroll
-    for (int i = 0; i < NC; i += 4)
-      *reinterpret_cast<float4*>(to + s_row * D + s_col + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-    if (tid == 0) to[D * D] = (float)decay;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0 && !sh.abort && !((p.st->stall & MOE_STALL_GRID_BARRIER) && blockIdx.x == 0))
-      store_release(&cp.flags[blockIdx.x], 1u);
-  };
-  // The state that this CTA's first part goes on from, from the CTAs before it.
-  const auto join = [&](const Part& t) {
-    const int from = blockIdx.x - (int)((t.c0 + run - 1) / run);  // the CTA that begins the chain
-    if (tid < blockIdx.x - from) {
-      const uint64_t t0 = globaltimer();
-      while (!load_acquire(&cp.flags[from + tid])) {
-        __nanosleep(64);
-        if (globaltimer() - t0 > LC_WAIT_NS) {
-          if (atomicOr(&p.st->flags, FLAG_TIMEOUT) == 0) p.st->timeout_site = 64;
-          sh.abort = 1;
-          break;
-        }
-      }
-    }
-    __syncthreads();
-    if (sh.abort) return;
-    for (int b = from; b < (int)blockIdx.x; ++b) {
-      const float* at = cp.pub + b * pub_floats(D);
-      const float f = b == from ? 0.f : exp2f(__ldcg(at + D * D));
-#pragma unroll
-      for (int i = 0; i < NC; i += 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(at + s_row * D + s_col + i));
-        if (b == from) {
-          S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
-        } else {
-          S[i] = fmaf(S[i], f, v.x), S[i + 1] = fmaf(S[i + 1], f, v.y), S[i + 2] = fmaf(S[i + 2], f, v.z),
-          S[i + 3] = fmaf(S[i + 3], f, v.w);
-        }
-      }
-    }
-  };
-
   if (a < b) {
-    // where the first and the last chunk are
     int before = 0;
     for (int s0 = 0; s0 < p.n_seq; s0 += LC_THREADS) {
       const int s = s0 + tid, c = s < p.n_seq ? chunks_of(p, s, false) : 0;
@@ -568,7 +319,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1) linear_chunk_kernel(ChunkParams
       if (lane == 31) sh.scan[warp] = in;
       __syncthreads();
       int base = before;
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < LC_THREADS / 32; ++i) {
         if (i < warp) base += sh.scan[i];
         before += sh.scan[i];
       }
@@ -577,86 +328,515 @@ __global__ void __launch_bounds__(LC_THREADS, 1) linear_chunk_kernel(ChunkParams
       if (lo < b && b <= hi) sh.at[1][0] = s, sh.at[1][1] = base + in - c;
     }
     __syncthreads();
-    const auto part_of = [&](int s, int head) {
-      Part t;
-      t.s = s;
-      t.head = head;
-      linear_sequence(p, s, t.row, t.n, t.slot_in, t.slot_out);
-      t.c0 = 0;
-      t.c1 = t.nc = chunks_of(p, s, false);
-      return t;
-    };
-    Part first, last;
-    {
-      const int s = sh.at[0][0], nc = chunks_of(p, s, false);
-      const int64_t off = a - (int64_t)sh.at[0][1] * p.hv;
-      first = part_of(s, (int)(off / nc));
-      first.c0 = (int)(off % nc);
-      first.c1 = (int)min((int64_t)nc, first.c0 + (b - a));
-    }
-    {
-      const int s = sh.at[1][0], nc = chunks_of(p, s, false);
-      const int64_t off = b - 1 - (int64_t)sh.at[1][1] * p.hv;
-      last = part_of(s, (int)(off / nc));
-      last.c1 = (int)(off % nc) + 1;
-    }
-    const auto same = [](const Part& x, const Part& y) { return x.s == y.s && x.head == y.head; };
-    if (same(first, last)) last.c0 = first.c0, first.c1 = last.c1;
-    // 0: the part that other CTAs go on with, so that they need not wait long;
-    // inside a chain, what it adds.  1: whole chains.  2: the part that others began.
-    int stage = last.c1 < last.nc ? 0 : 1;
-    Part next = first;
-    bool left = true;  // next has not been looked at
-    while (!sh.abort) {
-      Part t;
-      bool full = true;
-      if (stage == 0) {
-        t = last;
-        full = t.c0 == 0;
-      } else if (stage == 1) {
-        bool found = false;
-        while (left && !found) {
-          t = next;
-          found = t.c0 == 0 && t.c1 == t.nc;
-          if (same(next, last)) {
-            left = false;
-          } else {
-            int s = next.s, head = next.head + 1;
-            if (head == p.hv) {
-              head = 0;
-              do ++s;
-              while (chunks_of(p, s, false) == 0);  // the last part's sequence has some
-            }
-            next = part_of(s, head);
-            if (same(next, last)) next = last;
-          }
-        }
-        if (!found) {
-          if (first.c0 == 0) break;
-          stage = 2;
-        }
-      }
-      if (stage == 2) {
-        t = first;
-        join(t);
-        if (sh.abort) break;
-      } else {
-        begin_chain(t, full);
-      }
-      const double decay = run_part(t, full);
-      if (stage == 0)
-        publish(decay);
-      else if (t.c1 == t.nc)
-        end_chain(t);
-      if (stage == 2) break;
-      stage = 1;
+    if (tid == 0) {
+      Part t = part_of(p, sh.at[0][0], 0);
+      int64_t off = a - (int64_t)sh.at[0][1] * p.hv;
+      t.head = (int)(off / t.nc);
+      t.c0 = (int)(off % t.nc);
+      t.c1 = (int)min((int64_t)t.nc, t.c0 + (b - a));
+      sh.first = t;
+      Part u = part_of(p, sh.at[1][0], 0);
+      off = b - 1 - (int64_t)sh.at[1][1] * p.hv;
+      u.head = (int)(off / u.nc);
+      u.c1 = (int)(off % u.nc) + 1;
+      sh.last = u.s == t.s && u.head == t.head ? t : u;
     }
   }
-  cp_wait<0>();
+  __syncthreads();
+  tc_fence_after();
+
+  volatile int* abort = &sh.abort;
+  const auto wait = [&](uint64_t* bar, uint32_t& phase, int site) {
+    const bool ok = __all_sync(~0u, mbar_wait(bar, phase, abort, LC_WAIT_NS));  // a warp goes on or gives up as one
+    phase ^= 1;
+    if (!ok && !*abort) {
+      if (atomicOr(&p.st->flags, FLAG_TIMEOUT) == 0) p.st->timeout_site = site;
+      *abort = 1;
+    }
+    return ok;
+  };
+
+  if (warp >= W_ISSUE) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LC_REGS_REST));
+    if (warp == W_ISSUE && a < b) {
+      // ---- tiles and products
+      const uint32_t sb = smem_u32(smem), v0 = sb + L::V0, x0 = sb + L::X0;
+      uint32_t f_qk[2] = {}, f_v = 0, f_s = 0, f_p = 0, f_k = 0, f_o = 0, f_ds = 0, out_qk = 0, out_v = 0;
+      const auto load = [&](const CUtensorMap* tm, int col, int row, int at, uint64_t* bar) {
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) tma_load_2d(smem + at + h * L::HALF, tm, col + 64 * h, row, bar);
+      };
+      const auto load_qk = [&](const Walk& w, int buf) {
+        if (elect_one()) {
+          const int col = w.t.head / (p.hv / p.hk) * D, row = w.t.row + w.c * CHUNK;
+          mbar_arrive_expect_tx(&sh.qk_full[buf], w.t.full ? 2 * L::TILE : L::TILE);
+          if (w.t.full) load(&tm_q, col, row, L::Q0 + buf * L::TILE, &sh.qk_full[buf]);
+          load(&tm_k, col, row, L::K0 + buf * L::TILE, &sh.qk_full[buf]);
+        }
+        __syncwarp();
+        out_qk |= 1u << buf;
+      };
+      const auto load_v = [&](const Walk& w) {
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sh.v_full, L::TILE);
+          load(&tm_v, w.t.head * D, w.t.row + w.c * CHUNK, L::V0, &sh.v_full);
+        }
+        __syncwarp();
+        out_v = 1;
+      };
+      const auto scores = [&](int buf) {
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t q0 = sb + L::Q0 + buf * L::TILE, k0 = sb + L::K0 + buf * L::TILE;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = (k >> 2) * L::HALF + (k & 3) * 32;
+            mma_bf16(tmem + L::T_S, desc_sw128(q0 + o), desc_sw128(k0 + o), idesc(128, 128, false, false), k > 0);
+          }
+          mma_commit(&sh.qk_done);
+        }
+        __syncwarp();
+      };
+      Walk now, next, ahead;  // the chunk, the one behind it, the one behind that
+      now.begin(p, sh);
+      load_qk(now, 0);
+      load_v(now);
+      next = now;
+      next.next(p, sh);
+      ahead = next;
+      if (next.more()) {
+        load_qk(next, 1);
+        ahead.next(p, sh);
+      }
+      bool ok = wait(&sh.qk_full[0], f_qk[0], 60);
+      out_qk &= ~1u;
+      if (ok && now.t.full) scores(0);
+      for (int buf = 0; ok && now.more(); buf ^= 1) {
+        const bool full = now.t.full;
+        const uint32_t q0 = sb + L::Q0 + buf * L::TILE, k0 = sb + L::K0 + buf * L::TILE;
+        if (!(ok = wait(&sh.s_ready, f_s, 61))) break;
+        tc_fence_after();
+        if (full) {
+          if (elect_one()) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_bf16(tmem + L::T_SQ, desc_sw128(q0 + (k >> 2) * L::HALF + (k & 3) * 32),
+                         desc_rows(x0 + part * L::S_PART + k * 2048, L::S_HALF), idesc(128, D, false, true), part + k > 0);
+            mma_commit(&sh.sq_done);
+          }
+          __syncwarp();
+        }
+        if (!(ok = wait(&sh.v_full, f_v, 62))) break;
+        out_v = 0;
+        if (full) {
+          if (!(ok = wait(&sh.p_ready, f_p, 63))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int k = 0; k < CHUNK / 16; ++k)
+                mma_bf16_ta(tmem + L::T_PV, tmem + L::T_S + 64 * (k >> 2) + 32 * ((k >> 1) & 1) + 16 * part + 8 * (k & 1),
+                            desc_rows(v0 + k * 2048, L::HALF), idesc(128, D, false, true), part + k > 0);
+            mma_commit(&sh.pv_done);
+          }
+          __syncwarp();
+        }
+        if (!(ok = wait(&sh.k_ready, f_k, 64))) break;
+        if (elect_one()) {
+          // with D = 64 the keys' 64 channels count twice, as the product's 128 rows
+          constexpr uint32_t outer = D == 128 ? L::HALF : 0;
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            const uint32_t from = part == 0 ? k0 : x0 + (part - 1) * L::TILE;
+#pragma unroll
+            for (int k = 0; k < CHUNK / 16; ++k)
+              mma_bf16(tmem + L::T_DS, desc_rows(from + k * 2048, outer), desc_rows(v0 + k * 2048, L::HALF),
+                       idesc(128, D, true, true), part + k > 0);
+          }
+          mma_commit(&sh.ds_done);
+        }
+        __syncwarp();
+        if (next.more()) {  // its scores take the weights' place: products run in order
+          if (!(ok = wait(&sh.qk_full[buf ^ 1], f_qk[buf ^ 1], 60))) break;
+          out_qk &= ~(1u << (buf ^ 1));
+          if (next.t.full) scores(buf ^ 1);
+        }
+        if (full) {
+          if (!(ok = wait(&sh.o_ready, f_o, 65))) break;
+          if (now.rows() == CHUNK) {
+            if (elect_one()) {
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+                tma_store_2d(&tm_o, now.t.head * D + 64 * h, now.t.row + now.c * CHUNK, smem + L::Q0 + buf * L::TILE + h * L::HALF);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            __syncwarp();
+          }
+        }
+        if (!(ok = wait(&sh.ds_done, f_ds, 66))) break;
+        if (next.more()) load_v(next);
+        if (ahead.more()) load_qk(ahead, buf);
+        now = next;
+        next = ahead;
+        if (ahead.more()) ahead.next(p, sh);
+      }
+      if (!ok) {  // what is in flight ends before its memory goes
+        const int never = 0;
+        if (elect_one()) mma_commit(&sh.drain);
+        __syncwarp();
+        mbar_wait(&sh.drain, 0, &never, LC_WAIT_NS);
+        for (int i = 0; i < 2; ++i)
+          if (out_qk >> i & 1) mbar_wait(&sh.qk_full[i], f_qk[i], &never, LC_WAIT_NS);
+        if (out_v) mbar_wait(&sh.v_full, f_v, &never, LC_WAIT_NS);
+      }
+      if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      __syncwarp();
+    } else if (warp == W_GAIN && a < b) {
+      // ---- decays: four rows a lane, a chunk ahead in registers
+      Walk w;
+      w.begin(p, sh);
+      uint32_t f_empty = 1;
+      while (w.more()) {
+        double v[4], at = 0.0;
+        const int rows = w.rows();
+        float g[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 4 * lane + i;
+          g[i] = r < rows ? decay_of(p.log_decay[(size_t)(w.t.row + w.c * CHUNK + r) * p.decay_stride + w.t.head]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const double l = (double)g[i] * 1.4426950408889634;
+          at += l < LEAST ? LEAST : l;
+          v[i] = at;
+        }
+        double in = at;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double u = __shfl_up_sync(~0u, in, o);
+          if (lane >= o) in += u;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += in - at;
+        const double end = __shfl_sync(~0u, v[3], 31);
+        const double ref0 = __shfl_sync(~0u, v[0], lane & 24);
+        float rel[4], last[4], off[3][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          rel[i] = (float)(v[i] - ref0);
+          last[i] = ex2((float)(end - v[i]));
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          const double ref = __shfl_sync(~0u, v[0], 8 * q + 8);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) off[q][i] = ex2((float)(ref - v[i]));
+        }
+        const double n = rint(end);
+        const float whole = (float)end;
+        const bool slow = whole > -0.5f;
+        const float keep = slow ? expm1f(whole * LN2) : exp2f(whole);
+        if (!wait(&sh.g_empty, f_empty, 67)) break;
+        Gains& to = sh.g;
+        const int r = 4 * lane;
+        *reinterpret_cast<float4*>(&to.rel[r]) = make_float4(rel[0], rel[1], rel[2], rel[3]);
+        *reinterpret_cast<float4*>(&to.last[r]) = make_float4(last[0], last[1], last[2], last[3]);
+        *reinterpret_cast<float4*>(&to.first[r]) = make_float4(ex2((float)v[0]), ex2((float)v[1]), ex2((float)v[2]), ex2((float)v[3]));
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          if (lane < 8 * q + 8)
+            *reinterpret_cast<float4*>(&to.off[16 * q * (q + 1) + r]) = make_float4(off[q][0], off[q][1], off[q][2], off[q][3]);
+        if (lane == 31) to.n = (float)n, to.f = (float)(end - n), to.keep = keep, to.slow = slow;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.g_full);
+        w.next(p, sh);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LC_REGS));
+    const int quarter = warp & 3, group = warp >> 2;
+    const int row = 32 * quarter + lane;  // of the chunk, in the products whose rows are the queries'
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    uint32_t f_qk[2] = {}, f_v = 0, f_g = 0, f_sc = 0, f_sq = 0, f_pv = 0, f_ds = 0;
+    float S[NC];
+    // rows of the state in TMEM: lanes, the upper 64 a copy of the lower with D = 64
+    const int s_row = row % D;
+    const int s_col = D == 128 ? 64 * group : 16 * ((quarter >> 1) + 2 * group);
+
+    const auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    const auto sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(LC_COMPUTE) : "memory"); };
+    const auto write_state = [&]() {  // both bf16 parts, as the operand of the products with the queries
+#pragma unroll
+      for (int c = 0; c < NC; c += 8) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float u = S[c + 2 * i], v = S[c + 2 * i + 1];
+          hi[i] = take_bf16(u, v);
+          lo[i] = pack_bf16x2(u, v);
+        }
+        const int col = s_col + c;
+        unsigned char* to = smem + L::X0 + (col >> 6) * L::S_HALF + sw128_off(s_row, (col & 63) >> 3);
+        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(to + L::S_PART) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_async_smem();
+    };
+    const auto state_at = [&](int slot, int head) {
+      return p.states + ((size_t)slot * p.hv + head) * D * D + s_row * D + s_col;
+    };
+    // The state that the CTA's first part goes on from, from the CTAs before it.
+    const auto join = [&](const Part& t) {
+      const int from = blockIdx.x - (int)((t.c0 + run - 1) / run);  // the CTA that begins the chain
+      if (tid < (int)blockIdx.x - from) {
+        const uint64_t t0 = globaltimer();
+        while (!load_acquire(&cp.flags[from + tid])) {
+          __nanosleep(64);
+          if (*abort) break;
+          if (globaltimer() - t0 > LC_WAIT_NS) {
+            if (atomicOr(&p.st->flags, FLAG_TIMEOUT) == 0) p.st->timeout_site = 68;
+            *abort = 1;
+            break;
+          }
+        }
+      }
+      sync();
+      if (*abort) return;
+      for (int b = from; b < (int)blockIdx.x; ++b) {
+        const float* at = cp.pub + b * pub_floats(D);
+        const float f = b == from ? 0.f : exp2f(__ldcg(at + D * D) + __ldcg(at + D * D + 1));
+#pragma unroll
+        for (int i = 0; i < NC; i += 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(at + s_row * D + s_col + i));
+          if (b == from) {
+            S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
+          } else {
+            S[i] = fmaf(S[i], f, v.x), S[i + 1] = fmaf(S[i + 1], f, v.y), S[i + 2] = fmaf(S[i + 2], f, v.z),
+            S[i + 3] = fmaf(S[i + 3], f, v.w);
+          }
+        }
+      }
+    };
+
+    Walk w;
+    if (a < b) w.begin(p, sh);
+    else w.stage = 3;
+    float decay_n = 0.f, decay_f = 0.f;
+    for (int buf = 0; w.more() && !*abort; buf ^= 1) {
+      const bool full = w.t.full;
+      if (w.c == w.t.c0) {  // a part begins
+        decay_n = decay_f = 0.f;
+        if (w.stage == 2) {
+          join(w.t);
+          if (*abort) break;
+        } else {
+#pragma unroll
+          for (int i = 0; i < NC; i += 4) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (full && w.t.slot_in >= 0) v = *reinterpret_cast<const float4*>(state_at(w.t.slot_in, w.t.head) + i);
+            S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
+          }
+        }
+        if (full) write_state();
+        tc_fence_before();
+        arrive(&sh.s_ready);
+      }
+      const int rows = w.rows();
+      if (!wait(&sh.g_full, f_g, 70)) break;
+      const float keep = sh.g.keep;
+      const bool slow = sh.g.slow;
+      decay_n += sh.g.n;
+      decay_f += sh.g.f;
+      if (full) {
+        // weights: scores times the decays between key and query, in two bf16
+        // parts over the scores' own columns.  32 keys at a time; those that
+        // all of the warp's rows are behind take a row's and a key's factor.
+        if (!wait(&sh.qk_done, f_sc, 71)) break;
+        tc_fence_after();
+        const float rel = sh.g.rel[row], mine = ex2(rel);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int j0 = 64 * group + 32 * j;
+          const uint32_t at = lanes + L::T_S + j0;
+          uint32_t hi[16], lo[16];
+          if (j0 > 32 * quarter) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0;
+          } else {
+            uint32_t r[2][16];
+            tmem_ld16(at, r[0]);
+            tmem_ld16(at + 16, r[1]);
+            tmem_ld_wait();
+            tmem_ld_fence(r[0]);
+            tmem_ld_fence(r[1]);
+            if (j0 < 32 * quarter) {
+              const float* off = &sh.g.off[16 * quarter * (quarter - 1) + j0];
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const float4 f = *reinterpret_cast<const float4*>(off + 2 * i);
+                const uint32_t* z = &r[i >> 3][2 * (i & 7)];
+                float x0 = __uint_as_float(z[0]) * (mine * f.x), x1 = __uint_as_float(z[1]) * (mine * f.y);
+                float x2 = __uint_as_float(z[2]) * (mine * f.z), x3 = __uint_as_float(z[3]) * (mine * f.w);
+                hi[i] = take_bf16(x0, x1);
+                lo[i] = pack_bf16x2(x0, x1);
+                hi[i + 1] = take_bf16(x2, x3);
+                lo[i + 1] = pack_bf16x2(x2, x3);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const float4 f = *reinterpret_cast<const float4*>(&sh.g.rel[j0 + 2 * i]);
+                const uint32_t* z = &r[i >> 3][2 * (i & 7)];
+                float x0 = 2 * i <= lane ? __uint_as_float(z[0]) * ex2(rel - f.x) : 0.f;
+                float x1 = 2 * i + 1 <= lane ? __uint_as_float(z[1]) * ex2(rel - f.y) : 0.f;
+                float x2 = 2 * i + 2 <= lane ? __uint_as_float(z[2]) * ex2(rel - f.z) : 0.f;
+                float x3 = 2 * i + 3 <= lane ? __uint_as_float(z[3]) * ex2(rel - f.w) : 0.f;
+                hi[i] = take_bf16(x0, x1);
+                lo[i] = pack_bf16x2(x0, x1);
+                hi[i + 1] = take_bf16(x2, x3);
+                lo[i + 1] = pack_bf16x2(x2, x3);
+              }
+            }
+          }
+          tmem_st<16>(at, hi);
+          tmem_st<16>(at + 16, lo);
+        }
+        tmem_st_wait();
+      }
+      if (!wait(&sh.qk_full[buf], f_qk[buf], 72) || !wait(&sh.v_full, f_v, 73)) break;
+      if (rows < CHUNK) {  // rows of no sequence or of another
+        for (int e = tid; e < (CHUNK - max(rows, 0)) * (D / 8); e += LC_COMPUTE) {
+          const int r = CHUNK - 1 - e / (D / 8), ch = e % (D / 8);
+          const int to = (ch >> 3) * L::HALF + sw128_off(r, ch & 7);
+          *reinterpret_cast<uint4*>(smem + L::V0 + to) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        sync();
+      }
+      if (full) {
+        tc_fence_before();
+        arrive(&sh.p_ready);
+        if (!wait(&sh.sq_done, f_sq, 74)) break;  // the state's operand is free
+      }
+      // keys times the decays behind them, in three parts: one in the keys'
+      // place, two in that of the state's
+      {
+        const int r = tid >> 1, half = tid & 1;
+        const float f = sh.g.last[r];
+        unsigned char* kp = smem + L::K0 + buf * L::TILE;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int ch = half * (D / 16) + i;
+          const uint32_t off = (ch >> 3) * L::HALF + sw128_off(r, ch & 7);
+          uint4 v = *reinterpret_cast<const uint4*>(kp + off);
+          if (r >= rows) v = make_uint4(0, 0, 0, 0);
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[3][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x = bf16lo(in[j]) * f, y = bf16hi(in[j]) * f;
+            o[0][j] = take_bf16(x, y);
+            o[1][j] = take_bf16(x, y);
+            o[2][j] = pack_bf16x2(x, y);
+          }
+          *reinterpret_cast<uint4*>(kp + off) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+          *reinterpret_cast<uint4*>(smem + L::X0 + off) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
+          *reinterpret_cast<uint4*>(smem + L::X0 + L::TILE + off) = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
+        }
+      }
+      fence_async_smem();
+      arrive(&sh.k_ready);
+      if (full) {
+        const float first = sh.g.first[row];
+        if (!wait(&sh.pv_done, f_pv, 75)) break;
+        tc_fence_after();
+        const int row0 = w.t.row + w.c * CHUNK;
+        uint16_t* out = p.out + ((size_t)(row0 + row) * p.hv + w.t.head) * D;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const int col = group * (D / 2) + 16 * j;
+          uint32_t x[16], y[16];
+          tmem_ld16(lanes + L::T_SQ + col, x);
+          tmem_ld16(lanes + L::T_PV + col, y);
+          tmem_ld_wait();
+          tmem_ld_fence(x);
+          tmem_ld_fence(y);
+          float o[16], finite = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            finite = fmaf(__uint_as_float(y[i]), 0.f, finite);
+            o[i] = p.scale * fmaf(first, __uint_as_float(x[i]), __uint_as_float(y[i]));
+          }
+          if (finite != 0.f && row < rows) {  // NaN: a value that is not finite has met the rows before its own
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (!isfinite(__uint_as_float(y[i])))
+                o[i] = p.scale * fmaf(first, __uint_as_float(x[i]), weighted_values(p, D, row0, row, w.t.head, col + i));
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i += 8) {
+            const uint4 v = make_uint4(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]),
+                                       pack_bf16x2(o[i + 4], o[i + 5]), pack_bf16x2(o[i + 6], o[i + 7]));
+            const int ch = (col + i) >> 3;
+            if (rows == CHUNK)  // over the queries, which no product reads any more
+              *reinterpret_cast<uint4*>(smem + L::Q0 + buf * L::TILE + (ch >> 3) * L::HALF + sw128_off(row, ch & 7)) = v;
+            else if (row < rows)
+              *reinterpret_cast<uint4*>(out + col + i) = v;
+          }
+        }
+        fence_async_smem();
+        arrive(&sh.o_ready);
+      }
+      arrive(&sh.g_empty);
+      if (!wait(&sh.ds_done, f_ds, 76)) break;
+      tc_fence_after();
+      // a slow decay as in the recurrent kernel
+#pragma unroll
+      for (int j = 0; j < NC / 16; ++j) {
+        uint32_t x[16];
+        tmem_ld16(lanes + L::T_DS + s_col + 16 * j, x);
+        tmem_ld_wait();
+        tmem_ld_fence(x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float& s = S[16 * j + i];
+          s = fmaf(s, keep, slow ? s + __uint_as_float(x[i]) : __uint_as_float(x[i]));
+        }
+      }
+      if (w.c + 1 < w.t.c1) {
+        if (full) write_state();
+        tc_fence_before();
+        arrive(&sh.s_ready);
+      } else if (w.stage == 0) {  // others go on from here
+        float* to = cp.pub + blockIdx.x * pub_floats(D);
+#pragma unroll
+        for (int i = 0; i < NC; i += 4)
+          *reinterpret_cast<float4*>(to + s_row * D + s_col + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+        if (tid == 0) to[D * D] = decay_n, to[D * D + 1] = decay_f;
+        __threadfence();
+        sync();
+        if (tid == 0 && !((p.st->stall & MOE_STALL_GRID_BARRIER) && blockIdx.x == 0))
+          store_release(&cp.flags[blockIdx.x], 1u);
+      } else if (w.t.c1 == w.t.nc && w.t.slot_out >= 0) {
+#pragma unroll
+        for (int i = 0; i < NC; i += 4)
+          *reinterpret_cast<float4*>(state_at(w.t.slot_out, w.t.head) + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+      }
+      w.next(p, sh);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  if (warp == W_ISSUE) tmem_dealloc(tmem, 512);
   // the last CTA clears what the next call counts on
   if (tid == 0) {
     __threadfence();
@@ -670,11 +850,23 @@ __global__ void __launch_bounds__(LC_THREADS, 1) linear_chunk_kernel(ChunkParams
 }
 
 template <int D>
-cudaError_t launch(const ChunkParams& p, int grid, cudaStream_t s) {
+cudaError_t launch(const ChunkParams& c, int grid, cudaStream_t s) {
   auto* kern = linear_chunk_kernel<D>;
   cudaError_t e = set_smem_limit_once(kern, Lc<D>::TOTAL);
+  const LinearParams& p = c.p;
+  CUtensorMap q, k, v, o;
+  const auto map = [&](CUtensorMap* m, const void* base, int heads, int64_t stride) {
+    if (e == cudaSuccess)
+      e = tmap_2d(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)heads * D, p.t, (uint64_t)stride * 2, 64, CHUNK,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  map(&q, p.q, p.hk, p.q_stride);
+  map(&k, p.k, p.hk, p.k_stride);
+  map(&v, p.v, p.hv, p.v_stride);
+  map(&o, p.out, p.hv, (int64_t)p.hv * D);
   if (e != cudaSuccess) return e;
-  MOE_LAUNCH("linear_chunk", s, { e = launch_k(kern, dim3(grid), dim3(LC_THREADS), (size_t)Lc<D>::TOTAL, s, p); });
+  MOE_LAUNCH("linear_chunk", s,
+             { e = launch_k(kern, dim3(grid), dim3(LC_THREADS), (size_t)Lc<D>::TOTAL, s, c, q, k, v, o); });
   return e;
 }
 
