@@ -53,6 +53,19 @@ struct Part {
   bool full;
 };
 
+// What the warps need to know of a chunk.
+struct Ticket {
+  int row, rows;          // its first row, how many it has
+  int head;
+  int slot_in, slot_out;  // of the part
+  int before;             // chunks of the chain before the part
+  bool full;
+  bool begins, ends;      // the part
+  int stage;              // of the walk: 0 the part is published, 1 a whole chain, 2 others began it
+  bool closes;            // the part ends its chain
+  bool on;                // there is a chunk
+};
+
 // The decays of a chunk's rows: G_i is the log2 of the product of rows 0 .. i's.
 struct Gains {
   float rel[CHUNK];    // G_i less that of the first of its 32 rows
@@ -62,6 +75,7 @@ struct Gains {
   float n, f;          // G_127, whole part and rest
   float keep;          // what a state is multiplied by: 2^G_127, less 1 if slow
   int slow;
+  Ticket chunk;
 };
 
 struct LcShared {
@@ -75,7 +89,7 @@ struct LcShared {
   int scan[LC_THREADS / 32];
   int total, longest;
   uint32_t tmem;
-  int abort;
+  int abort;  // 0, or the wait that gave up
 };
 
 template <int D>
@@ -115,6 +129,11 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, int x, int y
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(tm), "r"(x), "r"(y),
                "r"(smem_u32(src))
                : "memory");
+}
+
+// One column of the warp's lanes, waited for.
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
 }
 
 // Two fp32 values as a bf16 pair; what is left of them takes their place.
@@ -179,7 +198,7 @@ struct Walk {
       next_part(p, sh);
     }
   }
-  __device__ void next_part(const LinearParams& p, const LcShared& sh) {
+  __device__ __noinline__ void next_part(const LinearParams& p, const LcShared& sh) {
     while (stage < 2 && left) {
       const bool is_last = s == sh.last.s && head == sh.last.head;
       bool whole;
@@ -215,7 +234,10 @@ struct Walk {
     if (++c == t.c1) next_part(p, sh);
   }
   __device__ __forceinline__ bool more() const { return stage < 3; }
-  __device__ __forceinline__ int rows() const { return min(CHUNK, t.n - c * CHUNK); }
+  __device__ __forceinline__ Ticket ticket() const {
+    return {t.row + c * CHUNK, min(CHUNK, t.n - c * CHUNK), t.head, t.slot_in, t.slot_out, t.c0, t.full, c == t.c0, c + 1 == t.c1,
+            stage, t.c1 == t.nc, stage < 3};
+  }
 };
 
 // sum_(j <= i) w_ij (q_i . k_j) v_j of one row and channel, for those whose
@@ -346,13 +368,16 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
   tc_fence_after();
 
   volatile int* abort = &sh.abort;
+  // A bounded wait, for whole warps: one goes on or gives up as one.  `site` is reported at the end.
   const auto wait = [&](uint64_t* bar, uint32_t& phase, int site) {
-    const bool ok = __all_sync(~0u, mbar_wait(bar, phase, abort, LC_WAIT_NS));  // a warp goes on or gives up as one
-    phase ^= 1;
-    if (!ok && !*abort) {
-      if (atomicOr(&p.st->flags, FLAG_TIMEOUT) == 0) p.st->timeout_site = site;
-      *abort = 1;
+    bool ok = __all_sync(~0u, mbar_try_wait(bar, phase));
+    if (!ok) {
+      const uint64_t t0 = globaltimer();
+      do ok = __all_sync(~0u, mbar_try_wait_sleep(bar, phase, 200000u));
+      while (!ok && !__any_sync(~0u, *abort || globaltimer() - t0 > LC_WAIT_NS));
+      if (!ok && !*abort) *abort = site;
     }
+    phase ^= 1;
     return ok;
   };
 
@@ -360,26 +385,34 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LC_REGS_REST));
     if (warp == W_ISSUE && a < b) {
       // ---- tiles and products
-      const uint32_t sb = smem_u32(smem), v0 = sb + L::V0, x0 = sb + L::X0;
+      const uint32_t sb = smem_u32(smem);
+      // descriptors: tiles of queries and keys with channels as the inner dimension, of keys, values and states with rows
+      constexpr uint32_t BUF = L::TILE >> 4, ROWS16 = 2048 >> 4;
+      const uint64_t qd = desc_sw128(sb + L::Q0), kd = desc_sw128(sb + L::K0);
+      // with D = 64 the keys' 64 channels count twice, as the product's 128 rows
+      const uint64_t kr = desc_rows(sb + L::K0, D == 128 ? L::HALF : 0), xr = desc_rows(sb + L::X0, D == 128 ? L::HALF : 0);
+      const uint64_t vr = desc_rows(sb + L::V0, L::HALF), sr = desc_rows(sb + L::X0, L::S_HALF);
+      const auto step = [](int k) { return (uint32_t)((k >> 2) * L::HALF + (k & 3) * 32) >> 4; };
       uint32_t f_qk[2] = {}, f_v = 0, f_s = 0, f_p = 0, f_k = 0, f_o = 0, f_ds = 0, out_qk = 0, out_v = 0;
       const auto load = [&](const CUtensorMap* tm, int col, int row, int at, uint64_t* bar) {
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) tma_load_2d(smem + at + h * L::HALF, tm, col + 64 * h, row, bar);
       };
-      const auto load_qk = [&](const Walk& w, int buf) {
+      const int heads = p.hv / p.hk;
+      const auto load_qk = [&](const Ticket& c, int buf) {
         if (elect_one()) {
-          const int col = w.t.head / (p.hv / p.hk) * D, row = w.t.row + w.c * CHUNK;
-          mbar_arrive_expect_tx(&sh.qk_full[buf], w.t.full ? 2 * L::TILE : L::TILE);
-          if (w.t.full) load(&tm_q, col, row, L::Q0 + buf * L::TILE, &sh.qk_full[buf]);
-          load(&tm_k, col, row, L::K0 + buf * L::TILE, &sh.qk_full[buf]);
+          const int col = c.head / heads * D;
+          mbar_arrive_expect_tx(&sh.qk_full[buf], c.full ? 2 * L::TILE : L::TILE);
+          if (c.full) load(&tm_q, col, c.row, L::Q0 + buf * L::TILE, &sh.qk_full[buf]);
+          load(&tm_k, col, c.row, L::K0 + buf * L::TILE, &sh.qk_full[buf]);
         }
         __syncwarp();
         out_qk |= 1u << buf;
       };
-      const auto load_v = [&](const Walk& w) {
+      const auto load_v = [&](const Ticket& c) {
         if (elect_one()) {
           mbar_arrive_expect_tx(&sh.v_full, L::TILE);
-          load(&tm_v, w.t.head * D, w.t.row + w.c * CHUNK, L::V0, &sh.v_full);
+          load(&tm_v, c.head * D, c.row, L::V0, &sh.v_full);
         }
         __syncwarp();
         out_v = 1;
@@ -387,43 +420,42 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       const auto scores = [&](int buf) {
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t q0 = sb + L::Q0 + buf * L::TILE, k0 = sb + L::K0 + buf * L::TILE;
+          const uint64_t qb = qd + buf * BUF, kb = kd + buf * BUF;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = (k >> 2) * L::HALF + (k & 3) * 32;
-            mma_bf16(tmem + L::T_S, desc_sw128(q0 + o), desc_sw128(k0 + o), idesc(128, 128, false, false), k > 0);
-          }
+          for (int k = 0; k < D / 16; ++k)
+            mma_bf16(tmem + L::T_S, qb + step(k), kb + step(k), idesc(128, 128, false, false), k > 0);
           mma_commit(&sh.qk_done);
         }
         __syncwarp();
       };
-      Walk now, next, ahead;  // the chunk, the one behind it, the one behind that
-      now.begin(p, sh);
+      Walk w;  // two chunks ahead of the products
+      w.begin(p, sh);
+      Ticket now = w.ticket(), next, ahead;
+      const auto advance = [&]() {
+        if (w.more()) w.next(p, sh);
+        return w.ticket();
+      };
       load_qk(now, 0);
       load_v(now);
-      next = now;
-      next.next(p, sh);
-      ahead = next;
-      if (next.more()) {
-        load_qk(next, 1);
-        ahead.next(p, sh);
-      }
+      next = advance();
+      if (next.on) load_qk(next, 1);
+      ahead = advance();
       bool ok = wait(&sh.qk_full[0], f_qk[0], 60);
       out_qk &= ~1u;
-      if (ok && now.t.full) scores(0);
-      for (int buf = 0; ok && now.more(); buf ^= 1) {
-        const bool full = now.t.full;
-        const uint32_t q0 = sb + L::Q0 + buf * L::TILE, k0 = sb + L::K0 + buf * L::TILE;
+      if (ok && now.full) scores(0);
+      for (int buf = 0; ok && now.on; buf ^= 1) {
+        const bool full = now.full;
         if (!(ok = wait(&sh.s_ready, f_s, 61))) break;
         tc_fence_after();
         if (full) {
           if (elect_one()) {
+            const uint64_t qb = qd + buf * BUF;
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
-                mma_bf16(tmem + L::T_SQ, desc_sw128(q0 + (k >> 2) * L::HALF + (k & 3) * 32),
-                         desc_rows(x0 + part * L::S_PART + k * 2048, L::S_HALF), idesc(128, D, false, true), part + k > 0);
+                mma_bf16(tmem + L::T_SQ, qb + step(k), sr + (part * (L::S_PART >> 4) + k * ROWS16), idesc(128, D, false, true),
+                         part + k > 0);
             mma_commit(&sh.sq_done);
           }
           __syncwarp();
@@ -438,51 +470,52 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int k = 0; k < CHUNK / 16; ++k)
-                mma_bf16_ta(tmem + L::T_PV, tmem + L::T_S + 64 * (k >> 2) + 32 * ((k >> 1) & 1) + 16 * part + 8 * (k & 1),
-                            desc_rows(v0 + k * 2048, L::HALF), idesc(128, D, false, true), part + k > 0);
+                mma_bf16_ta(tmem + L::T_PV, tmem + L::T_S + 16 * k + 8 * part, vr + k * ROWS16,
+                            idesc(128, D, false, true), part + k > 0);
             mma_commit(&sh.pv_done);
           }
           __syncwarp();
         }
         if (!(ok = wait(&sh.k_ready, f_k, 64))) break;
         if (elect_one()) {
-          // with D = 64 the keys' 64 channels count twice, as the product's 128 rows
-          constexpr uint32_t outer = D == 128 ? L::HALF : 0;
+          const uint64_t kb = kr + buf * BUF;
 #pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            const uint32_t from = part == 0 ? k0 : x0 + (part - 1) * L::TILE;
+          for (int part = 0; part < 3; ++part)
 #pragma unroll
             for (int k = 0; k < CHUNK / 16; ++k)
-              mma_bf16(tmem + L::T_DS, desc_rows(from + k * 2048, outer), desc_rows(v0 + k * 2048, L::HALF),
+              mma_bf16(tmem + L::T_DS, (part == 0 ? kb : xr + (part - 1) * BUF) + k * ROWS16, vr + k * ROWS16,
                        idesc(128, D, true, true), part + k > 0);
-          }
           mma_commit(&sh.ds_done);
         }
         __syncwarp();
-        if (next.more()) {  // its scores take the weights' place: products run in order
+        if (next.on) {  // its scores take the weights' place: products run in order
           if (!(ok = wait(&sh.qk_full[buf ^ 1], f_qk[buf ^ 1], 60))) break;
           out_qk &= ~(1u << (buf ^ 1));
-          if (next.t.full) scores(buf ^ 1);
+          if (next.full) scores(buf ^ 1);
         }
+        const Ticket beyond = advance();
         if (full) {
           if (!(ok = wait(&sh.o_ready, f_o, 65))) break;
-          if (now.rows() == CHUNK) {
+          if (now.rows == CHUNK) {
             if (elect_one()) {
 #pragma unroll
               for (int h = 0; h < D / 64; ++h)
-                tma_store_2d(&tm_o, now.t.head * D + 64 * h, now.t.row + now.c * CHUNK, smem + L::Q0 + buf * L::TILE + h * L::HALF);
+                tma_store_2d(&tm_o, now.head * D + 64 * h, now.row, smem + L::Q0 + buf * L::TILE + h * L::HALF);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             }
             __syncwarp();
           }
         }
         if (!(ok = wait(&sh.ds_done, f_ds, 66))) break;
-        if (next.more()) load_v(next);
-        if (ahead.more()) load_qk(ahead, buf);
+        if (next.on) load_v(next);
+        if (ahead.on) {
+          if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+          load_qk(ahead, buf);
+        }
         now = next;
         next = ahead;
-        if (ahead.more()) ahead.next(p, sh);
+        ahead = beyond;
       }
       if (!ok) {  // what is in flight ends before its memory goes
         const int never = 0;
@@ -502,12 +535,16 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       uint32_t f_empty = 1;
       while (w.more()) {
         double v[4], at = 0.0;
-        const int rows = w.rows();
+        const Ticket c = w.ticket();
+        if (c.begins && c.full && c.stage < 2 && c.slot_in >= 0) {  // the state that the part begins from
+          const float* from = p.states + ((size_t)c.slot_in * p.hv + c.head) * D * D;
+          for (int i = lane; i < D * D / 32; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + 32 * i));
+        }
         float g[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 4 * lane + i;
-          g[i] = r < rows ? decay_of(p.log_decay[(size_t)(w.t.row + w.c * CHUNK + r) * p.decay_stride + w.t.head]) : 0.f;
+          g[i] = r < c.rows ? decay_of(p.log_decay[(size_t)(c.row + r) * p.decay_stride + c.head]) : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -541,6 +578,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         const float whole = (float)end;
         const bool slow = whole > -0.5f;
         const float keep = slow ? expm1f(whole * LN2) : exp2f(whole);
+        w.next(p, sh);
         if (!wait(&sh.g_empty, f_empty, 67)) break;
         Gains& to = sh.g;
         const int r = 4 * lane;
@@ -552,9 +590,14 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           if (lane < 8 * q + 8)
             *reinterpret_cast<float4*>(&to.off[16 * q * (q + 1) + r]) = make_float4(off[q][0], off[q][1], off[q][2], off[q][3]);
         if (lane == 31) to.n = (float)n, to.f = (float)(end - n), to.keep = keep, to.slow = slow;
+        if (lane == 30) to.chunk = c;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_full);
-        w.next(p, sh);
+      }
+      if (wait(&sh.g_empty, f_empty, 67)) {  // the end
+        if (lane == 0) sh.g.chunk.on = false;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.g_full);
       }
     }
   } else {
@@ -594,16 +637,15 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       return p.states + ((size_t)slot * p.hv + head) * D * D + s_row * D + s_col;
     };
     // The state that the CTA's first part goes on from, from the CTAs before it.
-    const auto join = [&](const Part& t) {
-      const int from = blockIdx.x - (int)((t.c0 + run - 1) / run);  // the CTA that begins the chain
+    const auto join = [&](int chunks) {
+      const int from = blockIdx.x - (int)((chunks + run - 1) / run);  // the CTA that begins the chain
       if (tid < (int)blockIdx.x - from) {
         const uint64_t t0 = globaltimer();
         while (!load_acquire(&cp.flags[from + tid])) {
           __nanosleep(64);
           if (*abort) break;
           if (globaltimer() - t0 > LC_WAIT_NS) {
-            if (atomicOr(&p.st->flags, FLAG_TIMEOUT) == 0) p.st->timeout_site = 68;
-            *abort = 1;
+            *abort = 68;
             break;
           }
         }
@@ -626,88 +668,78 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       }
     };
 
-    Walk w;
-    if (a < b) w.begin(p, sh);
-    else w.stage = 3;
     float decay_n = 0.f, decay_f = 0.f;
-    for (int buf = 0; w.more() && !*abort; buf ^= 1) {
-      const bool full = w.t.full;
-      if (w.c == w.t.c0) {  // a part begins
+    for (int buf = 0; a < b; buf ^= 1) {
+      if (!wait(&sh.g_full, f_g, 70)) break;
+      const Ticket t = sh.g.chunk;
+      if (!t.on) break;
+      const bool full = t.full, slow = sh.g.slow;
+      const int rows = t.rows;
+      const float keep = sh.g.keep;
+      if (t.begins) {
         decay_n = decay_f = 0.f;
-        if (w.stage == 2) {
-          join(w.t);
+        if (t.stage == 2) {
+          join(t.before);
           if (*abort) break;
         } else {
 #pragma unroll
           for (int i = 0; i < NC; i += 4) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (full && w.t.slot_in >= 0) v = *reinterpret_cast<const float4*>(state_at(w.t.slot_in, w.t.head) + i);
+            if (full && t.slot_in >= 0) v = *reinterpret_cast<const float4*>(state_at(t.slot_in, t.head) + i);
             S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
           }
         }
-        if (full) write_state();
-        tc_fence_before();
-        arrive(&sh.s_ready);
       }
-      const int rows = w.rows();
-      if (!wait(&sh.g_full, f_g, 70)) break;
-      const float keep = sh.g.keep;
-      const bool slow = sh.g.slow;
+      if (full) write_state();
+      tc_fence_before();
+      arrive(&sh.s_ready);
       decay_n += sh.g.n;
       decay_f += sh.g.f;
       if (full) {
         // weights: scores times the decays between key and query, in two bf16
-        // parts over the scores' own columns.  32 keys at a time; those that
-        // all of the warp's rows are behind take a row's and a key's factor.
+        // parts over the scores' own columns.  Keys that all of the warp's rows
+        // are behind take a row's and a key's factor.
         if (!wait(&sh.qk_done, f_sc, 71)) break;
         tc_fence_after();
         const float rel = sh.g.rel[row], mine = ex2(rel);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int j0 = 64 * group + 32 * j;
-          const uint32_t at = lanes + L::T_S + j0;
-          uint32_t hi[16], lo[16];
-          if (j0 > 32 * quarter) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0;
-          } else {
-            uint32_t r[2][16];
-            tmem_ld16(at, r[0]);
-            tmem_ld16(at + 16, r[1]);
+        // The loops over blocks stay loops: unrolled, a chunk is some 80 KB of
+        // code, and fetching it takes longer than running it.
+#pragma unroll 1
+        for (int j0 = 64 * group; j0 < 64 * group + 64; j0 += 16) {
+          uint32_t w[16] = {};  // eight columns of first parts, eight of second ones
+          if (j0 < 32 * quarter + 32) {
+            uint32_t z[16];
+            tmem_ld16(lanes + L::T_S + j0, z);
             tmem_ld_wait();
-            tmem_ld_fence(r[0]);
-            tmem_ld_fence(r[1]);
-            if (j0 < 32 * quarter) {
-              const float* off = &sh.g.off[16 * quarter * (quarter - 1) + j0];
+            tmem_ld_fence(z);
+            const bool all = j0 < 32 * quarter;
+            const float* by = all ? &sh.g.off[16 * quarter * (quarter - 1) + j0] : &sh.g.rel[j0];
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const float4 f = *reinterpret_cast<const float4*>(off + 2 * i);
-                const uint32_t* z = &r[i >> 3][2 * (i & 7)];
-                float x0 = __uint_as_float(z[0]) * (mine * f.x), x1 = __uint_as_float(z[1]) * (mine * f.y);
-                float x2 = __uint_as_float(z[2]) * (mine * f.z), x3 = __uint_as_float(z[3]) * (mine * f.w);
-                hi[i] = take_bf16(x0, x1);
-                lo[i] = pack_bf16x2(x0, x1);
-                hi[i + 1] = take_bf16(x2, x3);
-                lo[i + 1] = pack_bf16x2(x2, x3);
+            for (int i = 0; i < 4; ++i) {
+              float4 f = *reinterpret_cast<const float4*>(by + 4 * i);
+              if (all) {
+                f.x *= mine, f.y *= mine, f.z *= mine, f.w *= mine;
+              } else {
+                const int j = j0 + 4 * i;
+                f.x = j <= row ? ex2(rel - f.x) : 0.f;
+                f.y = j + 1 <= row ? ex2(rel - f.y) : 0.f;
+                f.z = j + 2 <= row ? ex2(rel - f.z) : 0.f;
+                f.w = j + 3 <= row ? ex2(rel - f.w) : 0.f;
+                // a score that is not finite counts only where its key is seen
+                z[4 * i] = j <= row ? z[4 * i] : 0;
+                z[4 * i + 1] = j + 1 <= row ? z[4 * i + 1] : 0;
+                z[4 * i + 2] = j + 2 <= row ? z[4 * i + 2] : 0;
+                z[4 * i + 3] = j + 3 <= row ? z[4 * i + 3] : 0;
               }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const float4 f = *reinterpret_cast<const float4*>(&sh.g.rel[j0 + 2 * i]);
-                const uint32_t* z = &r[i >> 3][2 * (i & 7)];
-                float x0 = 2 * i <= lane ? __uint_as_float(z[0]) * ex2(rel - f.x) : 0.f;
-                float x1 = 2 * i + 1 <= lane ? __uint_as_float(z[1]) * ex2(rel - f.y) : 0.f;
-                float x2 = 2 * i + 2 <= lane ? __uint_as_float(z[2]) * ex2(rel - f.z) : 0.f;
-                float x3 = 2 * i + 3 <= lane ? __uint_as_float(z[3]) * ex2(rel - f.w) : 0.f;
-                hi[i] = take_bf16(x0, x1);
-                lo[i] = pack_bf16x2(x0, x1);
-                hi[i + 1] = take_bf16(x2, x3);
-                lo[i + 1] = pack_bf16x2(x2, x3);
-              }
+              float x0 = __uint_as_float(z[4 * i]) * f.x, x1 = __uint_as_float(z[4 * i + 1]) * f.y;
+              float x2 = __uint_as_float(z[4 * i + 2]) * f.z, x3 = __uint_as_float(z[4 * i + 3]) * f.w;
+              w[2 * i] = take_bf16(x0, x1);
+              w[8 + 2 * i] = pack_bf16x2(x0, x1);
+              w[2 * i + 1] = take_bf16(x2, x3);
+              w[9 + 2 * i] = pack_bf16x2(x2, x3);
             }
           }
-          tmem_st<16>(at, hi);
-          tmem_st<16>(at + 16, lo);
+          tmem_st<16>(lanes + L::T_S + j0, w);
         }
         tmem_st_wait();
       }
@@ -729,14 +761,16 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       // keys times the decays behind them, in three parts: one in the keys'
       // place, two in that of the state's
       {
-        const int r = tid >> 1, half = tid & 1;
+        const int r = tid % CHUNK, half = tid / CHUNK;  // neighbours hold neighbouring rows: no bank twice
         const float f = sh.g.last[r];
         unsigned char* kp = smem + L::K0 + buf * L::TILE;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
+        const auto off = [&](int i) {
           const int ch = half * (D / 16) + i;
-          const uint32_t off = (ch >> 3) * L::HALF + sw128_off(r, ch & 7);
-          uint4 v = *reinterpret_cast<const uint4*>(kp + off);
+          return (ch >> 3) * L::HALF + sw128_off(r, ch & 7);
+        };
+#pragma unroll 2
+        for (int i = 0; i < D / 16; ++i) {
+          uint4 v = *reinterpret_cast<const uint4*>(kp + off(i));
           if (r >= rows) v = make_uint4(0, 0, 0, 0);
           const uint32_t in[4] = {v.x, v.y, v.z, v.w};
           uint32_t o[3][4];
@@ -747,9 +781,9 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
             o[1][j] = take_bf16(x, y);
             o[2][j] = pack_bf16x2(x, y);
           }
-          *reinterpret_cast<uint4*>(kp + off) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-          *reinterpret_cast<uint4*>(smem + L::X0 + off) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
-          *reinterpret_cast<uint4*>(smem + L::X0 + L::TILE + off) = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
+          *reinterpret_cast<uint4*>(kp + off(i)) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+          *reinterpret_cast<uint4*>(smem + L::X0 + off(i)) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
+          *reinterpret_cast<uint4*>(smem + L::X0 + L::TILE + off(i)) = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
         }
       }
       fence_async_smem();
@@ -758,38 +792,42 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         const float first = sh.g.first[row];
         if (!wait(&sh.pv_done, f_pv, 75)) break;
         tc_fence_after();
-        const int row0 = w.t.row + w.c * CHUNK;
-        uint16_t* out = p.out + ((size_t)(row0 + row) * p.hv + w.t.head) * D;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          const int col = group * (D / 2) + 16 * j;
+        uint16_t* out = p.out + ((size_t)(t.row + row) * p.hv + t.head) * D;
+        unsigned char* stage = smem + L::Q0 + buf * L::TILE;  // the queries' place: no product reads them any more
+        const auto put = [&](int col, auto v) {  // to the row's channels col, ...
+          if (rows == CHUNK)
+            *reinterpret_cast<decltype(v)*>(stage + (col >> 6) * L::HALF + sw128_off(row, (col & 63) >> 3) + (col & 7) * 2) = v;
+          else if (row < rows)
+            *reinterpret_cast<decltype(v)*>(out + col) = v;
+        };
+        float finite = 0.f;  // NaN: a value that is not finite has met the rows before its own
+#pragma unroll 1
+        for (int col = group * (D / 2); col < (group + 1) * (D / 2); col += 16) {
           uint32_t x[16], y[16];
           tmem_ld16(lanes + L::T_SQ + col, x);
           tmem_ld16(lanes + L::T_PV + col, y);
           tmem_ld_wait();
           tmem_ld_fence(x);
           tmem_ld_fence(y);
-          float o[16], finite = 0.f;
+          uint32_t o[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            finite = fmaf(__uint_as_float(y[i]), 0.f, finite);
-            o[i] = p.scale * fmaf(first, __uint_as_float(x[i]), __uint_as_float(y[i]));
+          for (int i = 0; i < 16; i += 2) {
+            const float u = __uint_as_float(y[i]), v = __uint_as_float(y[i + 1]);
+            finite = fmaf(u, 0.f, fmaf(v, 0.f, finite));
+            o[i / 2] = pack_bf16x2(p.scale * fmaf(first, __uint_as_float(x[i]), u), p.scale * fmaf(first, __uint_as_float(x[i + 1]), v));
           }
-          if (finite != 0.f && row < rows) {  // NaN: a value that is not finite has met the rows before its own
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (!isfinite(__uint_as_float(y[i])))
-                o[i] = p.scale * fmaf(first, __uint_as_float(x[i]), weighted_values(p, D, row0, row, w.t.head, col + i));
-          }
-#pragma unroll
-          for (int i = 0; i < 16; i += 8) {
-            const uint4 v = make_uint4(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]),
-                                       pack_bf16x2(o[i + 4], o[i + 5]), pack_bf16x2(o[i + 6], o[i + 7]));
-            const int ch = (col + i) >> 3;
-            if (rows == CHUNK)  // over the queries, which no product reads any more
-              *reinterpret_cast<uint4*>(smem + L::Q0 + buf * L::TILE + (ch >> 3) * L::HALF + sw128_off(row, ch & 7)) = v;
-            else if (row < rows)
-              *reinterpret_cast<uint4*>(out + col + i) = v;
+          put(col, make_uint4(o[0], o[1], o[2], o[3]));
+          put(col + 8, make_uint4(o[4], o[5], o[6], o[7]));
+        }
+        if (__any_sync(~0u, finite != 0.f && row < rows)) {
+#pragma unroll 1
+          for (int col = group * (D / 2); col < (group + 1) * (D / 2); ++col) {
+            uint32_t x, y;
+            tmem_ld1(lanes + L::T_SQ + col, x);
+            tmem_ld1(lanes + L::T_PV + col, y);
+            if (!isfinite(__uint_as_float(y)) && row < rows)
+              put(col, f2bf(p.scale * fmaf(first, __uint_as_float(x), weighted_values(p, D, t.row, row, t.head, col))));
+            __syncwarp();
           }
         }
         fence_async_smem();
@@ -811,11 +849,8 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           s = fmaf(s, keep, slow ? s + __uint_as_float(x[i]) : __uint_as_float(x[i]));
         }
       }
-      if (w.c + 1 < w.t.c1) {
-        if (full) write_state();
-        tc_fence_before();
-        arrive(&sh.s_ready);
-      } else if (w.stage == 0) {  // others go on from here
+      if (!t.ends) continue;
+      if (t.stage == 0) {  // others go on from here
         float* to = cp.pub + blockIdx.x * pub_floats(D);
 #pragma unroll
         for (int i = 0; i < NC; i += 4)
@@ -825,18 +860,18 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         sync();
         if (tid == 0 && !((p.st->stall & MOE_STALL_GRID_BARRIER) && blockIdx.x == 0))
           store_release(&cp.flags[blockIdx.x], 1u);
-      } else if (w.t.c1 == w.t.nc && w.t.slot_out >= 0) {
+      } else if (t.closes && t.slot_out >= 0) {
 #pragma unroll
         for (int i = 0; i < NC; i += 4)
-          *reinterpret_cast<float4*>(state_at(w.t.slot_out, w.t.head) + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+          *reinterpret_cast<float4*>(state_at(t.slot_out, t.head) + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
       }
-      w.next(p, sh);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == W_ISSUE) tmem_dealloc(tmem, 512);
+  if (tid == 0 && sh.abort && atomicOr(&p.st->flags, FLAG_TIMEOUT) == 0) p.st->timeout_site = sh.abort;
   // the last CTA clears what the next call counts on
   if (tid == 0) {
     __threadfence();
