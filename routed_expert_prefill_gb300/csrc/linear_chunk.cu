@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         tc_fence_after();
         if (elect_one()) {
           const uint64_t qb = qd + buf * BUF, kb = kd + buf * BUF;
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < D / 16; ++k)
             mma_bf16(tmem + L::T_S, qb + step(k), kb + step(k), idesc(128, 128, false, false), k > 0);
           mma_commit(&sh.qk_done);
@@ -450,9 +450,9 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         if (full) {
           if (elect_one()) {
             const uint64_t qb = qd + buf * BUF;
-#pragma unroll
+#pragma unroll 1
             for (int part = 0; part < 2; ++part)
-#pragma unroll
+#pragma unroll 1
               for (int k = 0; k < D / 16; ++k)
                 mma_bf16(tmem + L::T_SQ, qb + step(k), sr + (part * (L::S_PART >> 4) + k * ROWS16), idesc(128, D, false, true),
                          part + k > 0);
@@ -466,9 +466,9 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           if (!(ok = wait(&sh.p_ready, f_p, 63))) break;
           tc_fence_after();
           if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
             for (int part = 0; part < 2; ++part)
-#pragma unroll
+#pragma unroll 1
               for (int k = 0; k < CHUNK / 16; ++k)
                 mma_bf16_ta(tmem + L::T_PV, tmem + L::T_S + 16 * k + 8 * part, vr + k * ROWS16,
                             idesc(128, D, false, true), part + k > 0);
@@ -479,9 +479,9 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         if (!(ok = wait(&sh.k_ready, f_k, 64))) break;
         if (elect_one()) {
           const uint64_t kb = kr + buf * BUF;
-#pragma unroll
+#pragma unroll 1
           for (int part = 0; part < 3; ++part)
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < CHUNK / 16; ++k)
               mma_bf16(tmem + L::T_DS, (part == 0 ? kb : xr + (part - 1) * BUF) + k * ROWS16, vr + k * ROWS16,
                        idesc(128, D, true, true), part + k > 0);
