@@ -15,10 +15,11 @@ namespace {
 using namespace tc;
 
 constexpr int CHUNK = 128;
-// Warps: 0-7 compute, 8 brings the tiles and issues the products, 9 works out
-// the decays, 10 and 11 fill the warpgroup.  Registers: 384 * 168 at launch,
-// 256 * 224 + 128 * 56 after the split.
-constexpr int LC_COMPUTE = 256, LC_THREADS = 384, W_ISSUE = 8, W_GAIN = 9;
+// Warps: 0-7 compute, 8 issues the products, 9 works out the decays, 10 brings
+// the tiles, 11 takes the results away.  Registers: 384 * 168 at launch, 256 *
+// 224 + 128 * 56 after the split.
+constexpr int LC_COMPUTE = 256, LC_THREADS = 384, W_ISSUE = 8, W_GAIN = 9, W_LOAD = 10,
+              W_STORE = 11;
 constexpr int LC_REGS = 224, LC_REGS_REST = 56;
 constexpr uint64_t LC_WAIT_NS = 2000000000ull;
 constexpr float LN2 = 0.6931471805599453f;
@@ -67,14 +68,13 @@ struct Ticket {
 };
 
 // The decays of a chunk's rows: G_i is the log2 of the product of rows 0 .. i's.
-struct Gains {
+struct alignas(16) Gains {  // read four at a time
   float rel[CHUNK];    // G_i less that of the first of its 32 rows
   float last[CHUNK];   // 2^(G_127 - G_i)
   float first[CHUNK];  // 2^G_i
   float off[192];      // rows 32 q .. of q = 1, 2, 3, for i < 32 q: 2^(G_32q - G_i)
   float n, f;          // G_127, whole part and rest
-  float keep;          // what a state is multiplied by: 2^G_127, less 1 if slow
-  int slow;
+  float keep, slow;    // a state is multiplied by keep + slow = 2^G_127; slow is 1 for slow decays, else 0
   Ticket chunk;
 };
 
@@ -82,6 +82,7 @@ struct LcShared {
   uint64_t qk_full[2], v_full, g_full, g_empty;
   uint64_t qk_done, sq_done, pv_done, ds_done;  // products
   uint64_t s_ready, p_ready, k_ready, o_ready;  // their operands, and the results
+  uint64_t q_free;                              // the results have been read
   uint64_t drain;
   Gains g;
   Part first, last;
@@ -136,11 +137,33 @@ __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
 }
 
-// Two fp32 values as a bf16 pair; what is left of them takes their place.
-__device__ __forceinline__ uint32_t take_bf16(float& a, float& b) {
-  const uint32_t w = pack_bf16x2(a, b);
-  a -= bf16lo(w);
-  b -= bf16hi(w);
+// Two fp32 values at a time.
+__device__ __forceinline__ unsigned long long bits2(float2 v) { return *reinterpret_cast<unsigned long long*>(&v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 pair(const uint32_t* r) { return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
+
+// Two values as a bf16 pair, rounded; what is left of them takes their place.
+__device__ __forceinline__ uint32_t take_rounded(float2& v) {
+  const uint32_t w = pack_bf16x2(v.x, v.y);
+  v = fma2(make_float2(bf16lo(w), bf16hi(w)), both(-1.f), v);
+  return w;
+}
+// The same, cut to 8 bits: after two of these 8 are left, so that three parts are the value.
+__device__ __forceinline__ uint32_t cut(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
+__device__ __forceinline__ uint32_t take_cut(float2& v) {
+  const uint32_t w = cut(v);
+  v = fma2(make_float2(__uint_as_float(__float_as_uint(v.x) & 0xFFFF0000u), __uint_as_float(__float_as_uint(v.y) & 0xFFFF0000u)),
+           both(-1.f), v);
   return w;
 }
 
@@ -295,7 +318,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
     tmem_alloc(&sh.tmem, 512);
     if (lane == 0) {
       for (uint64_t* b : {&sh.qk_full[0], &sh.qk_full[1], &sh.v_full, &sh.g_full, &sh.qk_done, &sh.sq_done, &sh.pv_done,
-                          &sh.ds_done, &sh.drain})
+                          &sh.ds_done, &sh.drain, &sh.q_free})
         mbar_init(b, 1);
       for (uint64_t* b : {&sh.g_empty, &sh.s_ready, &sh.p_ready, &sh.k_ready, &sh.o_ready}) mbar_init(b, LC_COMPUTE / 32);
       fence_mbar_init();
@@ -384,7 +407,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
   if (warp >= W_ISSUE) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LC_REGS_REST));
     if (warp == W_ISSUE && a < b) {
-      // ---- tiles and products
+      // ---- products
       const uint32_t sb = smem_u32(smem);
       // descriptors: tiles of queries and keys with channels as the inner dimension, of keys, values and states with rows
       constexpr uint32_t BUF = L::TILE >> 4, ROWS16 = 2048 >> 4;
@@ -393,30 +416,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       const uint64_t kr = desc_rows(sb + L::K0, D == 128 ? L::HALF : 0), xr = desc_rows(sb + L::X0, D == 128 ? L::HALF : 0);
       const uint64_t vr = desc_rows(sb + L::V0, L::HALF), sr = desc_rows(sb + L::X0, L::S_HALF);
       const auto step = [](int k) { return (uint32_t)((k >> 2) * L::HALF + (k & 3) * 32) >> 4; };
-      uint32_t f_qk[2] = {}, f_v = 0, f_s = 0, f_p = 0, f_k = 0, f_o = 0, f_ds = 0, out_qk = 0, out_v = 0;
-      const auto load = [&](const CUtensorMap* tm, int col, int row, int at, uint64_t* bar) {
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) tma_load_2d(smem + at + h * L::HALF, tm, col + 64 * h, row, bar);
-      };
-      const int heads = p.hv / p.hk;
-      const auto load_qk = [&](const Ticket& c, int buf) {
-        if (elect_one()) {
-          const int col = c.head / heads * D;
-          mbar_arrive_expect_tx(&sh.qk_full[buf], c.full ? 2 * L::TILE : L::TILE);
-          if (c.full) load(&tm_q, col, c.row, L::Q0 + buf * L::TILE, &sh.qk_full[buf]);
-          load(&tm_k, col, c.row, L::K0 + buf * L::TILE, &sh.qk_full[buf]);
-        }
-        __syncwarp();
-        out_qk |= 1u << buf;
-      };
-      const auto load_v = [&](const Ticket& c) {
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&sh.v_full, L::TILE);
-          load(&tm_v, c.head * D, c.row, L::V0, &sh.v_full);
-        }
-        __syncwarp();
-        out_v = 1;
-      };
+      uint32_t f_qk[2] = {}, f_v = 0, f_s = 0, f_p = 0, f_k = 0;
       const auto scores = [&](int buf) {
         tc_fence_after();
         if (elect_one()) {
@@ -428,23 +428,15 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         }
         __syncwarp();
       };
-      Walk w;  // two chunks ahead of the products
+      Walk w;  // a chunk ahead of the products
       w.begin(p, sh);
-      Ticket now = w.ticket(), next, ahead;
-      const auto advance = [&]() {
-        if (w.more()) w.next(p, sh);
-        return w.ticket();
-      };
-      load_qk(now, 0);
-      load_v(now);
-      next = advance();
-      if (next.on) load_qk(next, 1);
-      ahead = advance();
+      Ticket now = w.ticket();
       bool ok = wait(&sh.qk_full[0], f_qk[0], 60);
-      out_qk &= ~1u;
       if (ok && now.full) scores(0);
       for (int buf = 0; ok && now.on; buf ^= 1) {
         const bool full = now.full;
+        w.next(p, sh);
+        const Ticket next = w.ticket();
         if (!(ok = wait(&sh.s_ready, f_s, 61))) break;
         tc_fence_after();
         if (full) {
@@ -461,7 +453,6 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           __syncwarp();
         }
         if (!(ok = wait(&sh.v_full, f_v, 62))) break;
-        out_v = 0;
         if (full) {
           if (!(ok = wait(&sh.p_ready, f_p, 63))) break;
           tc_fence_after();
@@ -490,41 +481,92 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         __syncwarp();
         if (next.on) {  // its scores take the weights' place: products run in order
           if (!(ok = wait(&sh.qk_full[buf ^ 1], f_qk[buf ^ 1], 60))) break;
-          out_qk &= ~(1u << (buf ^ 1));
           if (next.full) scores(buf ^ 1);
         }
-        const Ticket beyond = advance();
-        if (full) {
-          if (!(ok = wait(&sh.o_ready, f_o, 65))) break;
-          if (now.rows == CHUNK) {
-            if (elect_one()) {
-#pragma unroll
-              for (int h = 0; h < D / 64; ++h)
-                tma_store_2d(&tm_o, now.head * D + 64 * h, now.row, smem + L::Q0 + buf * L::TILE + h * L::HALF);
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
-            __syncwarp();
-          }
-        }
-        if (!(ok = wait(&sh.ds_done, f_ds, 66))) break;
-        if (next.on) load_v(next);
-        if (ahead.on) {
-          if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          __syncwarp();
-          load_qk(ahead, buf);
-        }
         now = next;
-        next = ahead;
-        ahead = beyond;
       }
       if (!ok) {  // what is in flight ends before its memory goes
         const int never = 0;
         if (elect_one()) mma_commit(&sh.drain);
         __syncwarp();
         mbar_wait(&sh.drain, 0, &never, LC_WAIT_NS);
+      }
+    } else if (warp == W_LOAD && a < b) {
+      // ---- queries and keys two chunks ahead, values one
+      uint32_t f_ds = 0, f_q = 0;
+      const auto load = [&](const CUtensorMap* tm, int col, int row, int at, uint64_t* bar) {
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) tma_load_2d(smem + at + h * L::HALF, tm, col + 64 * h, row, bar);
+      };
+      const int heads = p.hv / p.hk;
+      uint32_t n_qk = 0, n_v = 0;
+      const auto load_qk = [&](const Ticket& c) {
+        const int buf = n_qk++ & 1;
+        if (elect_one()) {
+          const int col = c.head / heads * D;
+          mbar_arrive_expect_tx(&sh.qk_full[buf], c.full ? 2 * L::TILE : L::TILE);
+          load(&tm_k, col, c.row, L::K0 + buf * L::TILE, &sh.qk_full[buf]);
+          if (c.full) load(&tm_q, col, c.row, L::Q0 + buf * L::TILE, &sh.qk_full[buf]);
+        }
+        __syncwarp();
+      };
+      const auto load_v = [&](const Ticket& c) {
+        ++n_v;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sh.v_full, L::TILE);
+          load(&tm_v, c.head * D, c.row, L::V0, &sh.v_full);
+        }
+        __syncwarp();
+      };
+      Walk w;
+      w.begin(p, sh);
+      const auto advance = [&]() {
+        if (w.more()) w.next(p, sh);
+        return w.ticket();
+      };
+      Ticket now = w.ticket();
+      load_qk(now);
+      load_v(now);
+      Ticket next = advance();
+      if (next.on) load_qk(next);
+      bool ok = true;
+      while (now.on) {
+        const Ticket ahead = advance();
+        if (!(ok = wait(&sh.ds_done, f_ds, 66))) break;
+        if (next.on) load_v(next);
+        if (now.full && !(ok = wait(&sh.q_free, f_q, 69))) break;
+        if (ahead.on) load_qk(ahead);
+        now = next;
+        next = ahead;
+      }
+      if (!ok) {  // what is in flight ends before its memory goes: the last tiles asked for
+        const int never = 0;
         for (int i = 0; i < 2; ++i)
-          if (out_qk >> i & 1) mbar_wait(&sh.qk_full[i], f_qk[i], &never, LC_WAIT_NS);
-        if (out_v) mbar_wait(&sh.v_full, f_v, &never, LC_WAIT_NS);
+          if (n_qk > (uint32_t)i) mbar_wait(&sh.qk_full[i], ((n_qk - 1 - i) / 2) & 1, &never, LC_WAIT_NS);
+        mbar_wait(&sh.v_full, (n_v - 1) & 1, &never, LC_WAIT_NS);
+      }
+    } else if (warp == W_STORE && a < b) {
+      // ---- results, from the queries' place
+      Walk w;
+      w.begin(p, sh);
+      uint32_t f_o = 0;
+      for (int buf = 0; w.more(); buf ^= 1) {
+        const Ticket c = w.ticket();
+        if (c.full) {
+          if (!wait(&sh.o_ready, f_o, 65)) break;
+          if (elect_one()) {
+            if (c.rows == CHUNK) {
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+                tma_store_2d(&tm_o, c.head * D + 64 * h, c.row, smem + L::Q0 + buf * L::TILE + h * L::HALF);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            mbar_arrive(&sh.q_free);
+          }
+          __syncwarp();
+        }
+        w.next(p, sh);
       }
       if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       __syncwarp();
@@ -578,18 +620,25 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         const float whole = (float)end;
         const bool slow = whole > -0.5f;
         const float keep = slow ? expm1f(whole * LN2) : exp2f(whole);
+        float first[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          first[i] = ex2((float)v[i]);
+          // worked out before the wait, not behind it
+          asm volatile("" : "+f"(rel[i]), "+f"(last[i]), "+f"(first[i]), "+f"(off[0][i]), "+f"(off[1][i]), "+f"(off[2][i]));
+        }
         w.next(p, sh);
         if (!wait(&sh.g_empty, f_empty, 67)) break;
         Gains& to = sh.g;
         const int r = 4 * lane;
         *reinterpret_cast<float4*>(&to.rel[r]) = make_float4(rel[0], rel[1], rel[2], rel[3]);
         *reinterpret_cast<float4*>(&to.last[r]) = make_float4(last[0], last[1], last[2], last[3]);
-        *reinterpret_cast<float4*>(&to.first[r]) = make_float4(ex2((float)v[0]), ex2((float)v[1]), ex2((float)v[2]), ex2((float)v[3]));
+        *reinterpret_cast<float4*>(&to.first[r]) = make_float4(first[0], first[1], first[2], first[3]);
 #pragma unroll
         for (int q = 0; q < 3; ++q)
           if (lane < 8 * q + 8)
             *reinterpret_cast<float4*>(&to.off[16 * q * (q + 1) + r]) = make_float4(off[q][0], off[q][1], off[q][2], off[q][3]);
-        if (lane == 31) to.n = (float)n, to.f = (float)(end - n), to.keep = keep, to.slow = slow;
+        if (lane == 31) to.n = (float)n, to.f = (float)(end - n), to.keep = keep, to.slow = slow ? 1.f : 0.f;
         if (lane == 30) to.chunk = c;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_full);
@@ -622,9 +671,9 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float u = S[c + 2 * i], v = S[c + 2 * i + 1];
-          hi[i] = take_bf16(u, v);
-          lo[i] = pack_bf16x2(u, v);
+          float2 v = make_float2(S[c + 2 * i], S[c + 2 * i + 1]);
+          hi[i] = take_rounded(v);
+          lo[i] = pack_bf16x2(v.x, v.y);
         }
         const int col = s_col + c;
         unsigned char* to = smem + L::X0 + (col >> 6) * L::S_HALF + sw128_off(s_row, (col & 63) >> 3);
@@ -673,9 +722,9 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       if (!wait(&sh.g_full, f_g, 70)) break;
       const Ticket t = sh.g.chunk;
       if (!t.on) break;
-      const bool full = t.full, slow = sh.g.slow;
+      const bool full = t.full;
       const int rows = t.rows;
-      const float keep = sh.g.keep;
+      const float keep = sh.g.keep, slow = sh.g.slow;
       if (t.begins) {
         decay_n = decay_f = 0.f;
         if (t.stage == 2) {
@@ -718,7 +767,8 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
             for (int i = 0; i < 4; ++i) {
               float4 f = *reinterpret_cast<const float4*>(by + 4 * i);
               if (all) {
-                f.x *= mine, f.y *= mine, f.z *= mine, f.w *= mine;
+                const float2 u = mul2(make_float2(f.x, f.y), both(mine)), v = mul2(make_float2(f.z, f.w), both(mine));
+                f = make_float4(u.x, u.y, v.x, v.y);
               } else {
                 const int j = j0 + 4 * i;
                 f.x = j <= row ? ex2(rel - f.x) : 0.f;
@@ -731,12 +781,11 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
                 z[4 * i + 2] = j + 2 <= row ? z[4 * i + 2] : 0;
                 z[4 * i + 3] = j + 3 <= row ? z[4 * i + 3] : 0;
               }
-              float x0 = __uint_as_float(z[4 * i]) * f.x, x1 = __uint_as_float(z[4 * i + 1]) * f.y;
-              float x2 = __uint_as_float(z[4 * i + 2]) * f.z, x3 = __uint_as_float(z[4 * i + 3]) * f.w;
-              w[2 * i] = take_bf16(x0, x1);
-              w[8 + 2 * i] = pack_bf16x2(x0, x1);
-              w[2 * i + 1] = take_bf16(x2, x3);
-              w[9 + 2 * i] = pack_bf16x2(x2, x3);
+              float2 u = mul2(pair(z + 4 * i), make_float2(f.x, f.y)), v = mul2(pair(z + 4 * i + 2), make_float2(f.z, f.w));
+              w[2 * i] = take_rounded(u);
+              w[8 + 2 * i] = pack_bf16x2(u.x, u.y);
+              w[2 * i + 1] = take_rounded(v);
+              w[9 + 2 * i] = pack_bf16x2(v.x, v.y);
             }
           }
           tmem_st<16>(lanes + L::T_S + j0, w);
@@ -758,8 +807,8 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         arrive(&sh.p_ready);
         if (!wait(&sh.sq_done, f_sq, 74)) break;  // the state's operand is free
       }
-      // keys times the decays behind them, in three parts: one in the keys'
-      // place, two in that of the state's
+      // keys times the decays behind them, in three parts of 8 bits: one in the
+      // keys' place, two in that of the state's
       {
         const int r = tid % CHUNK, half = tid / CHUNK;  // neighbours hold neighbouring rows: no bank twice
         const float f = sh.g.last[r];
@@ -776,10 +825,10 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           uint32_t o[3][4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float x = bf16lo(in[j]) * f, y = bf16hi(in[j]) * f;
-            o[0][j] = take_bf16(x, y);
-            o[1][j] = take_bf16(x, y);
-            o[2][j] = pack_bf16x2(x, y);
+            float2 x = mul2(make_float2(bf16lo(in[j]), bf16hi(in[j])), both(f));
+            o[0][j] = take_cut(x);
+            o[1][j] = take_cut(x);
+            o[2][j] = cut(x);
           }
           *reinterpret_cast<uint4*>(kp + off(i)) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
           *reinterpret_cast<uint4*>(smem + L::X0 + off(i)) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
@@ -800,7 +849,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           else if (row < rows)
             *reinterpret_cast<decltype(v)*>(out + col) = v;
         };
-        float finite = 0.f;  // NaN: a value that is not finite has met the rows before its own
+        float2 finite = both(0.f);  // NaN: a value that is not finite has met the rows before its own
 #pragma unroll 1
         for (int col = group * (D / 2); col < (group + 1) * (D / 2); col += 16) {
           uint32_t x[16], y[16];
@@ -812,14 +861,14 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           uint32_t o[8];
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float u = __uint_as_float(y[i]), v = __uint_as_float(y[i + 1]);
-            finite = fmaf(u, 0.f, fmaf(v, 0.f, finite));
-            o[i / 2] = pack_bf16x2(p.scale * fmaf(first, __uint_as_float(x[i]), u), p.scale * fmaf(first, __uint_as_float(x[i + 1]), v));
+            finite = fma2(pair(y + i), both(0.f), finite);
+            const float2 v = mul2(fma2(pair(x + i), both(first), pair(y + i)), both(p.scale));
+            o[i / 2] = pack_bf16x2(v.x, v.y);
           }
           put(col, make_uint4(o[0], o[1], o[2], o[3]));
           put(col + 8, make_uint4(o[4], o[5], o[6], o[7]));
         }
-        if (__any_sync(~0u, finite != 0.f && row < rows)) {
+        if (__any_sync(~0u, finite.x + finite.y != 0.f && row < rows)) {
 #pragma unroll 1
           for (int col = group * (D / 2); col < (group + 1) * (D / 2); ++col) {
             uint32_t x, y;
@@ -844,9 +893,10 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         tmem_ld_wait();
         tmem_ld_fence(x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float& s = S[16 * j + i];
-          s = fmaf(s, keep, slow ? s + __uint_as_float(x[i]) : __uint_as_float(x[i]));
+        for (int i = 0; i < 16; i += 2) {
+          float* s = S + 16 * j + i;
+          const float2 v = make_float2(s[0], s[1]), w = fma2(v, both(slow), fma2(v, both(keep), pair(x + i)));
+          s[0] = w.x, s[1] = w.y;
         }
       }
       if (!t.ends) continue;
