@@ -22,10 +22,11 @@ constexpr int LC_COMPUTE = 256, LC_THREADS = 384, W_ISSUE = 8, W_GAIN = 9, W_LOA
               W_STORE = 11;
 constexpr int LC_REGS = 224, LC_REGS_REST = 56;
 constexpr uint64_t LC_WAIT_NS = 2000000000ull;
-constexpr float LN2 = 0.6931471805599453f;
+constexpr float LOG2E = 1.44269502f, LOG2E_REST = 1.92596299e-8f, LN2 = 0.693147181f;
+constexpr float NOT_A_NUMBER = __builtin_nanf("");
 // A row's log2 decay as it counts: below it the state of one row is 0 in the
 // next whatever it was (2^-512 of an fp32 number).
-constexpr double LEAST = -512.0;
+constexpr float LEAST = -512.f;
 
 // What one CTA leaves for those that go on with its last chain: the state
 // behind its part (or, if its part does not begin the chain, what the part
@@ -571,63 +572,77 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       __syncwarp();
     } else if (warp == W_GAIN && a < b) {
-      // ---- decays: four rows a lane, a chunk ahead in registers
-      Walk w;
-      w.begin(p, sh);
-      uint32_t f_empty = 1;
-      while (w.more()) {
-        double v[4], at = 0.0;
-        const Ticket c = w.ticket();
+      // ---- decays: four rows a lane, a chunk ahead in registers, their values another one ahead.
+      // G as whole numbers of 2^-40: sums and differences are exact (in fp64 they took 6000 clocks a chunk).
+      constexpr float UNIT = 0x1p40f, PER_UNIT = 0x1p-40f;
+      const auto load = [&](const Ticket& c, float (&g)[4]) {
+        if (!c.on) return;
         if (c.begins && c.full && c.stage < 2 && c.slot_in >= 0) {  // the state that the part begins from
           const float* from = p.states + ((size_t)c.slot_in * p.hv + c.head) * D * D;
           for (int i = lane; i < D * D / 32; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + 32 * i));
         }
-        float g[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 4 * lane + i;
           g[i] = r < c.rows ? decay_of(p.log_decay[(size_t)(c.row + r) * p.decay_stride + c.head]) : 0.f;
         }
+      };
+      Walk w;
+      w.begin(p, sh);
+      uint32_t f_empty = 1;
+      Ticket c = w.ticket();
+      float g[4];
+      load(c, g);
+      while (c.on) {
+        w.next(p, sh);
+        const Ticket ahead = w.ticket();
+        float later[4] = {};
+        load(ahead, later);
+        long long v[4], at = 0;
+        bool nan = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const double l = (double)g[i] * 1.4426950408889634;
-          at += l < LEAST ? LEAST : l;
+          // log2(e) in two parts, the product's rounding kept
+          const float l = g[i] * LOG2E, rest = fmaf(g[i], LOG2E_REST, fmaf(g[i], LOG2E, -l));
+          nan |= g[i] != g[i];
+          at += l < LEAST ? (long long)LEAST * (1ll << 40) : __float2ll_rn(l * UNIT) + __float2ll_rn(rest * UNIT);
           v[i] = at;
         }
-        double in = at;
+        long long in = at;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const double u = __shfl_up_sync(~0u, in, o);
+          const long long u = __shfl_up_sync(~0u, in, o);
           if (lane >= o) in += u;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] += in - at;
-        const double end = __shfl_sync(~0u, v[3], 31);
-        const double ref0 = __shfl_sync(~0u, v[0], lane & 24);
-        float rel[4], last[4], off[3][4];
+        const auto value = [&](long long x) { return __ll2float_rn(x) * PER_UNIT; };
+        const long long end = __shfl_sync(~0u, v[3], 31);
+        const long long ref0 = __shfl_sync(~0u, v[0], lane & 24);
+        // a row whose decay is NaN, and those behind it
+        const uint32_t nans = __ballot_sync(~0u, nan);
+        bool bad[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bad[i] = (nans & ((1u << lane) - 1)) || (i ? bad[i - 1] : false) || g[i] != g[i];
+        float rel[4], last[4], first[4], off[3][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          rel[i] = (float)(v[i] - ref0);
-          last[i] = ex2((float)(end - v[i]));
+          rel[i] = value(v[i] - ref0);
+          last[i] = nans ? NOT_A_NUMBER : ex2(value(end - v[i]));
+          first[i] = bad[i] ? NOT_A_NUMBER : ex2(value(v[i]));
         }
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
-          const double ref = __shfl_sync(~0u, v[0], 8 * q + 8);
+          const long long ref = __shfl_sync(~0u, v[0], 8 * q + 8);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) off[q][i] = ex2((float)(ref - v[i]));
+          for (int i = 0; i < 4; ++i) off[q][i] = ex2(value(ref - v[i]));
         }
-        const double n = rint(end);
-        const float whole = (float)end;
+        const float whole = value(end);
         const bool slow = whole > -0.5f;
-        const float keep = slow ? expm1f(whole * LN2) : exp2f(whole);
-        float first[4];
+        float keep = nans ? NOT_A_NUMBER : slow ? expm1f(whole * LN2) : exp2f(whole);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          first[i] = ex2((float)v[i]);
-          // worked out before the wait, not behind it
-          asm volatile("" : "+f"(rel[i]), "+f"(last[i]), "+f"(first[i]), "+f"(off[0][i]), "+f"(off[1][i]), "+f"(off[2][i]));
-        }
-        w.next(p, sh);
+        for (int i = 0; i < 4; ++i)  // worked out before the wait, not behind it
+          asm volatile("" : "+f"(rel[i]), "+f"(last[i]), "+f"(first[i]), "+f"(off[0][i]), "+f"(off[1][i]), "+f"(off[2][i]), "+f"(keep));
         if (!wait(&sh.g_empty, f_empty, 67)) break;
         Gains& to = sh.g;
         const int r = 4 * lane;
@@ -638,10 +653,19 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         for (int q = 0; q < 3; ++q)
           if (lane < 8 * q + 8)
             *reinterpret_cast<float4*>(&to.off[16 * q * (q + 1) + r]) = make_float4(off[q][0], off[q][1], off[q][2], off[q][3]);
-        if (lane == 31) to.n = (float)n, to.f = (float)(end - n), to.keep = keep, to.slow = slow ? 1.f : 0.f;
+        if (lane == 31) {
+          const long long n = end >> 40;
+          to.n = nans ? NOT_A_NUMBER : (float)n;
+          to.f = value(end - (n << 40));
+          to.keep = keep;
+          to.slow = slow ? 1.f : 0.f;
+        }
         if (lane == 30) to.chunk = c;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_full);
+        c = ahead;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = later[i];
       }
       if (wait(&sh.g_empty, f_empty, 67)) {  // the end
         if (lane == 0) sh.g.chunk.on = false;
