@@ -17,10 +17,10 @@ using namespace tc;
 constexpr int CHUNK = 128;
 // Warps: 0-7 compute, 8 issues the products, 9 works out the decays, 10 brings
 // the tiles, 11 takes the results away.  Registers: 384 * 168 at launch, 256 *
-// 224 + 128 * 56 after the split.
+// 208 + 128 * 88 after the split.
 constexpr int LC_COMPUTE = 256, LC_THREADS = 384, W_ISSUE = 8, W_GAIN = 9, W_LOAD = 10,
               W_STORE = 11;
-constexpr int LC_REGS = 224, LC_REGS_REST = 56;
+constexpr int LC_REGS = 208, LC_REGS_REST = 88;
 constexpr uint64_t LC_WAIT_NS = 2000000000ull;
 constexpr float LOG2E = 1.44269502f, LOG2E_REST = 1.92596299e-8f, LN2 = 0.693147181f;
 constexpr float NOT_A_NUMBER = __builtin_nanf("");
@@ -222,7 +222,7 @@ struct Walk {
       next_part(p, sh);
     }
   }
-  __device__ __noinline__ void next_part(const LinearParams& p, const LcShared& sh) {
+  __device__ __forceinline__ void next_part(const LinearParams& p, const LcShared& sh) {
     while (stage < 2 && left) {
       const bool is_last = s == sh.last.s && head == sh.last.head;
       bool whole;
