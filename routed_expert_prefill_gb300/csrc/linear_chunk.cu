@@ -30,7 +30,7 @@ constexpr float LEAST = -512.f;
 
 // What one CTA leaves for those that go on with its last chain: the state
 // behind its part (or, if its part does not begin the chain, what the part
-// adds) and the part's decay.
+// adds) in the order in which its threads hold it, and the part's decay.
 constexpr int PUB_EXTRA = 64;  // floats behind the state: log2 of the decay, whole part and rest
 __host__ __device__ constexpr size_t pub_floats(int d) { return (size_t)d * d + PUB_EXTRA; }
 
@@ -725,12 +725,13 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       }
       sync();
       if (*abort) return;
+#pragma unroll 1
       for (int b = from; b < (int)blockIdx.x; ++b) {
         const float* at = cp.pub + b * pub_floats(D);
         const float f = b == from ? 0.f : exp2f(__ldcg(at + D * D) + __ldcg(at + D * D + 1));
 #pragma unroll
         for (int i = 0; i < NC; i += 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(at + s_row * D + s_col + i));
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(at + i * LC_COMPUTE + 4 * tid));
           if (b == from) {
             S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
           } else {
@@ -778,41 +779,43 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         // The loops over blocks stay loops: unrolled, a chunk is some 80 KB of
         // code, and fetching it takes longer than running it.
 #pragma unroll 1
-        for (int j0 = 64 * group; j0 < 64 * group + 64; j0 += 16) {
-          uint32_t w[16] = {};  // eight columns of first parts, eight of second ones
-          if (j0 < 32 * quarter + 32) {
-            uint32_t z[16];
-            tmem_ld16(lanes + L::T_S + j0, z);
-            tmem_ld_wait();
-            tmem_ld_fence(z);
-            const bool all = j0 < 32 * quarter;
-            const float* by = all ? &sh.g.off[16 * quarter * (quarter - 1) + j0] : &sh.g.rel[j0];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float4 f = *reinterpret_cast<const float4*>(by + 4 * i);
-              if (all) {
-                const float2 u = mul2(make_float2(f.x, f.y), both(mine)), v = mul2(make_float2(f.z, f.w), both(mine));
-                f = make_float4(u.x, u.y, v.x, v.y);
-              } else {
-                const int j = j0 + 4 * i;
-                f.x = j <= row ? ex2(rel - f.x) : 0.f;
-                f.y = j + 1 <= row ? ex2(rel - f.y) : 0.f;
-                f.z = j + 2 <= row ? ex2(rel - f.z) : 0.f;
-                f.w = j + 3 <= row ? ex2(rel - f.w) : 0.f;
-                // a score that is not finite counts only where its key is seen
-                z[4 * i] = j <= row ? z[4 * i] : 0;
-                z[4 * i + 1] = j + 1 <= row ? z[4 * i + 1] : 0;
-                z[4 * i + 2] = j + 2 <= row ? z[4 * i + 2] : 0;
-                z[4 * i + 3] = j + 3 <= row ? z[4 * i + 3] : 0;
-              }
-              float2 u = mul2(pair(z + 4 * i), make_float2(f.x, f.y)), v = mul2(pair(z + 4 * i + 2), make_float2(f.z, f.w));
-              w[2 * i] = take_rounded(u);
-              w[8 + 2 * i] = pack_bf16x2(u.x, u.y);
-              w[2 * i + 1] = take_rounded(v);
-              w[9 + 2 * i] = pack_bf16x2(v.x, v.y);
-            }
+        for (int j0 = 64 * group; j0 < 64 * group + 64; j0 += 32) {
+          if (j0 > 32 * quarter) {
+            const uint32_t none[32] = {};
+            tmem_st<32>(lanes + L::T_S + j0, none);
+            continue;
           }
-          tmem_st<16>(lanes + L::T_S + j0, w);
+          uint32_t z[2][16];
+          tmem_ld16(lanes + L::T_S + j0, z[0]);
+          tmem_ld16(lanes + L::T_S + j0 + 16, z[1]);
+          tmem_ld_wait();
+          tmem_ld_fence(z[0]);
+          tmem_ld_fence(z[1]);
+          const bool all = j0 < 32 * quarter;
+          const float* by = all ? &sh.g.off[16 * quarter * (quarter - 1) + j0] : &sh.g.rel[j0];
+          uint32_t w[32];  // of 16 keys each: eight columns of first parts, eight of second ones
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float4 f = *reinterpret_cast<const float4*>(by + 4 * i);
+            uint32_t* s = &z[i >> 2][4 * (i & 3)];
+            if (all) {
+              const float2 u = mul2(make_float2(f.x, f.y), both(mine)), v = mul2(make_float2(f.z, f.w), both(mine));
+              f = make_float4(u.x, u.y, v.x, v.y);
+            } else {  // a score counts only where its key is seen, whatever it is
+              const int j = 4 * i;
+              f.x = j <= lane ? ex2(rel - f.x) : 0.f, s[0] = j <= lane ? s[0] : 0;
+              f.y = j + 1 <= lane ? ex2(rel - f.y) : 0.f, s[1] = j + 1 <= lane ? s[1] : 0;
+              f.z = j + 2 <= lane ? ex2(rel - f.z) : 0.f, s[2] = j + 2 <= lane ? s[2] : 0;
+              f.w = j + 3 <= lane ? ex2(rel - f.w) : 0.f, s[3] = j + 3 <= lane ? s[3] : 0;
+            }
+            float2 u = mul2(pair(s), make_float2(f.x, f.y)), v = mul2(pair(s + 2), make_float2(f.z, f.w));
+            uint32_t* o = w + 16 * (i >> 2) + 2 * (i & 3);
+            o[0] = take_rounded(u);
+            o[8] = pack_bf16x2(u.x, u.y);
+            o[1] = take_rounded(v);
+            o[9] = pack_bf16x2(v.x, v.y);
+          }
+          tmem_st<32>(lanes + L::T_S + j0, w);
         }
         tmem_st_wait();
       }
@@ -841,7 +844,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           const int ch = half * (D / 16) + i;
           return (ch >> 3) * L::HALF + sw128_off(r, ch & 7);
         };
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < D / 16; ++i) {
           uint4 v = *reinterpret_cast<const uint4*>(kp + off(i));
           if (r >= rows) v = make_uint4(0, 0, 0, 0);
@@ -875,22 +878,28 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         };
         float2 finite = both(0.f);  // NaN: a value that is not finite has met the rows before its own
 #pragma unroll 1
-        for (int col = group * (D / 2); col < (group + 1) * (D / 2); col += 16) {
-          uint32_t x[16], y[16];
-          tmem_ld16(lanes + L::T_SQ + col, x);
-          tmem_ld16(lanes + L::T_PV + col, y);
-          tmem_ld_wait();
-          tmem_ld_fence(x);
-          tmem_ld_fence(y);
-          uint32_t o[8];
+        for (int col = group * (D / 2); col < (group + 1) * (D / 2); col += 32) {
+          uint32_t x[2][16], y[2][16];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            finite = fma2(pair(y + i), both(0.f), finite);
-            const float2 v = mul2(fma2(pair(x + i), both(first), pair(y + i)), both(p.scale));
-            o[i / 2] = pack_bf16x2(v.x, v.y);
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld16(lanes + L::T_SQ + col + 16 * h, x[h]);
+            tmem_ld16(lanes + L::T_PV + col + 16 * h, y[h]);
           }
-          put(col, make_uint4(o[0], o[1], o[2], o[3]));
-          put(col + 8, make_uint4(o[4], o[5], o[6], o[7]));
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld_fence(x[h]);
+            tmem_ld_fence(y[h]);
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              finite = fma2(pair(y[h] + i), both(0.f), finite);
+              const float2 v = mul2(fma2(pair(x[h] + i), both(first), pair(y[h] + i)), both(p.scale));
+              o[i / 2] = pack_bf16x2(v.x, v.y);
+            }
+            put(col + 16 * h, make_uint4(o[0], o[1], o[2], o[3]));
+            put(col + 16 * h + 8, make_uint4(o[4], o[5], o[6], o[7]));
+          }
         }
         if (__any_sync(~0u, finite.x + finite.y != 0.f && row < rows)) {
 #pragma unroll 1
@@ -910,17 +919,22 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       if (!wait(&sh.ds_done, f_ds, 76)) break;
       tc_fence_after();
       // a slow decay as in the recurrent kernel
+      constexpr int AT_ONCE = NC < 32 ? 1 : 2;
 #pragma unroll
-      for (int j = 0; j < NC / 16; ++j) {
-        uint32_t x[16];
-        tmem_ld16(lanes + L::T_DS + s_col + 16 * j, x);
+      for (int j = 0; j < NC / 16; j += AT_ONCE) {
+        uint32_t x[AT_ONCE][16];
+#pragma unroll
+        for (int h = 0; h < AT_ONCE; ++h) tmem_ld16(lanes + L::T_DS + s_col + 16 * (j + h), x[h]);
         tmem_ld_wait();
-        tmem_ld_fence(x);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          float* s = S + 16 * j + i;
-          const float2 v = make_float2(s[0], s[1]), w = fma2(v, both(slow), fma2(v, both(keep), pair(x + i)));
-          s[0] = w.x, s[1] = w.y;
+        for (int h = 0; h < AT_ONCE; ++h) {
+          tmem_ld_fence(x[h]);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float* s = S + 16 * (j + h) + i;
+            const float2 v = make_float2(s[0], s[1]), w = fma2(v, both(slow), fma2(v, both(keep), pair(x[h] + i)));
+            s[0] = w.x, s[1] = w.y;
+          }
         }
       }
       if (!t.ends) continue;
@@ -928,7 +942,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         float* to = cp.pub + blockIdx.x * pub_floats(D);
 #pragma unroll
         for (int i = 0; i < NC; i += 4)
-          *reinterpret_cast<float4*>(to + s_row * D + s_col + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+          *reinterpret_cast<float4*>(to + i * LC_COMPUTE + 4 * tid) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
         if (tid == 0) to[D * D] = decay_n, to[D * D + 1] = decay_f;
         __threadfence();
         sync();
