@@ -12,10 +12,11 @@ namespace moe {
 namespace {
 
 constexpr int LP_THREADS = 256;
-constexpr int LP_VECS = 4;        // 16-byte loads of a thread in flight
+constexpr int LP_ELEMS = 16;      // elements of a thread's part of a tile
+constexpr int LP_RING = 16;       // 16-byte vectors of a thread on their way or in use
+constexpr int LP_GROUP = 4;       // tiles between two rankings
 constexpr int LP_TOP = 32;        // alternatives, at most
 constexpr int LP_CAND = 1024;     // candidates that wait to be ranked
-constexpr int LP_RANK_AT = 96;    // so many are ranked before more come
 constexpr int LP_CLUSTER = 8;     // CTAs of a row, at most
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float FAR = -1e30f;     // stands for -inf where it is multiplied by zero
@@ -103,9 +104,22 @@ struct Shared {
   int total;
 };
 
+// Each thread copies the vectors that it reads itself, so that its own copies
+// are all that it waits for.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The `top` largest of the candidates to their first places and to best, in
-// order.  All threads call it after a barrier; what it leaves is visible to all.
-__device__ void rank_candidates(Shared& sh, int top) {
+// order; returns how many there are.  All threads call it after a barrier;
+// what it leaves is visible to all.
+__device__ int rank_candidates(Shared& sh, int top) {
   const int c = sh.count;
   for (int i = threadIdx.x; i < c; i += LP_THREADS) {
     const uint64_t mine = sh.cand[i];
@@ -121,26 +135,29 @@ __device__ void rank_candidates(Shared& sh, int top) {
     if (kept == top) sh.thr = value_of(sh.best[top - 1]);
   }
   __syncthreads();
+  return kept;
 }
 
-// One row by a cluster of CTAs, each of which walks every csize-th tile of it
-// and keeps no more than a tile in registers: memory is read once, which is
-// what bounds the kernel where there are many rows; where there are few, the
-// CTAs of a cluster share one.
+// One row by a cluster of CTAs, each of which walks every csize-th tile of it:
+// memory is read once, which is what bounds the kernel where there are many
+// rows; where there are few, the CTAs of a cluster share one.
 //
 // Sums: a thread rebases its sums where its part of a tile has a new maximum,
 // so that an element costs one exponential.  Alternatives: an element becomes
 // a candidate if it is above the top-th largest value so far, which a thread
-// first asks of its part's maximum.  A CTA's elements come in ascending order,
-// tile by tile, so that an equal value of a later tile takes no earlier one's
-// place.  While there are too few candidates for such a bound, the maxima of
-// 32 groups of threads give one: the top-th largest of them is reached by as
-// many elements.  -inf never becomes a candidate; a row that has too few other
-// values is filled up at the end.
+// first asks of its part's maximum; after LP_GROUP tiles the candidates are
+// ranked, which gives the next bound (a barrier after every tile instead of
+// four cost 2048 rows of 131072 logits 110 us of 280).  A CTA's elements come in
+// ascending order, tile by tile, so that an equal value of a later group takes
+// no earlier one's place.  While there are too few candidates for a bound, the
+// maxima of 32 groups of threads give one: the top-th largest of them is
+// reached by as many elements.  -inf never becomes a candidate; a row that has
+// too few other values is filled up at the end.
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(LogprobParams p, int csize) {
+__global__ void __launch_bounds__(LP_THREADS, 3) logprobs_kernel(LogprobParams p, int csize) {
   __shared__ Shared sh;
-  constexpr int N = Vec<T>::N, E = N * LP_VECS, TILE = LP_THREADS * LP_VECS;
+  extern __shared__ uint4 ring[];  // [stage][vector][thread]
+  constexpr int N = Vec<T>::N, E = LP_ELEMS, VECS = E / N, TILE = LP_THREADS * VECS, STAGES = LP_RING / VECS;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -150,6 +167,16 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(LogprobParams p, i
   const int head = min(p.n, (int)((16 - (uintptr_t)x % 16) % 16 / sizeof(T)));
   const int nv = (p.n - head) / N, edge = p.n - nv * N;  // edge: head and rest together, fewer than 2 N
   const uint4* body = reinterpret_cast<const uint4*>(x + head);
+  const auto fetch = [&](int v0, int stage) {
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+      const int v = v0 + j * LP_THREADS + tid;
+      if (v < nv) copy16(&ring[(stage * VECS + j) * LP_THREADS + tid], body + v);
+    }
+    copies_end_group();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch((rank + i * csize) * TILE, i);
   float given = NOT_A_NUMBER;
   if (rank == 0 && tid < p.n_ids) {
     const size_t at = (size_t)row * p.n_ids + tid;
@@ -157,14 +184,14 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(LogprobParams p, i
     if (id >= 0 && id < p.n) given = Vec<T>::load(x + id);
   }
   Stats a{-FLT_MAX, 0.f, 0.f};
+  int kept = 0;          // candidates as the last ranking left them
+  bool fresh = false;    // this thread has added some since
   if (TOP) {
     if (tid == 0) sh.count = 0, sh.thr = -INFINITY;
     __syncthreads();
   }
 
-  // Takes a thread's part of a tile, elements e[i] at index(i).  `ties`: an
-  // element may come after others of a higher index.
-  const auto take = [&](const float* e, auto index, bool ties) {
+  const auto sums = [&](const float* e) {  // and the largest of a thread's part
     float lm = -INFINITY;
 #pragma unroll
     for (int i = 0; i < E; ++i) lm = fmaxf(lm, e[i]);
@@ -175,84 +202,111 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(LogprobParams p, i
       a.s += q;
       a.u = fmaf(q, fmaxf(d, FAR), a.u);
     }
-    if (!TOP) return;
-    float thr = sh.thr;
-    const bool loose = thr == -INFINITY;  // the same for the whole CTA
-    if (loose) {
-      constexpr int G = LP_THREADS / 32;  // threads of a group
-      float g = lm;
+    return lm;
+  };
+  // A bound from the largest values of 32 groups of threads.
+  const auto bound = [&](float lm) {
+    constexpr int G = LP_THREADS / 32;  // threads of a group
+    float g = lm;
 #pragma unroll
-      for (int o = G / 2; o; o >>= 1) g = fmaxf(g, __shfl_xor_sync(~0u, g, o));
-      if (tid % G == 0) sh.group[tid / G] = g;
-      __syncthreads();
-      g = sh.group[lane];
-      int above = 0;
-      for (int j = 0; j < 32; ++j) {
-        const float o = __shfl_sync(~0u, g, j);
-        above += o > g || (o == g && j < lane);
+    for (int o = G / 2; o; o >>= 1) g = fmaxf(g, __shfl_xor_sync(~0u, g, o));
+    if (tid % G == 0) sh.group[tid / G] = g;
+    __syncthreads();
+    g = sh.group[lane];
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) {
+      const float o = __shfl_sync(~0u, g, j);
+      above += o > g || (o == g && j < lane);
+    }
+    const uint32_t who = __ballot_sync(~0u, above == p.top - 1);
+    return __shfl_sync(~0u, g, __ffs(who) - 1);
+  };
+  // The elements above thr (ties: or equal to it) become candidates; those past the list's end are dropped, but counted.
+  const auto add = [&](const float* e, auto index, float thr, bool ties) {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (e[i] > -INFINITY && (e[i] > thr || (ties && e[i] == thr))) {
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < LP_CAND) sh.cand[at] = key_of(e[i], index(i));
+        fresh = true;
       }
-      const uint32_t who = __ballot_sync(~0u, above == p.top - 1);
-      thr = __shfl_sync(~0u, g, __ffs(who) - 1);
-      ties = true;
+  };
+  const auto index_at = [&](int v0) {
+    const int first = head + (v0 + tid) * N;
+    return [first](int i) { return first + i / N * (LP_THREADS * N) + i % N; };
+  };
+  // Ranks what has come since the last ranking, tiles v0, v0 + csize * TILE, ... before v1.
+  const auto settle = [&](int v0, int v1) {
+    if (!__syncthreads_or(fresh)) return;
+    fresh = false;
+    if (sh.count <= LP_CAND) {
+      kept = rank_candidates(sh, p.top);
+      return;
     }
-    bool full = loose;
-    uint32_t in = 0;  // elements among the first LP_RANK_AT candidates
-    if (lm > thr || (ties && lm == thr)) {
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (e[i] > -INFINITY && (e[i] > thr || (ties && e[i] == thr))) {
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < LP_CAND) sh.cand[at] = key_of(e[i], index(i));
-          if (at < LP_RANK_AT)
-            in |= 1u << i;
-          else
-            full = true;
-        }
-    }
-    if (!__syncthreads_or(full)) return;
-    if (sh.count > LP_CAND) {
-      // More than the list holds, all but LP_RANK_AT of them of this tile.
-      // The top-th largest key of the tile is found bit by bit; those from it
-      // on that are not among the first LP_RANK_AT take the others' places.
+    // More than the list holds.  The tiles are read again, one by one: a
+    // tile's top-th largest key is found bit by bit, and those from it on are
+    // candidates.
+    for (int v = v0; v < v1; v += csize * TILE) {
+      const auto index = index_at(v);
+      const auto element = [&](int i) {
+        const int at = v + i / N * LP_THREADS + tid;
+        return at < nv ? Vec<T>::load(x + index(i)) : -INFINITY;
+      };
       uint64_t low = 0;
       for (int bit = 63; bit >= 0; --bit) {
         __syncthreads();
-        if (tid == 0) sh.total = 0;
+        if (tid == 0) sh.total = 0, sh.count = kept;
         __syncthreads();
         const uint64_t key = low | (uint64_t)1 << bit;
         int c = 0;
-#pragma unroll
-        for (int i = 0; i < E; ++i) c += e[i] > -INFINITY && key_of(e[i], index(i)) >= key;
+#pragma unroll 1
+        for (int i = 0; i < E; ++i) {
+          const float f = element(i);
+          c += f > -INFINITY && key_of(f, index(i)) >= key;
+        }
         c = __reduce_add_sync(~0u, c);
         if (lane == 0 && c) atomicAdd(&sh.total, c);
         __syncthreads();
         if (sh.total >= p.top) low = key;
       }
-      if (tid == 0) sh.count = LP_RANK_AT;
-      __syncthreads();
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < E; ++i) {
-        const uint64_t key = key_of(e[i], index(i));
-        if (e[i] > -INFINITY && key >= low && !(in >> i & 1)) sh.cand[atomicAdd(&sh.count, 1)] = key;
+        const float f = element(i);
+        if (f > -INFINITY && key_of(f, index(i)) >= low) sh.cand[atomicAdd(&sh.count, 1)] = key_of(f, index(i));
       }
       __syncthreads();
+      kept = rank_candidates(sh, p.top);
     }
-    rank_candidates(sh, p.top);
   };
 
+  int stage = 0, group = 0, first_v = rank * TILE;
+  float thr = -INFINITY;
   for (int v0 = rank * TILE; v0 < nv; v0 += csize * TILE) {
+    copies_wait<STAGES - 2>();
     float e[E];
 #pragma unroll
-    for (int j = 0; j < LP_VECS; ++j) {
-      const int v = v0 + j * LP_THREADS + tid;
-      if (v < nv) {
-        Vec<T>::unpack(__ldcs(body + v), e + j * N);
+    for (int j = 0; j < VECS; ++j) {
+      if (v0 + j * LP_THREADS + tid < nv) {
+        Vec<T>::unpack(ring[(stage * VECS + j) * LP_THREADS + tid], e + j * N);
       } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) e[j * N + i] = -INFINITY;
       }
     }
-    take(e, [&](int i) { return head + (v0 + i / N * LP_THREADS + tid) * N + i % N; }, false);
+    fetch(v0 + (STAGES - 1) * csize * TILE, (stage + STAGES - 1) % STAGES);
+    stage = (stage + 1) % STAGES;
+    const float lm = sums(e);
+    if (!TOP) continue;
+    if (group == 0) thr = sh.thr;
+    const bool loose = thr == -INFINITY;  // the same for the whole CTA
+    const float least = loose ? bound(lm) : thr;
+    if (lm > least || (loose && lm == least)) add(e, index_at(v0), least, loose);
+    if (loose || ++group == LP_GROUP || v0 + csize * TILE >= nv) {
+      settle(first_v, v0 + 1);
+      group = 0;
+      first_v = v0 + csize * TILE;
+    }
   }
   if (rank == 0 && edge) {
     const int at = tid < head ? tid : p.n - edge + tid;
@@ -260,7 +314,11 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(LogprobParams p, i
 #pragma unroll
     for (int i = 0; i < E; ++i) e[i] = -INFINITY;
     if (tid < edge) e[0] = Vec<T>::load(x + at);
-    take(e, [&](int) { return at; }, true);
+    sums(e);
+    if (TOP) {
+      add(e, [&](int) { return at; }, sh.thr, true);  // too few to overflow the list
+      settle(0, 0);
+    }
   }
 
   // the CTA's sums, then the cluster's
@@ -269,7 +327,6 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(LogprobParams p, i
     a = join(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o), __shfl_xor_sync(~0u, a.u, o)});
   if (lane == 0) sh.part[warp] = a;
   __syncthreads();
-  if (TOP) rank_candidates(sh, p.top);
   a = sh.part[0];
 #pragma unroll
   for (int i = 1; i < LP_THREADS / 32; ++i) a = join(a, sh.part[i]);
@@ -292,7 +349,7 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(LogprobParams p, i
       __syncthreads();
       if (far) sh.cand[atomicAdd(&sh.count, 1)] = far;
       __syncthreads();
-      rank_candidates(sh, p.top);
+      kept = rank_candidates(sh, p.top);
     }
   }
   const float ln_s = logf(a.s);
@@ -304,7 +361,6 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(LogprobParams p, i
     if (p.entropy) p.entropy[row] = h < 0.f ? 0.f : h;
   }
   if (!TOP) return;
-  const int kept = sh.count;
   const size_t to = (size_t)row * p.top;
   if (!whole) {
     if (tid < p.top) p.top_ids[to + tid] = -1, p.top_logprobs[to + tid] = NOT_A_NUMBER;
@@ -322,11 +378,14 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(LogprobParams p, i
   }
 }
 
+constexpr int LP_RING_BYTES = LP_RING * LP_THREADS * 16;
+
 template <typename T, bool TOP>
 cudaError_t launch_logprobs(const LogprobParams& p, int csize, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.t * csize);
   cfg.blockDim = dim3(LP_THREADS);
+  cfg.dynamicSmemBytes = LP_RING_BYTES;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -336,7 +395,8 @@ cudaError_t launch_logprobs(const LogprobParams& p, int csize, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = csize > 1 ? 2 : 1;
-  cudaError_t e = cudaSuccess;
+  cudaError_t e = set_smem_limit_once(logprobs_kernel<T, TOP>, LP_RING_BYTES);
+  if (e != cudaSuccess) return e;
   MOE_LAUNCH("logprobs", s, { e = cudaLaunchKernelEx(&cfg, logprobs_kernel<T, TOP>, p, csize); });
   return e;
 }
@@ -365,7 +425,7 @@ extern "C" int moe_logprobs(const void* logits, int64_t stride, int32_t logits_f
   TRY(check_ptr(top_logprobs, "top_logprobs", 4, top == 0));
   const LogprobParams p{logits, stride, t, n, ids, ids_int64, n_ids, top, logprob, entropy, lse, top_ids, top_logprobs};
   // CTAs of a row: as many as leave every SM two, while each has a tile
-  const int tile = LP_THREADS * LP_VECS * (logits_fp32 ? 4 : 8);
+  const int tile = LP_THREADS * LP_ELEMS;
   int csize = 1;
   while (csize < LP_CLUSTER && (int64_t)t * csize * 2 <= 2 * sm_count() && (int64_t)n >= 2 * csize * tile) csize *= 2;
   cudaStream_t s = (cudaStream_t)stream;

@@ -508,8 +508,9 @@ def moe_kv_plan(fresh: torch.Tensor, cache: KvCache, pages: KvPages, t: int, len
         raise MoeError(-2, f"t={t} outside [1, 65536]")
     # one allocation: the maps of 8 bytes a row, then those of 4, then the starts
     whole = _empty((4 * t + cache.n_seq + 1,), torch.int32, fresh, stream)
-    slot = whole[:2 * t].view(torch.int64)
-    seq, pos, starts = whole[2 * t:3 * t], whole[3 * t:4 * t], whole[4 * t:]
+    seq, pos, starts = (whole.as_strided((t,), (1,), 2 * t), whole.as_strided((t,), (1,), 3 * t),
+                        whole.as_strided((cache.n_seq + 1,), (1,), 4 * t))
+    slot = whole.as_strided((2 * t,), (1,), 0).view(torch.int64)
     at = whole.data_ptr()
     n_seq, n_pages, max_blocks, block = pages._sizes
     status = lib.moe_kv_plan(fresh.data_ptr(), before.data_ptr(), cache._c.lens, pages._table, pages._ref, n_seq, n_pages,
@@ -658,19 +659,20 @@ def moe_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top: int
     if not 0 <= top <= 32:
         raise MoeError(-2, f"top={top} outside [0, 32]")
     logprob = top_ids = top_logprobs = None
-    m = 0
+    m = 0 if ids is None else 1 if ids.dim() == 1 else ids.shape[1]
+    # one allocation for all results (a view costs a third of one)
+    whole = _empty((t * (2 + m + 2 * top),), torch.float32, logits, stream)
+    at = whole.data_ptr()
+    entropy, lse = whole.as_strided((t,), (1,), 0), whole.as_strided((t,), (1,), t)
     if ids is not None:
-        m = 1 if ids.dim() == 1 else ids.shape[1]
-        logprob = _empty(ids.shape, torch.float32, logits, stream)
-    entropy, lse = _empty((2, t), torch.float32, logits, stream).unbind(0)
+        logprob = whole.as_strided(ids.shape, ids.stride(), 2 * t)
     if top:
-        top_ids = _empty((t, top), torch.int32, logits, stream)
-        top_logprobs = _empty((t, top), torch.float32, logits, stream)
+        top_logprobs = whole.as_strided((t, top), (top, 1), t * (2 + m))
+        top_ids = whole.view(torch.int32).as_strided((t, top), (top, 1), t * (2 + m + top))
     status = lib.moe_logprobs(
-        logits.data_ptr(), _row_stride(logits), f32, t, n, None if not m else ids.data_ptr(),
-        ids is not None and ids.dtype is torch.int64, m, top, None if not m else logprob.data_ptr(), entropy.data_ptr(),
-        lse.data_ptr(), None if not top else top_ids.data_ptr(), None if not top else top_logprobs.data_ptr(),
-        _raw(stream, dev))
+        logits.data_ptr(), _row_stride(logits), f32, t, n, ids.data_ptr() if m else None,
+        ids is not None and ids.dtype is torch.int64, m, top, at + 8 * t if m else None, at, at + 4 * t,
+        at + 4 * t * (2 + m + top) if top else None, at + 4 * t * (2 + m) if top else None, _raw(stream, dev))
     if status:
         _check(status)
     return Logprobs(logprob, entropy, lse, top_ids, top_logprobs)
