@@ -37,7 +37,7 @@ struct PlanParams {
 // One sequence's part: what it adds, takes and gives back.
 struct PlanItem {
   int held, grow, take, give, len;
-  bool bad;
+  bool bad, ends;
 };
 
 __device__ __forceinline__ PlanItem plan_item(const PlanParams& p, int s) {
@@ -50,6 +50,7 @@ __device__ __forceinline__ PlanItem plan_item(const PlanParams& p, int s) {
   r.bad = held < 0 || held > p.max_blocks || r.grow > p.t || before < 0 || before > held * p.block ||
           need > p.max_blocks;
   if (fresh < 0) r.bad = held < 0 || held > p.max_blocks;
+  r.ends = fresh < 0;
   r.take = fresh < 0 || r.bad ? 0 : (int)max((int64_t)0, need - held);
   r.give = fresh < 0 && !r.bad ? (int)held : 0;
   r.len = fresh < 0 ? 0 : (int)len;
@@ -62,146 +63,177 @@ struct PlanSums {
 };
 __device__ __forceinline__ PlanSums operator+(PlanSums a, PlanSums b) { return {a.grow + b.grow, a.take + b.take, a.give + b.give}; }
 
+__device__ __forceinline__ PlanSums warp_scan(PlanSums v, int lane) {  // this lane's included
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const PlanSums u{__shfl_up_sync(~0u, v.grow, o), __shfl_up_sync(~0u, v.take, o), __shfl_up_sync(~0u, v.give, o)};
+    if (lane >= o) v = v + u;
+  }
+  return v;
+}
+__device__ __forceinline__ PlanSums of_lane(PlanSums v, int from) {
+  return {__shfl_sync(~0u, v.grow, from), __shfl_sync(~0u, v.take, from), __shfl_sync(~0u, v.give, from)};
+}
+
 // Sums over the threads before this one, and over all, of the CTA.
 __device__ PlanSums cta_scan(PlanSums v, PlanSums (&part)[32], PlanSums& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  PlanSums in = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const PlanSums u{__shfl_up_sync(~0u, in.grow, o), __shfl_up_sync(~0u, in.take, o), __shfl_up_sync(~0u, in.give, o)};
-    if (lane >= o) in = in + u;
-  }
+  const PlanSums in = warp_scan(v, lane);
   __syncthreads();  // part may still be read
   if (lane == 31) part[warp] = in;
   __syncthreads();
-  PlanSums before{0, 0, 0};
-  all = before;
-  for (int i = 0; i < PLAN_THREADS / 32; ++i) {
-    if (i == warp) before = all;
-    all = all + part[i];
-  }
-  return {before.grow + in.grow - v.grow, before.take + in.take - v.take, before.give + in.give - v.give};
+  const PlanSums to = warp_scan(part[lane], lane);
+  all = of_lane(to, 31);
+  const PlanSums before = of_lane(to, warp ? warp - 1 : 0);
+  const PlanSums off{in.grow - v.grow, in.take - v.take, in.give - v.give};
+  return warp ? off + before : off;
 }
 
-// Rows and pages first, first + step, ... of what the first kernel decided.
-__device__ __forceinline__ void plan_rows(const PlanParams& p, int first, int step) {
-  const PlanHeader h = *p.head;
+// What the rows' maps are made from: in shared memory where one kernel does all.
+struct PlanView {
+  const int32_t* starts;
+  const int32_t* lens;
+  const int32_t* held;      // before the call
+  const int32_t* take_off;  // pages taken by the sequences before
+  PlanHeader h;
+};
+
+// The last of n places whose value is at most x (the first one's is): the
+// places of the same value before it are empty.
+__device__ __forceinline__ int last_at_most(const int32_t* v, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Rows and pages first, first + step, ... of what was decided.
+__device__ __forceinline__ void plan_rows(const PlanParams& p, const PlanView& w, int first, int step) {
   for (int i = first; i < p.t; i += step) {
     int seq = -1, pos = -1;
     int64_t slot = -1;
-    if (i < h.rows) {
-      // the last sequence that starts at or before row i: it owns the row, those that start there too are empty
-      int lo = 0, hi = p.n_seq;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.starts[mid] <= i) lo = mid; else hi = mid;
-      }
-      seq = lo;
-      const int from = p.starts[seq], n = p.starts[seq + 1] - from;
-      pos = p.lens[seq] - n + i - from;
-      const int b = pos / p.block, held = p.held_before[seq];
+    if (i < w.h.rows) {
+      seq = last_at_most(w.starts, p.n_seq, i);
+      const int from = w.starts[seq], n = w.starts[seq + 1] - from;
+      pos = w.lens[seq] - n + i - from;
+      const int b = pos / p.block, held = w.held[seq];
       const int page = b < held ? p.table[(size_t)seq * p.max_blocks + b]
-                                : p.pages.free[h.top - 1 - (p.take_off[seq] + b - held)];
+                                : p.pages.free[w.h.top - 1 - (w.take_off[seq] + b - held)];
       slot = (int64_t)page * p.block + pos % p.block;
     }
     if (p.seq) p.seq[i] = seq;
     if (p.pos) p.pos[i] = pos;
     if (p.slot) p.slot[i] = slot;
   }
-  for (int i = first; i < h.taken; i += step) {  // a page for each: as many as rows, at most
-    int lo = 0, hi = p.n_seq;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.take_off[mid] <= i) lo = mid; else hi = mid;
-    }
-    p.table[(size_t)lo * p.max_blocks + p.held_before[lo] + i - p.take_off[lo]] = p.pages.free[h.top - 1 - i];
+  for (int i = first; i < w.h.taken; i += step) {  // no more pages than rows are taken
+    const int s = last_at_most(w.take_off, p.n_seq, i);
+    p.table[(size_t)s * p.max_blocks + w.held[s] + i - w.take_off[s]] = p.pages.free[w.h.top - 1 - i];
   }
 }
 
 // Decides about the whole batch, then changes lengths and accounts and gives
 // back pages.  One CTA: a batch has a few thousand sequences at most, and the
-// decision needs all of their sums.  What bounds it is latency: the loads of
-// its checks, two scans.  With ALL it goes on to the rows' maps.
+// decision needs all of their sums.  What bounds it is latency: loads of what
+// it checks, a scan, barriers.  ALL (up to PLAN_SEQS sequences, a thread each,
+// and PLAN_ROWS rows): it goes on to the rows' maps, from shared memory.
 template <bool ALL>
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PlanParams p) {
   __shared__ PlanSums part[32];
-  __shared__ int bad_pages;
+  __shared__ int32_t kept[4][ALL ? PLAN_SEQS + 1 : 1];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int count = *p.pages.count;
-  if (tid == 0) bad_pages = 0;
-  PlanSums all{0, 0, 0};
+  PlanItem mine{};
+  PlanSums mine_off{0, 0, 0}, sum;
   bool bad = false;
-  for (int s = tid; s < p.n_seq; s += PLAN_THREADS) {
-    const PlanItem r = plan_item(p, s);
-    bad |= r.bad;
-    all = all + PlanSums{r.grow, r.take, r.give};
+  if (ALL) {
+    if (tid < p.n_seq) mine = plan_item(p, tid);
+    bad = mine.bad;
+    mine_off = cta_scan({mine.grow, mine.take, mine.give}, part, sum);
+  } else {
+    PlanSums all{0, 0, 0};
+    for (int s = tid; s < p.n_seq; s += PLAN_THREADS) {
+      const PlanItem r = plan_item(p, s);
+      bad |= r.bad;
+      all = all + PlanSums{r.grow, r.take, r.give};
+    }
+    cta_scan(all, part, sum);
   }
-  PlanSums sum;
-  cta_scan(all, part, sum);
   bad = __syncthreads_or(bad) || count < 0 || count > p.n_pages || sum.grow > p.t || count + sum.give > p.n_pages;
   const bool few = !bad && sum.take > count + sum.give;
-  if (!bad && !few) {
-    // pages that change hands have to exist
-    bool off = false;
-    const int top = (int)(count - max(0LL, sum.take - sum.give));  // free pages below it stay
-    for (int i = top + tid; i < count; i += PLAN_THREADS) off |= (unsigned)p.pages.free[i] >= (unsigned)p.n_pages;
-    if (sum.give)
-      for (int s = warp; s < p.n_seq; s += PLAN_THREADS / 32)
-        if (p.fresh[s] < 0)
-          for (int b = lane; b < p.pages.held[s]; b += 32)
-            off |= (unsigned)p.table[(size_t)s * p.max_blocks + b] >= (unsigned)p.n_pages;
-    if (off) bad_pages = 1;
-    __syncthreads();
-    bad = bad_pages;
-  }
-  if (bad || few) {  // nothing is changed, no sequence has rows
-    if (tid == 0) {
-      raise_flag(p.st, bad ? FLAG_BAD_CACHE : FLAG_NO_PAGES);
-      *p.head = PlanHeader{0, 0, count, 0};
+  // The pages that a warp's sequences give back, a sequence at a time.
+  const auto given = [&](int s, const PlanItem& r, const PlanSums& off, auto f) {
+    for (uint32_t m = __ballot_sync(~0u, r.give > 0); m; m &= m - 1) {
+      const int from = __ffs(m) - 1, n = __shfl_sync(~0u, r.give, from);
+      const int to = count + __shfl_sync(~0u, (int)off.give, from);
+      const int32_t* row = p.table + (size_t)__shfl_sync(~0u, s, from) * p.max_blocks;
+      for (int b = lane; b < n; b += 32) f(to + b, row[b]);
     }
+  };
+  // All sequences, PLAN_THREADS at a time.
+  const auto sequences = [&](auto f) {
+    if (ALL) {
+      f(tid, mine, mine_off);
+    } else {
+      PlanSums base{0, 0, 0}, some;
+      for (int s0 = 0; s0 < p.n_seq; s0 += PLAN_THREADS) {
+        const PlanItem r = s0 + tid < p.n_seq ? plan_item(p, s0 + tid) : PlanItem{};
+        const PlanSums off = base + cta_scan({r.grow, r.take, r.give}, part, some);
+        base = base + some;
+        f(s0 + tid, r, off);
+      }
+    }
+  };
+  if (!bad && !few) {  // pages that change hands have to exist
+    bool none = false;
+    const int top = (int)(count - max(0LL, sum.take - sum.give));  // free pages below it stay
+    for (int i = top + tid; i < count; i += PLAN_THREADS) none |= (unsigned)p.pages.free[i] >= (unsigned)p.n_pages;
+    if (sum.give)
+      sequences([&](int s, const PlanItem& r, const PlanSums& off) {
+        given(s, r, off, [&](int, int page) { none |= (unsigned)page >= (unsigned)p.n_pages; });
+      });
+    bad = __syncthreads_or(none);
+  }
+  PlanHeader head{0, 0, count, 0};
+  if (bad || few) {  // nothing is changed, no sequence has rows
+    if (tid == 0) raise_flag(p.st, bad ? FLAG_BAD_CACHE : FLAG_NO_PAGES);
     for (int s = tid; s <= p.n_seq; s += PLAN_THREADS) p.starts[s] = 0;
   } else {
-    PlanSums base{0, 0, 0};
-    for (int s0 = 0; s0 < p.n_seq; s0 += PLAN_THREADS) {
-      const int s = s0 + tid;
-      PlanItem r{};
-      if (s < p.n_seq) r = plan_item(p, s);
-      PlanSums some;
-      const PlanSums off = base + cta_scan({r.grow, r.take, r.give}, part, some);
-      base = base + some;
-      if (s < p.n_seq) {
-        p.starts[s] = (int)off.grow;
-        p.take_off[s] = (int)off.take;
+    head = {(int)sum.grow, (int)sum.take, (int)(count + sum.give), 0};
+    sequences([&](int s, const PlanItem& r, const PlanSums& off) {
+      given(s, r, off, [&](int to, int page) { p.pages.free[to] = page; });
+      if (s >= p.n_seq) return;
+      p.starts[s] = (int)off.grow;
+      p.lens[s] = r.len;
+      p.pages.held[s] = r.ends ? 0 : r.held + r.take;
+      if (ALL) {
+        kept[0][s] = (int)off.grow, kept[1][s] = r.len, kept[2][s] = r.held, kept[3][s] = (int)off.take;
+      } else {
         p.held_before[s] = r.held;
-        p.lens[s] = r.len;
+        p.take_off[s] = (int)off.take;
       }
-      // the pages of 32 sequences at a time, those of one by a whole warp
-      for (uint32_t m = __ballot_sync(~0u, r.give > 0); m; m &= m - 1) {
-        const int from = __ffs(m) - 1, n = __shfl_sync(~0u, r.give, from);
-        const int to = count + __shfl_sync(~0u, (int)off.give, from);
-        const int32_t* row = p.table + (size_t)__shfl_sync(~0u, s, from) * p.max_blocks;
-        for (int b = lane; b < n; b += 32) p.pages.free[to + b] = row[b];
-      }
-      if (s < p.n_seq) p.pages.held[s] = p.fresh[s] < 0 ? 0 : r.held + r.take;
-    }
+    });
     if (tid == 0) {
       p.starts[p.n_seq] = (int)sum.grow;
+      if (ALL) kept[0][p.n_seq] = (int)sum.grow;
       *p.pages.count = (int)(count + sum.give - sum.take);
-      *p.head = PlanHeader{(int)sum.grow, (int)sum.take, (int)(count + sum.give), 0};
     }
   }
   if (ALL) {
     __syncthreads();
-    plan_rows(p, tid, PLAN_THREADS);
+    plan_rows(p, {kept[0], kept[1], kept[2], kept[3], head}, tid, PLAN_THREADS);
+  } else if (tid == 0) {
+    *p.head = head;
   }
 }
 
 __global__ void __launch_bounds__(256) plan_rows_kernel(PlanParams p) {
   pdl_wait();
   pdl_trigger();
-  plan_rows(p, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
+  plan_rows(p, {p.starts, p.lens, p.held_before, p.take_off, *p.head}, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
 size_t plan_ws_bytes(int n_seq) { return sizeof(DeviceStatus) + 256 + 2 * align_up((size_t)n_seq * 4, 256); }

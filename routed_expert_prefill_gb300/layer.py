@@ -506,15 +506,13 @@ def moe_kv_plan(fresh: torch.Tensor, cache: KvCache, pages: KvPages, t: int, len
         _on_current_device(fresh=fresh, lens=before, codes=cache.codes)
     if not 1 <= t <= 65536:  # before memory is asked for
         raise MoeError(-2, f"t={t} outside [1, 65536]")
-    # one allocation: the maps of 8 bytes a row, then those of 4, then the starts
-    whole = _empty((4 * t + cache.n_seq + 1,), torch.int32, fresh, stream)
-    seq, pos, starts = (whole.as_strided((t,), (1,), 2 * t), whole.as_strided((t,), (1,), 3 * t),
-                        whole.as_strided((cache.n_seq + 1,), (1,), 4 * t))
-    slot = whole.as_strided((2 * t,), (1,), 0).view(torch.int64)
-    at = whole.data_ptr()
     n_seq, n_pages, max_blocks, block = pages._sizes
+    starts = _empty((n_seq + 1,), torch.int32, fresh, stream)
+    seq, pos = _empty((t,), torch.int32, fresh, stream), _empty((t,), torch.int32, fresh, stream)
+    slot = _empty((t,), torch.int64, fresh, stream)
     status = lib.moe_kv_plan(fresh.data_ptr(), before.data_ptr(), cache._c.lens, pages._table, pages._ref, n_seq, n_pages,
-                             max_blocks, block, t, at + 16 * t, at + 8 * t, at + 12 * t, at, *pages._ws, _raw(stream, dev))
+                             max_blocks, block, t, starts.data_ptr(), seq.data_ptr(), pos.data_ptr(), slot.data_ptr(),
+                             *pages._ws, _raw(stream, dev))
     if status:
         _check(status)
     return KvPlan(starts, seq, pos, slot)
@@ -660,19 +658,17 @@ def moe_logprobs(logits: torch.Tensor, ids: torch.Tensor | None = None, top: int
         raise MoeError(-2, f"top={top} outside [0, 32]")
     logprob = top_ids = top_logprobs = None
     m = 0 if ids is None else 1 if ids.dim() == 1 else ids.shape[1]
-    # one allocation for all results (a view costs a third of one)
-    whole = _empty((t * (2 + m + 2 * top),), torch.float32, logits, stream)
-    at = whole.data_ptr()
-    entropy, lse = whole.as_strided((t,), (1,), 0), whole.as_strided((t,), (1,), t)
+    # tensors of their own: a view of a new tensor costs more than another tensor
+    entropy, lse = _empty((t,), torch.float32, logits, stream), _empty((t,), torch.float32, logits, stream)
     if ids is not None:
-        logprob = whole.as_strided(ids.shape, ids.stride(), 2 * t)
+        logprob = _empty(ids.shape, torch.float32, logits, stream)
     if top:
-        top_logprobs = whole.as_strided((t, top), (top, 1), t * (2 + m))
-        top_ids = whole.view(torch.int32).as_strided((t, top), (top, 1), t * (2 + m + top))
+        top_ids = _empty((t, top), torch.int32, logits, stream)
+        top_logprobs = _empty((t, top), torch.float32, logits, stream)
     status = lib.moe_logprobs(
         logits.data_ptr(), _row_stride(logits), f32, t, n, ids.data_ptr() if m else None,
-        ids is not None and ids.dtype is torch.int64, m, top, at + 8 * t if m else None, at, at + 4 * t,
-        at + 4 * t * (2 + m + top) if top else None, at + 4 * t * (2 + m) if top else None, _raw(stream, dev))
+        ids is not None and ids.dtype is torch.int64, m, top, logprob.data_ptr() if m else None, entropy.data_ptr(),
+        lse.data_ptr(), top_ids.data_ptr() if top else None, top_logprobs.data_ptr() if top else None, _raw(stream, dev))
     if status:
         _check(status)
     return Logprobs(logprob, entropy, lse, top_ids, top_logprobs)
