@@ -152,105 +152,178 @@ struct GatedParams {
   moe_gate gate;
 };
 
-enum { GATE_NONE, GATE_ROW, GATE_CHANNEL };  // a gate value for each row, or for each channel
+// A gate value for each row, or for each channel as it is or through the sigmoid
+// (apart: chosen inside the loop, both were worked out for every value).
+enum { GATE_NONE, GATE_ROW, GATE_CHANNEL, GATE_SIGMOID };
+
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+__device__ __forceinline__ void copy16(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+               : "memory");
+}
 
 // As norm_kernel, with two sums of squares: the block's output is normed,
 // gated and added to the scaled residual in registers, and that sum is normed
-// again.  All of a row's loads are issued before the first sum, so that the
-// second one waits on the barrier alone.
-template <int VPT, bool Q8, int GATE>
-__global__ void __launch_bounds__(512) gated_norm_kernel(GatedParams gp, int rt) {
+// again.
+//
+// MANY: the grid fills the SMs and each row group walks its rows, the next
+// STAGES - 1 of them on their way into shared memory (a thread copies what it
+// reads itself, so that its own copies are all that it waits for), the weights
+// in registers.  4096 rows of 4096 channels, 8 bytes a channel (19.8 us at the
+// copy rate): 25.9 us, 29.7 with a gate (31.9 and 30.7 with a CTA for each row,
+// whose weights are as much L2 traffic as its rows); what is left is the
+// instructions of conversions and sums.  Three CTAs of 256 threads an SM, two
+// vectors a thread: four or one vectors, two CTAs or 512 threads took 27.8 to
+// 38 us.  Otherwise a group takes one row: a decoded token's call (2.1 us),
+// which is bound by the latency of its loads and two sums.
+template <int VPT, bool Q8, int GATE, bool MANY>
+__global__ void __launch_bounds__(VPT == 4 ? 512 : 256, VPT == 4 ? 1 : 3) gated_norm_kernel(GatedParams gp, int rt, int stages) {
   __shared__ float part[2][16];
+  extern __shared__ uint4 ring[];  // [stage][x, residual, gate][vector][thread]
   pdl_wait();
   pdl_trigger();
   const NormParams& p = gp.n;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
   const int ti = threadIdx.x % rt, rw = rt >> 5;
-  const int row = blockIdx.x * (blockDim.x / rt) + threadIdx.x / rt;
-  const bool live = row < p.t;
+  const int step = gridDim.x * (threads / rt);
+  int row = blockIdx.x * (threads / rt) + threadIdx.x / rt;
   const int nv = p.h >> 3;
-  float a[VPT][8];
-  uint4 r[VPT], g[GATE == GATE_CHANNEL ? VPT : 1];
-  float row_gate = 1.f;
-  if (GATE == GATE_ROW && live) row_gate = bf16f(gp.gate.values[(size_t)row * gp.gate.row_stride]);
-  float ss = 0.f;
+  const bool rows_gate = GATE >= GATE_CHANNEL && gp.gate.row_stride > 0;  // a row of gates for each row
+  const uint4 none = make_uint4(0, 0, 0, 0), ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  uint4 post[VPT], gamma[VPT], gate[GATE >= GATE_CHANNEL ? VPT : 1];
+  uint4* const mine = ring + threadIdx.x;
+  const auto fetch = [&](int r, int stage) {
+    uint4* to = mine + stage * 3 * VPT * threads;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = ti + i * rt;
-    const bool on = live && v < nv;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    r[i] = u;
-    if (GATE == GATE_CHANNEL) g[i] = u;
-    if (on) {
-      u = *reinterpret_cast<const uint4*>(p.x + (size_t)row * p.x_stride + 8 * v);
-      if (p.residual) r[i] = *reinterpret_cast<const uint4*>(p.residual + (size_t)row * p.r_stride + 8 * v);
-      if (GATE == GATE_CHANNEL)
-        g[i] = *reinterpret_cast<const uint4*>(gp.gate.values + (size_t)row * gp.gate.row_stride + 8 * v);
-    }
-    const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a[i][2 * j] = bf16lo(uu[j]);
-      a[i][2 * j + 1] = bf16hi(uu[j]);
-      ss = fmaf(a[i][2 * j], a[i][2 * j], ss);
-      ss = fmaf(a[i][2 * j + 1], a[i][2 * j + 1], ss);
-    }
-  }
-  float rstd = 1.f;
-  if (gp.post_gamma) {
-    ss = row_sum(ss, part[0], lane, warp, rw);
-    rstd = 1.f / sqrtf(ss / (float)p.h + p.eps);
-  }
-  if (GATE == GATE_ROW && gp.gate.sigmoid) row_gate = 1.f / (1.f + expf(-row_gate));
-  ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = ti + i * rt;
-    const bool on = live && v < nv;
-    const uint4 w = on && gp.post_gamma ? *reinterpret_cast<const uint4*>(gp.post_gamma + 8 * v)
-                                        : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w}, rr[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-    uint32_t gg[4] = {};
-    if (GATE == GATE_CHANNEL) gg[0] = g[i].x, gg[1] = g[i].y, gg[2] = g[i].z, gg[3] = g[i].w;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float b = a[i][j] * rstd * (j & 1 ? bf16hi(ww[j >> 1]) : bf16lo(ww[j >> 1]));
-      if (GATE == GATE_ROW) b *= row_gate;
-      if (GATE == GATE_CHANNEL) {
-        const float z = j & 1 ? bf16hi(gg[j >> 1]) : bf16lo(gg[j >> 1]);
-        b *= gp.gate.sigmoid ? 1.f / (1.f + expf(-z)) : z;
+    for (int i = 0; i < VPT; ++i) {
+      const int v = ti + i * rt;
+      if (r < p.t && v < nv) {
+        copy16(to + i * threads, p.x + (size_t)r * p.x_stride + 8 * v);
+        if (p.residual) copy16(to + (VPT + i) * threads, p.residual + (size_t)r * p.r_stride + 8 * v);
+        if (rows_gate) copy16(to + (2 * VPT + i) * threads, gp.gate.values + (size_t)r * gp.gate.row_stride + 8 * v);
       }
-      a[i][j] = p.residual ? fmaf(gp.residual_scale, j & 1 ? bf16hi(rr[j >> 1]) : bf16lo(rr[j >> 1]), b) : b;
-      ss = fmaf(a[i][j], a[i][j], ss);
     }
-    if (on && p.sum) *reinterpret_cast<uint4*>(p.sum + (size_t)row * p.h + 8 * v) = pack8(a[i]);
-  }
-  if (!p.y && !Q8) return;  // the same for the whole grid
-  ss = row_sum(ss, part[1], lane, warp, rw);
-  rstd = 1.f / sqrtf(ss / (float)p.h + p.eps);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (MANY)
+    for (int i = 0; i < stages - 1; ++i) fetch(row + i * step, i);
+  uint4 u[VPT], r[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = ti + i * rt;
-    const bool on = live && v < nv;
-    const uint4 w = on ? *reinterpret_cast<const uint4*>(p.gamma + 8 * v) : make_uint4(0, 0, 0, 0);
-    store_normed<Q8>(p.y, p.codes, p.scales, p.h, row, v, on, lane, a[i], rstd, w);
+    const bool on = v < nv && row < p.t;
+    if (!MANY) {
+      u[i] = on ? *reinterpret_cast<const uint4*>(p.x + (size_t)row * p.x_stride + 8 * v) : none;
+      r[i] = on && p.residual ? *reinterpret_cast<const uint4*>(p.residual + (size_t)row * p.r_stride + 8 * v) : none;
+    }
+    if (GATE >= GATE_CHANNEL)
+      gate[i] = on && !(MANY && rows_gate)
+                    ? *reinterpret_cast<const uint4*>(gp.gate.values + (size_t)row * gp.gate.row_stride + 8 * v)
+                    : none;
+    post[i] = on && gp.post_gamma ? *reinterpret_cast<const uint4*>(gp.post_gamma + 8 * v) : ones;
+    gamma[i] = on ? *reinterpret_cast<const uint4*>(p.gamma + 8 * v) : none;
   }
+  int stage = 0;
+  do {
+    const bool live = row < p.t;
+    float row_gate = 1.f;
+    if (GATE == GATE_ROW && live) row_gate = bf16f(gp.gate.values[(size_t)row * gp.gate.row_stride]);
+    if (MANY) {
+      if (stages == 2)
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      else
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      const uint4* from = mine + stage * 3 * VPT * threads;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const bool on = live && ti + i * rt < nv;
+        u[i] = on ? from[i * threads] : none;
+        r[i] = on && p.residual ? from[(VPT + i) * threads] : none;
+        if (GATE >= GATE_CHANNEL && rows_gate) gate[i] = on ? from[(2 * VPT + i) * threads] : none;
+      }
+      const int free = stage == 0 ? stages - 1 : stage - 1;  // read in the last step
+      fetch(row + (stages - 1) * step, free);
+      stage = stage + 1 == stages ? 0 : stage + 1;
+    }
+    float a[VPT][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const uint32_t uu[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a[i][2 * j] = bf16lo(uu[j]);
+        a[i][2 * j + 1] = bf16hi(uu[j]);
+        ss = fmaf(a[i][2 * j], a[i][2 * j], ss);
+        ss = fmaf(a[i][2 * j + 1], a[i][2 * j + 1], ss);
+      }
+    }
+    float rstd = 1.f;
+    if (gp.post_gamma) {
+      ss = row_sum(ss, part[0], lane, warp, rw);
+      rstd = 1.f / sqrtf(ss / (float)p.h + p.eps);
+    }
+    if (GATE == GATE_ROW) rstd *= gp.gate.sigmoid ? sigmoid(row_gate) : row_gate;
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = ti + i * rt;
+      const uint32_t ww[4] = {post[i].x, post[i].y, post[i].z, post[i].w}, rr[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+      uint32_t gg[4] = {};
+      if (GATE >= GATE_CHANNEL) gg[0] = gate[i].x, gg[1] = gate[i].y, gg[2] = gate[i].z, gg[3] = gate[i].w;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float b = a[i][j] * rstd * (j & 1 ? bf16hi(ww[j >> 1]) : bf16lo(ww[j >> 1]));
+        if (GATE >= GATE_CHANNEL) {
+          const float z = j & 1 ? bf16hi(gg[j >> 1]) : bf16lo(gg[j >> 1]);
+          b *= GATE == GATE_SIGMOID ? sigmoid(z) : z;
+        }
+        a[i][j] = p.residual ? fmaf(gp.residual_scale, j & 1 ? bf16hi(rr[j >> 1]) : bf16lo(rr[j >> 1]), b) : b;
+        ss = fmaf(a[i][j], a[i][j], ss);
+      }
+      if (live && v < nv && p.sum) *reinterpret_cast<uint4*>(p.sum + (size_t)row * p.h + 8 * v) = pack8(a[i]);
+    }
+    if (p.y || Q8) {  // the same for the whole grid
+      ss = row_sum(ss, part[1], lane, warp, rw);
+      rstd = 1.f / sqrtf(ss / (float)p.h + p.eps);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = ti + i * rt;
+        store_normed<Q8>(p.y, p.codes, p.scales, p.h, row, v, live && v < nv, lane, a[i], rstd, gamma[i]);
+      }
+    }
+    row += step;
+    // a CTA's groups go on together: the sums have barriers, and one between
+    // two uses of the same places where only one of the sums is taken
+    if (MANY && rw > 1 && !(gp.post_gamma && (p.y || Q8))) __syncthreads();
+  } while (MANY && row - (int)(threadIdx.x / rt) < p.t);
 }
 
 template <int VPT>
 cudaError_t launch_gated(const GatedParams& p, int rt, cudaStream_t s) {
-  const int rows = rt >= 256 ? 1 : 256 / rt;  // rows per CTA
-  const dim3 grid((p.n.t + rows - 1) / rows), block(rt * rows);
-  const auto go = [&](auto q8, auto gate) {
-    cudaError_t e = cudaSuccess;
-    MOE_LAUNCH("gated_rms_norm", s,
-               { e = launch_k(gated_norm_kernel<VPT, decltype(q8)::value, decltype(gate)::value>, grid, block, 0, s, p, rt); });
+  const int rows = rt >= 256 ? 1 : 256 / rt, threads = rt * rows;  // rows at a time of a CTA
+  const int stage_bytes = 3 * VPT * threads * 16, stages = 3 * stage_bytes <= 108 * 1024 ? 3 : 2;
+  // as many CTAs an SM as their rings leave room for, two at least where the registers do
+  const int fit = 220 * 1024 / (stages * stage_bytes), most = VPT < 4 ? 3 : threads > 256 ? 1 : 2;
+  const int full = sm_count() * (fit < most ? fit : most);
+  // rows of the walk: three steps and more, below that a CTA for each row is as good
+  const bool many = p.n.t >= 3 * full * rows;
+  const dim3 grid(many ? full : (p.n.t + rows - 1) / rows), block(threads);
+  const int ring = many ? stages * stage_bytes : 0;
+  const auto go = [&](auto q8, auto gate, auto walk) {
+    const auto kern = gated_norm_kernel<VPT, decltype(q8)::value, decltype(gate)::value, decltype(walk)::value>;
+    cudaError_t e = ring ? set_smem_limit_once(kern, ring) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    MOE_LAUNCH("gated_rms_norm", s, { e = launch_k(kern, grid, block, (size_t)ring, s, p, rt, stages); });
     return e;
   };
+  const auto by_size = [&](auto q8, auto gate) { return many ? go(q8, gate, std::true_type{}) : go(q8, gate, std::false_type{}); };
   const auto by_gate = [&](auto q8) {
-    if (!p.gate.values) return go(q8, std::integral_constant<int, GATE_NONE>{});
-    return p.gate.per_channel ? go(q8, std::integral_constant<int, GATE_CHANNEL>{})
-                              : go(q8, std::integral_constant<int, GATE_ROW>{});
+    if (!p.gate.values) return by_size(q8, std::integral_constant<int, GATE_NONE>{});
+    if (!p.gate.per_channel) return by_size(q8, std::integral_constant<int, GATE_ROW>{});
+    return p.gate.sigmoid ? by_size(q8, std::integral_constant<int, GATE_SIGMOID>{})
+                          : by_size(q8, std::integral_constant<int, GATE_CHANNEL>{});
   };
   return p.n.codes ? by_gate(std::true_type{}) : by_gate(std::false_type{});
 }
@@ -323,7 +396,13 @@ extern "C" int moe_gated_rms_norm(const uint16_t* x, int64_t x_stride, const uin
       return set_error(MOE_ESHAPE, "gate rows must be a multiple of 8 elements apart, not negative");
   }
   if (!isfinite(residual_scale)) return set_error(MOE_EINVAL, "residual_scale is not finite");
-  const int nv = h / 8, vpt = nv <= 256 ? 1 : nv <= 512 ? 2 : 4, rt = row_threads(h, vpt);
+  // As above (so that without a norm or a gate behind the block the two calls
+  // agree to the last bit), but of many short rows a warp takes each: its sums
+  // have no barriers (65536 rows of 512 channels: 59 -> 48 us; of 1024: 112 -> 97).
+  const int nv = h / 8;
+  const bool by_warp = t >= 8192 && nv <= 128;
+  const int vpt = by_warp ? (nv <= 32 ? 1 : nv <= 64 ? 2 : 4) : nv <= 256 ? 1 : nv <= 512 ? 2 : 4;
+  const int rt = row_threads(h, vpt);
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = vpt == 1 ? launch_gated<1>(p, rt, s) : vpt == 2 ? launch_gated<2>(p, rt, s)
                                                                          : launch_gated<4>(p, rt, s);
