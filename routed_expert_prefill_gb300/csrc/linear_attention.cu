@@ -2,6 +2,8 @@
 // recurrent kernel, argument checks and the choice of kernel.
 #include <math.h>
 
+#include <type_traits>
+
 #include "api_checks.cuh"
 #include "linear_common.cuh"
 
@@ -9,79 +11,94 @@ namespace moe {
 
 namespace {
 
-// One sequence and head a CTA, one column j of its state S a thread: S[.][j]
-// stays in D registers while the rows pass, each of which decays it, adds
-// k_i v_j and sums q_i S[i][j].  Columns do not mix, so nothing is joined.
-// With one row a sequence the state's bytes bound it, read and written once
-// (D independent loads of a thread hide the latency); with more, 3 D
-// operations a row and column do.
+// One sequence and head a CTA, half of two columns of its state S a thread:
+// lanes 16 apart share the columns j, j + 1 and hold the rows i below and from
+// D / 2 on.  They stay in D registers while the tokens pass, each of which
+// decays them, adds k_i v_j and sums q_i S[i][j]; the halves of a sum are
+// joined by a shuffle.  With one token a sequence the state's bytes bound it,
+// read and written once, D / 2 independent loads of a thread on their way (64
+// sequences of 32 heads, 268 MB: 0.87 of the copy rate); with more, three
+// operations a value and token do, and the reads of keys and queries from
+// shared memory, one of 16 bytes for eight values.
 template <int D>
 __global__ void __launch_bounds__(D) linear_recurrent_kernel(LinearParams p) {
   __shared__ __align__(16) float kq[2][2][D];
+  constexpr int H = D / 2;  // rows of a thread
   pdl_wait();
   pdl_trigger();
-  const int j = threadIdx.x, head = blockIdx.x % p.hv, s = blockIdx.x / p.hv;
+  const int tid = threadIdx.x, lane = tid & 31, head = blockIdx.x % p.hv, s = blockIdx.x / p.hv;
+  const int i0 = (lane >> 4) * H, j = 2 * ((tid >> 5) * 16 + (lane & 15));
   int row, n, slot_in, slot_out;
   if (!linear_sequence(p, s, row, n, slot_in, slot_out)) {
-    if (j == 0) raise_flag(p.st, FLAG_BAD_STATE);
+    if (tid == 0) raise_flag(p.st, FLAG_BAD_STATE);
     return;
   }
   if (n == 0 && slot_in == slot_out) return;
-  float S[D];
+  float2 S[H];
   if (slot_in >= 0) {
-    const float* from = p.states + ((size_t)slot_in * p.hv + head) * D * D + j;
+    const float2* from = reinterpret_cast<const float2*>(p.states + ((size_t)slot_in * p.hv + head) * D * D + i0 * D + j);
 #pragma unroll
-    for (int i = 0; i < D; ++i) S[i] = __ldcs(from + i * D);
+    for (int i = 0; i < H; ++i) S[i] = __ldcs(from + i * (D / 2));
   } else {
 #pragma unroll
-    for (int i = 0; i < D; ++i) S[i] = 0.f;
+    for (int i = 0; i < H; ++i) S[i] = make_float2(0.f, 0.f);
   }
   const int hk = head / (p.hv / p.hk);
-  const uint16_t* q = p.q + (size_t)row * p.q_stride + hk * D + j;
-  const uint16_t* k = p.k + (size_t)row * p.k_stride + hk * D + j;
-  const uint16_t* v = p.v + (size_t)row * p.v_stride + head * D + j;
+  const uint16_t* q = p.q + (size_t)row * p.q_stride + hk * D + tid;
+  const uint16_t* k = p.k + (size_t)row * p.k_stride + hk * D + tid;
+  const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + (size_t)row * p.v_stride + head * D + j);
   const float* g = p.log_decay + (size_t)row * p.decay_stride + head;
-  uint16_t* out = p.out + ((size_t)row * p.hv + head) * D + j;
-  uint16_t nq = 0, nk = 0, nv = 0;
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + ((size_t)row * p.hv + head) * D + j);
+  uint16_t nq = 0, nk = 0;
+  uint32_t nv = 0;
   float ng = 0.f;
   if (n) nq = *q, nk = *k, nv = *v, ng = *g;
   for (int r = 0; r < n; ++r) {
     float(*at)[D] = kq[r & 1];
-    at[0][j] = bf16f(nk);
-    at[1][j] = bf16f(nq);
-    const float vj = bf16f(nv), gr = decay_of(ng);
+    at[0][tid] = bf16f(nk);
+    at[1][tid] = bf16f(nq);
+    const float va = bf16lo(nv), vb = bf16hi(nv), gr = decay_of(ng);
     __syncthreads();
     if (r + 1 < n) {
-      q += p.q_stride, k += p.k_stride, v += p.v_stride, g += p.decay_stride;
+      q += p.q_stride, k += p.k_stride, v += p.v_stride / 2, g += p.decay_stride;
       nq = *q, nk = *k, nv = *v, ng = *g;
     }
-    float o[4] = {};
     // S exp(g) is S + S (exp(g) - 1) for a slow decay: exp(g) rounded to fp32
-    // would be off by the same 2^-25 in every row, over 1 / (1 - exp(g)) rows
+    // would be off by the same 2^-25 for every token, over 1 / (1 - exp(g)) of them
     const bool slow = gr > -0.5f;
     const float f = slow ? expm1f(gr) : expf(gr);
-#define MOE_LINEAR_ROW(STEP)                                                                                          \
-  _Pragma("unroll") for (int i = 0; i < D; i += 4) {                                                                  \
-    const float4 kk = *reinterpret_cast<const float4*>(&at[0][i]), qq = *reinterpret_cast<const float4*>(&at[1][i]);  \
-    S[i] = STEP(S[i], kk.x), o[0] = fmaf(qq.x, S[i], o[0]);                                                           \
-    S[i + 1] = STEP(S[i + 1], kk.y), o[1] = fmaf(qq.y, S[i + 1], o[1]);                                               \
-    S[i + 2] = STEP(S[i + 2], kk.z), o[2] = fmaf(qq.z, S[i + 2], o[2]);                                               \
-    S[i + 3] = STEP(S[i + 3], kk.w), o[3] = fmaf(qq.w, S[i + 3], o[3]);                                               \
-  }
-#define MOE_LINEAR_SLOW(s, kk) fmaf(s, f, fmaf(kk, vj, s))
-#define MOE_LINEAR_FAST(s, kk) fmaf(s, f, kk * vj)
-    if (slow) {
-      MOE_LINEAR_ROW(MOE_LINEAR_SLOW)
-    } else {
-      MOE_LINEAR_ROW(MOE_LINEAR_FAST)
-    }
-    *out = f2bf(p.scale * ((o[0] + o[1]) + (o[2] + o[3])));
-    out += (size_t)p.hv * D;
+    float x = 0.f, y = 0.f;
+    const auto take = [&](auto is_slow) {
+      float oa[2] = {}, ob[2] = {};
+#pragma unroll
+      for (int i = 0; i < H; i += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(&at[0][i0 + i]), q4 = *reinterpret_cast<const float4*>(&at[1][i0 + i]);
+        const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          float2& a = S[i + h];
+          a.x = fmaf(a.x, f, decltype(is_slow)::value ? fmaf(kk[h], va, a.x) : kk[h] * va);
+          a.y = fmaf(a.y, f, decltype(is_slow)::value ? fmaf(kk[h], vb, a.y) : kk[h] * vb);
+          oa[h & 1] = fmaf(qq[h], a.x, oa[h & 1]);
+          ob[h & 1] = fmaf(qq[h], a.y, ob[h & 1]);
+        }
+      }
+      x = oa[0] + oa[1];
+      y = ob[0] + ob[1];
+    };
+    if (slow)  // the same for the whole CTA
+      take(std::true_type{});
+    else
+      take(std::false_type{});
+    x += __shfl_xor_sync(~0u, x, 16);
+    y += __shfl_xor_sync(~0u, y, 16);
+    if (lane < 16) *out = pack_bf16x2(p.scale * x, p.scale * y);
+    out += (size_t)p.hv * D / 2;
   }
   if (slot_out >= 0) {
-    float* to = p.states + ((size_t)slot_out * p.hv + head) * D * D + j;
+    float2* to = reinterpret_cast<float2*>(p.states + ((size_t)slot_out * p.hv + head) * D * D + i0 * D + j);
 #pragma unroll
-    for (int i = 0; i < D; ++i) __stcs(to + i * D, S[i]);
+    for (int i = 0; i < H; ++i) __stcs(to + i * (D / 2), S[i]);
   }
 }
 
@@ -104,8 +121,9 @@ namespace {
 
 size_t linear_ws_bytes(int d) { return sizeof(DeviceStatus) + linear_chunk_ws_bytes(d); }
 
-// Rows of a sequence on average, from which on the chunk kernel takes the call.
-constexpr int CHUNK_ROWS = 24;
+// Rows of a sequence on average, from which on the chunk kernel takes the call
+// (a chunk of 128 takes as long however few of them are rows).
+constexpr int chunk_rows(int d) { return d == 128 ? 24 : 40; }
 
 }  // namespace
 
@@ -151,7 +169,7 @@ int moe_linear_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k,
   cudaStream_t s = (cudaStream_t)stream;
   // rows that lie over one another (one row for all) are no tiles
   const bool apart = q_stride >= (int64_t)hk * d && k_stride >= (int64_t)hk * d && v_stride >= (int64_t)hv * d;
-  const cudaError_t e = apart && t > (int64_t)CHUNK_ROWS * n_seq
+  const cudaError_t e = apart && t > (int64_t)chunk_rows(d) * n_seq
                             ? launch_linear_chunk(p, d, (unsigned char*)ws + sizeof(DeviceStatus), s)
                             : launch_linear_recurrent(p, d, s);
   return cuda_status(e, "moe_linear_attention launch");
