@@ -13,10 +13,10 @@ namespace {
 
 constexpr int LP_THREADS = 256;
 constexpr int LP_ELEMS = 16;      // elements of a thread's part of a tile
-constexpr int LP_RING = 16;       // 16-byte vectors of a thread on their way or in use
-constexpr int LP_GROUP = 4;       // tiles between two rankings
+constexpr int LP_RING = 12;       // 16-byte vectors of a thread on their way or in use
+constexpr int LP_GROUP = 8;       // tiles between two rankings, at most
 constexpr int LP_TOP = 32;        // alternatives, at most
-constexpr int LP_CAND = 1024;     // candidates that wait to be ranked
+constexpr int LP_CAND = 512;      // candidates that wait to be ranked
 constexpr int LP_CLUSTER = 8;     // CTAs of a row, at most
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float FAR = -1e30f;     // stands for -inf where it is multiplied by zero
@@ -98,7 +98,7 @@ struct Shared {
   uint64_t best[LP_TOP];
   Stats part[LP_THREADS / 32];
   Stats all;
-  float group[32];
+  alignas(16) float group[32];
   float thr;  // the top-th largest value so far, once there are as many; -inf before
   int count;
   int total;
@@ -120,12 +120,16 @@ __device__ __forceinline__ void copies_wait() {
 // order; returns how many there are.  All threads call it after a barrier;
 // what it leaves is visible to all.
 __device__ int rank_candidates(Shared& sh, int top) {
-  const int c = sh.count;
-  for (int i = threadIdx.x; i < c; i += LP_THREADS) {
-    const uint64_t mine = sh.cand[i];
+  const int c = sh.count, quarter = threadIdx.x & 3;
+  for (int i0 = 0; i0 < c; i0 += LP_THREADS / 4) {  // four threads a candidate
+    const int i = i0 + (threadIdx.x >> 2);
+    const uint64_t mine = i < c ? sh.cand[i] : ~0ull;
     int rank = 0;
-    for (int j = 0; j < c; ++j) rank += sh.cand[j] > mine;
-    if (rank < top) sh.best[rank] = mine;
+#pragma unroll 4
+    for (int j = quarter; j < c; j += 4) rank += sh.cand[j] > mine;
+    rank += __shfl_xor_sync(~0u, rank, 1);
+    rank += __shfl_xor_sync(~0u, rank, 2);
+    if (quarter == 0 && i < c && rank < top) sh.best[rank] = mine;
   }
   __syncthreads();
   const int kept = min(c, top);
@@ -154,7 +158,7 @@ __device__ int rank_candidates(Shared& sh, int top) {
 // reached by as many elements.  -inf never becomes a candidate; a row that has
 // too few other values is filled up at the end.
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS, 3) logprobs_kernel(LogprobParams p, int csize) {
+__global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(LogprobParams p, int csize) {
   __shared__ Shared sh;
   extern __shared__ uint4 ring[];  // [stage][vector][thread]
   constexpr int N = Vec<T>::N, E = LP_ELEMS, VECS = E / N, TILE = LP_THREADS * VECS, STAGES = LP_RING / VECS;
@@ -214,23 +218,19 @@ __global__ void __launch_bounds__(LP_THREADS, 3) logprobs_kernel(LogprobParams p
     __syncthreads();
     g = sh.group[lane];
     int above = 0;
-#pragma unroll 8
-    for (int j = 0; j < 32; ++j) {
-      const float o = __shfl_sync(~0u, g, j);
-      above += o > g || (o == g && j < lane);
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(sh.group + j);
+      above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g) + (o.x == g & j < lane) + (o.y == g & j + 1 < lane) +
+               (o.z == g & j + 2 < lane) + (o.w == g & j + 3 < lane);
     }
     const uint32_t who = __ballot_sync(~0u, above == p.top - 1);
     return __shfl_sync(~0u, g, __ffs(who) - 1);
   };
-  // The elements above thr (ties: or equal to it) become candidates; those past the list's end are dropped, but counted.
-  const auto add = [&](const float* e, auto index, float thr, bool ties) {
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (e[i] > -INFINITY && (e[i] > thr || (ties && e[i] == thr))) {
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < LP_CAND) sh.cand[at] = key_of(e[i], index(i));
-        fresh = true;
-      }
+  const auto add = [&](float f, int index) {  // past the list's end it is dropped, but counted
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < LP_CAND) sh.cand[at] = key_of(f, index);
+    fresh = true;
   };
   const auto index_at = [&](int v0) {
     const int first = head + (v0 + tid) * N;
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(LP_THREADS, 3) logprobs_kernel(LogprobParams p
     }
   };
 
-  int stage = 0, group = 0, first_v = rank * TILE;
+  int stage = 0, group = 0, length = 1, first_v = rank * TILE;
   float thr = -INFINITY;
   for (int v0 = rank * TILE; v0 < nv; v0 += csize * TILE) {
     copies_wait<STAGES - 2>();
@@ -294,16 +294,27 @@ __global__ void __launch_bounds__(LP_THREADS, 3) logprobs_kernel(LogprobParams p
         for (int i = 0; i < N; ++i) e[j * N + i] = -INFINITY;
       }
     }
+    const float lm = sums(e);
+    const T* part = reinterpret_cast<const T*>(ring + stage * VECS * LP_THREADS);
     fetch(v0 + (STAGES - 1) * csize * TILE, (stage + STAGES - 1) % STAGES);
     stage = (stage + 1) % STAGES;
-    const float lm = sums(e);
     if (!TOP) continue;
     if (group == 0) thr = sh.thr;
     const bool loose = thr == -INFINITY;  // the same for the whole CTA
     const float least = loose ? bound(lm) : thr;
-    if (lm > least || (loose && lm == least)) add(e, index_at(v0), least, loose);
-    if (loose || ++group == LP_GROUP || v0 + csize * TILE >= nv) {
+    if (lm > -INFINITY && (lm > least || (loose && lm == least))) {
+      const auto index = index_at(v0);
+      uint32_t which = 0;
+#pragma unroll
+      for (int i = 0; i < E; ++i) which |= (uint32_t)(e[i] > least || (loose && e[i] == least && e[i] > -INFINITY)) << i;
+      for (; which; which &= which - 1) {  // one at a time, read again: few threads have any
+        const int i = __ffs(which) - 1;
+        add(Vec<T>::load(part + (i / N * LP_THREADS + tid) * N + i % N), index(i));
+      }
+    }
+    if (loose || ++group == length || v0 + csize * TILE >= nv) {
       settle(first_v, v0 + 1);
+      if (!loose && length < LP_GROUP) length *= 2;
       group = 0;
       first_v = v0 + csize * TILE;
     }
@@ -316,7 +327,7 @@ __global__ void __launch_bounds__(LP_THREADS, 3) logprobs_kernel(LogprobParams p
     if (tid < edge) e[0] = Vec<T>::load(x + at);
     sums(e);
     if (TOP) {
-      add(e, [&](int) { return at; }, sh.thr, true);  // too few to overflow the list
+      if (e[0] > -INFINITY && e[0] >= sh.thr) add(e[0], at);  // too few to overflow the list
       settle(0, 0);
     }
   }
