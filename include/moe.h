@@ -486,7 +486,8 @@ int moe_read_device_status(void* ws, void* stream);
  *     warps of moe_kv_attention's tensor-core kernel in its first CTA (the
  *     others go on, so what is joined across CTAs is left in between);
  *   MOE_STALL_GRID_BARRIER: the grid barrier of the fused decode launch
- *     waits for one arrival more than the grid has.
+ *     waits for one arrival more than the grid has; the first CTA of
+ *     moe_linear_attention's tensor-core kernel does not hand on its state.
  * Each such wait gives up after its limit (2 s of device time), records
  * MOE_ETIMEOUT, and its CTA lets the copies and MMAs in flight land, frees
  * its tensor memory and returns; later calls on a cleared workspace run
