@@ -18,8 +18,7 @@ constexpr int CHUNK = 128;
 // Warps: 0-7 compute, 8 issues the products, 9 works out the decays, 10 brings
 // the tiles, 11 takes the results away.  Registers: 384 * 168 at launch, 256 *
 // 208 + 128 * 88 after the split.
-constexpr int LC_COMPUTE = 256, LC_THREADS = 384, W_ISSUE = 8, W_GAIN = 9, W_LOAD = 10,
-              W_STORE = 11;
+constexpr int LC_COMPUTE = 256, LC_THREADS = 384, W_ISSUE = 8, W_GAIN = 9, W_LOAD = 10, W_STORE = 11;
 constexpr int LC_REGS = 208, LC_REGS_REST = 88;
 constexpr uint64_t LC_WAIT_NS = 2000000000ull;
 constexpr float LOG2E = 1.44269502f, LOG2E_REST = 1.92596299e-8f, LN2 = 0.693147181f;
@@ -108,6 +107,9 @@ struct Lc {
   static constexpr int T_S = 0, T_SQ = 128, T_PV = 128 + D, T_DS = 128 + 2 * D;
 };
 static_assert(Lc<128>::TOTAL <= 227 * 1024, "shared memory of a CTA");
+// CTAs wait for one another's states; two calls that run at once must not also
+// wait for one another's tensor memory, so no SM has room for two CTAs.
+static_assert(2 * (Lc<64>::TOTAL + 1024) > 228 * 1024, "one CTA an SM");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -285,9 +287,16 @@ __device__ __noinline__ float weighted_values(const LinearParams& p, int d, int 
 // whole run lies inside a chain, what it adds is worked out first, without
 // results.
 //
-// What bounds it: of a chunk's some 4100 clocks of products (D = 128), all but
-// the state's own chain (sum, conversion, products with the keys) run beside
-// the conversions.
+// What bounds it (D = 128): a chunk takes some 11800 clocks.  Its 64 products
+// of 128 x 128 x 16 take 6500 (100 each beside the conversions' traffic, 66
+// alone) and shared memory moves 800 KB, 6300 clocks' worth, more than half of
+// it the products' operands; the conversions (weights, keys in three parts, the
+// state in two) are as long as the products and overlap with them in part:
+// queries times state beside the weights, weights times values beside the
+// keys, keys times values beside the results.  Six prompts of 13355 rows and 32
+// heads, 355 MB: 148 us, 0.35 of the copy rate; heads of 64 take 6800 clocks a
+// chunk.  Slower: 16 compute warps of 96 registers (158 us), the keys' parts in
+// bf16 arithmetic (154), a chunk's code unrolled (180 KB; 208).
 template <int D>
 __global__ void __launch_bounds__(LC_THREADS, 1)
     linear_chunk_kernel(const __grid_constant__ ChunkParams cp, const __grid_constant__ CUtensorMap tm_q,

@@ -149,14 +149,18 @@ __device__ int rank_candidates(Shared& sh, int top) {
 // Sums: a thread rebases its sums where its part of a tile has a new maximum,
 // so that an element costs one exponential.  Alternatives: an element becomes
 // a candidate if it is above the top-th largest value so far, which a thread
-// first asks of its part's maximum; after LP_GROUP tiles the candidates are
-// ranked, which gives the next bound (a barrier after every tile instead of
-// four cost 2048 rows of 131072 logits 110 us of 280).  A CTA's elements come in
+// first asks of its part's maximum; after 1, 2, 4, 8, 8, ... tiles the
+// candidates are ranked, which gives the next bound.  A CTA's elements come in
 // ascending order, tile by tile, so that an equal value of a later group takes
 // no earlier one's place.  While there are too few candidates for a bound, the
 // maxima of 32 groups of threads give one: the top-th largest of them is
 // reached by as many elements.  -inf never becomes a candidate; a row that has
 // too few other values is filled up at the end.
+//
+// 2048 rows of 131072 fp32 logits, 1074 MB: 152 us without alternatives (the
+// copy rate), 159 with five, 170 with twenty.  A ranking after every tile took
+// 280, after every fourth 197 (three CTAs an SM).  One row by eight CTAs: 4.6
+// and 9.3 us, the latency of its barriers.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(LogprobParams p, int csize) {
   __shared__ Shared sh;
