@@ -757,7 +757,8 @@ size_t moe_kv_plan_workspace_bytes(int32_t n_seq);
  * key head a / (hv / hk).  q, k bf16 [t][hk][d], v bf16 [t][hv][d], heads
  * contiguous, rows `*_stride` elements apart (multiples of 8); log_decay fp32
  * [t][hv], rows decay_stride apart (0: one value a head for all rows); a value
- * above zero counts as zero.  out bf16 [t][hv][d].  Sequence s owns rows
+ * above zero counts as zero.  out bf16 [t][hv][d], apart from the inputs (heads
+ * share them).  Sequence s owns rows
  * starts[s] .. starts[s+1]-1 (starts int32 [n_seq+1], device); rows that no
  * sequence owns are not read, and their results are not written.
  *
@@ -770,7 +771,8 @@ size_t moe_kv_plan_workspace_bytes(int32_t n_seq);
  *
  * Sums and states are fp32, the result is rounded once.  An infinity or NaN in
  * a row's q, k or v shows in that row's results and, from k or v, in those
- * behind it and in the state; rows before it are not touched.
+ * behind it and in the state (so does a NaN in log_decay); rows before it are
+ * not touched.
  *
  * Starts or slots out of range leave their sequence's rows and state
  * unwritten and raise MOE_EDEVICE in moe_read_device_status.

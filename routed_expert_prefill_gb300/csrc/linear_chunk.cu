@@ -26,6 +26,9 @@ constexpr float NOT_A_NUMBER = __builtin_nanf("");
 // A row's log2 decay as it counts: below it the state of one row is 0 in the
 // next whatever it was (2^-512 of an fp32 number).
 constexpr float LEAST = -512.f;
+// How far a key's factor may go above 1 (log2): beside scores and values, far
+// from the end of fp32's range; what passes it all the same is worked out again.
+constexpr float MILD = 40.f;
 
 // What one CTA leaves for those that go on with its last chain: the state
 // behind its part (or, if its part does not begin the chain, what the part
@@ -69,11 +72,14 @@ struct Ticket {
 
 // The decays of a chunk's rows: G_i is the log2 of the product of rows 0 .. i's.
 struct alignas(16) Gains {  // read four at a time
-  float rel[CHUNK];    // G_i less that of the first of its 32 rows
+  // with R_i = G_i less that of the first of its 32 rows: 2^-R_i where none of
+  // the 32 is above 2^MILD (bit i / 32 of mild), else R_i
+  float own[CHUNK];
   float last[CHUNK];   // 2^(G_127 - G_i)
   float first[CHUNK];  // 2^G_i
   float off[192];      // rows 32 q .. of q = 1, 2, 3, for i < 32 q: 2^(G_32q - G_i)
   float n, f;          // G_127, whole part and rest
+  uint32_t mild;
   float keep, slow;    // a state is multiplied by keep + slow = 2^G_127; slow is 1 for slow decays, else 0
   Ticket chunk;
 };
@@ -620,10 +626,13 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         bool bad[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) bad[i] = (nans & ((1u << lane) - 1)) || (i ? bad[i - 1] : false) || g[i] != g[i];
-        float rel[4], last[4], first[4], off[3][4];
+        float own[4], last[4], first[4], off[3][4];
+        const bool mild = value(__shfl_sync(~0u, v[3], lane | 7) - ref0) >= -MILD;
+        const uint32_t milds = __ballot_sync(~0u, mild);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          rel[i] = value(v[i] - ref0);
+          const float rel = value(v[i] - ref0);
+          own[i] = mild ? ex2(-rel) : rel;
           last[i] = nans ? NOT_A_NUMBER : ex2(value(end - v[i]));
           first[i] = bad[i] ? NOT_A_NUMBER : ex2(value(v[i]));
         }
@@ -638,11 +647,11 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         float keep = nans ? NOT_A_NUMBER : slow ? expm1f(whole * LN2) : exp2f(whole);
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // worked out before the wait, not behind it
-          asm volatile("" : "+f"(rel[i]), "+f"(last[i]), "+f"(first[i]), "+f"(off[0][i]), "+f"(off[1][i]), "+f"(off[2][i]), "+f"(keep));
+          asm volatile("" : "+f"(own[i]), "+f"(last[i]), "+f"(first[i]), "+f"(off[0][i]), "+f"(off[1][i]), "+f"(off[2][i]), "+f"(keep));
         if (!wait(&sh.g_empty, f_empty, 67)) break;
         Gains& to = sh.g;
         const int r = 4 * lane;
-        *reinterpret_cast<float4*>(&to.rel[r]) = make_float4(rel[0], rel[1], rel[2], rel[3]);
+        *reinterpret_cast<float4*>(&to.own[r]) = make_float4(own[0], own[1], own[2], own[3]);
         *reinterpret_cast<float4*>(&to.last[r]) = make_float4(last[0], last[1], last[2], last[3]);
         *reinterpret_cast<float4*>(&to.first[r]) = make_float4(first[0], first[1], first[2], first[3]);
 #pragma unroll
@@ -653,6 +662,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           const long long n = end >> 40;
           to.n = nans ? NOT_A_NUMBER : (float)n;
           to.f = value(end - (n << 40));
+          to.mild = (milds & 1) | (milds >> 8 & 1) << 1 | (milds >> 16 & 1) << 2 | (milds >> 24 & 1) << 3;
           to.keep = keep;
           to.slow = slow ? 1.f : 0.f;
         }
@@ -746,6 +756,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       const bool full = t.full;
       const int rows = t.rows;
       const float keep = sh.g.keep, slow = sh.g.slow;
+      const bool mild = sh.g.mild >> quarter & 1;
       if (t.begins) {
         decay_n = decay_f = 0.f;
         if (t.stage == 2) {
@@ -767,11 +778,13 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       decay_f += sh.g.f;
       if (full) {
         // weights: scores times the decays between key and query, in two bf16
-        // parts over the scores' own columns.  Keys that all of the warp's rows
-        // are behind take a row's and a key's factor.
+        // parts over the scores' own columns.  The decay is a row's factor
+        // times a key's, both relative to the first of the warp's rows; the
+        // row's waits for the results, unless that would make the keys' of the
+        // warp's own rows too large.
         if (!wait(&sh.qk_done, f_sc, 71)) break;
         tc_fence_after();
-        const float rel = sh.g.rel[row], mine = ex2(rel);
+        const float own = sh.g.own[row], mine = mild ? 1.f : ex2(own);
         // The loops over blocks stay loops: unrolled, a chunk is some 80 KB of
         // code, and fetching it takes longer than running it.
 #pragma unroll 1
@@ -788,22 +801,23 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           tmem_ld_fence(z[0]);
           tmem_ld_fence(z[1]);
           const bool all = j0 < 32 * quarter;
-          const float* by = all ? &sh.g.off[16 * quarter * (quarter - 1) + j0] : &sh.g.rel[j0];
+          if (!all) {  // a score counts only where its key is seen, whatever it is
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i >> 4][i & 15] = i <= lane ? z[i >> 4][i & 15] : 0;
+          }
+          const float* by = all ? &sh.g.off[16 * quarter * (quarter - 1) + j0] : &sh.g.own[j0];
           uint32_t w[32];  // of 16 keys each: eight columns of first parts, eight of second ones
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float4 f = *reinterpret_cast<const float4*>(by + 4 * i);
-            uint32_t* s = &z[i >> 2][4 * (i & 3)];
-            if (all) {
-              const float2 u = mul2(make_float2(f.x, f.y), both(mine)), v = mul2(make_float2(f.z, f.w), both(mine));
-              f = make_float4(u.x, u.y, v.x, v.y);
-            } else {  // a score counts only where its key is seen, whatever it is
-              const int j = 4 * i;
-              f.x = j <= lane ? ex2(rel - f.x) : 0.f, s[0] = j <= lane ? s[0] : 0;
-              f.y = j + 1 <= lane ? ex2(rel - f.y) : 0.f, s[1] = j + 1 <= lane ? s[1] : 0;
-              f.z = j + 2 <= lane ? ex2(rel - f.z) : 0.f, s[2] = j + 2 <= lane ? s[2] : 0;
-              f.w = j + 3 <= lane ? ex2(rel - f.w) : 0.f, s[3] = j + 3 <= lane ? s[3] : 0;
+            if (!mild) {
+              if (all)
+                f = make_float4(f.x * mine, f.y * mine, f.z * mine, f.w * mine);
+              else  // (of keys behind the row, not above 1)
+                f = make_float4(ex2(fminf(own - f.x, 0.f)), ex2(fminf(own - f.y, 0.f)), ex2(fminf(own - f.z, 0.f)),
+                                ex2(fminf(own - f.w, 0.f)));
             }
+            const uint32_t* s = &z[i >> 2][4 * (i & 3)];
             float2 u = mul2(pair(s), make_float2(f.x, f.y)), v = mul2(pair(s + 2), make_float2(f.z, f.w));
             uint32_t* o = w + 16 * (i >> 2) + 2 * (i & 3);
             o[0] = take_rounded(u);
@@ -815,8 +829,10 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         }
         tmem_st_wait();
       }
-      if (!wait(&sh.qk_full[buf], f_qk[buf], 72) || !wait(&sh.v_full, f_v, 73)) break;
+      if (!wait(&sh.qk_full[buf], f_qk[buf], 72)) break;
       if (rows < CHUNK) {  // rows of no sequence or of another
+        if (!wait(&sh.v_full, f_v, 73)) break;
+        f_v ^= 1;  // taken back below
         for (int e = tid; e < (CHUNK - max(rows, 0)) * (D / 8); e += LC_COMPUTE) {
           const int r = CHUNK - 1 - e / (D / 8), ch = e % (D / 8);
           const int to = (ch >> 3) * L::HALF + sw128_off(r, ch & 7);
@@ -825,6 +841,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         fence_async_smem();
         sync();
       }
+      f_v ^= 1;  // this chunk's
       if (full) {
         tc_fence_before();
         arrive(&sh.p_ready);
@@ -861,7 +878,8 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       fence_async_smem();
       arrive(&sh.k_ready);
       if (full) {
-        const float first = sh.g.first[row];
+        const float first = sh.g.first[row], mine = mild ? __frcp_rn(sh.g.own[row]) : 1.f;
+        arrive(&sh.g_empty);  // all of the chunk's decays have been read
         if (!wait(&sh.pv_done, f_pv, 75)) break;
         tc_fence_after();
         uint16_t* out = p.out + ((size_t)(t.row + row) * p.hv + t.head) * D;
@@ -890,7 +908,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               finite = fma2(pair(y[h] + i), both(0.f), finite);
-              const float2 v = mul2(fma2(pair(x[h] + i), both(first), pair(y[h] + i)), both(p.scale));
+              const float2 v = fma2(pair(x[h] + i), both(p.scale * first), mul2(pair(y[h] + i), both(p.scale * mine)));
               o[i / 2] = pack_bf16x2(v.x, v.y);
             }
             put(col + 16 * h, make_uint4(o[0], o[1], o[2], o[3]));
@@ -910,8 +928,9 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         }
         fence_async_smem();
         arrive(&sh.o_ready);
+      } else {
+        arrive(&sh.g_empty);
       }
-      arrive(&sh.g_empty);
       if (!wait(&sh.ds_done, f_ds, 76)) break;
       tc_fence_after();
       // a slow decay as in the recurrent kernel

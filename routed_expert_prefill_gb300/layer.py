@@ -560,7 +560,7 @@ def moe_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     Sequence s begins from the state in slot ``slots[s]`` (int32 [n_seq]; -1:
     zero; default: slot s) and leaves its last one in ``slots_out[s]`` (-1:
     nowhere; default: the same slots).  ``scale`` defaults to 1 / sqrt(d).
-    Returns bf16 [t, hv, d].
+    Returns bf16 [t, hv, d] (``out``, which does not overlap the inputs).
     """
     lib = load_library()
     if not isinstance(state, LinearState):

@@ -151,6 +151,45 @@ def test_linear_attention_states_past_32_bits(layer):
     assert not states[:-2].any() and state.read_device_status() == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_linear_attention_two_calls_at_once(layer, d):
+    """Pools of their own on streams of their own, each call's CTAs waiting for one another's states."""
+    g = gen(31)
+    calls = []
+    for n, hv in ((1500, 3), (1100, 5)):
+        q, k, v = (randn(g, n, hv, d).bfloat16() for _ in range(3))
+        logs = -0.1 * torch.rand(n, hv, generator=g, device="cuda")
+        starts = i32([0, n // 3, n])
+        state = layer.LinearState.new(2, hv, d)
+        out = layer.moe_linear_attention(q, k, v, logs, starts, state)
+        calls.append((q, k, v, logs, starts, out, state.states.clone(), layer.LinearState.new(2, hv, d), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for q, k, v, logs, starts, _, _, state, stream in calls:
+            with torch.cuda.stream(stream):
+                state.states.zero_()
+                got.append(layer.moe_linear_attention(q, k, v, logs, starts, state))
+        torch.cuda.synchronize()
+        for out, (*_, ref, states, state, _) in zip(got, calls):
+            assert torch.equal(out, ref) and torch.equal(state.states, states) and state.read_device_status() == 0
+
+
+@pytest.mark.parametrize("n", [6, 250])
+def test_linear_attention_decay_that_is_nan(layer, n):
+    """From its row on that head is NaN; rows before it and other heads are not touched."""
+    g = gen(17)
+    q, k, v = (randn(g, n, 2, 64).bfloat16() for _ in range(3))
+    logs = torch.full((n, 2), -0.1, device="cuda")
+    a, b = layer.LinearState.new(1, 2, 64), layer.LinearState.new(1, 2, 64)
+    ref = layer.moe_linear_attention(q, k, v, logs, i32([0, n]), a)
+    logs[n // 2, 0] = math.nan
+    out = layer.moe_linear_attention(q, k, v, logs, i32([0, n]), b)
+    assert torch.equal(out[:, 1], ref[:, 1]) and torch.equal(b.states[:, 1], a.states[:, 1])
+    assert torch.equal(out[:n // 2, 0], ref[:n // 2, 0])
+    assert out[n // 2:, 0].isnan().all() and b.states[0, 0].isnan().all()
+
+
 def test_two_pools_in_one_captured_graph(layer):
     """Calls of both kernels in a graph, replayed while the same leaves are used eagerly between."""
     g = gen(14)
