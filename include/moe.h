@@ -769,10 +769,11 @@ size_t moe_kv_plan_workspace_bytes(int32_t n_seq);
  * states are kept in place.  A slot that is written is named once in
  * slots_out, and no other sequence reads it in the same call.
  *
- * Sums and states are fp32, the result is rounded once.  An infinity or NaN in
- * a row's q, k or v shows in that row's results and, from k or v, in those
- * behind it and in the state (so does a NaN in log_decay); rows before it are
- * not touched.
+ * Sums, states and, in calls of many rows, the products of q and k are fp32
+ * (values whose products pass its range do not belong here), the result is
+ * rounded once.  An infinity or NaN in a row's q, k or v shows in that row's
+ * results and, from k or v, in those behind it and in the state (so does a NaN
+ * in log_decay); rows before it are not touched.
  *
  * Starts or slots out of range leave their sequence's rows and state
  * unwritten and raise MOE_EDEVICE in moe_read_device_status.

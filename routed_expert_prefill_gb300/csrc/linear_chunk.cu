@@ -89,6 +89,7 @@ struct LcShared {
   uint64_t qk_done, sq_done, pv_done, ds_done;  // products
   uint64_t s_ready, p_ready, k_ready, o_ready;  // their operands, and the results
   uint64_t q_free;                              // the results have been read
+  uint64_t met;                                 // the compute warps, all of them
   uint64_t drain;
   Gains g;
   Part first, last;
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       for (uint64_t* b : {&sh.qk_full[0], &sh.qk_full[1], &sh.v_full, &sh.g_full, &sh.qk_done, &sh.sq_done, &sh.pv_done,
                           &sh.ds_done, &sh.drain, &sh.q_free})
         mbar_init(b, 1);
-      for (uint64_t* b : {&sh.g_empty, &sh.s_ready, &sh.p_ready, &sh.k_ready, &sh.o_ready}) mbar_init(b, LC_COMPUTE / 32);
+      for (uint64_t* b : {&sh.g_empty, &sh.s_ready, &sh.p_ready, &sh.k_ready, &sh.o_ready, &sh.met}) mbar_init(b, LC_COMPUTE / 32);
       fence_mbar_init();
       sh.abort = 0;
     }
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
     const int quarter = warp & 3, group = warp >> 2;
     const int row = 32 * quarter + lane;  // of the chunk, in the products whose rows are the queries'
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-    uint32_t f_qk[2] = {}, f_v = 0, f_g = 0, f_sc = 0, f_sq = 0, f_pv = 0, f_ds = 0;
+    uint32_t f_qk[2] = {}, f_v = 0, f_g = 0, f_sc = 0, f_sq = 0, f_pv = 0, f_ds = 0, f_met = 0;
     float S[NC];
     // rows of the state in TMEM: lanes, the upper 64 a copy of the lower with D = 64
     const int s_row = row % D;
@@ -691,7 +692,11 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    const auto sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(LC_COMPUTE) : "memory"); };
+    // All compute warps; bounded like every wait, since a warp that gave up does not come.
+    const auto meet = [&]() {
+      arrive(&sh.met);
+      return wait(&sh.met, f_met, 77);
+    };
     const auto write_state = [&]() {  // both bf16 parts, as the operand of the products with the queries
 #pragma unroll
       for (int c = 0; c < NC; c += 8) {
@@ -726,8 +731,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           }
         }
       }
-      sync();
-      if (*abort) return;
+      if (!meet() || __any_sync(~0u, *abort)) return false;
 #pragma unroll 1
       for (int b = from; b < (int)blockIdx.x; ++b) {
         const float* at = cp.pub + b * pub_floats(D);
@@ -743,6 +747,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           }
         }
       }
+      return true;
     };
 
     float decay_n = 0.f, decay_f = 0.f;
@@ -757,8 +762,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       if (t.begins) {
         decay_n = decay_f = 0.f;
         if (t.stage == 2) {
-          join(t.before);
-          if (*abort) break;
+          if (!join(t.before)) break;
         } else {
 #pragma unroll
           for (int i = 0; i < NC; i += 4) {
@@ -836,7 +840,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           *reinterpret_cast<uint4*>(smem + L::V0 + to) = make_uint4(0, 0, 0, 0);
         }
         fence_async_smem();
-        sync();
+        if (!meet()) break;
       }
       f_v ^= 1;  // this chunk's
       if (full) {
@@ -957,7 +961,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           *reinterpret_cast<float4*>(to + i * LC_COMPUTE + 4 * tid) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
         if (tid == 0) to[D * D] = decay_n, to[D * D + 1] = decay_f;
         __threadfence();
-        sync();
+        if (!meet()) break;
         if (tid == 0 && !((p.st->stall & MOE_STALL_GRID_BARRIER) && blockIdx.x == 0))
           store_release(&cp.flags[blockIdx.x], 1u);
       } else if (t.closes && t.slot_out >= 0) {

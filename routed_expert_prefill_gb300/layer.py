@@ -300,8 +300,9 @@ class KvCache:
     lens int32 [n_seq] its tokens.  The caller assigns pages in ``table`` and
     sets ``lens`` (the new tokens included) before moe_kv_append, in place
     (``cache.lens.copy_(...)``, ``cache.table[s, b] = page``), or has
-    moe_kv_plan do both; they are read on the device.  The tensors are kept, not copied, and cannot be replaced by
-    others: calls that use one cache are ordered on one stream.
+    moe_kv_plan do both; they are read on the device.  The tensors are kept, not
+    copied, and cannot be replaced by others: calls that use one cache are
+    ordered on one stream.
 
     held int32 [n_seq, 2], made here, says up to which token each half of a
     sequence's tail is filled (0: not known); moe_kv_append keeps it, and
