@@ -81,19 +81,18 @@ struct alignas(16) Gains {  // read four at a time
   float n, f;          // G_127, whole part and rest
   uint32_t mild;
   float keep, slow;    // a state is multiplied by keep + slow = 2^G_127; slow is 1 for slow decays, else 0
-  Ticket chunk;
 };
 
 struct LcShared {
-  uint64_t qk_full[2], v_full, g_full, g_empty;
+  uint64_t t_full, qk_full[2], v_full, g_full, g_empty;
   uint64_t qk_done, sq_done, pv_done, ds_done;  // products
   uint64_t s_ready, p_ready, k_ready, o_ready;  // their operands, and the results
   uint64_t q_free;                              // the results have been read
   uint64_t met;                                 // the compute warps, all of them
   uint64_t drain;
   Gains g;
-  Part first, last;
-  int at[2][2];  // where the CTA's first and last chunk are: sequence, chunks before it
+  Part first, last;  // the chains of the CTA's first and last chunk
+  Ticket begin, next[2];  // for the compute warps: the first chunk, that behind the one at work
   int scan[LC_THREADS / 32];
   int total, longest;
   uint32_t tmem;
@@ -164,6 +163,41 @@ __device__ __forceinline__ uint32_t take_cut(float2& v) {
   return w;
 }
 
+// A thread's values of a state, 32 bytes at a time (where they begin at a
+// multiple of that): a warp's lanes hold different rows, and with 16 each
+// sector would be asked for twice, with more of them on their way than L1 holds.
+template <int N>
+__device__ __forceinline__ void load_state(float (&S)[N], const float* from) {
+  if ((uintptr_t)from % 32 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(S[i]), "=f"(S[i + 1]), "=f"(S[i + 2]), "=f"(S[i + 3]), "=f"(S[i + 4]), "=f"(S[i + 5]), "=f"(S[i + 6]),
+                     "=f"(S[i + 7])
+                   : "l"(from + i)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(from + i);
+      S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_state(float* to, const float (&S)[N]) {
+  if ((uintptr_t)to % 32 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + i), "f"(S[i]), "f"(S[i + 1]),
+                   "f"(S[i + 2]), "f"(S[i + 3]), "f"(S[i + 4]), "f"(S[i + 5]), "f"(S[i + 6]), "f"(S[i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+  }
+}
+
 __device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
   uint32_t v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -190,7 +224,16 @@ __device__ __forceinline__ Part part_of(const LinearParams& p, int s, int head) 
   t.head = head;
   linear_sequence(p, s, t.row, t.n, t.slot_in, t.slot_out);
   t.c0 = 0;
-  t.c1 = t.nc = chunks_of(p, s, false);
+  t.c1 = t.nc = t.n ? (t.n + CHUNK - 1) / CHUNK : 1;  // of a sequence that has any
+  t.full = true;
+  return t;
+}
+
+// Another head's whole chain of the same sequence.
+__device__ __forceinline__ Part chain_of(Part t, int head) {
+  t.head = head;
+  t.c0 = 0;
+  t.c1 = t.nc;
   t.full = true;
   return t;
 }
@@ -226,7 +269,12 @@ struct Walk {
         t = sh.first;
         whole = t.c0 == 0 && t.c1 == t.nc;
       } else {
-        t = is_last ? sh.last : part_of(p, s, head);
+        if (is_last)
+          t = sh.last;
+        else if (s == sh.first.s || s == sh.last.s)
+          t = chain_of(s == sh.first.s ? sh.first : sh.last, head);
+        else
+          t = part_of(p, s, head);
         whole = t.c1 == t.nc;
       }
       if (is_last) {
@@ -234,7 +282,7 @@ struct Walk {
       } else if (++head == p.hv) {
         head = 0;
         do ++s;
-        while (chunks_of(p, s, false) == 0);  // the last part's sequence has some
+        while (s != sh.last.s && chunks_of(p, s, false) == 0);
       }
       if (whole) {
         stage = 1;
@@ -321,7 +369,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
   if (warp == W_ISSUE) {
     tmem_alloc(&sh.tmem, 512);
     if (lane == 0) {
-      for (uint64_t* b : {&sh.qk_full[0], &sh.qk_full[1], &sh.v_full, &sh.g_full, &sh.qk_done, &sh.sq_done, &sh.pv_done,
+      for (uint64_t* b : {&sh.t_full, &sh.qk_full[0], &sh.qk_full[1], &sh.v_full, &sh.g_full, &sh.qk_done, &sh.sq_done, &sh.pv_done,
                           &sh.ds_done, &sh.drain, &sh.q_free})
         mbar_init(b, 1);
       for (uint64_t* b : {&sh.g_empty, &sh.s_ready, &sh.p_ready, &sh.k_ready, &sh.o_ready, &sh.met}) mbar_init(b, LC_COMPUTE / 32);
@@ -331,10 +379,12 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
   }
 
   // ---- the CTA's run
+  int own_chunks = 0;  // of the thread's first sequence
   {
     int total = 0, longest = 0;
     for (int s = tid; s < p.n_seq; s += LC_THREADS) {
       const int c = chunks_of(p, s, blockIdx.x == 0);
+      if (s == tid) own_chunks = c;
       total += c;
       longest = max(longest, c);
     }
@@ -358,7 +408,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
   if (a < b) {
     int before = 0;
     for (int s0 = 0; s0 < p.n_seq; s0 += LC_THREADS) {
-      const int s = s0 + tid, c = s < p.n_seq ? chunks_of(p, s, false) : 0;
+      const int s = s0 + tid, c = s0 == 0 ? own_chunks : s < p.n_seq ? chunks_of(p, s, false) : 0;
       int in = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -374,22 +424,20 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         before += sh.scan[i];
       }
       const int64_t lo = (int64_t)(base + in - c) * p.hv, hi = lo + (int64_t)c * p.hv;
-      if (lo <= a && a < hi) sh.at[0][0] = s, sh.at[0][1] = base + in - c;
-      if (lo < b && b <= hi) sh.at[1][0] = s, sh.at[1][1] = base + in - c;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      Part t = part_of(p, sh.at[0][0], 0);
-      int64_t off = a - (int64_t)sh.at[0][1] * p.hv;
-      t.head = (int)(off / t.nc);
-      t.c0 = (int)(off % t.nc);
-      t.c1 = (int)min((int64_t)t.nc, t.c0 + (b - a));
-      sh.first = t;
-      Part u = part_of(p, sh.at[1][0], 0);
-      off = b - 1 - (int64_t)sh.at[1][1] * p.hv;
-      u.head = (int)(off / u.nc);
-      u.c1 = (int)(off % u.nc) + 1;
-      sh.last = u.s == t.s && u.head == t.head ? t : u;
+      if (lo <= a && a < hi) {
+        const int off = (int)(a - lo);
+        Part t = part_of(p, s, off / c);
+        t.c0 = off % c;
+        t.c1 = (int)min((int64_t)c, t.c0 + (b - a));
+        sh.first = t;
+      }
+      if (lo < b && b <= hi) {
+        const int off = (int)(b - 1 - lo);
+        Part t = part_of(p, s, off / c);
+        t.c0 = (int)max((int64_t)0, a - lo - (int64_t)t.head * c);
+        t.c1 = off % c + 1;
+        sh.last = t;
+      }
     }
   }
   __syncthreads();
@@ -531,11 +579,13 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       };
       Ticket now = w.ticket();
       load_qk(now);
+      // all CTAs begin at once: what the first chunk needs first goes ahead of the rest
+      uint32_t f_first = 0;
+      bool ok = wait(&sh.qk_full[0], f_first, 79);
       load_v(now);
       Ticket next = advance();
       if (next.on) load_qk(next);
-      bool ok = true;
-      while (now.on) {
+      while (ok && now.on) {
         const Ticket ahead = advance();
         if (!(ok = wait(&sh.ds_done, f_ds, 66))) break;
         if (next.on) load_v(next);
@@ -581,36 +631,40 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       constexpr float UNIT = 0x1p40f, PER_UNIT = 0x1p-40f;
       const auto load = [&](const Ticket& c, float (&g)[4]) {
         if (!c.on) return;
-        if (c.begins && c.full && c.stage < 2 && c.slot_in >= 0) {  // the state that the part begins from
-          const float* from = p.states + ((size_t)c.slot_in * p.hv + c.head) * D * D;
-          for (int i = lane; i < D * D / 32; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + 32 * i));
-        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 4 * lane + i;
-          g[i] = r < c.rows ? decay_of(p.log_decay[(size_t)(c.row + r) * p.decay_stride + c.head]) : 0.f;
+          g[i] = r < c.rows ? p.log_decay[(size_t)(c.row + r) * p.decay_stride + c.head] : 0.f;
         }
       };
       Walk w;
       w.begin(p, sh);
       uint32_t f_empty = 1;
       Ticket c = w.ticket();
+      if (lane == 0) {
+        sh.begin = c;
+        mbar_arrive(&sh.t_full);
+      }
       float g[4];
       load(c, g);
-      while (c.on) {
+      for (int buf = 0; c.on; buf ^= 1) {
         long long v[4], at = 0;
         bool bad[4], nan = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // log2(e) in two parts, the product's rounding kept
-          const float l = g[i] * LOG2E, rest = fmaf(g[i], LOG2E_REST, fmaf(g[i], LOG2E, -l));
-          bad[i] = nan |= g[i] != g[i];
+          const float x = decay_of(g[i]), l = x * LOG2E, rest = fmaf(x, LOG2E_REST, fmaf(x, LOG2E, -l));
+          bad[i] = nan |= x != x;
           at += l < LEAST ? (long long)LEAST * (1ll << 40) : __float2ll_rn(l * UNIT) + __float2ll_rn(rest * UNIT);
           v[i] = at;
         }
         w.next(p, sh);
         const Ticket ahead = w.ticket();
         load(ahead, g);  // their values come while this chunk's are worked out
+        if (ahead.on && ahead.begins && ahead.full && ahead.stage < 2 && ahead.slot_in >= 0) {  // the state that a part begins from
+          const float* from = p.states + ((size_t)ahead.slot_in * p.hv + ahead.head) * D * D;
+          for (int i = lane; i < D * D / 32; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + 32 * i));
+        }
         long long in = at;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -666,15 +720,10 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           to.keep = keep;
           to.slow = slow ? 1.f : 0.f;
         }
-        if (lane == 30) to.chunk = c;
+        if (lane == 30) sh.next[buf] = ahead;  // the compute warps have read the one of two chunks ago
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.g_full);
         c = ahead;
-      }
-      if (wait(&sh.g_empty, f_empty, 67)) {  // the end
-        if (lane == 0) sh.g.chunk.on = false;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.g_full);
       }
     }
   } else {
@@ -682,7 +731,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
     const int quarter = warp & 3, group = warp >> 2;
     const int row = 32 * quarter + lane;  // of the chunk, in the products whose rows are the queries'
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-    uint32_t f_qk[2] = {}, f_v = 0, f_g = 0, f_sc = 0, f_sq = 0, f_pv = 0, f_ds = 0, f_met = 0;
+    uint32_t f_qk[2] = {}, f_v = 0, f_g = 0, f_sc = 0, f_sq = 0, f_pv = 0, f_ds = 0, f_met = 0, f_t = 0;
     float S[NC];
     // rows of the state in TMEM: lanes, the upper 64 a copy of the lower with D = 64
     const int s_row = row % D;
@@ -751,30 +800,28 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
     };
 
     float decay_n = 0.f, decay_f = 0.f;
-    for (int buf = 0; a < b; buf ^= 1) {
-      if (!wait(&sh.g_full, f_g, 70)) break;
-      const Ticket t = sh.g.chunk;
-      if (!t.on) break;
+    Ticket t;
+    t.on = a < b && wait(&sh.t_full, f_t, 78);
+    if (t.on) t = sh.begin;
+    for (int buf = 0; t.on; t = sh.next[buf], buf ^= 1) {
       const bool full = t.full;
       const int rows = t.rows;
-      const float keep = sh.g.keep, slow = sh.g.slow;
-      const bool mild = sh.g.mild >> quarter & 1;
       if (t.begins) {
         decay_n = decay_f = 0.f;
         if (t.stage == 2) {
           if (!join(t.before)) break;
         } else {
 #pragma unroll
-          for (int i = 0; i < NC; i += 4) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (full && t.slot_in >= 0) v = *reinterpret_cast<const float4*>(state_at(t.slot_in, t.head) + i);
-            S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
-          }
+          for (int i = 0; i < NC; ++i) S[i] = 0.f;
+          if (full && t.slot_in >= 0) load_state(S, state_at(t.slot_in, t.head));
         }
       }
       if (full) write_state();
       tc_fence_before();
       arrive(&sh.s_ready);
+      if (!wait(&sh.g_full, f_g, 70)) break;
+      const float keep = sh.g.keep, slow = sh.g.slow;
+      const bool mild = sh.g.mild >> quarter & 1;
       decay_n += sh.g.n;
       decay_f += sh.g.f;
       if (full) {
@@ -965,9 +1012,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         if (tid == 0 && !((p.st->stall & MOE_STALL_GRID_BARRIER) && blockIdx.x == 0))
           store_release(&cp.flags[blockIdx.x], 1u);
       } else if (t.closes && t.slot_out >= 0) {
-#pragma unroll
-        for (int i = 0; i < NC; i += 4)
-          *reinterpret_cast<float4*>(state_at(t.slot_out, t.head) + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+        store_state(state_at(t.slot_out, t.head), S);
       }
     }
   }
