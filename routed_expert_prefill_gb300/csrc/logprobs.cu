@@ -17,6 +17,7 @@ constexpr int LP_RING = 12;       // 16-byte vectors of a thread on their way or
 constexpr int LP_GROUP = 8;       // tiles between two rankings, at most
 constexpr int LP_TOP = 32;        // alternatives, at most
 constexpr int LP_CAND = 512;      // candidates that wait to be ranked
+constexpr int LP_GROUPS = 64;     // of threads, whose largest values bound the alternatives
 constexpr int LP_CLUSTER = 8;     // CTAs of a row, at most
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float FAR = -1e30f;     // stands for -inf where it is multiplied by zero
@@ -98,7 +99,9 @@ struct Shared {
   uint64_t best[LP_TOP];
   Stats part[LP_THREADS / 32];
   Stats all;
-  alignas(16) float group[32];
+  float largest[LP_THREADS];
+  alignas(16) float group[LP_GROUPS];
+  float bound;
   float thr;  // the top-th largest value so far, once there are as many; -inf before
   int count;
   int total;
@@ -153,7 +156,7 @@ __device__ int rank_candidates(Shared& sh, int top) {
 // candidates are ranked, which gives the next bound.  A CTA's elements come in
 // ascending order, tile by tile, so that an equal value of a later group takes
 // no earlier one's place.  While there are too few candidates for a bound, the
-// maxima of 32 groups of threads give one: the top-th largest of them is
+// maxima of 64 groups of threads give one: the top-th largest of them is
 // reached by as many elements.  -inf never becomes a candidate; a row that has
 // too few other values is filled up at the end.
 //
@@ -212,24 +215,35 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(LogprobParams p
     }
     return lm;
   };
-  // A bound from the largest values of 32 groups of threads.
+  // A bound from the largest values of groups of threads.  A group's threads
+  // are LP_GROUPS apart, so that a short row has values in most of them (4096
+  // bf16 rows of 1000, 20 alternatives: 39 us; with 32 groups of neighbours,
+  // most of them empty, the bound was -inf and all values candidates: 785).
   const auto bound = [&](float lm) {
-    constexpr int G = LP_THREADS / 32;  // threads of a group
-    float g = lm;
-#pragma unroll
-    for (int o = G / 2; o; o >>= 1) g = fmaxf(g, __shfl_xor_sync(~0u, g, o));
-    if (tid % G == 0) sh.group[tid / G] = g;
+    sh.largest[tid] = lm;
     __syncthreads();
-    g = sh.group[lane];
+    if (tid < LP_GROUPS) {
+      float g = lm;
+#pragma unroll
+      for (int i = LP_GROUPS; i < LP_THREADS; i += LP_GROUPS) g = fmaxf(g, sh.largest[tid + i]);
+      sh.group[tid] = g;
+    }
+    __syncthreads();
+    constexpr int SHARE = LP_THREADS / LP_GROUPS, OTHERS = LP_GROUPS / SHARE;  // threads of a value; what each compares it with
+    const int mine = tid / SHARE, j0 = tid % SHARE * OTHERS;
+    const float g = sh.group[mine];
     int above = 0;
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
+    for (int j = j0; j < j0 + OTHERS; j += 4) {
       const float4 o = *reinterpret_cast<const float4*>(sh.group + j);
-      above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g) + (o.x == g & j < lane) + (o.y == g & j + 1 < lane) +
-               (o.z == g & j + 2 < lane) + (o.w == g & j + 3 < lane);
+      above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g) + (o.x == g & j < mine) + (o.y == g & j + 1 < mine) +
+               (o.z == g & j + 2 < mine) + (o.w == g & j + 3 < mine);
     }
-    const uint32_t who = __ballot_sync(~0u, above == p.top - 1);
-    return __shfl_sync(~0u, g, __ffs(who) - 1);
+#pragma unroll
+    for (int o = 1; o < SHARE; o <<= 1) above += __shfl_xor_sync(~0u, above, o);
+    if (tid % SHARE == 0 && above == p.top - 1) sh.bound = g;
+    __syncthreads();
+    return sh.bound;
   };
   const auto add = [&](float f, int index) {  // past the list's end it is dropped, but counted
     const int at = atomicAdd(&sh.count, 1);
