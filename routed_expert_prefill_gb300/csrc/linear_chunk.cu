@@ -402,7 +402,10 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
   // Equal runs, but none so short that joining a chain's runs (a state from L2
   // each) takes longer than the runs do (a twentieth against a twelfth: 2000
   // rows of a head of 128 in 37 us against 41, 8191 rows of four such heads in 58 against 55).
-  const int64_t run = max((all + gridDim.x - 1) / gridDim.x, (int64_t)ceilf(sqrtf(sh.longest / 20.f)));
+  // A chain little longer than a run is not worth a cut, since a run inside it
+  // is passed twice (seven prompts of 5741, 16 heads of 64: 226 us with 34 chunks a run, 201 with a chain's 45).
+  int64_t run = max((all + gridDim.x - 1) / gridDim.x, (int64_t)ceilf(sqrtf(sh.longest / 20.f)));
+  if (sh.longest <= 1.6f * run) run = max(run, (int64_t)sh.longest);
   const int64_t a = run * blockIdx.x, b = min(a + run, all);
   const uint32_t tmem = sh.tmem;
   if (a < b) {
@@ -905,7 +908,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           const int ch = half * (D / 16) + i;
           return (ch >> 3) * L::HALF + sw128_off(r, ch & 7);
         };
-#pragma unroll 4
+#pragma unroll(D == 128 ? 4 : 2)
         for (int i = 0; i < D / 16; ++i) {
           uint4 v = *reinterpret_cast<const uint4*>(kp + off(i));
           if (r >= rows) v = make_uint4(0, 0, 0, 0);

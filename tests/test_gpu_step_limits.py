@@ -83,6 +83,29 @@ def test_linear_attention_chains_that_ctas_share(layer, d, lens, hk, hv):
     check_linear(layer, lens, hk, hv, d, True, seed=len(lens))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,hk,hv", [([600] * 7, 4, 16), ([700, 600, 513] * 5, 2, 8), ([1100, 30, 0, 1000] * 4, 4, 8)])
+def test_linear_attention_runs_about_as_long_as_chains(layer, d, lens, hk, hv):
+    check_linear(layer, lens, hk, hv, d, True, seed=len(lens) + d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [5, 300])
+def test_linear_attention_states_at_an_odd_place(layer, d, n):
+    """A pool that begins at a multiple of 16 bytes that is none of 32."""
+    g = gen(d + n)
+    q, k, v = (randn(g, 2 * n, 2, d).bfloat16() for _ in range(3))
+    logs = -torch.rand(2 * n, 2, generator=g, device="cuda")
+    starts = i32([0, n, 2 * n])
+    first = randn(g, 2, 2, d, d)
+    a = layer.LinearState(first.clone())
+    b = layer.LinearState(torch.empty(first.numel() + 4, device="cuda")[4:].view(first.shape).copy_(first))
+    assert a.states.data_ptr() % 32 == 0 and b.states.data_ptr() % 32 == 16
+    assert torch.equal(layer.moe_linear_attention(q, k, v, logs, starts, a), layer.moe_linear_attention(q, k, v, logs, starts, b))
+    assert torch.equal(a.states, b.states)
+    assert a.read_device_status() == 0 == b.read_device_status()
+
+
 def test_linear_attention_moves_states_of_sequences_without_rows(layer):
     """Between long ones: a sequence without rows leaves its state in another slot, or keeps it."""
     check_linear(layer, [300, 0, 0, 200, 0], 2, 4, 64, True, n_slots=9, pick=([7, 1, 3, -1, -1], [2, 1, 5, 8, 0]))
