@@ -342,16 +342,20 @@ __device__ __noinline__ float weighted_values(const LinearParams& p, int d, int 
 // whole run lies inside a chain, what it adds is worked out first, without
 // results.
 //
-// What bounds it (D = 128): a chunk takes some 11800 clocks.  Its 64 products
+// What bounds it (D = 128): a chunk takes some 9000 clocks.  Its 64 products
 // of 128 x 128 x 16 take 6500 (100 each beside the conversions' traffic, 66
 // alone) and shared memory moves 800 KB, 6300 clocks' worth, more than half of
 // it the products' operands; the conversions (weights, keys in three parts, the
 // state in two) are as long as the products and overlap with them in part:
 // queries times state beside the weights, weights times values beside the
-// keys, keys times values beside the results.  Six prompts of 13355 rows and 32
-// heads, 355 MB: 148 us, 0.35 of the copy rate; heads of 64 take 6800 clocks a
-// chunk.  Slower: 16 compute warps of 96 registers (158 us), the keys' parts in
-// bf16 arithmetic (154), a chunk's code unrolled (180 KB; 208).
+// keys, keys times values beside the results.  A chunk's code is run once a
+// chunk and fetched as often, so that short loops beat unrolled ones.  Six
+// prompts of 13355 rows and 32 heads, 355 MB: 128 us, 0.41 of the copy rate; of
+// heads of 64, 89 us.  Slower: 16 compute warps of 96 registers, the keys' parts
+// in bf16 arithmetic, keys converted in halves with the first one's products
+// beside the second, queries in TMEM for both of their products, loops over 32
+// keys and results instead of 16 (138; heads of 64: 107), a chunk's code
+// unrolled (180 KB; 208).
 template <int D>
 __global__ void __launch_bounds__(LC_THREADS, 1)
     linear_chunk_kernel(const __grid_constant__ ChunkParams cp, const __grid_constant__ CUtensorMap tm_q,
@@ -839,44 +843,50 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         // The loops over blocks stay loops: unrolled, a chunk is some 80 KB of
         // code, and fetching it takes longer than running it.
 #pragma unroll 1
-        for (int j0 = 64 * group; j0 < 64 * group + 64; j0 += 32) {
-          if (j0 > 32 * quarter) {
-            const uint32_t none[32] = {};
-            tmem_st<32>(lanes + L::T_S + j0, none);
+        for (int j0 = 64 * group; j0 < 64 * group + 64; j0 += 16) {
+          const int j32 = j0 & ~31;
+          if (j32 > 32 * quarter) {
+            const uint32_t none[16] = {};
+            tmem_st<16>(lanes + L::T_S + j0, none);
             continue;
           }
-          uint32_t z[2][16];
-          tmem_ld16(lanes + L::T_S + j0, z[0]);
-          tmem_ld16(lanes + L::T_S + j0 + 16, z[1]);
+          uint32_t z[16];
+          tmem_ld16(lanes + L::T_S + j0, z);
           tmem_ld_wait();
-          tmem_ld_fence(z[0]);
-          tmem_ld_fence(z[1]);
-          const bool all = j0 < 32 * quarter;
+          tmem_ld_fence(z);
+          const bool all = j32 < 32 * quarter;
           if (!all) {  // a score counts only where its key is seen, whatever it is
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[i >> 4][i & 15] = i <= lane ? z[i >> 4][i & 15] : 0;
+            for (int i = 0; i < 16; ++i) z[i] = i + (j0 & 16) <= lane ? z[i] : 0;
           }
           const float* by = all ? &sh.g.off[16 * quarter * (quarter - 1) + j0] : &sh.g.own[j0];
-          uint32_t w[32];  // of 16 keys each: eight columns of first parts, eight of second ones
+          uint32_t w[16];  // of 16 keys each: eight columns of first parts, eight of second ones
+          float4 by4[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float4 f = *reinterpret_cast<const float4*>(by + 4 * i);
-            if (!mild) {
+          for (int i = 0; i < 4; ++i) by4[i] = *reinterpret_cast<const float4*>(by + 4 * i);
+          if (!mild) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float4& f = by4[i];
               if (all)
                 f = make_float4(f.x * mine, f.y * mine, f.z * mine, f.w * mine);
               else  // (of keys behind the row, not above 1)
                 f = make_float4(ex2(fminf(own - f.x, 0.f)), ex2(fminf(own - f.y, 0.f)), ex2(fminf(own - f.z, 0.f)),
                                 ex2(fminf(own - f.w, 0.f)));
             }
-            const uint32_t* s = &z[i >> 2][4 * (i & 3)];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 f = by4[i];
+            const uint32_t* s = &z[4 * i];
             float2 u = mul2(pair(s), make_float2(f.x, f.y)), v = mul2(pair(s + 2), make_float2(f.z, f.w));
-            uint32_t* o = w + 16 * (i >> 2) + 2 * (i & 3);
+            uint32_t* o = w + 2 * i;
             o[0] = take_rounded(u);
             o[8] = pack_bf16x2(u.x, u.y);
             o[1] = take_rounded(v);
             o[9] = pack_bf16x2(v.x, v.y);
           }
-          tmem_st<32>(lanes + L::T_S + j0, w);
+          tmem_st<16>(lanes + L::T_S + j0, w);
         }
         tmem_st_wait();
       }
@@ -908,7 +918,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           const int ch = half * (D / 16) + i;
           return (ch >> 3) * L::HALF + sw128_off(r, ch & 7);
         };
-#pragma unroll(D == 128 ? 4 : 2)
+#pragma unroll 2
         for (int i = 0; i < D / 16; ++i) {
           uint4 v = *reinterpret_cast<const uint4*>(kp + off(i));
           if (r >= rows) v = make_uint4(0, 0, 0, 0);
@@ -943,28 +953,21 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
         };
         float2 finite = both(0.f);  // NaN: a value that is not finite has met the rows before its own
 #pragma unroll 1
-        for (int col = group * (D / 2); col < (group + 1) * (D / 2); col += 32) {
-          uint32_t x[2][16], y[2][16];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tmem_ld16(lanes + L::T_SQ + col + 16 * h, x[h]);
-            tmem_ld16(lanes + L::T_PV + col + 16 * h, y[h]);
-          }
+        for (int col = group * (D / 2); col < (group + 1) * (D / 2); col += 16) {
+          uint32_t x[16], y[16], o[8];
+          tmem_ld16(lanes + L::T_SQ + col, x);
+          tmem_ld16(lanes + L::T_PV + col, y);
           tmem_ld_wait();
+          tmem_ld_fence(x);
+          tmem_ld_fence(y);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tmem_ld_fence(x[h]);
-            tmem_ld_fence(y[h]);
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              finite = fma2(pair(y[h] + i), both(0.f), finite);
-              const float2 v = fma2(pair(x[h] + i), both(p.scale * first), mul2(pair(y[h] + i), both(p.scale * mine)));
-              o[i / 2] = pack_bf16x2(v.x, v.y);
-            }
-            put(col + 16 * h, make_uint4(o[0], o[1], o[2], o[3]));
-            put(col + 16 * h + 8, make_uint4(o[4], o[5], o[6], o[7]));
+          for (int i = 0; i < 16; i += 2) {
+            finite = fma2(pair(y + i), both(0.f), finite);
+            const float2 v = fma2(pair(x + i), both(p.scale * first), mul2(pair(y + i), both(p.scale * mine)));
+            o[i / 2] = pack_bf16x2(v.x, v.y);
           }
+          put(col, make_uint4(o[0], o[1], o[2], o[3]));
+          put(col + 8, make_uint4(o[4], o[5], o[6], o[7]));
         }
         if (__any_sync(~0u, finite.x + finite.y != 0.f && row < rows)) {
 #pragma unroll 1
