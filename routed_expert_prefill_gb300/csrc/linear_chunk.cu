@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
   // each) takes longer than the runs do (a twentieth against a twelfth: 2000
   // rows of a head of 128 in 37 us against 41, 8191 rows of four such heads in 58 against 55).
   // A chain little longer than a run is not worth a cut, since a run inside it
-  // is passed twice (seven prompts of 5741, 16 heads of 64: 226 us with 34 chunks a run, 201 with a chain's 45).
+  // is passed twice (seven prompts of 5741, 16 heads of 64: 226 us with 34 chunks a run, 195 with a chain's 45).
   int64_t run = max((all + gridDim.x - 1) / gridDim.x, (int64_t)ceilf(sqrtf(sh.longest / 20.f)));
   if (sh.longest <= 1.6f * run) run = max(run, (int64_t)sh.longest);
   const int64_t a = run * blockIdx.x, b = min(a + run, all);
