@@ -33,7 +33,7 @@ constexpr float MILD = 40.f;
 // What one CTA leaves for those that go on with its last chain: the state
 // behind its part (or, if its part does not begin the chain, what the part
 // adds) in the order in which its threads hold it, and the part's decay.
-constexpr int PUB_EXTRA = 64;  // floats behind the state: log2 of the decay, whole part and rest
+constexpr int PUB_EXTRA = 64;  // floats behind the state: the decay's factor, as Gains' keep and slow
 __host__ __device__ constexpr size_t pub_floats(int d) { return (size_t)d * d + PUB_EXTRA; }
 
 // Behind the status block of the workspace.
@@ -70,6 +70,20 @@ struct Ticket {
   bool on;                // there is a chunk
 };
 
+// Log2 decays as whole numbers of 2^-40: their sums and differences are exact.
+constexpr float UNIT = 0x1p40f, PER_UNIT = 0x1p-40f;
+// A part's decay as it counts: below it, it is 0.
+constexpr long long PART_LEAST = -(1ll << 52);
+
+// A state is multiplied by keep + slow = 2^g, slow 1 where the decay is slow:
+// 2^g rounded to fp32 would be off by the same 2^-25 for every chunk.  (A
+// function of its own: inlined at both places it made all chunks slower.)
+__device__ __noinline__ void factor_of(float g, float& keep, float& slow) {
+  const bool is_slow = g > -0.5f;
+  keep = is_slow ? expm1f(g * LN2) : exp2f(g);
+  slow = is_slow ? 1.f : 0.f;
+}
+
 // The decays of a chunk's rows: G_i is the log2 of the product of rows 0 .. i's.
 struct alignas(16) Gains {  // read four at a time
   // with R_i = G_i less that of the first of its 32 rows: 2^-R_i where none of
@@ -78,7 +92,7 @@ struct alignas(16) Gains {  // read four at a time
   float last[CHUNK];   // 2^(G_127 - G_i)
   float first[CHUNK];  // 2^G_i
   float off[192];      // rows 32 q .. of q = 1, 2, 3, for i < 32 q: 2^(G_32q - G_i)
-  float n, f;          // G_127, whole part and rest
+  long long end;       // G_127 in whole numbers of 2^-40
   uint32_t mild;
   float keep, slow;    // a state is multiplied by keep + slow = 2^G_127; slow is 1 for slow decays, else 0
 };
@@ -634,8 +648,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       __syncwarp();
     } else if (warp == W_GAIN && a < b) {
       // ---- decays: four rows a lane, a chunk ahead in registers, their values another one ahead.
-      // G as whole numbers of 2^-40: sums and differences are exact (in fp64 they took 6000 clocks a chunk).
-      constexpr float UNIT = 0x1p40f, PER_UNIT = 0x1p-40f;
+      // (In fp64 their sums took 6000 clocks a chunk.)
       const auto load = [&](const Ticket& c, float (&g)[4]) {
         if (!c.on) return;
 #pragma unroll
@@ -703,9 +716,9 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) off[q][i] = ex2(value(ref - v[i]));
         }
-        const float whole = value(end);
-        const bool slow = whole > -0.5f;
-        float keep = nans ? NOT_A_NUMBER : slow ? expm1f(whole * LN2) : exp2f(whole);
+        float keep, slow;
+        factor_of(value(end), keep, slow);
+        if (nans) keep = NOT_A_NUMBER;
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // worked out before the wait, not behind it
           asm volatile("" : "+f"(own[i]), "+f"(last[i]), "+f"(first[i]), "+f"(off[0][i]), "+f"(off[1][i]), "+f"(off[2][i]), "+f"(keep));
@@ -720,12 +733,10 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
           if (lane < 8 * q + 8)
             *reinterpret_cast<float4*>(&to.off[16 * q * (q + 1) + r]) = make_float4(off[q][0], off[q][1], off[q][2], off[q][3]);
         if (lane == 31) {
-          const long long n = end >> 40;
-          to.n = nans ? NOT_A_NUMBER : (float)n;
-          to.f = value(end - (n << 40));
           to.mild = (milds & 1) | (milds >> 8 & 1) << 1 | (milds >> 16 & 1) << 2 | (milds >> 24 & 1) << 3;
           to.keep = keep;
-          to.slow = slow ? 1.f : 0.f;
+          to.slow = slow;
+          to.end = end;
         }
         if (lane == 30) sh.next[buf] = ahead;  // the compute warps have read the one of two chunks ago
         __syncwarp();
@@ -791,22 +802,22 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
 #pragma unroll 1
       for (int b = from; b < (int)blockIdx.x; ++b) {
         const float* at = cp.pub + b * pub_floats(D);
-        const float f = b == from ? 0.f : exp2f(__ldcg(at + D * D) + __ldcg(at + D * D + 1));
+        const float keep = __ldcg(at + D * D), slow = __ldcg(at + D * D + 1);
 #pragma unroll
         for (int i = 0; i < NC; i += 4) {
           const float4 v = __ldcg(reinterpret_cast<const float4*>(at + i * LC_COMPUTE + 4 * tid));
           if (b == from) {
             S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
           } else {
-            S[i] = fmaf(S[i], f, v.x), S[i + 1] = fmaf(S[i + 1], f, v.y), S[i + 2] = fmaf(S[i + 2], f, v.z),
-            S[i + 3] = fmaf(S[i + 3], f, v.w);
+            S[i] = fmaf(S[i], slow, fmaf(S[i], keep, v.x)), S[i + 1] = fmaf(S[i + 1], slow, fmaf(S[i + 1], keep, v.y));
+            S[i + 2] = fmaf(S[i + 2], slow, fmaf(S[i + 2], keep, v.z)), S[i + 3] = fmaf(S[i + 3], slow, fmaf(S[i + 3], keep, v.w));
           }
         }
       }
       return true;
     };
 
-    float decay_n = 0.f, decay_f = 0.f;
+    long long decay = 0;  // of the part, exact (one that is NaN shows in its state)
     Ticket t;
     t.on = a < b && wait(&sh.t_full, f_t, 78);
     if (t.on) t = sh.begin;
@@ -814,7 +825,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       const bool full = t.full;
       const int rows = t.rows;
       if (t.begins) {
-        decay_n = decay_f = 0.f;
+        decay = 0;
         if (t.stage == 2) {
           if (!join(t.before)) break;
         } else {
@@ -829,8 +840,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       if (!wait(&sh.g_full, f_g, 70)) break;
       const float keep = sh.g.keep, slow = sh.g.slow;
       const bool mild = sh.g.mild >> quarter & 1;
-      decay_n += sh.g.n;
-      decay_f += sh.g.f;
+      decay = max(decay + sh.g.end, PART_LEAST);
       if (full) {
         // weights: scores times the decays between key and query, in two bf16
         // parts over the scores' own columns.  The decay is a row's factor
@@ -1012,7 +1022,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < NC; i += 4)
           *reinterpret_cast<float4*>(to + i * LC_COMPUTE + 4 * tid) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-        if (tid == 0) to[D * D] = decay_n, to[D * D + 1] = decay_f;
+        if (tid == 0) factor_of((float)decay * PER_UNIT, to[D * D], to[D * D + 1]);
         __threadfence();
         if (!meet()) break;
         if (tid == 0 && !((p.st->stall & MOE_STALL_GRID_BARRIER) && blockIdx.x == 0))
