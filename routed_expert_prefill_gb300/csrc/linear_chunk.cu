@@ -999,6 +999,7 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
       tc_fence_after();
       // a slow decay as in the recurrent kernel
       constexpr int AT_ONCE = NC < 32 ? 1 : 2;
+      if (rows > 0)  // else the state is carried over as it is
 #pragma unroll
       for (int j = 0; j < NC / 16; j += AT_ONCE) {
         uint32_t x[AT_ONCE][16];

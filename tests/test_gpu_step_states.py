@@ -61,3 +61,29 @@ def test_linear_attention_states_of_slow_decays(layer, n, hk, hv, d, each):
     bound = (100 + 4 * math.sqrt(2 * chunks + 3 * min(chunks, 152)) + 4 * total.abs()) * F32
     off = (state.states[0].to(F64) - ref).norm(dim=(1, 2)) / ref.norm(dim=(1, 2))
     assert (off <= bound).all(), f"worst {float((off / bound).max()):.3g} of the bound, off by {float(off.max()):.3g}"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[300, 0, 0, 200, 0], [3, 0, 0, 1, 0], [0, 0, 700, 0, 0]])
+def test_linear_attention_carries_states_over_bit_for_bit(layer, d, lens):
+    """A sequence without rows: the state in its other slot is the one that it had, whatever its values."""
+    g = gen(d + lens[0])
+    n, hv = sum(lens), 3
+    q, k, v = (randn(g, n, hv, d).bfloat16() for _ in range(3))
+    starts = [0]
+    for x in lens:
+        starts.append(starts[-1] + x)
+    first = randn(g, 10, hv, d, d)
+    first[:, 0, 0, :4] = torch.tensor([math.inf, -math.inf, -0.0, 1e-42], device="cuda")
+    first[:, 1, 5] = 3.4028e38
+    first[:, 2, :, 7].view(torch.int32).fill_(0x7fa00001)  # a NaN of its own
+    state = layer.LinearState(first.clone())
+    slots, slots_out = [0, 1, -1, 3, 4], [5, 6, 7, 8, 9]
+    layer.moe_linear_attention(q, k, v, torch.full((hv,), -0.1, device="cuda"), i32(starts), state, i32(slots), i32(slots_out))
+    assert state.read_device_status() == 0
+    bits = lambda x: x.view(torch.int32)  # noqa: E731
+    for s, (a, b) in enumerate(zip(slots, slots_out)):
+        if lens[s] == 0:
+            was = first[a] if a >= 0 else torch.zeros_like(first[0])
+            assert torch.equal(bits(state.states[b]), bits(was)), f"sequence {s}"
+    assert torch.equal(bits(state.states[:5]), bits(first[:5]))
