@@ -12,7 +12,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_layer import F64, gen, i32, layer, randn  # noqa: E402, F401
+from test_gpu_layer import F64, gen, i32, layer, randn, within  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -61,6 +61,25 @@ def test_linear_attention_states_of_slow_decays(layer, n, hk, hv, d, each):
     bound = (100 + 4 * math.sqrt(2 * chunks + 3 * min(chunks, 152)) + 4 * total.abs()) * F32
     off = (state.states[0].to(F64) - ref).norm(dim=(1, 2)) / ref.norm(dim=(1, 2))
     assert (off <= bound).all(), f"worst {float((off / bound).max()):.3g} of the bound, off by {float(off.max()):.3g}"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [0, 37, 99])
+def test_linear_attention_keeps_the_bits_of_a_key(layer, d, at):
+    """One row of a chunk: its key times the decays behind it and its value, to fp32's last bits."""
+    g = gen(at + d)
+    n, hv = 100, 4
+    q, k, v = (randn(g, n, h, d).bfloat16() for h in (1, 1, hv))
+    k[:at], k[at + 1:] = 0, 0
+    logs = -0.02 * torch.rand(n, hv, generator=g, device="cuda")
+    state = layer.LinearState.new(1, hv, d)
+    layer.moe_linear_attention(q, k, v, logs, i32([0, n]), state)
+    behind = torch.exp(logs[at + 1:].to(F64).sum(0))
+    ref = behind[:, None, None] * k[at, 0].to(F64)[None, :, None] * v[at].to(F64)[:, None, :]
+    # the exponent, at most 3, as fp32 (3), the exponential (4), its product
+    # with the key (1), the sums of its three parts, cut (6), and into the
+    # state (2): 16 times 2^-24.  Without the third part it would be 2^-16.
+    within(state.states[0], ref, 16 * F32 * ref.abs() + 1e-38)
 
 
 @pytest.mark.parametrize("d", [64, 128])
