@@ -183,3 +183,12 @@ def test_logprobs_binding_refuses(layer):
         f(x, torch.zeros(4))
     with pytest.raises(ValueError, match="CUDA device"):
         f(x, torch.zeros(4, dtype=torch.int64))
+
+
+def test_names_of_the_package(layer):
+    """The calls and handles are names of the package itself, as those of the other layer operators."""
+    import routed_expert_prefill_gb300 as package
+
+    for name in ("moe_gated_rms_norm", "KvPages", "moe_kv_plan", "LinearState", "moe_linear_attention", "moe_logprobs"):
+        assert name in package.__all__
+        assert getattr(package, name) is getattr(layer, name)
