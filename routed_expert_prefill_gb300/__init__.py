@@ -3,8 +3,9 @@
 The compute runs in the CUDA library ``libmoe_gb300.so`` (see
 ``routed_expert_prefill_gb300.moe`` for the Python binding of the routed block
 and ``routed_expert_prefill_gb300.layer`` for that of the layer operators
-around it and of those of a serving step).  Importing this package does not load the library; ``import
-routed_expert_prefill_gb300.moe`` (or touching one of the names below) does.
+around it and of those of a serving step).  Importing this package does not
+load the library; ``import routed_expert_prefill_gb300.moe`` (or touching one
+of the names below) does.
 """
 
 _MOE = ["moe_route_topk", "moe_build_csr", "moe_experts_fwd"]

@@ -121,8 +121,16 @@ namespace {
 
 size_t linear_ws_bytes(int d) { return sizeof(DeviceStatus) + linear_chunk_ws_bytes(d); }
 
-// Rows of a sequence on average, from which on the chunk kernel takes the call
-// (a chunk of 128 takes as long however few of them are rows).
+// Rows of a sequence on average, above which the chunk kernel takes the call (a
+// chunk of 128 takes as long however few of them are rows).  With 32 heads of
+// 128, recurrent against chunk kernel, caches cold: 64 sequences of 16 rows 118
+// and 138 us, of 24 155 and 140; 8 sequences of 16 26 and 31, of 24 33 and 32.
+// Heads of 64: 64 sequences of 40 71 and 81, of 56 93 and 80; 8 sequences of 16
+// 19 and 22, of 40 33 and 23.
+// What the host knows of a call is t and n_seq, not the lengths: the recurrent
+// kernel's time is that of the longest sequence, so that a prompt among many
+// sequences of a row is slow in it (256 of one row and one of 4096: 3430 us;
+// the two calls apart 167 and 78).
 constexpr int chunk_rows(int d) { return d == 128 ? 24 : 40; }
 
 }  // namespace

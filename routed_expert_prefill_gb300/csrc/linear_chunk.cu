@@ -364,8 +364,8 @@ __device__ __noinline__ float weighted_values(const LinearParams& p, int d, int 
 // queries times state beside the weights, weights times values beside the
 // keys, keys times values beside the results.  A chunk's code is run once a
 // chunk and fetched as often, so that short loops beat unrolled ones.  Six
-// prompts of 13355 rows and 32 heads, 355 MB: 128 us, 0.41 of the copy rate; of
-// heads of 64, 89 us.  Slower: 16 compute warps of 96 registers, the keys' parts
+// prompts of 13355 rows and 32 heads, 355 MB: 127 us, 0.41 of the copy rate; of
+// heads of 64, 93 us.  Slower: 16 compute warps of 96 registers, the keys' parts
 // in bf16 arithmetic, keys converted in halves with the first one's products
 // beside the second, queries in TMEM for both of their products, loops over 32
 // keys and results instead of 16 (138; heads of 64: 107), a chunk's code
@@ -418,10 +418,13 @@ __global__ void __launch_bounds__(LC_THREADS, 1)
   }
   const int64_t all = (int64_t)sh.total * p.hv;
   // Equal runs, but none so short that joining a chain's runs (a state from L2
-  // each) takes longer than the runs do (a twentieth against a twelfth: 2000
-  // rows of a head of 128 in 37 us against 41, 8191 rows of four such heads in 58 against 55).
+  // each) takes longer than the runs do (a twentieth against a twelfth, caches
+  // cold: 2000 rows of a head of 128 in 38 us against 41, 8191 rows of four such
+  // heads in 65 against 59, of heads of 64 in 43 against 42).
   // A chain little longer than a run is not worth a cut, since a run inside it
-  // is passed twice (seven prompts of 5741, 16 heads of 64: 226 us with 34 chunks a run, 195 with a chain's 45).
+  // is passed twice (seven prompts of 5741, 16 heads of 64: 203 us with 34 chunks
+  // a run, 159 with a chain's 45; of heads of 128 259 and 207; but two prompts of
+  // 3108, 32 heads, 25 chunks a chain: 110 with 11 a run, 122 uncut).
   int64_t run = max((all + gridDim.x - 1) / gridDim.x, (int64_t)ceilf(sqrtf(sh.longest / 20.f)));
   if (sh.longest <= 1.6f * run) run = max(run, (int64_t)sh.longest);
   const int64_t a = run * blockIdx.x, b = min(a + run, all);

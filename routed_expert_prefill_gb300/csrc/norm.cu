@@ -172,8 +172,10 @@ __device__ __forceinline__ void copy16(uint4* to, const void* from) {
 // reads itself, so that its own copies are all that it waits for), the weights
 // in registers.  4096 rows of 4096 channels, 8 bytes a channel (19.8 us at the
 // copy rate): 25.9 us, 29.7 with a gate (31.9 and 30.7 with a CTA for each row,
-// whose weights are as much L2 traffic as its rows); what is left is the
-// instructions of conversions and sums.  Three CTAs of 256 threads an SM, two
+// whose weights are as much L2 traffic as its rows).  No unit is at its limit
+// (issue slots 60 %, ALU 41 %, of the warps 35 %): what is left is the
+// latency of a row's steps, conversions and two sums with barriers one after
+// another, with as many warps as the registers leave room for.  Three CTAs of 256 threads an SM, two
 // vectors a thread: four or one vectors, two CTAs or 512 threads took 27.8 to
 // 38 us.  Otherwise a group takes one row: a decoded token's call (2.1 us),
 // which is bound by the latency of its loads and two sums.
@@ -398,7 +400,8 @@ extern "C" int moe_gated_rms_norm(const uint16_t* x, int64_t x_stride, const uin
   if (!isfinite(residual_scale)) return set_error(MOE_EINVAL, "residual_scale is not finite");
   // As above (so that without a norm or a gate behind the block the two calls
   // agree to the last bit), but of many short rows a warp takes each: its sums
-  // have no barriers (65536 rows of 512 channels: 59 -> 48 us; of 1024: 112 -> 97).
+  // have no barriers (65536 rows of 512 channels: 59 -> 48 us; of 1024: 112 -> 97;
+  // 8192 rows, launch and cold caches in it: 16.5 -> 14.5 and 23 -> 21).
   const int nv = h / 8;
   const bool by_warp = t >= 8192 && nv <= 128;
   const int vpt = by_warp ? (nv <= 32 ? 1 : nv <= 64 ? 2 : 4) : nv <= 256 ? 1 : nv <= 512 ? 2 : 4;

@@ -561,6 +561,8 @@ def moe_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     Sequence s begins from the state in slot ``slots[s]`` (int32 [n_seq]; -1:
     zero; default: slot s) and leaves its last one in ``slots_out[s]`` (-1:
     nowhere; default: the same slots).  ``scale`` defaults to 1 / sqrt(d).
+    Long prompts beside many sequences of a row or two cost far less in a call
+    of their own: t / n_seq chooses one kernel for all (moe.h).
     Returns bf16 [t, hv, d] (``out``, which does not overlap the inputs).
     """
     lib = load_library()
