@@ -8,12 +8,13 @@ for ``value``; ``e2e`` copies x in from pinned host memory and the block
 output back every step.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME]
-                    [--workloads LIST|none] [--impl ours|reference]
+                    [--workloads LIST|none] [--impl ours|reference] [--details FILE]
 
 The headline workload is t=4096, h=4096, inter=1536, E=256, k=8 (the largest
 single-GPU configuration); the same line carries, under ``workloads``, the
-skewed t=4096 chunk, the t=512 chunk and the decode-shaped t=1/2/4/8 chunks,
-each timed the same way.
+milliseconds a step of the skewed t=4096 chunk, the t=512 chunk and the
+decode-shaped t=1/2/4/8 chunks, each timed the same way; ``--details FILE``
+keeps their whole records (rates, roofline, kernels).
 
 Timing: W untimed warm-up steps, then exactly K timed steps, each a replay of
 the step captured as a CUDA graph, bracketed by CUDA events on the launching
@@ -702,6 +703,27 @@ def workload_config(w: synth.Workload, m: dict) -> dict:
             "step_t_star_us": sr["t_star_us"]}
 
 
+def short_line(line: dict):
+    """The output line as text, and the records that it only sums up.
+
+    Numbers have seven digits, a kernel is the milliseconds of its launches, an
+    extra workload those of a step, so that the line stays within what the end
+    of a log holds.
+    """
+    def rounded(v, digits=7):
+        if isinstance(v, dict):
+            return {k: rounded(x, digits) for k, x in v.items()}
+        if isinstance(v, list):
+            return [rounded(x, digits) for x in v]
+        return float(f"{v:.{digits}g}") if isinstance(v, float) else v
+
+    details = {key: line[key] for key in ("kernels", "workloads")}
+    short = rounded(line)
+    short["kernels"] = {k: rounded(v["ms"], 5) for k, v in line["kernels"].items()}
+    short["workloads"] = {k: rounded(v["ms_per_step"], 5) for k, v in line["workloads"].items()}
+    return json.dumps(short, separators=(",", ":")), details
+
+
 def run_ours(args, w: synth.Workload, pool):
     ctx = Ctx(args)
     inp = pool.inp if pool is not None else synth.make_inputs(w)
@@ -755,7 +777,11 @@ def run_ours(args, w: synth.Workload, pool):
         "clocks": m["clocks"],
         "workloads": extras,
     }
-    print(json.dumps(line), flush=True)
+    text, details = short_line(line)
+    if args.details:
+        with open(args.details, "w") as f:
+            json.dump(details, f)
+    print(text, flush=True)
     ctx.barrier()
     if ctx.world > 1:
         ctx.dist.destroy_process_group()
@@ -768,6 +794,7 @@ def main():
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--impl", choices=("ours", "reference"), default="ours")
     ap.add_argument("--workload", default=DEFAULT_WORKLOAD, choices=sorted(synth.WORKLOADS))
+    ap.add_argument("--details", help="file for the records of kernels and extra workloads that the line sums up")
     ap.add_argument("--workloads", default="default",
                     help="extra workloads timed in the same run: comma list, 'none', or 'default' "
                          "(the other benchmark workloads when the headline one is timed)")

@@ -97,6 +97,37 @@ def test_job_throughput_and_single_rank_max():
     assert bench.max_over_ranks(3.5, "cpu") == 3.5
 
 
+def test_gpu_arm_json_line_is_short():
+    """All workloads in the default run: the line stays within the 3000 characters that a log keeps of an output's end."""
+    x = 1 / 3
+    kernels = {f"a_kernel_name_{i}": {"launches": 200, "ms": 10 * x} for i in range(12)}
+    roofline = dict(bound="tensor", achieved=1e4 * x, peak=1e4 * x, unit="TFLOP/s", frac=x, traffic=1e9 * x, kernel="gateup",
+                    peak_source="measured (burst)", kernel_ms_per_launch=x, kernel_share_of_step=x,
+                    algorithmic_bytes_per_launch=1e10 * x, algorithmic_flops_per_launch=1e12 * x)
+    e2e = dict(value=1e7 * x, unit="tokens/s", h2d_bytes_per_step=33554432, d2h_bytes_per_step=33554432,
+               timing="steps back to back, copies overlapping neighbouring steps (step bytes exceed L2)")
+    clocks = dict(sm_mhz=1000 * x, sm_max_mhz=2070.0, reasons=["sw_power_cap"], samples=14, samples_under_load=7, power_w_max=400 * x)
+    sustained = dict(runs=672, median_ms=x, mean_ms=x, p10_ms=x, p90_ms=x, wall_s=x, device_s=x)
+    config = {f"key_of_config_{i}": 1e6 * x for i in range(20)} | {"timing": "t" * 120, "l2": "l" * 100}
+    record = dict(value=1e7 * x, unit="tokens/s", ms_per_step=x, config=config, roofline=roofline, e2e=e2e, gpu_launches=200,
+                  sustained=sustained, clocks=clocks, kernels=kernels)
+    line = dict(metric=bench.METRIC, value=1e7 * x, unit="tokens/s", n_gpus=8, steps=20, warmup=5, ms_per_step=x,
+                higher_is_better=True, scaling="weak", vs_baseline=None, dtype="bf16", data="synthetic", config=config,
+                step_roofline_frac=x, roofline=roofline, cpu_baseline=dict(value=100 * x, unit="tokens/s", cores=16, kind="oracle",
+                                                                           sample="s" * 110), e2e=e2e, gpu_launches=200,
+                sustained=sustained, kernels=kernels, clocks=clocks,
+                workloads={f"t4096_h4096_e256_streamed_{i}": record for i in range(11)})
+    text, details = bench.short_line(line)
+    assert len(text) < 2900 and "\n" not in text
+    short = json.loads(text)
+    assert list(short) == list(line) and short["value"] == pytest.approx(line["value"], rel=1e-6)
+    for key in ("metric", "n_gpus", "steps", "warmup", "scaling", "dtype", "data", "gpu_launches", "vs_baseline"):
+        assert short[key] == line[key]
+    assert short["clocks"]["reasons"] == clocks["reasons"] and short["e2e"]["h2d_bytes_per_step"] == 33554432
+    assert short["workloads"] == {k: pytest.approx(x, rel=1e-4) for k in line["workloads"]}
+    assert details["workloads"] == line["workloads"] and details["kernels"] == kernels
+
+
 def test_measured_traffic_is_tied_to_the_kernel_sources():
     assert bench.measured_traffic("no_such_workload", "gateup", 16) is None
     for (wl, fam, fl), m in bench.MEASURED_TRAFFIC.items():
